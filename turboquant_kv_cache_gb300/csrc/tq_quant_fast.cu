@@ -356,10 +356,16 @@ int launch_fast(const CodecParams& P, FastQuantArgs& a, cudaStream_t st) {
       cudaDeviceGetAttribute(&smem_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev);
       cudaDeviceGetAttribute(&smem_blk_res, cudaDevAttrReservedSharedMemoryPerBlock, dev);
       // stages (+ 1024 bytes of alignment slack), B of every block, cell table
-      const size_t smem = 1024 + (size_t)kStages * 128 * kTileCols * 2 + (size_t)P.nb * BLK * BLK * 2 +
-                          (size_t)(kMaxCells + 1) * 32 * 4;
+      auto smem_of = [](int nb) {
+        return 1024 + (size_t)kStages * 128 * kTileCols * 2 + (size_t)nb * BLK * BLK * 2 +
+               (size_t)(kMaxCells + 1) * 32 * 4;
+      };
+      const size_t smem = smem_of(P.nb);
       cudaFuncAttributes fa;
-      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+      // one limit for every head_dim, the largest: the kernel is shared by
+      // them, and a smaller head_dim's first call must not lower it
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(kMaxDim / BLK)) !=
+              cudaSuccess ||
           cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess ||
           cudaFuncGetAttributes(&fa, kern) != cudaSuccess)
         return TQ_ERR_CUDA;
