@@ -368,6 +368,139 @@ int tq_prefill_attn(const tq_kv_view* K, const tq_kv_view* V, const uint16_t* q,
 int tq_prefill_workspace_bytes(int B, int Hq, int Hkv, int head_dim, int Tq, int64_t ctx,
                                size_t* bytes);
 
+/* Decode attention of a batch whose sequences share a prefix that is stored
+ * once (a system prompt, a document, the stem of parallel samples).  One
+ * query per (batch, q-head), as tq_decode_attn; batch b attends, in one
+ * softmax, to the prefix tokens [0, min(prefix_ctx, *prefix_len)) and to its
+ * own tokens [0, min(ctx, kv_len[b])).  The prefix's packed codes are decoded
+ * once for all B * Hq / Hkv query rows of a KV head instead of once per
+ * sequence.
+ *   Kp, Vp        the prefix: caches of one sequence, contiguous
+ *                 [1, Hkv, P_cap] or paged with a table of one row
+ *   prefix_len    device int32 [1], or NULL for prefix_ctx
+ *   prefix_ctx    0 <= prefix_ctx <= P_cap
+ *   K, V, S_cap, kv_len, ctx
+ *                 the sequences' own caches as in tq_decode_attn, for the
+ *                 tokens behind the prefix; K and V may be NULL when ctx is 0.
+ *                 Where one page table holds prefix and own pages, the own
+ *                 view's table pointer is moved on by the prefix's pages
+ *   n_split       parts of the own tokens (0: the library's choice; the
+ *                 prefix's parts are always its choice)
+ * K's layout is Kp's and V's is Vp's (every field, else TQ_ERR_ARG), and
+ * takes what tq_decode_attn takes.  workspace: at least
+ * tq_decode_shared_workspace_bytes(...) bytes, 16-byte aligned.  Layouts of
+ * 1..4 bits without QJL decode the prefix on the tensor cores for all rows at
+ * once; other layouts read it per sequence. */
+int tq_decode_attn_shared(const tq_kv_view* Kp, const tq_kv_view* Vp, int64_t P_cap, const int32_t* prefix_len,
+                          int64_t prefix_ctx, const tq_kv_view* K, const tq_kv_view* V, const uint16_t* q, int B,
+                          int Hq, int Hkv, int64_t S_cap, const int32_t* kv_len, int64_t ctx, float softmax_scale,
+                          uint16_t* out, void* workspace, size_t workspace_bytes, int n_split, void* stream);
+
+/* Workspace bytes for tq_decode_attn_shared with these sizes (host). */
+int tq_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int head_dim, int64_t prefix_ctx, int64_t ctx,
+                                     int n_split, size_t* bytes);
+
+/* The projection's rows of new tokens made ready for the cache and the
+ * attention, in one pass: RMS norm of every query and key head, rotary
+ * position, and the layouts that tq_append_kv, tq_decode_attn_window and the
+ * attention calls take.
+ *   qkv        device, token row b*T + j at qkv + (b*T + j)*row_stride
+ *              elements (x_dtype fp16 or fp32, 16-byte aligned rows): Hq query
+ *              heads, Hkv key heads, Hkv value heads of head_dim values
+ *   q_weight, k_weight
+ *              device fp32 [head_dim], or NULL for no norm of that kind:
+ *              y = x / sqrt(mean(x^2) + eps) * weight, eps > 0
+ *   rope       device fp32 [n_pos, rot_dim]: row p holds the rot_dim/2 cosines
+ *              and then the rot_dim/2 sines of position p.  The first rot_dim
+ *              values of a query or key head are rotated, pair i being values
+ *              (i, i + rot_dim/2), or (2i, 2i + 1) when interleaved is 1; the
+ *              rest of the head is kept.  rot_dim 0: no rotation.  Multiples of
+ *              16 up to head_dim, else TQ_ERR_UNSUPPORTED
+ *   pos        device int32 [B] or NULL (0): token j of batch b has position
+ *              pos[b] + j.  With a rotation, tokens whose position is outside
+ *              [0, n_pos) are left out: nothing of theirs is written
+ *   new_len    device int32 [B] or NULL: batch b has new_len[b] tokens, and
+ *              what lies behind them is neither read nor written
+ *   q_out      device fp16 [B, Hq, T, head_dim]
+ *   k_out, v_out, kv_cap, slot
+ *              device fp16 [B, Hkv, kv_cap, head_dim]; token j of batch b goes
+ *              to slot slot[b] + j (slot: device int32 [B], NULL: 0); slots
+ *              outside [0, kv_cap) are not written.  With kv_cap = T and no
+ *              slot these are the rows that tq_append_kv takes; with the fp16
+ *              window's arrays, new tokens go straight into the window.  kv_cap
+ *              0 with NULL outputs: queries only
+ * All sums and products are fp32, rounded once to fp16.  Outputs do not
+ * overlap the input.  TQ_ERR_ALIGN where a pointer is not 16-byte aligned. */
+int tq_qkv_norm_rope(const void* qkv, tq_dtype x_dtype, int B, int T, int Hq, int Hkv, int head_dim,
+                     int64_t row_stride, const float* q_weight, const float* k_weight, float eps, const float* rope,
+                     int64_t n_pos, int rot_dim, int interleaved, const int32_t* pos, const int32_t* new_len,
+                     uint16_t* q_out, uint16_t* k_out, uint16_t* v_out, int64_t kv_cap, const int32_t* slot,
+                     void* stream);
+
+/* The page table of a paged cache and its books, all device memory owned by
+ * the caller.
+ *   page_table   int32 [n_seqs, pages_per_seq]: the tq_kv_view table
+ *   n_pages      int32 [n_seqs]: pages each sequence holds (its row's first
+ *                n_pages entries; the others have no meaning)
+ *   ref          int32 [num_pages]: how many sequences hold each page, 0 = free
+ *   page_size    tokens per page, a positive multiple of 32
+ * A new pool is all zeros in n_pages and ref.  The calls below keep the books
+ * right; they are ordered by the stream, and calls on one pool must not
+ * overlap on the GPU.  At most 2^20 pages per sequence and 2^28 in a pool. */
+typedef struct {
+  int32_t* page_table;
+  int32_t* n_pages;
+  int32_t* ref;
+  int32_t n_seqs;
+  int32_t pages_per_seq;
+  int32_t num_pages;
+  int32_t page_size;
+} tq_page_pool;
+
+/* Sequences begin, fork and grow: entry i (device int32 arrays of n) gives
+ * sequence child[i] pages for new_len[i] tokens.
+ *   parent[i] = -1          a new sequence: share_len[i] is 0
+ *   parent[i] another one   the child shares the pages that the parent's first
+ *                           share_len[i] tokens fill, by reference, and gets a
+ *                           copy of the page that they fill in part; the child
+ *                           must hold no pages
+ *   parent[i] = child[i]    the sequence grows: it keeps its pages, and where
+ *                           the page that token share_len[i] goes to is also
+ *                           held by others it is replaced by a copy of its own
+ * Fresh pages are the free pages in ascending order, dealt to the entries in
+ * order (an entry's by ascending position in its row).  Pages are copied in
+ * all of the caches (every layer's K and V, the views' arrays as
+ * [num_pages, Hkv, page_size] records; their page_table fields are not used).
+ *   result   device int32 [4] or NULL: {status, fresh pages taken, pages
+ *            copied, 0}.  status 0: done.  > 0: so many pages are missing.
+ *            -1: an entry is not valid (a sequence out of range, lengths that
+ *            do not fit, a child that holds pages, a child named twice, a
+ *            parent that is another entry's child).  Unless it is 0 nothing
+ *            has changed
+ *   n        at most n_seqs
+ *   workspace  tq_pages_workspace_bytes(n_seqs, num_pages, n) bytes, 16-byte
+ *            aligned */
+int tq_pages_fork(const tq_page_pool* pool, const tq_kv_view* caches, int n_caches, int Hkv, const int32_t* parent,
+                  const int32_t* child, const int32_t* share_len, const int32_t* new_len, int n, int32_t* result,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* The sequences named (device int32 [n]) give up the pages behind their first
+ * keep_len[i] tokens (device int32 [n]; NULL: all their pages).  A page whose
+ * last holder gives it up is free.  Entries out of range are skipped; a
+ * sequence named twice keeps the smaller length. */
+int tq_pages_free(const tq_page_pool* pool, const int32_t* seqs, const int32_t* keep_len, int n, void* stream);
+
+/* Moves the pages in use to the front of the pool: with n_live of them, the
+ * k-th free page below n_live takes the k-th used page from n_live on, in all
+ * of the caches, and tables and counts follow.
+ *   result   device int32 [4] or NULL: {0, n_live, pages moved, 0}
+ *   workspace  tq_pages_workspace_bytes(n_seqs, num_pages, 0) bytes */
+int tq_pages_compact(const tq_page_pool* pool, const tq_kv_view* caches, int n_caches, int Hkv, int32_t* result,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of the two calls above (host). */
+int tq_pages_workspace_bytes(int n_seqs, int num_pages, int n, size_t* bytes);
+
 /* ---- Device-side waits and status ----------------------------------------
  * The tensor-core prefill (tq_prefill_attn) and the fast quantiser
  * (tq_quantize_kv / tq_append_kv with fp16 input, block 32 or 64, 2-4 bits,

@@ -37,6 +37,12 @@ class tq_kv_view(ctypes.Structure):
                 ("page_table", ctypes.c_void_p), ("page_size", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32)]
 
 
+class tq_page_pool(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("n_pages", ctypes.c_void_p), ("ref", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32)]
+
+
 def _load():
     global _lib
     if _lib is not None:
@@ -67,6 +73,13 @@ def _load():
         "tq_decode_attn_static": (I, [P, P, P, I, I, I, I64, P, I64, ctypes.c_float, P, I, P]),
         "tq_prefill_attn": (I, [P, P, P, I, I, I, I, I64, I64, I, ctypes.c_float, P, P, SZ, P]),
         "tq_prefill_workspace_bytes": (I, [I, I, I, I, I, I64, P]),
+        "tq_decode_attn_shared": (I, [P, P, I64, P, I64, P, P, P, I, I, I, I64, P, I64, ctypes.c_float, P, P, SZ, I, P]),
+        "tq_decode_shared_workspace_bytes": (I, [I, I, I, I, I64, I64, I, P]),
+        "tq_qkv_norm_rope": (I, [P, I, I, I, I, I, I, I64, P, P, ctypes.c_float, P, I64, I, I, P, P, P, P, P, I64, P, P]),
+        "tq_pages_fork": (I, [P, P, I, I, P, P, P, P, I, P, P, SZ, P]),
+        "tq_pages_free": (I, [P, P, P, I, P]),
+        "tq_pages_compact": (I, [P, P, I, I, P, P, SZ, P]),
+        "tq_pages_workspace_bytes": (I, [I, I, I, P]),
         "tq_set_wait_limit_ns": (I, [ctypes.c_uint64]),
         "tq_device_status": (I, [I, I, P]),
         "tq_strerror": (ctypes.c_char_p, [I]),
@@ -101,6 +114,31 @@ def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+class _on:
+    """Makes a tensor's device current for the calls inside (free when it is
+    the current one already)."""
+
+    def __init__(self, t):
+        self.dev = t.device.index
+        self.prev = None
+
+    def __enter__(self):
+        cur = torch.cuda.current_device()
+        if self.dev is not None and self.dev != cur:
+            self.prev = cur
+            torch.cuda.set_device(self.dev)
+
+    def __exit__(self, *exc):
+        if self.prev is not None:
+            torch.cuda.set_device(self.prev)
+
+
+def _i32(t, n, name, like):
+    """Checks an int32 tensor of n values (or None) on like's device."""
+    if t is not None and (t.dtype != torch.int32 or t.numel() != n or t.device != like.device or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} values on {like.device}")
 
 
 def _check(st, where):
@@ -197,6 +235,29 @@ class PackedKV:
         self.rnorm = torch.empty(self.lead_shape, dtype=torch.float16, device=device) if qb else None
         self.S = S
 
+    @classmethod
+    def of(cls, layout, codes, scales, qjl=None, rnorm=None, S=None, page_table=None):
+        """A PackedKV over arrays that exist already (contiguous; the lead
+        shape is codes.shape[:-1]).  A table may be part of a wider one (its
+        rows then lie further apart than they are long)."""
+        cb, ns, qb = tq_layout_sizes(layout)
+        lead = tuple(codes.shape[:-1])
+        if qb and (qjl is None or rnorm is None):
+            raise ValueError("a layout with QJL has its sign bits and residual norms")
+        for t, dt, tail in ((codes, torch.uint8, (cb,)), (scales, torch.float16, (ns,)),
+                            (qjl if qb else None, torch.uint8, (qb,)), (rnorm if qb else None, torch.float16, ())):
+            if t is not None and (t.dtype != dt or tuple(t.shape) != lead + tail or not t.is_contiguous()
+                                  or t.device != codes.device):
+                raise ValueError("arrays must be contiguous, of one lead shape and device, as the layout has them")
+        if page_table is not None and (page_table.dtype != torch.int32 or page_table.dim() != 2 or len(lead) != 3
+                                       or page_table.device != codes.device or page_table.stride(1) != 1):
+            raise ValueError("paged cache: lead shape [num_pages, Hkv, page_size] and an int32 page table "
+                             "[B, pages_per_seq] on its device")
+        self = cls.__new__(cls)
+        self.layout, self.lead_shape, self.page_table, self.S = layout, lead, page_table, S
+        self.codes, self.scales, self.qjl, self.rnorm = codes, scales, qjl, rnorm
+        return self
+
     @property
     def n_vec(self):
         n = 1
@@ -226,7 +287,12 @@ class PackedKV:
                           self.rnorm.data_ptr() if self.rnorm is not None else None,
                           self.S.data_ptr() if self.S is not None else None, self.layout,
                           pt.data_ptr() if pt is not None else None,
-                          self.lead_shape[2] if pt is not None else 0, pt.shape[1] if pt is not None else 0)
+                          self.lead_shape[2] if pt is not None else 0, self._table_stride())
+
+    def _table_stride(self):
+        """Entries between two rows of the table (its width unless it is part of a wider one)."""
+        pt = self.page_table
+        return 0 if pt is None else pt.stride(0) if pt.shape[0] > 1 else pt.shape[1]
 
     def nbytes(self):
         n = self.codes.numel() + 2 * self.scales.numel()
@@ -273,7 +339,7 @@ def tq_append_kv(cache, x, pos, stream=None):
     pt = cache.page_table
     st = lib.tq_append_kv(ctypes.byref(layout), _ptr(x2), _dtype_code(x.dtype), B, H, n_new, x2.stride(0),
                           _ptr(pos.contiguous()), cache.capacity, _ptr(pt),
-                          cache.lead_shape[2] if pt is not None else 0, pt.shape[1] if pt is not None else 0,
+                          cache.lead_shape[2] if pt is not None else 0, cache._table_stride(),
                           _ptr(cache.S), _ptr(cache.codes), _ptr(cache.scales), _ptr(cache.qjl), _ptr(cache.rnorm),
                           _stream(stream))
     _check(st, "tq_append_kv")
@@ -376,6 +442,198 @@ def tq_decode_attn_window(K, V, q, k_win, v_win, ctx=None, kv_len=None, win_len=
                                    _ptr(out), _ptr(workspace), workspace.numel(), n_split, _stream(stream))
     _check(st, "tq_decode_attn_window")
     return out
+
+
+def tq_decode_shared_workspace_bytes(B, Hq, Hkv, head_dim, prefix_ctx, ctx, n_split=0):
+    lib = _load()
+    nb = ctypes.c_size_t()
+    _check(lib.tq_decode_shared_workspace_bytes(B, Hq, Hkv, head_dim, prefix_ctx, ctx, n_split, ctypes.byref(nb)),
+           "tq_decode_shared_workspace_bytes")
+    return nb.value
+
+
+def tq_decode_attn_shared(Kp, Vp, K, V, q, prefix_ctx=None, prefix_len=None, ctx=None, kv_len=None, softmax_scale=0.0,
+                          n_split=0, workspace=None, out=None, stream=None):
+    """Decode attention of q [B, Hq, d] fp16 over a prefix that all B
+    sequences share (Kp, Vp: PackedKV caches of one sequence) and each
+    sequence's own tokens behind it (K, V: caches as in tq_decode_attn, or
+    None when there are none yet).  prefix_len: int32 CUDA tensor of one
+    value, kv_len: int32 CUDA tensor [B]; prefix_ctx and ctx bound them."""
+    lib = _load()
+    if q.dim() != 3 or q.dtype != torch.float16 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous fp16 tensor [B, Hq, head_dim]")
+    B, Hq, d = q.shape
+    Hkv, P_cap = _cache_for(Kp, Vp, 1)
+    prefix_ctx = P_cap if prefix_ctx is None else prefix_ctx
+    S_cap = 0
+    if K is not None and V is not None:
+        heads, S_cap = _cache_for(K, V, B)
+        if heads != Hkv:
+            raise ValueError("prefix and own caches must hold the same heads")
+    ctx = S_cap if ctx is None else ctx
+    for c in (Kp, Vp, K, V):
+        if c is not None and (c.layout.head_dim != d or c.codes.device != q.device):
+            raise ValueError("caches must have q's head_dim and device")
+    _i32(prefix_len, 1, "prefix_len", q)
+    _i32(kv_len, B, "kv_len", q)
+    with _on(q):
+        if workspace is None:
+            need = tq_decode_shared_workspace_bytes(B, Hq, Hkv, d, prefix_ctx, ctx, n_split)
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        if out is None:
+            out = torch.empty_like(q)
+        elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or out.device != q.device:
+            raise ValueError("out must be a contiguous tensor like q")
+        kp, vp = Kp.view(), Vp.view()
+        kv, vv = (K.view(), V.view()) if K is not None and V is not None else (None, None)
+        st = lib.tq_decode_attn_shared(ctypes.byref(kp), ctypes.byref(vp), P_cap, _ptr(prefix_len), prefix_ctx,
+                                       ctypes.byref(kv) if kv else None, ctypes.byref(vv) if vv else None, _ptr(q), B,
+                                       Hq, Hkv, S_cap, _ptr(kv_len), ctx, float(softmax_scale), _ptr(out),
+                                       _ptr(workspace), workspace.numel() * workspace.element_size(), n_split,
+                                       _stream(stream))
+    _check(st, "tq_decode_attn_shared")
+    return out
+
+
+def tq_qkv_norm_rope(qkv, Hq, Hkv, head_dim, q_weight=None, k_weight=None, eps=1e-6, rope=None, interleaved=False,
+                     pos=None, new_len=None, slot=None, q_out=None, k_out=None, v_out=None, stream=None):
+    """Projection rows qkv [B, T, (Hq + 2 Hkv) head_dim] (fp16/fp32, CUDA; rows
+    may lie further apart than they are long) to normalised, rotated queries
+    [B, Hq, T, d] and keys, and values, [B, Hkv, cap, d], all fp16.  q_weight,
+    k_weight: fp32 [d] or None; rope: fp32 [n_pos, rot_dim] (cosines, then
+    sines) or None; pos, new_len, slot: int32 [B] or None.  k_out and v_out
+    default to new arrays of cap = T (cap: their third dimension).  In an
+    output that is given, what no token goes to is left as it was; new ones
+    start as zeros when new_len is given."""
+    lib = _load()
+    d = head_dim
+    if qkv.dim() != 3 or qkv.shape[2] != (Hq + 2 * Hkv) * d or qkv.stride(2) != 1:
+        raise ValueError("qkv must be [B, T, (Hq + 2 Hkv) head_dim] with a contiguous last dimension")
+    B, T, _ = qkv.shape
+    row = qkv.stride(1) if T > 1 else (qkv.stride(0) if B > 1 else qkv.shape[2])
+    if T > 1 and B > 1 and qkv.stride(0) != T * row:
+        qkv = qkv.contiguous()
+        row = qkv.shape[2]
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and (w.dtype != torch.float32 or tuple(w.shape) != (d,) or not w.is_contiguous()
+                              or w.device != qkv.device):
+            raise ValueError(f"{name} must be a contiguous fp32 tensor [head_dim] on qkv's device")
+    if rope is not None and (rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous()
+                             or rope.device != qkv.device):
+        raise ValueError("rope must be a contiguous fp32 tensor [n_pos, rot_dim] on qkv's device")
+    _i32(pos, B, "pos", qkv)
+    _i32(new_len, B, "new_len", qkv)
+    _i32(slot, B, "slot", qkv)
+    new = torch.empty if new_len is None and pos is None and slot is None else torch.zeros
+    if q_out is None:
+        q_out = new((B, Hq, T, d), dtype=torch.float16, device=qkv.device)
+    if k_out is None:
+        k_out = new((B, Hkv, T, d), dtype=torch.float16, device=qkv.device)
+    if v_out is None:
+        v_out = new(tuple(k_out.shape), dtype=torch.float16, device=qkv.device)
+    cap = k_out.shape[2] if k_out.dim() == 4 else -1
+    for o, shape in ((q_out, (B, Hq, T, d)), (k_out, (B, Hkv, cap, d)), (v_out, (B, Hkv, cap, d))):
+        if (o.dtype != torch.float16 or tuple(o.shape) != shape or not o.is_contiguous()
+                or o.device != qkv.device):
+            raise ValueError("outputs must be contiguous fp16 tensors [B, Hq, T, d], [B, Hkv, cap, d] on qkv's device")
+    n_pos, rot = rope.shape if rope is not None else (0, 0)
+    with _on(qkv):
+        st = lib.tq_qkv_norm_rope(_ptr(qkv), _dtype_code(qkv.dtype), B, T, Hq, Hkv, d, row, _ptr(q_weight),
+                                  _ptr(k_weight), float(eps), _ptr(rope), n_pos, rot, 1 if interleaved else 0,
+                                  _ptr(pos), _ptr(new_len), _ptr(q_out), _ptr(k_out), _ptr(v_out), cap, _ptr(slot),
+                                  _stream(stream))
+    _check(st, "tq_qkv_norm_rope")
+    return q_out, k_out, v_out
+
+
+# ------------------------------------------------------------------ page pool
+class PagePool:
+    """The page table of a paged cache and its books: page_table int32
+    [n_seqs, pages_per_seq], n_pages int32 [n_seqs] (pages each sequence
+    holds), ref int32 [num_pages] (sequences that hold each page), and the
+    caches whose pages they name (PackedKV of lead shape [num_pages, Hkv,
+    page_size]: every layer's K and V).  A new pool has zeros in n_pages and
+    ref (PagePool.new)."""
+
+    def __init__(self, page_table, n_pages, ref, page_size, caches=()):
+        for t, dim in ((page_table, 2), (n_pages, 1), (ref, 1)):
+            if t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous() or t.device != page_table.device:
+                raise ValueError("page_table [n_seqs, pages_per_seq], n_pages [n_seqs] and ref [num_pages] must be "
+                                 "contiguous int32 tensors on one device")
+        if n_pages.shape[0] != page_table.shape[0]:
+            raise ValueError("n_pages must have an entry for every row of page_table")
+        self.page_table, self.n_pages, self.ref, self.page_size = page_table, n_pages, ref, page_size
+        self.caches = tuple(caches)
+        self.heads = self.caches[0].lead_shape[1] if self.caches else 0
+        for c in self.caches:
+            if c.lead_shape != (ref.shape[0], self.heads, page_size) or c.codes.device != ref.device:
+                raise ValueError("caches must have lead shape [num_pages, Hkv, page_size] on the pool's device")
+        self.struct = tq_page_pool(page_table.data_ptr(), n_pages.data_ptr(), ref.data_ptr(), page_table.shape[0],
+                                   page_table.shape[1], ref.shape[0], page_size)
+        self.views = (tq_kv_view * max(1, len(self.caches)))(*[c.view() for c in self.caches])
+
+    @classmethod
+    def new(cls, n_seqs, pages_per_seq, num_pages, page_size, caches=(), device="cuda"):
+        z = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=device)  # noqa: E731
+        return cls(z(n_seqs, pages_per_seq), z(n_seqs), z(num_pages), page_size, caches)
+
+
+def tq_pages_workspace_bytes(n_seqs, num_pages, n):
+    nb = ctypes.c_size_t()
+    _check(_load().tq_pages_workspace_bytes(n_seqs, num_pages, n, ctypes.byref(nb)), "tq_pages_workspace_bytes")
+    return nb.value
+
+
+def _pool_call(pool, n, workspace, result):
+    if workspace is None:
+        workspace = torch.empty(tq_pages_workspace_bytes(pool.n_pages.shape[0], pool.ref.shape[0], n),
+                                dtype=torch.uint8, device=pool.ref.device)
+    if result is None:
+        result = torch.empty(4, dtype=torch.int32, device=pool.ref.device)
+    _i32(result, 4, "result", pool.ref)
+    return workspace, result
+
+
+def tq_pages_fork(pool, parent, child, share_len, new_len, workspace=None, result=None, stream=None):
+    """Sequences begin (parent -1), fork (share the full pages of the parent's
+    first share_len tokens, copy the part-filled one) and grow (parent equal
+    to child), so that child[i] holds pages for new_len[i] tokens.  int32 CUDA
+    tensors of one length.  Returns the result tensor {status, pages taken,
+    pages copied, 0}: status 0 done, > 0 pages missing, -1 an entry is not
+    valid; unless it is 0 nothing has changed."""
+    n = child.numel()
+    for t, name in ((parent, "parent"), (child, "child"), (share_len, "share_len"), (new_len, "new_len")):
+        _i32(t, n, name, pool.ref)
+    with _on(pool.ref):
+        workspace, result = _pool_call(pool, n, workspace, result)
+        st = _load().tq_pages_fork(ctypes.byref(pool.struct), pool.views, len(pool.caches), pool.heads, _ptr(parent),
+                                   _ptr(child), _ptr(share_len), _ptr(new_len), n, _ptr(result), _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "tq_pages_fork")
+    return result
+
+
+def tq_pages_free(pool, seqs, keep_len=None, stream=None):
+    """The sequences named (int32 CUDA tensor) give up their pages, or those
+    behind their first keep_len tokens."""
+    n = seqs.numel()
+    _i32(seqs, n, "seqs", pool.ref)
+    _i32(keep_len, n, "keep_len", pool.ref)
+    with _on(pool.ref):
+        st = _load().tq_pages_free(ctypes.byref(pool.struct), _ptr(seqs), _ptr(keep_len), n, _stream(stream))
+    _check(st, "tq_pages_free")
+
+
+def tq_pages_compact(pool, workspace=None, result=None, stream=None):
+    """Moves the pages in use to the front of the pool in all of its caches.
+    Returns the result tensor {0, pages in use, pages moved, 0}."""
+    with _on(pool.ref):
+        workspace, result = _pool_call(pool, 0, workspace, result)
+        st = _load().tq_pages_compact(ctypes.byref(pool.struct), pool.views, len(pool.caches), pool.heads,
+                                      _ptr(result), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                      _stream(stream))
+    _check(st, "tq_pages_compact")
+    return result
 
 
 def tq_to_blocks(pk, stream=None):

@@ -60,6 +60,8 @@ struct DecodeArgs {
   int slots;            // split slots per row (n_split, or more for extra partials)
   float qscale;         // softmax_scale * log2(e)
   int pdl;              // launched as a programmatic dependent of the kernel before it
+  int slot0 = 0;        // first split slot this launch writes
+  int shared = 0;       // every batch reads sequence 0 (a shared prefix; kv_len has one entry)
   // block layout (AOS kernels only): per token d/32 blocks of [fp16 norm of
   // the rotation block, 4*bits code bytes], read as 16-bit units
   const uint16_t* kblk = nullptr;
@@ -168,8 +170,9 @@ __global__ void __launch_bounds__(kDecThreads) decode_split_kernel(const CodecPa
   }
   __syncthreads();
 
+  const int seq = a.shared ? 0 : b;    // the cache's sequence
   int64_t len = a.ctx;
-  if (a.kv_len) len = imin64(len, (int64_t)a.kv_len[b]);
+  if (a.kv_len) len = imin64(len, (int64_t)a.kv_len[seq]);
   const int64_t per = (a.ctx + a.n_split - 1) / a.n_split;
   const int64_t t_begin = (int64_t)split * per;
   const int64_t t_end = imin64(t_begin + per, len);
@@ -186,7 +189,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_split_kernel(const CodecPa
   }
   const int mq = QV ? PV.m / 32 : 0;   // QJL words of a V record
   const int kwords = PK.code_bytes / 4, vwords = PV.code_bytes / 4;
-  auto rec_of = [&](int64_t t) { return cache_rec(a.pages, a.Hkv, a.S_cap, b, kvh, t); };
+  auto rec_of = [&](int64_t t) { return cache_rec(a.pages, a.Hkv, a.S_cap, seq, kvh, t); };
 
   for (int64_t c0 = t_begin + (int64_t)wid * 32; c0 < t_end; c0 += kWarps * 32) {
     const int64_t t = c0 + lane;
@@ -390,7 +393,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_split_kernel(const CodecPa
       }
       smem_wht<D>(s_proj, 1, PV.blk, PV.inv_sqrt_blk);
     }
-    float* dst = a.part + (((int64_t)b * a.Hq + h0 + h) * a.slots + split) * (D + 4);
+    float* dst = a.part + (((int64_t)b * a.Hq + h0 + h) * a.slots + a.slot0 + split) * (D + 4);
     for (int i = threadIdx.x; i < D + 2; i += kDecThreads) {
       float val = 0.f;
       if (i == 0) {
@@ -895,6 +898,17 @@ extern "C" int tq_decode_workspace_bytes(int B, int Hq, int Hkv, int head_dim, i
 namespace tq {
 namespace {
 
+// The CUDA-core split kernel for any layout, head_dim and group size it has.
+int launch_decode_any(const CodecParams& PK, const CodecParams& PV, const DecodeArgs& a, int B, const Codebook8& cbk,
+                      cudaStream_t s) {
+  const int G = a.Hq / a.Hkv;
+  switch (PK.d) {
+    case 64: return launch_decode_g<64>(G, PK, PV, a, B, cbk, s);
+    case 128: return launch_decode_g<128>(G, PK, PV, a, B, cbk, s);
+    default: return launch_decode_g<256>(G, PK, PV, a, B, cbk, s);
+  }
+}
+
 // The fp16 residual window of a decode call (see tq_decode_attn_window).
 struct Window {
   const uint16_t* k;
@@ -968,14 +982,121 @@ int decode_impl(const tq_kv_view* K, const tq_kv_view* V, const uint16_t* q, int
     st = launch_decode_tc(PK, PV, K, V, q, kv_len, a.part, decode_part_bytes(B, Hq, PK.d, slots), B, Hq, Hkv, S_cap,
                           ctx, ns, slots, a.pdl != 0, a.qscale, &cbk, s);
   } else {
-    switch (PK.d) {
-      case 64: st = launch_decode_g<64>(G, PK, PV, a, B, cbk, s); break;
-      case 128: st = launch_decode_g<128>(G, PK, PV, a, B, cbk, s); break;
-      default: st = launch_decode_g<256>(G, PK, PV, a, B, cbk, s); break;
-    }
+    st = launch_decode_any(PK, PV, a, B, cbk, s);
   }
   if (st != TQ_OK) return st;
   return decode_combine(PV, a.part, slots, out, B * Hq, s);
+}
+
+// A view's codes, layouts and paging as the decode takes them.
+int check_cache_pair(const tq_kv_view* K, const tq_kv_view* V, const CodecParams& PK, const CodecParams& PV,
+                     int64_t S_cap) {
+  if (!K->codes || !K->scales || !V->codes || !V->scales) return TQ_ERR_ARG;
+  if (PK.m && (!K->qjl_bits || !K->qjl_rnorm || !K->S)) return TQ_ERR_ARG;
+  if (PV.m && (!V->qjl_bits || !V->qjl_rnorm || !V->S)) return TQ_ERR_ARG;
+  if (check_paging(K, S_cap) != TQ_OK || !same_paging(K, V)) return TQ_ERR_ARG;
+  return aligned16(K->codes) && aligned16(V->codes) ? TQ_OK : TQ_ERR_ALIGN;
+}
+
+bool same_layout(const tq_layout& a, const tq_layout& b) {
+  return a.head_dim == b.head_dim && a.block == b.block && a.bits == b.bits && a.qjl_m == b.qjl_m &&
+         a.norm_correct == b.norm_correct && a.codebook == b.codebook && a.sign_seed == b.sign_seed;
+}
+
+DecodeArgs decode_args(const tq_kv_view* K, const tq_kv_view* V) {
+  DecodeArgs a{};
+  a.kc = reinterpret_cast<const uint32_t*>(K->codes);
+  a.ks = K->scales;
+  a.kq = reinterpret_cast<const uint32_t*>(K->qjl_bits);
+  a.kr = K->qjl_rnorm;
+  a.S = K->S;
+  a.vc = reinterpret_cast<const uint32_t*>(V->codes);
+  a.vs = V->scales;
+  a.vq = reinterpret_cast<const uint32_t*>(V->qjl_bits);
+  a.vr = V->qjl_rnorm;
+  a.Sv = V->S;
+  a.pages = {K->page_table, K->page_table ? K->page_size : 0, K->page_table ? K->pages_per_seq : 0};
+  return a;
+}
+
+// Decode over a shared prefix and the sequences' own tokens: the own tokens'
+// partials go to the first split slots, the prefix's behind them, one combine
+// merges all of them.
+int decode_shared_impl(const tq_kv_view* Kp, const tq_kv_view* Vp, int64_t P_cap, const int32_t* prefix_len,
+                       int64_t prefix_ctx, const tq_kv_view* K, const tq_kv_view* V, const uint16_t* q, int B, int Hq,
+                       int Hkv, int64_t S_cap, const int32_t* kv_len, int64_t ctx, float softmax_scale, uint16_t* out,
+                       void* workspace, size_t workspace_bytes, int n_split, cudaStream_t s) {
+  if (!Kp || !Vp || !q || !out || (ctx > 0 && (!K || !V))) return TQ_ERR_ARG;
+  CodecParams PK, PV;
+  int st = make_params(&Kp->layout, &PK);
+  if (st != TQ_OK) return st;
+  st = make_params(&Vp->layout, &PV);
+  if (st != TQ_OK) return st;
+  if (PK.d != PV.d || PV.m > kMaxQjlV || PV.bits > 4 || (PK.bits > 4 && PV.m)) return TQ_ERR_UNSUPPORTED;
+  Codebook8 cbk;
+  if (PK.bits == 8 && make_codebook8(&Kp->layout, &cbk) != TQ_OK) return TQ_ERR_UNSUPPORTED;
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || ctx < 0 || n_split < 0) return TQ_ERR_ARG;
+  if (prefix_ctx < 0 || prefix_ctx > P_cap || (ctx > 0 && ctx > S_cap)) return TQ_ERR_ARG;
+  const int G = Hq / Hkv;
+  if (G != 1 && G != 2 && G != 4 && G != 8) return TQ_ERR_UNSUPPORTED;
+  if ((int64_t)B * Hkv > 65535) return TQ_ERR_UNSUPPORTED;   // grid rows
+  if (prefix_ctx > 0 && (st = check_cache_pair(Kp, Vp, PK, PV, P_cap)) != TQ_OK) return st;
+  if (ctx > 0) {
+    if (!same_layout(Kp->layout, K->layout) || !same_layout(Vp->layout, V->layout)) return TQ_ERR_ARG;
+    if ((st = check_cache_pair(K, V, PK, PV, S_cap)) != TQ_OK) return st;
+  }
+  if (!aligned16(q) || !aligned16(out)) return TQ_ERR_ALIGN;
+  if (prefix_ctx == 0 && ctx == 0)   // no tokens: a zero output
+    return cudaMemsetAsync(out, 0, (size_t)B * Hq * PK.d * 2, s) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+  const bool tc = ctx > 0 && decode_tc_eligible(PK, PV, G, S_cap, K, V);
+  const int np = prefix_ctx > 0 ? decode_auto_splits(B, Hkv, prefix_ctx) : 0;
+  int own = 0;
+  if (ctx > 0) own = n_split ? n_split : decode_auto_splits(B, Hkv, ctx, tc ? decode_tc_ctas_per_sm(PK, PV) : 4);
+  const int slots = own + np;
+  const size_t need = decode_ws_bytes(B, Hq, PK.d, slots);
+  if (!workspace || workspace_bytes < need) return TQ_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return TQ_ERR_ALIGN;
+  const float qscale = (softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)PK.d)) * kLog2e;
+  float* part = static_cast<float*>(workspace);
+  if (np) {
+    DecodeArgs a = decode_args(Kp, Vp);
+    a.q = q;
+    a.kv_len = prefix_len;
+    a.part = part;
+    a.S_cap = P_cap;
+    a.ctx = prefix_ctx;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.n_split = np;
+    a.slots = slots;
+    a.slot0 = own;
+    a.shared = 1;
+    a.qscale = qscale;
+    st = launch_decode_any(PK, PV, a, B, cbk, s);
+    if (st != TQ_OK) return st;
+  }
+  if (own) {
+    if (tc) {
+      st = launch_decode_tc(PK, PV, K, V, q, kv_len, part, decode_part_bytes(B, Hq, PK.d, slots), B, Hq, Hkv, S_cap,
+                            ctx, own, slots, np > 0, qscale, &cbk, s);
+    } else {
+      DecodeArgs a = decode_args(K, V);
+      a.q = q;
+      a.kv_len = kv_len;
+      a.part = part;
+      a.S_cap = S_cap;
+      a.ctx = ctx;
+      a.Hq = Hq;
+      a.Hkv = Hkv;
+      a.n_split = own;
+      a.slots = slots;
+      a.qscale = qscale;
+      a.pdl = np > 0;
+      st = launch_decode_any(PK, PV, a, B, cbk, s);
+    }
+    if (st != TQ_OK) return st;
+  }
+  return decode_combine(PV, part, slots, out, B * Hq, s);
 }
 
 }  // namespace
@@ -1076,6 +1197,29 @@ extern "C" int tq_decode_attn_window(const tq_kv_view* K, const tq_kv_view* V, c
   const tq::Window w{k_win, v_win, win_len, win, W_cap};
   return tq::decode_impl(K, V, q, B, Hq, Hkv, S_cap, kv_len, ctx, softmax_scale, out, workspace, workspace_bytes,
                          n_split, stream, &w);
+}
+
+extern "C" int tq_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int head_dim, int64_t prefix_ctx, int64_t ctx,
+                                                int n_split, size_t* bytes) {
+  int ns = 0, np = 0;
+  size_t b0 = 0;
+  if (prefix_ctx < 0) return TQ_ERR_ARG;
+  int st = tq_decode_workspace_bytes(B, Hq, Hkv, head_dim, ctx, n_split, &b0, &ns);
+  if (st != TQ_OK) return st;
+  if (!bytes) return TQ_ERR_ARG;
+  if (prefix_ctx > 0) np = tq::decode_auto_splits(B, Hkv, prefix_ctx);
+  *bytes = tq::decode_ws_bytes(B, Hq, head_dim, ns + np);
+  return TQ_OK;
+}
+
+extern "C" int tq_decode_attn_shared(const tq_kv_view* Kp, const tq_kv_view* Vp, int64_t P_cap,
+                                     const int32_t* prefix_len, int64_t prefix_ctx, const tq_kv_view* K,
+                                     const tq_kv_view* V, const uint16_t* q, int B, int Hq, int Hkv, int64_t S_cap,
+                                     const int32_t* kv_len, int64_t ctx, float softmax_scale, uint16_t* out,
+                                     void* workspace, size_t workspace_bytes, int n_split, void* stream) {
+  return tq::decode_shared_impl(Kp, Vp, P_cap, prefix_len, prefix_ctx, K, V, q, B, Hq, Hkv, S_cap, kv_len, ctx,
+                                softmax_scale, out, workspace, workspace_bytes, n_split,
+                                static_cast<cudaStream_t>(stream));
 }
 
 // ---------------------------------------------------------------------------

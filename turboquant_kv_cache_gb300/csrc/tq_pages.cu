@@ -1,0 +1,594 @@
+// The page table's life on the device: sequences fork (sharing full pages by
+// reference, copying the part-filled one), grow, give up their pages, and the
+// pool is compacted.  Nothing is read back by the host: the number of pages
+// taken or moved is decided by kernels and the copies run over lists that
+// earlier kernels of the call wrote to the workspace.
+//
+// Order.  Fresh pages are the free pages in ascending order, dealt to the
+// entries in order; the k-th hole takes the k-th live page behind the live
+// count.  Both are ranks from prefix sums over the reference counts, so the
+// result does not depend on the order in which blocks run.  Reference counts
+// change by atomic adds, which commute.
+//
+// Steps (each a launch; the pool's counts are read once):
+//   count   free pages of every chunk of kChunk pages
+//   plan    one block: prefix sum over the chunks; for a fork also the checks
+//           of every entry, the pages it needs and their prefix sum
+//   assign  chunks deal their free pages by rank (fork), or list holes and
+//           pages to move by rank (compact)
+//   move    page contents, tables and counts
+#include <cuda_runtime.h>
+
+#include "tq_device.cuh"
+
+namespace tq {
+namespace {
+
+constexpr int kChunk = 1024;          // pages per block of count and assign
+constexpr int kThreads = 256;
+constexpr int kPlanThreads = 1024;
+constexpr int kMaxArrays = 128;       // cache arrays one move launch takes
+constexpr int kPiece = 8192;          // bytes one block copies at a time
+constexpr int kMaxPerSeq = 1 << 20;   // pages of a sequence: kPlanThreads of them sum below 2^31
+constexpr int kMaxPages = 1 << 28;    // pages of a pool
+constexpr int kManyPages = 1 << 29;   // more than any pool has
+
+// Workspace header, then the arrays of Work.
+struct Head {
+  int32_t ok;        // 0: the plan was refused, nothing changes
+  int32_t need;      // fresh pages the entries take together
+  int32_t n_live;    // compact: pages in use
+  int32_t moves;     // page copies
+};
+
+struct Work {
+  Head* head;
+  int32_t* chunk;    // [chunks] free pages of each chunk, then before each
+  int32_t* mark;     // [n_seqs] 1: a child of this call
+  int32_t* off;      // [n + 1] fresh pages before entry i
+  int32_t* first;    // [n] first table index a fresh page goes to
+  int32_t* cow;      // [n] table index of the shared page replaced, or -1
+  int32_t* src;      // [n] or [num_pages]: page copied
+  int32_t* dst;      // [n] or [num_pages]: page it is copied to
+  int32_t* drop;     // [n] page whose count falls by one, or -1
+  int32_t* rank;     // [num_pages] rank of a page that moves
+};
+
+size_t carve(void* ws, int n_seqs, int num_pages, int n, Work* w) {
+  uint8_t* p = static_cast<uint8_t*>(ws);
+  size_t at = 0;
+  auto take = [&](size_t count) {
+    int32_t* r = reinterpret_cast<int32_t*>(p + at);
+    at += (count * 4 + 255) / 256 * 256;
+    return r;
+  };
+  const int chunks = (num_pages + kChunk - 1) / kChunk;
+  const size_t lists = n > num_pages ? n : num_pages;
+  Work t;
+  t.head = reinterpret_cast<Head*>(take(sizeof(Head) / 4));
+  t.chunk = take(chunks + 1);
+  t.mark = take(n_seqs);
+  t.off = take((size_t)n + 1);
+  t.first = take(n);
+  t.cow = take(n);
+  t.src = take(lists);
+  t.dst = take(lists);
+  t.drop = take(n);
+  t.rank = take(num_pages);
+  if (w) *w = t;
+  return at;
+}
+
+// Sum of v over the block, and the sum of the threads before this one.
+// Every thread calls it; s_part holds blockDim.x / 32 + 1 values.
+__device__ __forceinline__ int block_scan(int v, int* s_part, int* total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kFull, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();   // the part sums of an earlier call have been read
+  if (lane == 31) s_part[w] = x;
+  __syncthreads();
+  if (w == 0) {
+    int p = lane < nw ? s_part[lane] : 0;
+    const int own = p;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kFull, p, o);
+      if (lane >= o) p += y;
+    }
+    if (lane < nw) s_part[lane] = p - own;
+    if (lane == 31) s_part[32] = p;
+  }
+  __syncthreads();
+  *total = s_part[32];
+  return s_part[w] + x - v;
+}
+
+__device__ __forceinline__ int free_at(const int32_t* ref, int p, int n) { return p < n && ref[p] == 0 ? 1 : 0; }
+
+__global__ void __launch_bounds__(kThreads) pages_count_kernel(const int32_t* __restrict__ ref, int num_pages, Work w) {
+  __shared__ int s_part[33];
+  int c = 0;
+  for (int i = threadIdx.x; i < kChunk; i += kThreads) c += free_at(ref, blockIdx.x * kChunk + i, num_pages);
+  int total;
+  block_scan(c, s_part, &total);
+  if (threadIdx.x == 0) w.chunk[blockIdx.x] = total;
+}
+
+// Exclusive prefix sum of w.chunk in place; returns the total.
+__device__ int scan_chunks(Work w, int chunks, int* s_part) {
+  int base = 0;
+  for (int c0 = 0; c0 < chunks; c0 += kPlanThreads) {
+    const int c = c0 + threadIdx.x;
+    const int v = c < chunks ? w.chunk[c] : 0;
+    int total;
+    const int before = block_scan(v, s_part, &total);
+    if (c < chunks) w.chunk[c] = base + before;
+    base += total;
+  }
+  return base;
+}
+
+struct ForkArgs {
+  tq_page_pool pool;
+  const int32_t* parent;
+  const int32_t* child;
+  const int32_t* share_len;
+  const int32_t* new_len;
+  int32_t* result;
+  int n;
+  Work w;
+};
+
+// What entry i of a fork takes.  ok: the entry can be done.
+struct Entry {
+  int parent, child, at, first, fresh, total, cow, src, drop;
+  bool ok;
+};
+
+__device__ Entry read_entry(const ForkArgs& a, int i) {
+  Entry e{};
+  const tq_page_pool& p = a.pool;
+  e.parent = a.parent[i];
+  e.child = a.child[i];
+  e.cow = e.src = e.drop = -1;
+  const int share = a.share_len[i], len = a.new_len[i];
+  e.ok = e.child >= 0 && e.child < p.n_seqs && e.parent >= -1 && e.parent < p.n_seqs && share >= 0 && len >= share;
+  if (!e.ok) return e;
+  const bool grow = e.parent == e.child;
+  const int held = e.parent >= 0 ? p.n_pages[e.parent] : 0;
+  const int64_t total = ((int64_t)len + p.page_size - 1) / p.page_size;
+  e.ok = held >= 0 && held <= p.pages_per_seq && total <= p.pages_per_seq && (int64_t)held * p.page_size >= share &&
+         (grow || p.n_pages[e.child] == 0);
+  if (!e.ok) return e;
+  e.total = (int)total;
+  e.at = share / p.page_size;          // the page that is written next
+  const int part = share % p.page_size;
+  const int32_t* row = e.parent >= 0 ? p.page_table + (int64_t)e.parent * p.pages_per_seq : nullptr;
+  if (grow) {
+    e.first = held;
+    e.fresh = e.total > held ? e.total - held : 0;
+    if (e.at < held) {
+      const int page = row[e.at];
+      if (page >= 0 && page < p.num_pages && p.ref[page] > 1) {   // shared: it would be written
+        e.cow = e.at;
+        e.drop = page;
+        ++e.fresh;
+        if (part) e.src = page;
+      }
+    }
+    if (e.total < held) e.total = held;
+  } else {
+    e.first = e.at;
+    e.fresh = e.total - e.at;
+    if (part) e.src = row[e.at];
+  }
+  if (e.src >= p.num_pages || (e.src < 0 && part && !(grow && e.cow < 0))) e.ok = false;   // a table entry that is no page
+  return e;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) pages_fork_plan_kernel(const ForkArgs a, int chunks) {
+  __shared__ int s_part[33];
+  const Work w = a.w;
+  const tq_page_pool& p = a.pool;
+  const int n_free = scan_chunks(w, chunks, s_part);
+  for (int i = threadIdx.x; i < p.n_seqs; i += kPlanThreads) w.mark[i] = 0;
+  __syncthreads();
+  int bad = 0;
+  for (int i = threadIdx.x; i < a.n; i += kPlanThreads) {
+    const int c = a.child[i];
+    if (c >= 0 && c < p.n_seqs && atomicExch(&w.mark[c], 1)) bad = 1;   // the same child twice
+  }
+  __syncthreads();
+  int base = 0, copies = 0;
+  for (int i0 = 0; i0 < a.n; i0 += kPlanThreads) {
+    const int i = i0 + threadIdx.x;
+    Entry e{};
+    e.ok = true;
+    if (i < a.n) {
+      e = read_entry(a, i);
+      // a parent that changes in this call
+      if (e.ok && e.parent >= 0 && e.parent != e.child && w.mark[e.parent]) e.ok = false;
+      if (!e.ok) {
+        bad = 1;
+        e.fresh = 0;
+      }
+    }
+    int total;
+    // an entry takes at most kMaxPerSeq pages, so a block's sum fits; the
+    // running sum saturates above any pool, whose size is checked against it
+    const int before = block_scan(e.fresh, s_part, &total);
+    if (i < a.n) {
+      w.off[i] = min(base + before, kManyPages);
+      w.first[i] = e.first;
+      w.cow[i] = e.cow;
+      w.src[i] = e.src;
+      w.drop[i] = e.drop;
+      w.dst[i] = -1;
+    }
+    base = min(base + total, kManyPages);
+    copies += i < a.n && e.ok && e.src >= 0 ? 1 : 0;
+  }
+  const int any_bad = __syncthreads_or(bad);
+  int n_copies;
+  block_scan(copies, s_part, &n_copies);
+  const bool ok = !any_bad && base <= n_free;
+  if (ok) {   // every count has been read: the sequences hold their new pages from here on
+    for (int i = threadIdx.x; i < a.n; i += kPlanThreads) {
+      const int c = a.child[i];
+      const int total = (int)(((int64_t)a.new_len[i] + p.page_size - 1) / p.page_size);
+      if (a.parent[i] != c || total > p.n_pages[c]) p.n_pages[c] = total;
+    }
+  }
+  if (threadIdx.x == 0) {
+    w.off[a.n] = base;
+    w.head->ok = ok;
+    w.head->need = base;
+    w.head->moves = ok ? a.n : 0;
+    if (a.result) {
+      a.result[0] = any_bad ? -1 : (ok ? 0 : base - n_free);
+      a.result[1] = ok ? base : 0;
+      a.result[2] = ok ? n_copies : 0;
+      a.result[3] = 0;
+    }
+  }
+}
+
+// Blocks [0, chunks): deal the chunk's free pages.  Blocks behind: entry
+// blockIdx.x - chunks shares its parent's full pages.
+__global__ void __launch_bounds__(kThreads) pages_fork_assign_kernel(const ForkArgs a, int chunks) {
+  __shared__ int s_part[33];
+  const Work w = a.w;
+  const tq_page_pool& p = a.pool;
+  if (!w.head->ok) return;
+  if ((int)blockIdx.x < chunks) {
+    const int need = w.head->need;
+    const int base = w.chunk[blockIdx.x];
+    if (base >= need) return;
+    constexpr int PER = kChunk / kThreads;
+    const int p0 = blockIdx.x * kChunk + threadIdx.x * PER;
+    int f[PER], c = 0;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) c += f[k] = free_at(p.ref, p0 + k, p.num_pages);
+    int total;
+    int r = base + block_scan(c, s_part, &total);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      if (!f[k]) continue;
+      if (r >= need) break;
+      // the entry whose fresh pages hold rank r: the last with off <= r
+      int lo = 0, hi = a.n;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (w.off[mid] <= r) lo = mid; else hi = mid;
+      }
+      int t = r - w.off[lo];
+      const int cow = w.cow[lo];
+      int idx;
+      if (cow >= 0) idx = t == 0 ? cow : w.first[lo] + t - 1;
+      else idx = w.first[lo] + t;
+      p.page_table[(int64_t)a.child[lo] * p.pages_per_seq + idx] = p0 + k;
+      p.ref[p0 + k] = 1;
+      // the copy of a part-filled page goes to the first fresh page
+      if (t == 0) w.dst[lo] = p0 + k;
+      ++r;
+    }
+    return;
+  }
+  const int i = blockIdx.x - chunks;
+  const int parent = a.parent[i], child = a.child[i];
+  if (parent < 0 || parent == child) return;
+  const int full = w.first[i];
+  const int32_t* from = p.page_table + (int64_t)parent * p.pages_per_seq;
+  int32_t* to = p.page_table + (int64_t)child * p.pages_per_seq;
+  for (int k = threadIdx.x; k < full; k += kThreads) {
+    const int page = from[k];
+    to[k] = page;
+    if (page >= 0 && page < p.num_pages) atomicAdd(&p.ref[page], 1);
+  }
+}
+
+// The caches' arrays as runs of bytes per page.
+struct Arrays {
+  uint8_t* base[kMaxArrays];
+  int32_t bytes[kMaxArrays];    // per page
+  int32_t piece0[kMaxArrays];   // pieces of a page before this array
+  int32_t n, pieces;            // arrays, pieces of a whole page
+};
+
+// Copies w.moves pages src[r] -> dst[r] (an entry of a fork without a copy
+// has src -1), one piece of one array per block and step.  Block 0 also lowers
+// the counts of the n_drop pages that a fork's entries replaced.
+__global__ void __launch_bounds__(kThreads) pages_move_kernel(Work w, const __grid_constant__ Arrays a,
+                                                              int32_t* ref, int num_pages, int n_drop) {
+  const int moves = w.head->moves;
+  if (blockIdx.x == 0 && moves) {
+    for (int i = threadIdx.x; i < n_drop; i += kThreads) {
+      const int page = w.drop[i];
+      if (page >= 0) atomicSub(&ref[page], 1);
+    }
+  }
+  const int64_t items = (int64_t)moves * a.pieces;
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const int r = (int)(it / a.pieces), pc = (int)(it - (int64_t)r * a.pieces);
+    const int src = w.src[r];
+    if (src < 0) continue;
+    const int dst = w.dst[r];
+    if (src >= num_pages || dst < 0 || dst >= num_pages) continue;
+    int lo = 0, hi = a.n;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (a.piece0[mid] <= pc) lo = mid; else hi = mid;
+    }
+    const int64_t bytes = a.bytes[lo];
+    const int64_t at = (int64_t)(pc - a.piece0[lo]) * kPiece;
+    const int n16 = (int)(imin64(kPiece, bytes - at) / 16);
+    const uint4* s = reinterpret_cast<const uint4*>(a.base[lo] + src * bytes + at);
+    uint4* d = reinterpret_cast<uint4*>(a.base[lo] + dst * bytes + at);
+    for (int k = threadIdx.x; k < n16; k += kThreads) d[k] = s[k];
+  }
+}
+
+struct CompactArgs {
+  tq_page_pool pool;
+  int32_t* result;
+  Work w;
+};
+
+__global__ void __launch_bounds__(kPlanThreads) pages_compact_plan_kernel(const CompactArgs a, int chunks) {
+  __shared__ int s_part[33];
+  const int n_free = scan_chunks(a.w, chunks, s_part);
+  const int n_live = a.pool.num_pages - n_free;
+  __syncthreads();
+  // holes: free pages before n_live
+  const int c = n_live / kChunk;
+  int part = 0;
+  for (int i = threadIdx.x; i < n_live - c * kChunk; i += kPlanThreads) part += a.pool.ref[c * kChunk + i] == 0 ? 1 : 0;
+  int holes;
+  block_scan(part, s_part, &holes);
+  if (threadIdx.x == 0) {
+    holes += c < chunks ? a.w.chunk[c] : n_free;
+    a.w.head->ok = 1;
+    a.w.head->n_live = n_live;
+    a.w.head->moves = holes;
+    if (a.result) {
+      a.result[0] = 0;
+      a.result[1] = n_live;
+      a.result[2] = holes;
+      a.result[3] = 0;
+    }
+  }
+}
+
+// Lists the holes before n_live and the live pages behind it, by rank.
+__global__ void __launch_bounds__(kThreads) pages_compact_list_kernel(const CompactArgs a) {
+  __shared__ int s_part[33];
+  const Work w = a.w;
+  const int n_live = w.head->n_live, moves = w.head->moves;
+  if (!moves) return;
+  constexpr int PER = kChunk / kThreads;
+  const int p0 = blockIdx.x * kChunk + threadIdx.x * PER;
+  int f[PER], c = 0;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) c += f[k] = free_at(a.pool.ref, p0 + k, a.pool.num_pages);
+  int total;
+  int before = w.chunk[blockIdx.x] + block_scan(c, s_part, &total);   // free pages before p0
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int page = p0 + k;
+    if (page >= a.pool.num_pages) break;
+    if (f[k]) {
+      if (page < n_live) {
+        if (before < moves) w.dst[before] = page;
+      } else {
+        w.rank[page] = -1;
+      }
+      ++before;
+    } else if (page >= n_live) {
+      // live pages before it, less those before n_live
+      const int r = page - before - (n_live - moves);
+      if (r >= 0 && r < moves) {
+        w.src[r] = page;
+        w.rank[page] = r;
+      }
+    }
+  }
+}
+
+// Tables and counts after the lists are there: a warp per sequence renames
+// its pages, and the counts move with the pages.
+__global__ void __launch_bounds__(kThreads) pages_compact_rename_kernel(const CompactArgs a) {
+  const Work w = a.w;
+  const tq_page_pool& p = a.pool;
+  const int n_live = w.head->n_live, moves = w.head->moves;
+  if (!moves) return;
+  const int64_t tid = (int64_t)blockIdx.x * kThreads + threadIdx.x, step = (int64_t)gridDim.x * kThreads;
+  for (int64_t r = tid; r < moves; r += step) {
+    p.ref[w.dst[r]] = p.ref[w.src[r]];
+    p.ref[w.src[r]] = 0;
+  }
+  const int lane = threadIdx.x & 31;
+  for (int64_t s = tid / 32; s < p.n_seqs; s += step / 32) {
+    int32_t* row = p.page_table + s * p.pages_per_seq;
+    const int held = min(p.n_pages[s], p.pages_per_seq);
+    for (int j = lane; j < held; j += 32) {
+      const int page = row[j];
+      if (page < n_live || page >= p.num_pages) continue;
+      const int r = w.rank[page];   // -1: a free page, which no table should name
+      if (r >= 0) row[j] = w.dst[r];
+    }
+  }
+}
+
+// A block per sequence named.
+__global__ void __launch_bounds__(kThreads) pages_free_kernel(const tq_page_pool p, const int32_t* __restrict__ seqs,
+                                                              const int32_t* __restrict__ keep_len) {
+  __shared__ int s_old, s_keep;
+  const int s = seqs[blockIdx.x];
+  if (s < 0 || s >= p.n_seqs) return;
+  if (threadIdx.x == 0) {
+    const int len = keep_len ? max(keep_len[blockIdx.x], 0) : 0;
+    const int keep = (int)imin64(((int64_t)len + p.page_size - 1) / p.page_size, p.pages_per_seq);
+    // the smaller of two entries for one sequence counts: each gives up what
+    // it finds above its own
+    s_old = min(atomicMin(&p.n_pages[s], keep), p.pages_per_seq);
+    s_keep = keep;
+  }
+  __syncthreads();
+  const int32_t* row = p.page_table + (int64_t)s * p.pages_per_seq;
+  for (int j = s_keep + threadIdx.x; j < s_old; j += kThreads) {
+    const int page = row[j];
+    if (page >= 0 && page < p.num_pages) atomicSub(&p.ref[page], 1);
+  }
+}
+
+int check_pool(const tq_page_pool* p) {
+  if (!p || !p->page_table || !p->n_pages || !p->ref) return TQ_ERR_ARG;
+  if (p->n_seqs <= 0 || p->pages_per_seq <= 0 || p->num_pages <= 0) return TQ_ERR_ARG;
+  if (p->page_size <= 0 || p->page_size % 32) return TQ_ERR_ARG;
+  if (p->pages_per_seq > kMaxPerSeq || p->num_pages > kMaxPages || p->n_seqs > kMaxPages) return TQ_ERR_UNSUPPORTED;
+  return TQ_OK;
+}
+
+int check_caches(const tq_kv_view* caches, int n_caches, int Hkv, int page_size) {
+  if (n_caches < 0 || (n_caches && (!caches || Hkv <= 0))) return TQ_ERR_ARG;
+  for (int i = 0; i < n_caches; ++i) {
+    const tq_kv_view& c = caches[i];
+    const int st = check_layout(&c.layout);
+    if (st != TQ_OK) return st;
+    if (!c.codes || !c.scales || (c.layout.qjl_m && (!c.qjl_bits || !c.qjl_rnorm))) return TQ_ERR_ARG;
+    if (!aligned16(c.codes) || !aligned16(c.scales) ||
+        (c.layout.qjl_m && (!aligned16(c.qjl_bits) || !aligned16(c.qjl_rnorm))))
+      return TQ_ERR_ALIGN;
+    if ((int64_t)Hkv * page_size * c.layout.head_dim > 0x7fffffff) return TQ_ERR_UNSUPPORTED;
+  }
+  return TQ_OK;
+}
+
+int launch_moves(const tq_kv_view* caches, int n_caches, int Hkv, const tq_page_pool& p, const Work& w, int64_t most,
+                 int n_drop, cudaStream_t st) {
+  Arrays a{};
+  bool launched = false;
+  auto flush = [&]() {
+    const int64_t items = most * a.pieces;
+    const int64_t grid = items < 1 ? 1 : (items > 152 * 8 ? 152 * 8 : items);
+    pages_move_kernel<<<(unsigned)grid, kThreads, 0, st>>>(w, a, p.ref, p.num_pages, launched ? 0 : n_drop);
+    launched = true;
+    a.n = a.pieces = 0;
+  };
+  auto add = [&](const void* base, int64_t bytes) {
+    a.base[a.n] = static_cast<uint8_t*>(const_cast<void*>(base));
+    a.bytes[a.n] = (int32_t)bytes;
+    a.piece0[a.n] = a.pieces;
+    a.pieces += (int32_t)((bytes + kPiece - 1) / kPiece);
+    ++a.n;
+  };
+  for (int i = 0; i < n_caches; ++i) {
+    const tq_kv_view& c = caches[i];
+    const int64_t rows = (int64_t)Hkv * p.page_size;
+    if (a.n + 4 > kMaxArrays) flush();
+    add(c.codes, rows * c.layout.head_dim * c.layout.bits / 8);
+    add(c.scales, rows * (c.layout.head_dim / c.layout.block) * 2);
+    if (c.layout.qjl_m) {
+      add(c.qjl_bits, rows * c.layout.qjl_m / 8);
+      add(c.qjl_rnorm, rows * 2);
+    }
+  }
+  if (a.n || (!launched && n_drop)) flush();
+  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace tq
+
+extern "C" int tq_pages_workspace_bytes(int n_seqs, int num_pages, int n, size_t* bytes) {
+  if (n_seqs <= 0 || num_pages <= 0 || n < 0 || !bytes) return TQ_ERR_ARG;
+  *bytes = tq::carve(nullptr, n_seqs, num_pages, n, nullptr);
+  return TQ_OK;
+}
+
+extern "C" int tq_pages_fork(const tq_page_pool* pool, const tq_kv_view* caches, int n_caches, int Hkv,
+                             const int32_t* parent, const int32_t* child, const int32_t* share_len,
+                             const int32_t* new_len, int n, int32_t* result, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  int st = tq::check_pool(pool);
+  if (st != TQ_OK) return st;
+  st = tq::check_caches(caches, n_caches, Hkv, pool->page_size);
+  if (st != TQ_OK) return st;
+  if (n < 0 || n > pool->n_seqs) return TQ_ERR_ARG;   // more entries than sequences: a child would be named twice
+  if (n && (!parent || !child || !share_len || !new_len)) return TQ_ERR_ARG;
+  tq::Work w;
+  if (!workspace || workspace_bytes < tq::carve(nullptr, pool->n_seqs, pool->num_pages, n, nullptr))
+    return TQ_ERR_WORKSPACE;
+  if (!tq::aligned16(workspace)) return TQ_ERR_ALIGN;
+  tq::carve(workspace, pool->n_seqs, pool->num_pages, n, &w);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const tq::ForkArgs a{*pool, parent, child, share_len, new_len, result, n, w};
+  const int chunks = (pool->num_pages + tq::kChunk - 1) / tq::kChunk;
+  tq::pages_count_kernel<<<chunks, tq::kThreads, 0, s>>>(pool->ref, pool->num_pages, w);
+  tq::pages_fork_plan_kernel<<<1, tq::kPlanThreads, 0, s>>>(a, chunks);
+  if (n) {
+    tq::pages_fork_assign_kernel<<<chunks + n, tq::kThreads, 0, s>>>(a, chunks);
+    if (cudaGetLastError() != cudaSuccess) return TQ_ERR_CUDA;
+    return tq::launch_moves(caches, n_caches, Hkv, *pool, w, n, n, s);
+  }
+  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+}
+
+extern "C" int tq_pages_free(const tq_page_pool* pool, const int32_t* seqs, const int32_t* keep_len, int n,
+                             void* stream) {
+  const int st = tq::check_pool(pool);
+  if (st != TQ_OK) return st;
+  if (n < 0 || (n && !seqs)) return TQ_ERR_ARG;
+  if (!n) return TQ_OK;
+  tq::pages_free_kernel<<<n, tq::kThreads, 0, static_cast<cudaStream_t>(stream)>>>(*pool, seqs, keep_len);
+  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+}
+
+extern "C" int tq_pages_compact(const tq_page_pool* pool, const tq_kv_view* caches, int n_caches, int Hkv,
+                                int32_t* result, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = tq::check_pool(pool);
+  if (st != TQ_OK) return st;
+  st = tq::check_caches(caches, n_caches, Hkv, pool->page_size);
+  if (st != TQ_OK) return st;
+  tq::Work w;
+  if (!workspace || workspace_bytes < tq::carve(nullptr, pool->n_seqs, pool->num_pages, 0, nullptr))
+    return TQ_ERR_WORKSPACE;
+  if (!tq::aligned16(workspace)) return TQ_ERR_ALIGN;
+  tq::carve(workspace, pool->n_seqs, pool->num_pages, 0, &w);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const tq::CompactArgs a{*pool, result, w};
+  const int chunks = (pool->num_pages + tq::kChunk - 1) / tq::kChunk;
+  tq::pages_count_kernel<<<chunks, tq::kThreads, 0, s>>>(pool->ref, pool->num_pages, w);
+  tq::pages_compact_plan_kernel<<<1, tq::kPlanThreads, 0, s>>>(a, chunks);
+  tq::pages_compact_list_kernel<<<chunks, tq::kThreads, 0, s>>>(a);
+  const int64_t work = pool->num_pages > (int64_t)pool->n_seqs * 32 ? pool->num_pages : (int64_t)pool->n_seqs * 32;
+  const int64_t blocks = (work + tq::kThreads - 1) / tq::kThreads;
+  tq::pages_compact_rename_kernel<<<(unsigned)(blocks > 1216 ? 1216 : blocks), tq::kThreads, 0, s>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return TQ_ERR_CUDA;
+  return tq::launch_moves(caches, n_caches, Hkv, *pool, w, pool->num_pages / 2 + 1, 0, s);
+}
