@@ -100,5 +100,6 @@ WaitLimits wait_limits();
 int quantize_fast_status(int clear, int* status);
 int quantize_qjl_tc_status(int clear, int* status);
 int prefill_tc_status(int clear, int* status);
+int shared_tc_status(int clear, int* status);
 
 }  // namespace tq
