@@ -16,9 +16,9 @@
 // not the 128 of a row-per-lane tile.  The sum l comes from the same rounded
 // p that multiplies V, as one more product with a tile of ones, so a softmax
 // thread (a token, half of the rows) keeps no per-row sums.  The reference m
-// of a row only moves when a score passes it by more than 2^8 (the first tile
+// of a row only moves when a score passes it by more than 2^12 (the first tile
 // always does): the common step needs no maximum over tokens, only one
-// barrier vote; the rare one takes the maxima by shuffles, and scales O and L.
+// barrier vote; the rare one takes the maxima and scales O and L.
 //
 // Warps: 0-7 softmax (warps 0-3 rows [0, NR/2), 4-7 the rest), 8 issues S,
 // 9 issues O and L, 10-25 decode.  A decoder thread takes one 32-code group
@@ -52,7 +52,9 @@ constexpr int kDecWarps = 16;
 constexpr int kDecThreads = 32 * kDecWarps;
 constexpr int kDec0 = 32 * (kSoftWarps + 2);          // first decoder thread
 constexpr int kThreadsSh = kDec0 + kDecThreads;       // 832
-constexpr float kLazySh = 8.0f;     // log2 units a score may pass the reference by
+// log2 units a score may pass its row's reference by: p stays below 2^12, far
+// inside fp16, and sums of p * v inside fp32
+constexpr float kLazySh = 12.0f;
 
 // first failure status of a launch since the last read (0 = none)
 __device__ int g_shared_status;
@@ -82,7 +84,7 @@ struct SharedArgs {
   PageMap pages;
   int64_t S_cap, ctx, per;     // per: tokens per split (multiple of kTile)
   uint64_t report_ns, hard_ns;
-  int B, Hq, Hkv, G, NR, slots, slot0;
+  int B, Hq, Hkv, G, lg, NR, slots, slot0;   // G = 1 << lg
   float qscale;
 };
 
@@ -123,6 +125,38 @@ __device__ __forceinline__ void arrive(uint32_t bar) {
 }
 __device__ __forceinline__ void bar_init(uint32_t bar, int count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(bar), "r"(count) : "memory");
+}
+
+// Wait for a phase of an mbarrier as tq_tc.cuh's, but without a sleep between
+// polls: try_wait suspends the warp until the phase completes, and a handoff
+// of this kernel is due within a microsecond.
+__device__ __forceinline__ bool bar_wait_near(uint32_t bar, uint32_t parity, uint64_t report_ns, uint64_t hard_ns,
+                                              int& late) {
+  uint32_t done = 0;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  if (done) return true;
+  const uint64_t t0 = global_ns();
+  for (;;) {
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "r"(1000000u)
+        : "memory");
+    const uint64_t el = global_ns() - t0;
+    if (el > report_ns) late = 1;
+    if (done) return true;
+    if (el > hard_ns) return false;
+  }
+}
+// maximum over the warp, in every lane
+__device__ __forceinline__ float warp_max_f(float x) {
+  float y;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // The packed words and norm of one 32-code group, loaded a tile ahead.
@@ -191,7 +225,7 @@ __device__ __forceinline__ void decode_group(int bits, const Group& g, uint32_t 
   }
 }
 
-template <int D>
+template <int D, bool PAGED>
 __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const CodecParams PK, const CodecParams PV,
                                                                       const SharedArgs a) {
   using C = ShCfg<D>;
@@ -231,7 +265,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
   auto wait = [&](uint32_t bar, uint32_t parity) {
     if (__any_sync(kFull, s_abort)) return false;   // one decision per warp
     int late = 0;
-    const bool ok = __all_sync(kFull, bar_wait(bar, parity, a.report_ns, a.hard_ns, late));
+    const bool ok = __all_sync(kFull, bar_wait_near(bar, parity, a.report_ns, a.hard_ns, late));
     if (late) s_late = 1;
     if (!ok) s_abort = 1;
     return ok;
@@ -276,7 +310,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] = 0.f;
       if (r < rows) {
-        const int rr = row0 + r, b = rr / a.G, h = kvh * a.G + rr % a.G;
+        const int rr = row0 + r, b = rr >> a.lg, h = kvh * a.G + (rr & (a.G - 1));
         const uint16_t* src = a.q + ((int64_t)b * a.Hq + h) * D + E * lane;
         uint32_t u[E / 2];
         if constexpr (E == 8) {
@@ -336,43 +370,43 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     const int dt = tid - kDec0;
     const int st = C::SPLIT ? dt % C::SIDE : dt;    // thread within its side
     const bool do_k = !C::SPLIT || dt < C::SIDE, do_v = !C::SPLIT || dt >= C::SIDE;
-    int tok[C::N], grp[C::N];
-    int64_t page[C::N];      // page (paged) of the next tile's token
-    int32_t off[C::N];       // its place in the page
-#pragma unroll
-    for (int k = 0; k < C::N; ++k) {
-      const int item = st + k * C::SIDE;
-      tok[k] = 8 * (item / (8 * C::G8)) + (item & 7);
-      grp[k] = (item >> 3) % C::G8;
-      page[k] = 0;
-      off[k] = 0;
-      if (a.pages.table) {
-        const int64_t t = t_lo + tok[k];
-        page[k] = t / a.pages.page_size;
-        off[k] = (int32_t)(t - page[k] * a.pages.page_size);
-      }
-    }
+    // the thread's groups: number grp of the tokens tok0 and, at head_dim 256,
+    // kStep tokens on.  Contiguous: pointers of the first that move on by a
+    // tile; paged: page and place in it of each.
+    constexpr int kStep = C::SIDE / C::G8;
+    static_assert(C::N == 1 || kStep % 8 == 0, "a thread's groups have one number");
+    const int tok0 = 8 * (st / (8 * C::G8)) + (st & 7), grp = (st >> 3) % C::G8;
     const int kbits = PK.bits, vbits = PV.bits;
-    Group gk[C::N], gv[C::N];
-    // record of group k's token in tile t, before off / page move on
-    auto rec_of = [&](int t, int k) -> int64_t {
-      if (!a.pages.table) return (int64_t)kvh * a.S_cap + t_lo + (int64_t)t * kTile + tok[k];
-      return ((int64_t)a.pages.table[page[k]] * a.Hkv + kvh) * a.pages.page_size + off[k];
-    };
-    auto load = [&](int t) {
-      const int64_t left = t_hi - (t_lo + (int64_t)t * kTile);
+    const uint8_t *kw = a.kc + grp * 4 * kbits, *kn = a.ks + 32 * grp / PK.blk * 2;
+    const uint8_t *vw = a.vc + grp * 4 * vbits, *vn = a.vs + 32 * grp / PV.blk * 2;
+    int32_t page[C::N], off[C::N];
+    if (PAGED) {
 #pragma unroll
       for (int k = 0; k < C::N; ++k) {
-        if (tok[k] < left) {
-          const int64_t r = rec_of(t, k);
-          if (do_k)
-            load_group_g(kbits, a.kc + r * PK.code_bytes + grp[k] * 4 * kbits, grp[k] & 1,
-                         a.ks + (r * PK.nb + 32 * grp[k] / PK.blk) * 2, gk[k]);
-          if (do_v)
-            load_group_g(vbits, a.vc + r * PV.code_bytes + grp[k] * 4 * vbits, grp[k] & 1,
-                         a.vs + (r * PV.nb + 32 * grp[k] / PV.blk) * 2, gv[k]);
+        const int64_t t = t_lo + tok0 + k * kStep;
+        page[k] = (int32_t)(t / a.pages.page_size);
+        off[k] = (int32_t)(t - (int64_t)page[k] * a.pages.page_size);
+      }
+    } else {
+      const int64_t r = (int64_t)kvh * a.S_cap + t_lo + tok0;
+      kw += r * PK.code_bytes;
+      vw += r * PV.code_bytes;
+      kn += r * PK.nb * 2;
+      vn += r * PV.nb * 2;
+    }
+    Group gk[C::N], gv[C::N];
+    auto left_of = [&](int t) { return (int)imin64(kTile, t_hi - (t_lo + (int64_t)t * kTile)); };
+    auto load = [&](int t) {
+      const int left = left_of(t);
+#pragma unroll
+      for (int k = 0; k < C::N; ++k) {
+        if (tok0 + k * kStep < left) {
+          int64_t r = k * kStep;
+          if (PAGED) r = ((int64_t)a.pages.table[page[k]] * a.Hkv + kvh) * a.pages.page_size + off[k];
+          if (do_k) load_group_g(kbits, kw + r * PK.code_bytes, grp & 1, kn + r * (PK.nb * 2), gk[k]);
+          if (do_v) load_group_g(vbits, vw + r * PV.code_bytes, grp & 1, vn + r * (PV.nb * 2), gv[k]);
         }
-        if (a.pages.table) {
+        if (PAGED) {
           off[k] += kTile;
           while (off[k] >= a.pages.page_size) {
             off[k] -= a.pages.page_size;
@@ -380,19 +414,25 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
           }
         }
       }
+      if (!PAGED) {
+        kw += kTile * PK.code_bytes;
+        vw += kTile * PV.code_bytes;
+        kn += kTile * PK.nb * 2;
+        vn += kTile * PV.nb * 2;
+      }
     };
     if (n_tiles > 0) load(0);
     for (int t = 0; t < n_tiles; ++t) {
       const int bf = t % NB;
-      const int64_t left = t_hi - (t_lo + (int64_t)t * kTile);
+      const int left = left_of(t);
       const uint32_t ph = (uint32_t)(t / NB - 1) & 1;
       if (do_k) {
         if (t >= NB) wait(kfree + 8 * bf, ph);
         if (!s_abort) {
 #pragma unroll
           for (int k = 0; k < C::N; ++k)
-            decode_group(kbits, gk[k], grp[k] & 1, PK.centroids, tok[k] < left,
-                         aK + bf * C::KB + cm_off(tok[k], 32 * grp[k], D));
+            decode_group(kbits, gk[k], grp & 1, PK.centroids, tok0 + k * kStep < left,
+                         aK + bf * C::KB + cm_off(tok0 + k * kStep, 32 * grp, D));
         }
         fence_async_smem();
         __syncwarp();
@@ -403,8 +443,8 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
         if (!s_abort) {
 #pragma unroll
           for (int k = 0; k < C::N; ++k)
-            decode_group(vbits, gv[k], grp[k] & 1, PV.centroids, tok[k] < left,
-                         aV + bf * C::VB + cm_off(tok[k], 32 * grp[k], C::DV));
+            decode_group(vbits, gv[k], grp & 1, PV.centroids, tok0 + k * kStep < left,
+                         aV + bf * C::VB + cm_off(tok0 + k * kStep, 32 * grp, C::DV));
         }
         fence_async_smem();
         __syncwarp();
@@ -468,20 +508,23 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
     const uint32_t pdst = aP + cm_off(tk, col0, NR);
     // p of 16 columns from c on, from their scores: stored to P; returns the
-    // largest s - m
+    // largest s - m.  A token past the slice has p = 0.
     auto emit = [&](uint32_t* v, int c, bool live) {
       float mx = -INFINITY;
       uint32_t o[8];
 #pragma unroll
       for (int j = 0; j < 16; j += 4) {
         const float4 m = *reinterpret_cast<const float4*>(&s_m[col0 + c + j]);
-        const float x0 = live ? __uint_as_float(v[j]) - m.x : -INFINITY;
-        const float x1 = live ? __uint_as_float(v[j + 1]) - m.y : -INFINITY;
-        const float x2 = live ? __uint_as_float(v[j + 2]) - m.z : -INFINITY;
-        const float x3 = live ? __uint_as_float(v[j + 3]) - m.w : -INFINITY;
+        const float x0 = __uint_as_float(v[j]) - m.x, x1 = __uint_as_float(v[j + 1]) - m.y;
+        const float x2 = __uint_as_float(v[j + 2]) - m.z, x3 = __uint_as_float(v[j + 3]) - m.w;
         mx = fmaxf(mx, fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)));
         o[j / 2] = pack2(ex2s(x0), ex2s(x1));
         o[j / 2 + 1] = pack2(ex2s(x2), ex2s(x3));
+      }
+      if (!live) {
+        mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = 0u;
       }
       sts16b(pdst + (c >> 3) * 128, o[0], o[1], o[2], o[3]);
       sts16b(pdst + (c >> 3) * 128 + 128, o[4], o[5], o[6], o[7]);
@@ -493,27 +536,31 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
       wait(s_full + 8 * (t & 1), (uint32_t)(t >> 1) & 1);
       if (t >= 1) wait(o_done, (uint32_t)(t - 1) & 1);   // P is free, O and L stand still
       fence_after();
-      float mx = -INFINITY;
-      for (int c = 0; c < nc; c += 16) {
-        uint32_t v[16];
-        TQ_LD16(sS + c, v);
-        ld_wait();
-        mx = fmaxf(mx, emit(v, c, live));
-      }
-      if (half_any(bid, mx > kLazySh)) {
-        // some row's reference moves: its maximum over the tile, O and L
-        // scaled, P written again
+      bool moved = t == 0;
+      if (!moved) {
+        float mx = -INFINITY;
         for (int c = 0; c < nc; c += 16) {
           uint32_t v[16];
           TQ_LD16(sS + c, v);
           ld_wait();
+          mx = fmaxf(mx, emit(v, c, live));
+        }
+        moved = half_any(bid, mx > kLazySh);
+      }
+      if (moved) {
+        // some row's reference moves (the first tile sets them): its maximum
+        // over the tile, O and L scaled, P written again
+        for (int c = 0; c < nc; c += 16) {
+          uint32_t v[16];
+          TQ_LD16(sS + c, v);
+          ld_wait();
+          float mine = 0.f;
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            float x = live ? __uint_as_float(v[j]) : -INFINITY;
-#pragma unroll
-            for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
-            if (lane == j) s_wm[quarter][col0 + c + j] = x;
+            const float x = warp_max_f(live ? __uint_as_float(v[j]) : -INFINITY);
+            if (lane == j) mine = x;
           }
+          if (lane < 16) s_wm[quarter][col0 + c + lane] = mine;
         }
         half_sync(bid);
         if ((tid & 127) < nc) {
@@ -577,7 +624,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
         for (int j = 0; j < 16; ++j) {
           const int r = col0 + c + j;
           if (r >= rows) continue;
-          const int rr = row0 + r, b = rr / a.G, h = kvh * a.G + rr % a.G;
+          const int rr = row0 + r, b = rr >> a.lg, h = kvh * a.G + (rr & (a.G - 1));
           float* dst = a.part + (((int64_t)b * a.Hq + h) * a.slots + a.slot0 + split) * (D + 4);
           if (dim < D) dst[2 + dim] = ok ? __uint_as_float(v[j]) : 0.f;
           if (m == 0 && quarter == 0 && lane == j) {
@@ -596,7 +643,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     fence_after();
     // every product has been committed and, on the normal path, has ended
     int late = 0;
-    __all_sync(kFull, bar_wait(drained, 0, a.report_ns, a.hard_ns, late));
+    __all_sync(kFull, bar_wait_near(drained, 0, a.report_ns, a.hard_ns, late));
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(tcols) : "memory");
     if (lane == 0 && (s_abort || s_late || late)) atomicCAS(&g_shared_status, 0, (int)TQ_ERR_TIMEOUT);
   }
@@ -607,9 +654,9 @@ size_t shared_smem(int NR) {
   return (size_t)ShCfg<D>::NB * (ShCfg<D>::KB + ShCfg<D>::VB) + (size_t)NR * D * 2 + (size_t)NR * kTile * 2 + 2048;
 }
 
-template <int D>
+template <int D, bool PAGED>
 int launch_shared(const CodecParams& PK, const CodecParams& PV, const SharedArgs& a, dim3 grid, cudaStream_t st) {
-  auto kern = shared_prefix_kernel<D>;
+  auto kern = shared_prefix_kernel<D, PAGED>;
   const size_t sm = shared_smem<D>(a.NR);
   static bool attr_set[64] = {};
   int dev = 0;
@@ -673,6 +720,7 @@ int launch_shared_tc(const CodecParams& PK, const CodecParams& PV, const tq_kv_v
   a.Hq = Hq;
   a.Hkv = Hkv;
   a.G = Hq / Hkv;
+  while ((1 << a.lg) < a.G) ++a.lg;
   a.slots = slots;
   a.slot0 = slot0;
   a.qscale = qscale;
@@ -680,9 +728,9 @@ int launch_shared_tc(const CodecParams& PK, const CodecParams& PV, const tq_kv_v
   shared_rows(PK.d, (int64_t)B * a.G, &tiles, &a.NR);
   const dim3 grid((unsigned)n_split, (unsigned)Hkv, (unsigned)tiles);
   switch (PK.d) {
-    case 64: return launch_shared<64>(PK, PV, a, grid, st);
-    case 128: return launch_shared<128>(PK, PV, a, grid, st);
-    default: return launch_shared<256>(PK, PV, a, grid, st);
+    case 64: return a.pages.table ? launch_shared<64, true>(PK, PV, a, grid, st) : launch_shared<64, false>(PK, PV, a, grid, st);
+    case 128: return a.pages.table ? launch_shared<128, true>(PK, PV, a, grid, st) : launch_shared<128, false>(PK, PV, a, grid, st);
+    default: return a.pages.table ? launch_shared<256, true>(PK, PV, a, grid, st) : launch_shared<256, false>(PK, PV, a, grid, st);
   }
 }
 
