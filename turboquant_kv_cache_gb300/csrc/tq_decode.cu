@@ -34,10 +34,11 @@ int launch_decode_tc(const CodecParams& PK, const CodecParams& PV, const tq_kv_v
                      cudaStream_t st);
 size_t decode_ws_bytes(int B, int Hq, int d, int n_split);
 bool shared_tc_eligible(const CodecParams& PK, const CodecParams& PV);
-int shared_tc_splits(int d, int B, int G, int Hkv, int64_t ctx);
-int launch_shared_tc(const CodecParams& PK, const CodecParams& PV, const tq_kv_view* K, const tq_kv_view* V,
-                     const uint16_t* q, const int32_t* prefix_len, float* part, int B, int Hq, int Hkv, int64_t S_cap,
-                     int64_t ctx, int n_split, int slots, int slot0, float qscale, cudaStream_t st);
+void shared_tc_splits(int d, int B, int G, int Hkv, int64_t prefix_ctx, int64_t ctx, int* n_prefix, int* n_own);
+int launch_shared_tc(const CodecParams& PK, const CodecParams& PV, const tq_kv_view* Kp, const tq_kv_view* Vp,
+                     int64_t P_cap, const int32_t* prefix_len, int64_t prefix_ctx, int n_prefix, const tq_kv_view* K,
+                     const tq_kv_view* V, int64_t S_cap, const int32_t* kv_len, int64_t ctx, int n_own,
+                     const uint16_t* q, float* part, int B, int Hq, int Hkv, float qscale, cudaStream_t st);
 
 namespace {
 
@@ -1053,23 +1054,32 @@ int decode_shared_impl(const tq_kv_view* Kp, const tq_kv_view* Vp, int64_t P_cap
   if (!aligned16(q) || !aligned16(out)) return TQ_ERR_ALIGN;
   if (prefix_ctx == 0 && ctx == 0)   // no tokens: a zero output
     return cudaMemsetAsync(out, 0, (size_t)B * Hq * PK.d * 2, s) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
-  const bool tc = ctx > 0 && decode_tc_eligible(PK, PV, G, S_cap, K, V);
-  // one decode of the prefix for all rows, or (QJL, 8-bit keys) the split
-  // kernel per sequence over the same records
+  // one kernel that decodes the prefix once for all rows and takes the own
+  // tokens beside it, or (QJL, 8-bit keys) the decode's kernels, the prefix
+  // read per sequence
   const bool tcp = shared_tc_eligible(PK, PV);
+  const bool tc = !tcp && ctx > 0 && decode_tc_eligible(PK, PV, G, S_cap, K, V);
   int np = 0, own = 0;
-  if (prefix_ctx > 0) np = tcp ? shared_tc_splits(PK.d, B, G, Hkv, prefix_ctx) : decode_auto_splits(B, Hkv, prefix_ctx);
-  if (ctx > 0) own = n_split ? n_split : decode_auto_splits(B, Hkv, ctx, tc ? decode_tc_ctas_per_sm(PK, PV) : 4);
+  if (tcp) {
+    shared_tc_splits(PK.d, B, G, Hkv, prefix_ctx, ctx, &np, &own);
+  } else {
+    if (prefix_ctx > 0) np = decode_auto_splits(B, Hkv, prefix_ctx);
+    if (ctx > 0) own = decode_auto_splits(B, Hkv, ctx, tc ? decode_tc_ctas_per_sm(PK, PV) : 4);
+  }
+  if (ctx > 0 && n_split) own = n_split;
   const int slots = own + np;
   const size_t need = decode_ws_bytes(B, Hq, PK.d, slots);
   if (!workspace || workspace_bytes < need) return TQ_ERR_WORKSPACE;
   if (!aligned16(workspace)) return TQ_ERR_ALIGN;
   const float qscale = (softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)PK.d)) * kLog2e;
   float* part = static_cast<float*>(workspace);
-  if (np && tcp) {
-    st = launch_shared_tc(PK, PV, Kp, Vp, q, prefix_len, part, B, Hq, Hkv, P_cap, prefix_ctx, np, slots, own, qscale, s);
+  if (tcp) {
+    st = launch_shared_tc(PK, PV, Kp, Vp, P_cap, prefix_len, prefix_ctx, np, K, V, S_cap, kv_len, ctx, own, q, part, B,
+                          Hq, Hkv, qscale, s);
     if (st != TQ_OK) return st;
-  } else if (np) {
+    return decode_combine(PV, part, slots, out, B * Hq, s);
+  }
+  if (np) {
     DecodeArgs a = decode_args(Kp, Vp);
     a.q = q;
     a.kv_len = prefix_len;
@@ -1218,11 +1228,12 @@ extern "C" int tq_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int head
   int st = tq_decode_workspace_bytes(B, Hq, Hkv, head_dim, ctx, n_split, &b0, &ns);
   if (st != TQ_OK) return st;
   if (!bytes) return TQ_ERR_ARG;
-  if (prefix_ctx > 0) {   // the layout decides which kernel reads the prefix
-    np = tq::decode_auto_splits(B, Hkv, prefix_ctx);
-    const int tc = tq::shared_tc_splits(head_dim, B, Hq / Hkv, Hkv, prefix_ctx);
-    if (tc > np) np = tc;
-  }
+  // the layout decides which kernel runs: the most parts of either
+  int tcp = 0, tco = 0;
+  tq::shared_tc_splits(head_dim, B, Hq / Hkv, Hkv, prefix_ctx, ctx, &tcp, &tco);
+  if (prefix_ctx > 0) np = tq::decode_auto_splits(B, Hkv, prefix_ctx);
+  if (tcp > np) np = tcp;
+  if (!n_split && tco > ns) ns = tco;
   *bytes = tq::decode_ws_bytes(B, Hq, head_dim, ns + np);
   return TQ_OK;
 }

@@ -9,25 +9,33 @@
 //   S^T [128 tokens x NR]  = K^ (A, smem, K-major) . Q^ (B, smem, K-major)
 //   P^T                    = exp2(S^T - m), fp16, to shared memory
 //   O^T [d x NR]          += V^ (A, smem, MN-major) . P^T (B, smem, MN-major)
-//   L   [64 x NR]         += ones . P^T      (every lane the sum of a row's p)
 //
 // Tokens are on the 128 TMEM lanes and rows on the columns, so the tensor
 // work and the softmax cost what the rows there are cost (a multiple of 32),
-// not the 128 of a row-per-lane tile.  The sum l comes from the same rounded
-// p that multiplies V, as one more product with a tile of ones, so a softmax
-// thread (a token, half of the rows) keeps no per-row sums.  The reference m
-// of a row only moves when a score passes it by more than 2^12 (the first tile
-// always does): the common step needs no maximum over tokens, only one
-// barrier vote; the rare one takes the maxima and scales O and L.
+// not the 128 of a row-per-lane tile.  A softmax thread has one token's p for
+// half of the rows; the sums l over tokens come from the same rounded p that
+// multiplies V, by mma.sync: with a packed register of two rows as its B
+// operand (every lane another token) and a 0/1 matrix A that sends the
+// register's halves to their rows, four products sum 16 rows over a warp.
+// The reference m of a row only moves when a score passes it by more than
+// 2^12 (the first tile always does): the common step needs no maximum over
+// tokens, only one barrier vote; the rare one takes the maxima and scales O
+// and l.
 //
-// Warps: 0-7 softmax (warps 0-3 rows [0, NR/2), 4-7 the rest), 8 issues S,
-// 9 issues O and L, 10-25 decode.  A decoder thread takes one 32-code group
-// (two at head_dim 256) of the K tile and of the V tile, its packed words
-// loaded a tile ahead; at head_dim 64 half of the decoder warps take K, half
-// V.  Handoffs are mbarriers:
-//   kfull/vfull[b] a decoded tile is in buffer b   kfree/vfree[b] its products are done
-//   s_full[i] S(t), t & 1 = i, is in TMEM          s_free[i] it has been read
-//   p_full    P(t) is written                      o_done    O += P(t) V(t) is done
+// The sequences' own tokens are the same work with other rows: a CTA then has
+// one sequence, its G rows and a slice of its tokens.  Prefix and own CTAs
+// are one launch.
+//
+// Warps: 0-7 softmax (warps 0-3 rows [0, NR/2), 4-7 the rest), which also
+// rotate the queries, 8 issues S, 9 issues O, 10-25 decode.  A decoder thread
+// takes one 32-code group (two at head_dim 256) of the K tile and of the V
+// tile, its packed words loaded a tile ahead; at head_dim 64 half of the
+// decoder warps take K, half V.  Handoffs are mbarriers:
+//   q_full        Q^ is written
+//   kfull/kfree   K^(t) is decoded / S(t) is done with it (one buffer)
+//   vfull/vfree[b] the same for V and O (two buffers; one at head_dim 256)
+//   s_full[i]     S(t), t & 1 = i, is in TMEM    s_free[i] it has been read
+//   p_full[i]     P(t) is written                o_done[i] O += V(t) P(t) is done
 // Every wait is bounded at two levels, as in tq_tc.cuh; a CTA that gives up
 // stops decoding and issuing, waits for the products in flight and frees its
 // TMEM.
@@ -61,10 +69,10 @@ __device__ int g_shared_status;
 
 template <int D>
 struct ShCfg {
-  static constexpr int NB = D == 256 ? 1 : 2;          // buffers of K and of V
+  static constexpr int NV = D == 256 ? 1 : 2;          // buffers of V (one of K)
   static constexpr int DV = D < 128 ? 128 : D;         // V tile width: whole M tiles of 128
   static constexpr int OT = DV / 128;                  // M tiles of O^T
-  static constexpr int MAXR = D == 256 ? 96 : 128;     // rows of a CTA: TMEM columns (2 + OT + 1) NR <= 512
+  static constexpr int MAXR = D == 256 ? 96 : 128;     // rows of a CTA, by shared memory
   static constexpr uint32_t KB = kTile * D * 2, VB = kTile * DV * 2;
   static constexpr int G8 = D / 32;                    // 32-code groups per token
   static constexpr bool SPLIT = D == 64;               // K and V on half of the decoder warps each
@@ -73,18 +81,28 @@ struct ShCfg {
   static_assert(N * SIDE == kTile * G8, "every decoder thread has the same number of groups");
 };
 
-struct SharedArgs {
+// One cache pair as the decoders read it.
+struct Source {
   const uint8_t* kc;
   const uint8_t* ks;
   const uint8_t* vc;
   const uint8_t* vs;
-  const uint16_t* q;
-  const int32_t* prefix_len;   // device [1] or NULL
-  float* part;                 // [B*Hq][slots][D + 4]
+  const int32_t* len;          // device lengths ([1] of the prefix, [B] of the sequences) or NULL
   PageMap pages;
-  int64_t S_cap, ctx, per;     // per: tokens per split (multiple of kTile)
+  int64_t S_cap, ctx;
+  int64_t per;                 // tokens per split (multiple of kTile)
+  int splits, slot0;
+};
+
+struct SharedArgs {
+  Source pre, own;
+  const uint16_t* q;
+  float* part;                 // [B*Hq][slots][D + 4]
   uint64_t report_ns, hard_ns;
-  int B, Hq, Hkv, G, lg, NR, slots, slot0;   // G = 1 << lg
+  int B, Hq, Hkv, G, lg, slots;   // G = 1 << lg
+  int NR;                      // rows of a prefix CTA (multiple of 32)
+  int row_tiles;               // prefix CTAs along the rows
+  int n_pre;                   // prefix CTAs, ahead of the sequences' own
   float qscale;
 };
 
@@ -127,29 +145,37 @@ __device__ __forceinline__ void bar_init(uint32_t bar, int count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(bar), "r"(count) : "memory");
 }
 
-// Wait for a phase of an mbarrier as tq_tc.cuh's, but without a sleep between
-// polls: try_wait suspends the warp until the phase completes, and a handoff
-// of this kernel is due within a microsecond.
-__device__ __forceinline__ bool bar_wait_near(uint32_t bar, uint32_t parity, uint64_t report_ns, uint64_t hard_ns,
-                                              int& late) {
-  uint32_t done = 0;
+__device__ __forceinline__ bool bar_done(uint32_t bar, uint32_t parity) {
+  uint32_t done;
   asm volatile(
       "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(done)
       : "r"(bar), "r"(parity)
       : "memory");
-  if (done) return true;
+  return done != 0;
+}
+// Wait of a whole warp for a phase of an mbarrier: one poll and a vote when it
+// has completed.  Otherwise try_wait suspends the warp until it completes (no
+// sleep between polls: a handoff of this kernel is due within a microsecond);
+// past report_ns of wall time it sets `late` and goes on, past hard_ns, or
+// once the CTA has given up, it returns false.
+__device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, uint64_t report_ns, uint64_t hard_ns,
+                                           volatile int* abort, int* late) {
   const uint64_t t0 = global_ns();
   for (;;) {
+    uint32_t done;
     asm volatile(
         "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(done)
         : "r"(bar), "r"(parity), "r"(1000000u)
         : "memory");
     const uint64_t el = global_ns() - t0;
-    if (el > report_ns) late = 1;
-    if (done) return true;
-    if (el > hard_ns) return false;
+    if (el > report_ns) *late = 1;
+    if (__all_sync(kFull, done)) return true;
+    if (__any_sync(kFull, el > hard_ns || *abort)) {
+      *abort = 1;
+      return false;
+    }
   }
 }
 // maximum over the warp, in every lane
@@ -157,6 +183,15 @@ __device__ __forceinline__ float warp_max_f(float x) {
   float y;
   asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// D += A B, one row of ones and zeros of A per row of D (see the sums l)
+__device__ __forceinline__ void hmma_sum(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // The packed words and norm of one 32-code group, loaded a tile ahead.
@@ -189,6 +224,24 @@ __device__ __forceinline__ void load_group_g(int bits, const uint8_t* c, uint32_
   asm volatile("ld.global.nc.u16 %0, [%1];" : "=r"(g.sc) : "l"(s));
 }
 
+// Four fp16x2 registers of a nibble word of 4-bit codes.  The codebook is
+// symmetric, c(15 - k) = -c(k): the upper eight levels in the byte tables, a
+// lower code looked up as 15 - k and its sign bit set in the high byte.
+__device__ __forceinline__ void lut8_sym(uint32_t n, const Tab& T, uint32_t* o) {
+  const uint32_t low = ~n & 0x88888888u;                        // nibbles of lower codes
+  const uint32_t idx = (n ^ (low - (low >> 3))) & 0x77777777u;  // their three bits flipped
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const uint32_t s = half ? __umulhi(idx, 1u << 16) : idx;
+    const uint32_t b = half ? n >> 17 : n >> 1;   // bit 3 of each code as bit 2 of a byte selector
+    const uint32_t lo = lut_prmt(T.t[0], T.t[1], s);
+    const uint32_t neg = lut_prmt(0xffffffffu, 0u, b);
+    const uint32_t hi = lut_prmt(T.t[2], T.t[3], s) ^ (neg & 0x80808080u);
+    o[2 * half] = lut_prmt(lo, hi, 0x5140);
+    o[2 * half + 1] = lut_prmt(lo, hi, 0x7362);
+  }
+}
+
 // One group's 32 values (centroid * norm, fp16) to the core-matrix tile: four
 // 16-byte chunks, one per core matrix.  Each (token, block) table holds the
 // fp32 products of centroids and norm, rounded once to fp16.
@@ -201,11 +254,12 @@ __device__ __forceinline__ void decode_group_b(const Group& g, uint32_t odd, con
   } else {
     chunk_words<BITS>(g.w, n);
   }
-  const Tab T = make_tab_f32<BITS>(cent, h2f((uint16_t)g.sc));
+  const Tab T = make_tab_f32<BITS == 4 ? 3 : BITS>(BITS == 4 ? cent + 8 : cent, h2f((uint16_t)g.sc));
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     uint32_t o[4];
-    lut8<BITS>(n[c], T, o);
+    if (BITS == 4) lut8_sym(n[c], T, o);
+    else lut8<BITS>(n[c], T, o);
     sts16b(dst + 128 * c, o[0], o[1], o[2], o[3]);
   }
 }
@@ -225,49 +279,57 @@ __device__ __forceinline__ void decode_group(int bits, const Group& g, uint32_t 
   }
 }
 
-template <int D, bool PAGED>
+template <int D>
 __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const CodecParams PK, const CodecParams PV,
-                                                                      const SharedArgs a) {
+                                                                      const __grid_constant__ SharedArgs a) {
   using C = ShCfg<D>;
-  constexpr int NB = C::NB, OT = C::OT;
+  constexpr int NV = C::NV, OT = C::OT;
   constexpr uint32_t kKGroup = (D / 8) * 128;       // bytes of 8 tokens of K, 8 rows of Q
   constexpr uint32_t kVGroup = (C::DV / 8) * 128;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ __align__(8) uint64_t bars[4 * NB + 7];
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t bars[2 * NV + 12];
   __shared__ uint32_t tmem_base;
   __shared__ volatile int s_abort;
   __shared__ int s_late;
   __shared__ __align__(16) float s_m[C::MAXR];      // the rows' softmax references
   __shared__ float s_al[C::MAXR];
-  __shared__ float s_wm[4][C::MAXR];                // maxima by TMEM lane quarter (rare path)
+  __shared__ float s_wm[4][C::MAXR];                // maxima, at the end sums, by TMEM lane quarter
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int NR = a.NR;
-  const int split = blockIdx.x, kvh = blockIdx.y, rt = blockIdx.z;
-  const int row0 = rt * NR;
-  const int rows = min(NR, a.B * a.G - row0);
-  int64_t len = a.ctx;
-  if (a.prefix_len) len = imin64(len, (int64_t)a.prefix_len[0]);
-  const int64_t t_lo = (int64_t)split * a.per;
-  const int64_t t_hi = imin64(t_lo + a.per, len);
-  const int n_tiles = t_hi > t_lo ? (int)((t_hi - t_lo + kTile - 1) / kTile) : 0;
+  // a prefix CTA: split fastest, then KV head, then row tile; behind them a
+  // sequence's own: split, KV head, sequence
+  const bool pre = (int)blockIdx.x < a.n_pre;
+  const Source& src = pre ? a.pre : a.own;
+  const int unit = pre ? blockIdx.x : blockIdx.x - a.n_pre;
+  const int split = unit % src.splits, kvh = unit / src.splits % a.Hkv, grp_z = unit / src.splits / a.Hkv;
+  const int NR = pre ? a.NR : 32;
+  const int row0 = pre ? grp_z * a.NR : grp_z * a.G;
+  const int rows = pre ? min(NR, a.B * a.G - row0) : a.G;
+  const int seq = pre ? 0 : grp_z;
+  const int slot = src.slot0 + split;
+  int64_t len = src.ctx;
+  if (src.len) len = imin64(len, (int64_t)src.len[seq]);
+  const int64_t t_lo = (int64_t)split * src.per;
+  const int64_t t_hi = imin64(t_lo + src.per, len);
+  const int n_tok = t_hi > t_lo ? (int)(t_hi - t_lo) : 0;
+  const int n_tiles = (n_tok + kTile - 1) / kTile;
 
-  // K buffers, V buffers, Q^, P, ones
-  const uint32_t aK = su32(smem), aV = aK + NB * C::KB, aQ = aV + NB * C::VB, aP = aQ + (uint32_t)NR * D * 2,
-                 aOnes = aP + (uint32_t)NR * kTile * 2;
-  const uint32_t kfull = su32(&bars[0]), vfull = su32(&bars[NB]), kfree = su32(&bars[2 * NB]),
-                 vfree = su32(&bars[3 * NB]), s_full = su32(&bars[4 * NB]), s_free = su32(&bars[4 * NB + 2]),
-                 p_full = su32(&bars[4 * NB + 4]), o_done = su32(&bars[4 * NB + 5]), drained = su32(&bars[4 * NB + 6]);
-  // TMEM columns
-  const uint32_t cO = 2u * NR, cL = cO + (uint32_t)OT * NR;
-  const uint32_t tcols = cL + NR > 256 ? 512u : (cL + NR > 128 ? 256u : 128u);
+  // K, V buffers, Q^, two P buffers
+  const uint32_t pbytes = (uint32_t)NR * kTile * 2;
+  const uint32_t aK = su32(smem), aV = aK + C::KB, aQ = aV + NV * C::VB, aP = aQ + (uint32_t)NR * D * 2;
+  const uint32_t b0 = su32(&bars[0]);
+  const uint32_t q_full = b0, kfull = b0 + 8, kfree = b0 + 16, s_full = b0 + 24, s_free = b0 + 40, p_full = b0 + 56,
+                 o_done = b0 + 72, drained = b0 + 88, vfull = b0 + 96, vfree = vfull + 8 * NV;
+  // TMEM columns: S twice, then O
+  const uint32_t cO = 2u * NR;
+  const uint32_t tused = cO + (uint32_t)OT * NR;
+  const uint32_t tcols = tused > 256 ? 512u : (tused > 128 ? 256u : 128u);
 
-  auto wait = [&](uint32_t bar, uint32_t parity) {
-    if (__any_sync(kFull, s_abort)) return false;   // one decision per warp
+  auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+    if (__all_sync(kFull, bar_done(bar, parity))) return true;
     int late = 0;
-    const bool ok = __all_sync(kFull, bar_wait_near(bar, parity, a.report_ns, a.hard_ns, late));
+    const bool ok = bar_wait_slow(bar, parity, a.report_ns, a.hard_ns, &s_abort, &late);
     if (late) s_late = 1;
-    if (!ok) s_abort = 1;
     return ok;
   };
 
@@ -275,91 +337,31 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     s_abort = 0;
     s_late = 0;
     constexpr int kSide = C::SIDE / 32;   // decoder warps that fill one side
-#pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      bar_init(kfull + 8 * i, kSide);
-      bar_init(vfull + 8 * i, kSide);
-      bar_init(kfree + 8 * i, 1);
-      bar_init(vfree + 8 * i, 1);
-    }
+    bar_init(q_full, kSoftWarps);
+    bar_init(kfull, kSide);
+    bar_init(kfree, 1);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       bar_init(s_full + 8 * i, 1);
       bar_init(s_free + 8 * i, kSoftWarps);
+      bar_init(p_full + 8 * i, kSoftWarps);
+      bar_init(o_done + 8 * i, 1);
     }
-    bar_init(p_full, kSoftWarps);
-    bar_init(o_done, 1);
     bar_init(drained, 2);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      bar_init(vfull + 8 * i, kSide);
+      bar_init(vfree + 8 * i, 1);
+    }
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
-  if (warp == 0) {
+  if (warp == kSoftWarps) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(su32(&tmem_base)),
                  "r"(tcols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
   }
   if (tid < NR) s_m[tid] = -INFINITY;
-  if (tid < 128) sts16b(aOnes + 16 * tid, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u);
-  // Q^ = H D q per K block, times softmax_scale * log2 e: a warp per row, a
-  // lane the D/32 consecutive values from E*lane on
-  if (n_tiles > 0) {
-    constexpr int E = D / 32;
-    const float qn = PK.inv_sqrt_blk * a.qscale;
-    for (int r = warp; r < NR; r += kThreadsSh / 32) {
-      float v[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = 0.f;
-      if (r < rows) {
-        const int rr = row0 + r, b = rr >> a.lg, h = kvh * a.G + (rr & (a.G - 1));
-        const uint16_t* src = a.q + ((int64_t)b * a.Hq + h) * D + E * lane;
-        uint32_t u[E / 2];
-        if constexpr (E == 8) {
-          const uint4 x = *reinterpret_cast<const uint4*>(src);
-          u[0] = x.x; u[1] = x.y; u[2] = x.z; u[3] = x.w;
-        } else if constexpr (E == 4) {
-          const uint2 x = *reinterpret_cast<const uint2*>(src);
-          u[0] = x.x; u[1] = x.y;
-        } else {
-          u[0] = *reinterpret_cast<const uint32_t*>(src);
-        }
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const int i = E * lane + e;
-          v[e] = flip(h2f((uint16_t)(u[e / 2] >> (16 * (e & 1)))), (PK.sign_bits[i >> 5] >> (i & 31)) & 1u);
-        }
-        for (int hs = 1; hs < E && hs < PK.blk; hs <<= 1) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            if ((e & hs) == 0 && e + hs < E) {
-              const float x = v[e], y = v[e + hs];
-              v[e] = x + y;
-              v[e + hs] = x - y;
-            }
-          }
-        }
-        for (int hs = E; hs < PK.blk; hs <<= 1) {
-          const int lo = hs / E;
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const float x = __shfl_xor_sync(kFull, v[e], lo);
-            v[e] = (lane & lo) ? (x - v[e]) : (v[e] + x);
-          }
-        }
-      }
-      const uint32_t dst = aQ + cm_off(r, E * lane, D);
-      uint32_t o[E / 2];
-#pragma unroll
-      for (int e = 0; e < E / 2; ++e) o[e] = pack2(v[2 * e] * qn, v[2 * e + 1] * qn);
-      if constexpr (E == 8) {
-        sts16b(dst, o[0], o[1], o[2], o[3]);
-      } else if constexpr (E == 4) {
-        asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(dst), "r"(o[0]), "r"(o[1]) : "memory");
-      } else {
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(o[0]) : "memory");
-      }
-    }
-  }
-  fence_async_smem();
   fence_before();
   __syncthreads();
   fence_after();
@@ -371,185 +373,313 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     const int st = C::SPLIT ? dt % C::SIDE : dt;    // thread within its side
     const bool do_k = !C::SPLIT || dt < C::SIDE, do_v = !C::SPLIT || dt >= C::SIDE;
     // the thread's groups: number grp of the tokens tok0 and, at head_dim 256,
-    // kStep tokens on.  Contiguous: pointers of the first that move on by a
-    // tile; paged: page and place in it of each.
+    // kStep tokens on.  Contiguous: byte offsets into the CTA's slice that
+    // move on by a tile; paged: page and place in it of each.
     constexpr int kStep = C::SIDE / C::G8;
     static_assert(C::N == 1 || kStep % 8 == 0, "a thread's groups have one number");
     const int tok0 = 8 * (st / (8 * C::G8)) + (st & 7), grp = (st >> 3) % C::G8;
+    const uint32_t odd = grp & 1;
     const int kbits = PK.bits, vbits = PV.bits;
-    const uint8_t *kw = a.kc + grp * 4 * kbits, *kn = a.ks + 32 * grp / PK.blk * 2;
-    const uint8_t *vw = a.vc + grp * 4 * vbits, *vn = a.vs + 32 * grp / PV.blk * 2;
+    const bool paged = src.pages.table != nullptr;
+    const uint32_t kwb = PK.code_bytes, vwb = PV.code_bytes, knb = 2 * PK.nb, vnb = 2 * PV.nb;
+    uint32_t kw = grp * 4 * kbits, kn = 32 * grp / PK.blk * 2, vw = grp * 4 * vbits, vn = 32 * grp / PV.blk * 2;
+    const int64_t rec0 = paged ? 0 : ((int64_t)seq * a.Hkv + kvh) * src.S_cap + t_lo;
+    const uint8_t *kc = src.kc + rec0 * kwb, *ks = src.ks + rec0 * knb, *vc = src.vc + rec0 * vwb,
+                  *vs = src.vs + rec0 * vnb;
+    const int32_t* table = paged ? src.pages.table + (int64_t)seq * src.pages.pages_per_seq : nullptr;
+    const int psize = src.pages.page_size;
     int32_t page[C::N], off[C::N];
-    if (PAGED) {
 #pragma unroll
-      for (int k = 0; k < C::N; ++k) {
+    for (int k = 0; k < C::N; ++k) {
+      page[k] = off[k] = 0;
+      if (paged) {
         const int64_t t = t_lo + tok0 + k * kStep;
-        page[k] = (int32_t)(t / a.pages.page_size);
-        off[k] = (int32_t)(t - (int64_t)page[k] * a.pages.page_size);
+        page[k] = (int32_t)(t / psize);
+        off[k] = (int32_t)(t - (int64_t)page[k] * psize);
       }
-    } else {
-      const int64_t r = (int64_t)kvh * a.S_cap + t_lo + tok0;
-      kw += r * PK.code_bytes;
-      vw += r * PV.code_bytes;
-      kn += r * PK.nb * 2;
-      vn += r * PV.nb * 2;
+    }
+    if (!paged) {
+      kw += tok0 * kwb;
+      vw += tok0 * vwb;
+      kn += tok0 * knb;
+      vn += tok0 * vnb;
     }
     Group gk[C::N], gv[C::N];
-    auto left_of = [&](int t) { return (int)imin64(kTile, t_hi - (t_lo + (int64_t)t * kTile)); };
-    auto load = [&](int t) {
-      const int left = left_of(t);
+    int32_t pgk[C::N];   // page of the next tile's tokens (paged)
+    // loads of one side of the tile whose tokens begin `at` tokens into the slice
+    auto load_k = [&](int at) {
 #pragma unroll
       for (int k = 0; k < C::N; ++k) {
-        if (tok0 + k * kStep < left) {
-          int64_t r = k * kStep;
-          if (PAGED) r = ((int64_t)a.pages.table[page[k]] * a.Hkv + kvh) * a.pages.page_size + off[k];
-          if (do_k) load_group_g(kbits, kw + r * PK.code_bytes, grp & 1, kn + r * (PK.nb * 2), gk[k]);
-          if (do_v) load_group_g(vbits, vw + r * PV.code_bytes, grp & 1, vn + r * (PV.nb * 2), gv[k]);
-        }
-        if (PAGED) {
-          off[k] += kTile;
-          while (off[k] >= a.pages.page_size) {
-            off[k] -= a.pages.page_size;
-            ++page[k];
-          }
+        if (tok0 + k * kStep + at >= n_tok) continue;
+        if (paged) {
+          const int64_t r = ((int64_t)pgk[k] * a.Hkv + kvh) * psize + off[k];
+          load_group_g(kbits, kc + r * kwb + kw, odd, ks + r * knb + kn, gk[k]);
+        } else {
+          load_group_g(kbits, kc + (kw + k * kStep * kwb), odd, ks + (kn + k * kStep * knb), gk[k]);
         }
       }
-      if (!PAGED) {
-        kw += kTile * PK.code_bytes;
-        vw += kTile * PV.code_bytes;
-        kn += kTile * PK.nb * 2;
-        vn += kTile * PV.nb * 2;
+      if (!paged) {
+        kw += kTile * kwb;
+        kn += kTile * knb;
       }
     };
-    if (n_tiles > 0) load(0);
+    auto load_v = [&](int at) {
+#pragma unroll
+      for (int k = 0; k < C::N; ++k) {
+        if (tok0 + k * kStep + at >= n_tok) continue;
+        if (paged) {
+          const int64_t r = ((int64_t)pgk[k] * a.Hkv + kvh) * psize + off[k];
+          load_group_g(vbits, vc + r * vwb + vw, odd, vs + r * vnb + vn, gv[k]);
+        } else {
+          load_group_g(vbits, vc + (vw + k * kStep * vwb), odd, vs + (vn + k * kStep * vnb), gv[k]);
+        }
+      }
+      if (!paged) {
+        vw += kTile * vwb;
+        vn += kTile * vnb;
+      }
+    };
+    // the pages of a tile's tokens: read before its loads, moved on after them
+    auto pages_of = [&](int at) {
+      if (!paged) return;
+#pragma unroll
+      for (int k = 0; k < C::N; ++k)
+        if (tok0 + k * kStep + at < n_tok) pgk[k] = table[page[k]];
+    };
+    auto pages_on = [&]() {
+      if (!paged) return;
+#pragma unroll
+      for (int k = 0; k < C::N; ++k) {
+        off[k] += kTile;
+        while (off[k] >= psize) {
+          off[k] -= psize;
+          ++page[k];
+        }
+      }
+    };
+    pages_of(0);
+    if (do_k) load_k(0);
+    if (do_v) load_v(0);
+    pages_on();
     for (int t = 0; t < n_tiles; ++t) {
-      const int bf = t % NB;
-      const int left = left_of(t);
-      const uint32_t ph = (uint32_t)(t / NB - 1) & 1;
+      const int vb = t % NV, at = t * kTile;
+      pages_of(at + kTile);
       if (do_k) {
-        if (t >= NB) wait(kfree + 8 * bf, ph);
+        if (t >= 1) wait(kfree, (uint32_t)(t - 1) & 1);
         if (!s_abort) {
 #pragma unroll
           for (int k = 0; k < C::N; ++k)
-            decode_group(kbits, gk[k], grp & 1, PK.centroids, tok0 + k * kStep < left,
-                         aK + bf * C::KB + cm_off(tok0 + k * kStep, 32 * grp, D));
+            decode_group(kbits, gk[k], odd, PK.centroids, at + tok0 + k * kStep < n_tok,
+                         aK + cm_off(tok0 + k * kStep, 32 * grp, D));
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) arrive(kfull + 8 * bf);
+        if (lane == 0) arrive(kfull);
+        if (t + 1 < n_tiles) load_k(at + kTile);
       }
       if (do_v) {
-        if (t >= NB) wait(vfree + 8 * bf, ph);
+        if (t >= NV) wait(vfree + 8 * vb, (uint32_t)(t / NV - 1) & 1);
         if (!s_abort) {
 #pragma unroll
           for (int k = 0; k < C::N; ++k)
-            decode_group(vbits, gv[k], grp & 1, PV.centroids, tok0 + k * kStep < left,
-                         aV + bf * C::VB + cm_off(tok0 + k * kStep, 32 * grp, C::DV));
+            decode_group(vbits, gv[k], odd, PV.centroids, at + tok0 + k * kStep < n_tok,
+                         aV + vb * C::VB + cm_off(tok0 + k * kStep, 32 * grp, C::DV));
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) arrive(vfull + 8 * bf);
+        if (lane == 0) arrive(vfull + 8 * vb);
+        if (t + 1 < n_tiles) load_v(at + kTile);
       }
-      if (t + 1 < n_tiles) load(t + 1);
+      pages_on();
     }
   } else if (warp == kSoftWarps) {
     // ================= S^T(t) = K^(t) Q^
     const uint32_t idesc = (1u << 4) | ((uint32_t)(NR >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
-    const uint64_t dq = sdesc(aQ, 128, kKGroup);
-    for (int t = 0; t < n_tiles; ++t) {
-      const int bf = t % NB;
-      if (!wait(kfull + 8 * bf, (uint32_t)(t / NB) & 1)) break;
-      if (t >= 2 && !wait(s_free + 8 * (t & 1), (uint32_t)((t >> 1) - 1) & 1)) break;
+    const uint64_t dq = sdesc(aQ, 128, kKGroup), dk = sdesc(aK, 128, kKGroup);
+    bool ok = n_tiles > 0 && wait(q_full, 0);
+    for (int t = 0; t < n_tiles && ok; ++t) {
+      ok = wait(kfull, (uint32_t)t & 1) && (t < 2 || wait(s_free + 8 * (t & 1), (uint32_t)((t >> 1) - 1) & 1));
+      if (!ok) break;
       fence_after();
       __syncwarp();
-      const uint64_t dk = sdesc(aK + bf * C::KB, 128, kKGroup);
 #pragma unroll
       for (int s = 0; s < D / 16; ++s)
         mma_ss_elect(tmem + (t & 1) * NR, dk + (uint64_t)(16 * s), dq + (uint64_t)(16 * s), idesc, s > 0);
       commit_elect(s_full + 8 * (t & 1));
-      commit_elect(kfree + 8 * bf);
+      commit_elect(kfree);
     }
     __syncwarp();
     commit_elect(drained);
   } else if (warp == kSoftWarps + 1) {
-    // ================= O^T += V^(t)^T P(t)^T, L += ones P(t)^T
+    // ================= O^T += V^(t)^T P(t)^T
     const uint32_t idesc = (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(NR >> 3) << 17) |
                            ((uint32_t)(128 >> 4) << 24);
-    const uint32_t idesc_l = (1u << 4) | (1u << 16) | ((uint32_t)(NR >> 3) << 17) | ((uint32_t)(64 >> 4) << 24);
     const uint32_t pg = (uint32_t)(NR >> 3) * 128;   // bytes of 8 tokens of P
-    const uint64_t dp = sdesc(aP, pg, 128), done = sdesc(aOnes, 128, 256);
     for (int t = 0; t < n_tiles; ++t) {
-      const int bf = t % NB;
-      if (!wait(vfull + 8 * bf, (uint32_t)(t / NB) & 1)) break;
-      if (!wait(p_full, (uint32_t)t & 1)) break;
+      const int vb = t % NV, pb = t & 1;
+      if (!wait(vfull + 8 * vb, (uint32_t)(t / NV) & 1)) break;
+      if (!wait(p_full + 8 * pb, (uint32_t)(t >> 1) & 1)) break;
       fence_after();
       __syncwarp();
+      const uint64_t dp = sdesc(aP + pb * pbytes, pg, 128);
 #pragma unroll
       for (int m = 0; m < OT; ++m) {
-        const uint64_t dv = sdesc(aV + bf * C::VB + m * 16 * 128, kVGroup, 128);
+        const uint64_t dv = sdesc(aV + vb * C::VB + m * 16 * 128, kVGroup, 128);
 #pragma unroll
         for (int s = 0; s < kTile / 16; ++s)
           mma_ss_elect(tmem + cO + m * NR, dv + (uint64_t)(s * (2 * kVGroup >> 4)),
                        dp + (uint64_t)(s * (2 * pg >> 4)), idesc, t > 0 || s > 0);
       }
-#pragma unroll
-      for (int s = 0; s < kTile / 16; ++s)
-        mma_ss_elect(tmem + cL, done, dp + (uint64_t)(s * (2 * pg >> 4)), idesc_l, t > 0 || s > 0);
-      commit_elect(o_done);
-      commit_elect(vfree + 8 * bf);
+      commit_elect(o_done + 8 * pb);
+      commit_elect(vfree + 8 * vb);
     }
     __syncwarp();
     commit_elect(drained);
   } else {
+    // ================= queries: Q^ = H D q per K block, times softmax_scale *
+    // log2 e; a warp per row, a lane the D/32 consecutive values from E*lane
+    // on, four rows in flight
+    if (n_tiles > 0) {
+      constexpr int E = D / 32, RB = 4;
+      const float qn = PK.inv_sqrt_blk * a.qscale;
+      for (int r0 = warp * RB; r0 < NR; r0 += kSoftWarps * RB) {
+        uint32_t u[RB][E / 2];
+#pragma unroll
+        for (int x = 0; x < RB; ++x) {
+          const int r = r0 + x;
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) u[x][e] = 0u;
+          if (r >= rows) continue;
+          const int rr = row0 + r, b = rr >> a.lg, h = kvh * a.G + (rr & (a.G - 1));
+          const uint16_t* qr = a.q + ((int64_t)b * a.Hq + h) * D + E * lane;
+          if constexpr (E == 8) {
+            const uint4 w = *reinterpret_cast<const uint4*>(qr);
+            u[x][0] = w.x; u[x][1] = w.y; u[x][2] = w.z; u[x][3] = w.w;
+          } else if constexpr (E == 4) {
+            const uint2 w = *reinterpret_cast<const uint2*>(qr);
+            u[x][0] = w.x; u[x][1] = w.y;
+          } else {
+            u[x][0] = *reinterpret_cast<const uint32_t*>(qr);
+          }
+        }
+        float v[RB][E];
+#pragma unroll
+        for (int x = 0; x < RB; ++x)
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const int i = E * lane + e;
+            v[x][e] = flip(h2f((uint16_t)(u[x][e / 2] >> (16 * (e & 1)))), (PK.sign_bits[i >> 5] >> (i & 31)) & 1u);
+          }
+#pragma unroll
+        for (int hs = 1; hs < E; hs <<= 1) {
+          if (hs >= PK.blk) break;
+#pragma unroll
+          for (int x = 0; x < RB; ++x)
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+              if ((e & hs) == 0) {
+                const float p = v[x][e], q = v[x][e + hs];
+                v[x][e] = p + q;
+                v[x][e + hs] = p - q;
+              }
+        }
+        for (int hs = E; hs < PK.blk; hs <<= 1) {
+          const int lo = hs / E;
+#pragma unroll
+          for (int x = 0; x < RB; ++x)
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              const float p = __shfl_xor_sync(kFull, v[x][e], lo);
+              v[x][e] = (lane & lo) ? (p - v[x][e]) : (v[x][e] + p);
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < RB; ++x) {
+          const uint32_t dst = aQ + cm_off(r0 + x, E * lane, D);
+          uint32_t o[E / 2];
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) o[e] = pack2(v[x][2 * e] * qn, v[x][2 * e + 1] * qn);
+          if constexpr (E == 8) {
+            sts16b(dst, o[0], o[1], o[2], o[3]);
+          } else if constexpr (E == 4) {
+            asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(dst), "r"(o[0]), "r"(o[1]) : "memory");
+          } else {
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(o[0]) : "memory");
+          }
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive(q_full);
+    }
     // ================= softmax: thread = token (TMEM lane) x half of the rows
     const int quarter = warp & 3, half = warp >> 2, bid = 1 + half;
     const int nc = NR / 2, col0 = half * nc;
     const int tk = 32 * quarter + lane;
     const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
-    const uint32_t pdst = aP + cm_off(tk, col0, NR);
-    // p of 16 columns from c on, from their scores: stored to P; returns the
-    // largest s - m.  A token past the slice has p = 0.
-    auto emit = [&](uint32_t* v, int c, bool live) {
-      float mx = -INFINITY;
-      uint32_t o[8];
+    const uint32_t pdst0 = aP + cm_off(tk, col0, NR);
+    // the sums' A operand: row g of ones at even (odd) k of the first or
+    // second register, for the columns 4i + 0 .. 3 of product i
+    const int g = lane >> 2;
+    const uint32_t ev = (g & 1) ? 0x3C000000u : 0x00003C00u;
+    const uint32_t x0 = (g >> 1) == 0 ? ev : 0u, y0 = (g >> 1) == 1 ? ev : 0u;
+    const uint32_t x1 = (g >> 1) == 2 ? ev : 0u, y1 = (g >> 1) == 3 ? ev : 0u;
+    constexpr int NCH = C::MAXR / 32;       // column chunks of 16
+    float lsum[NCH][4], lnew[NCH][4];
 #pragma unroll
-      for (int j = 0; j < 16; j += 4) {
-        const float4 m = *reinterpret_cast<const float4*>(&s_m[col0 + c + j]);
-        const float x0 = __uint_as_float(v[j]) - m.x, x1 = __uint_as_float(v[j + 1]) - m.y;
-        const float x2 = __uint_as_float(v[j + 2]) - m.z, x3 = __uint_as_float(v[j + 3]) - m.w;
-        mx = fmaxf(mx, fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)));
-        o[j / 2] = pack2(ex2s(x0), ex2s(x1));
-        o[j / 2 + 1] = pack2(ex2s(x2), ex2s(x3));
-      }
-      if (!live) {
-        mx = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = 0u;
-      }
-      sts16b(pdst + (c >> 3) * 128, o[0], o[1], o[2], o[3]);
-      sts16b(pdst + (c >> 3) * 128 + 128, o[4], o[5], o[6], o[7]);
-      return mx;
-    };
+    for (int i = 0; i < NCH; ++i) lsum[i][0] = lsum[i][1] = lsum[i][2] = lsum[i][3] = 0.f;
     for (int t = 0; t < n_tiles; ++t) {
-      const bool live = tk < t_hi - (t_lo + (int64_t)t * kTile);
+      const bool live = t * kTile + tk < n_tok;
       const uint32_t sS = lanes + (t & 1) * NR + col0;
+      const uint32_t pdst = pdst0 + (t & 1) * pbytes;
+      // p of every column from its score, to P and the sums; returns the
+      // largest s - m.  A token past the slice has p = 0.
+      auto emit = [&]() {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+          if (16 * i >= nc) break;
+          uint32_t v[16], o[8];
+          TQ_LD16(sS + 16 * i, v);
+          ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(&s_m[col0 + 16 * i + j]);
+            const float e0 = __uint_as_float(v[j]) - m.x, e1 = __uint_as_float(v[j + 1]) - m.y;
+            const float e2 = __uint_as_float(v[j + 2]) - m.z, e3 = __uint_as_float(v[j + 3]) - m.w;
+            mx = fmaxf(mx, fmaxf(fmaxf(e0, e1), fmaxf(e2, e3)));
+            o[j / 2] = pack2(ex2s(e0), ex2s(e1));
+            o[j / 2 + 1] = pack2(ex2s(e2), ex2s(e3));
+          }
+          if (!live) {
+            mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = 0u;
+          }
+          __syncwarp();
+          sts16b(pdst + 256 * i, o[0], o[1], o[2], o[3]);
+          sts16b(pdst + 256 * i + 128, o[4], o[5], o[6], o[7]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) lnew[i][j] = lsum[i][j];
+          hmma_sum(lnew[i], x0, 0u, y0, 0u, o[0], o[1]);
+          hmma_sum(lnew[i], x1, 0u, y1, 0u, o[2], o[3]);
+          hmma_sum(lnew[i], 0u, x0, 0u, y0, o[4], o[5]);
+          hmma_sum(lnew[i], 0u, x1, 0u, y1, o[6], o[7]);
+        }
+        return mx;
+      };
       wait(s_full + 8 * (t & 1), (uint32_t)(t >> 1) & 1);
-      if (t >= 1) wait(o_done, (uint32_t)(t - 1) & 1);   // P is free, O and L stand still
+      if (t >= 2) wait(o_done + 8 * (t & 1), (uint32_t)((t >> 1) - 1) & 1);   // P(t - 2) has been read
       fence_after();
       bool moved = t == 0;
-      if (!moved) {
-        float mx = -INFINITY;
-        for (int c = 0; c < nc; c += 16) {
-          uint32_t v[16];
-          TQ_LD16(sS + c, v);
-          ld_wait();
-          mx = fmaxf(mx, emit(v, c, live));
-        }
-        moved = half_any(bid, mx > kLazySh);
-      }
+      if (!moved) moved = half_any(bid, emit() > kLazySh);
       if (moved) {
         // some row's reference moves (the first tile sets them): its maximum
-        // over the tile, O and L scaled, P written again
+        // over the tile, O and l scaled, P written again
+        if (t >= 1) {
+          wait(o_done + 8 * ((t - 1) & 1), (uint32_t)((t - 1) >> 1) & 1);   // O stands still
+          fence_after();
+        }
         for (int c = 0; c < nc; c += 16) {
           uint32_t v[16];
           TQ_LD16(sS + c, v);
@@ -572,8 +702,17 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
         }
         half_sync(bid);
         if (t >= 1) {
+#pragma unroll
+          for (int i = 0; i < NCH; ++i) {
+            if (16 * i >= nc) break;
+            const float a0 = s_al[col0 + 16 * i + g], a1 = s_al[col0 + 16 * i + 8 + g];
+            lsum[i][0] *= a0;
+            lsum[i][1] *= a0;
+            lsum[i][2] *= a1;
+            lsum[i][3] *= a1;
+          }
 #pragma unroll 1
-          for (int m = 0; m <= OT; ++m) {   // O's M tiles, then L
+          for (int m = 0; m < OT; ++m) {
 #pragma unroll 1
             for (int c = 0; c < nc; c += 16) {
               uint32_t v[16];
@@ -587,77 +726,100 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
           }
           st_wait();
         }
-        for (int c = 0; c < nc; c += 16) {
-          uint32_t v[16];
-          TQ_LD16(sS + c, v);
-          ld_wait();
-          emit(v, c, live);
-        }
+        emit();
       }
+#pragma unroll
+      for (int i = 0; i < NCH; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) lsum[i][j] = lnew[i][j];
       fence_async_smem();
       fence_before();
       __syncwarp();
       if (lane == 0) {
-        arrive(p_full);
+        arrive(p_full + 8 * (t & 1));
         arrive(s_free + 8 * (t & 1));
       }
     }
-    if (n_tiles > 0) wait(o_done, (uint32_t)(n_tiles - 1) & 1);
-    fence_after();
-    const bool ok = n_tiles > 0 && !__any_sync(kFull, s_abort);
-    // partials: lane = dimension of O^T, column = row
-    for (int c = 0; c < nc; c += 16) {
-      uint32_t l[16];
-      if (ok && quarter == 0) {
-        TQ_LD16(lanes + cL + col0 + c, l);
-        ld_wait();
-      }
-#pragma unroll 1
-      for (int m = 0; m < OT; ++m) {
-        uint32_t v[16];
-        if (ok) {
-          TQ_LD16(lanes + cO + m * NR + col0 + c, v);
-          ld_wait();
-        }
-        const int dim = 128 * m + tk;
+    // the rows' sums over this warp's tokens
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int r = col0 + c + j;
-          if (r >= rows) continue;
-          const int rr = row0 + r, b = rr >> a.lg, h = kvh * a.G + (rr & (a.G - 1));
-          float* dst = a.part + (((int64_t)b * a.Hq + h) * a.slots + a.slot0 + split) * (D + 4);
-          if (dim < D) dst[2 + dim] = ok ? __uint_as_float(v[j]) : 0.f;
-          if (m == 0 && quarter == 0 && lane == j) {
-            dst[0] = ok ? s_m[r] : -INFINITY;
-            dst[1] = ok ? __uint_as_float(l[j]) : 0.f;
-          }
-        }
+    for (int i = 0; i < NCH; ++i) {
+      if (16 * i >= nc) break;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = lsum[i][2 * e] + lsum[i][2 * e + 1];
+        x += __shfl_xor_sync(kFull, x, 1);
+        x += __shfl_xor_sync(kFull, x, 2);
+        if ((lane & 3) == 0) s_wm[quarter][col0 + 16 * i + 8 * e + g] = x;
       }
     }
   }
   // the next kernel may be scheduled; it waits for this grid before it ends
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  __syncthreads();
+  if (n_tiles > 0) wait(o_done + 8 * ((n_tiles - 1) & 1), (uint32_t)((n_tiles - 1) >> 1) & 1);
+  fence_after();
+  // partials: lane = dimension of O^T, column = row; six groups of four warps
+  // (a TMEM lane quarter each) take 16 columns of one M tile at a time
+  const bool ok = n_tiles > 0 && !__any_sync(kFull, s_abort);
+  if (warp < 24) {
+    const int quarter = warp & 3;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
+    const int64_t rstep = (int64_t)a.slots * (D + 4);
+    for (int w = warp >> 2; w < OT * (NR / 16); w += 6) {
+      const int m = w % OT, c = w / OT * 16;
+      uint32_t v[16];
+      if (ok) {
+        TQ_LD16(lanes + cO + m * NR + c, v);
+        ld_wait();
+      }
+      const int dim = 128 * m + 32 * quarter + lane;
+      int hh = (row0 + c) & (a.G - 1);
+      float* dst = a.part + ((int64_t)((row0 + c) >> a.lg) * a.Hq + kvh * a.G + hh) * rstep + (int64_t)slot * (D + 4);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        if (c + j < rows) {
+          if (dim < D) dst[2 + dim] = ok ? __uint_as_float(v[j]) : 0.f;
+          if (m == 0 && quarter == 0 && lane == j) {
+            const int r = c + j;
+            dst[0] = ok ? s_m[r] : -INFINITY;
+            dst[1] = ok ? (s_wm[0][r] + s_wm[1][r]) + (s_wm[2][r] + s_wm[3][r]) : 0.f;
+          }
+        }
+        ++hh;
+        dst += rstep;
+        if (hh == a.G) {   // the next sequence's first head
+          hh = 0;
+          dst += (int64_t)(a.Hq - a.G) * rstep;
+        }
+      }
+    }
+  }
   fence_before();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == kSoftWarps) {
     fence_after();
     // every product has been committed and, on the normal path, has ended
-    int late = 0;
-    __all_sync(kFull, bar_wait_near(drained, 0, a.report_ns, a.hard_ns, late));
+    if (!__all_sync(kFull, bar_done(drained, 0))) {
+      int late = 0;
+      s_abort = 0;   // the others have left: wait for the products themselves
+      __syncwarp();
+      if (!bar_wait_slow(drained, 0, a.report_ns, a.hard_ns, &s_abort, &late) || late) s_late = 1;
+    }
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(tcols) : "memory");
-    if (lane == 0 && (s_abort || s_late || late)) atomicCAS(&g_shared_status, 0, (int)TQ_ERR_TIMEOUT);
+    if (lane == 0 && (s_abort || s_late)) atomicCAS(&g_shared_status, 0, (int)TQ_ERR_TIMEOUT);
   }
 }
 
 template <int D>
 size_t shared_smem(int NR) {
-  return (size_t)ShCfg<D>::NB * (ShCfg<D>::KB + ShCfg<D>::VB) + (size_t)NR * D * 2 + (size_t)NR * kTile * 2 + 2048;
+  using C = ShCfg<D>;
+  return (size_t)C::KB + (size_t)C::NV * C::VB + (size_t)NR * D * 2 + (size_t)2 * NR * kTile * 2;
 }
 
-template <int D, bool PAGED>
-int launch_shared(const CodecParams& PK, const CodecParams& PV, const SharedArgs& a, dim3 grid, cudaStream_t st) {
-  auto kern = shared_prefix_kernel<D, PAGED>;
-  const size_t sm = shared_smem<D>(a.NR);
+template <int D>
+int launch_shared(const CodecParams& PK, const CodecParams& PV, const SharedArgs& a, unsigned grid, cudaStream_t st) {
+  auto kern = shared_prefix_kernel<D>;
+  const size_t sm = shared_smem<D>(a.n_pre ? a.NR : 32);
   static bool attr_set[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return TQ_ERR_CUDA;
@@ -678,42 +840,63 @@ void shared_rows(int d, int64_t R, int* tiles, int* NR) {
   *NR = (int)(((R + *tiles - 1) / *tiles + 31) / 32 * 32);
 }
 
+Source source_of(const tq_kv_view* K, const tq_kv_view* V, const int32_t* len, int64_t S_cap, int64_t ctx, int splits,
+                 int slot0) {
+  Source s{};
+  s.kc = K->codes;
+  s.ks = reinterpret_cast<const uint8_t*>(K->scales);
+  s.vc = V->codes;
+  s.vs = reinterpret_cast<const uint8_t*>(V->scales);
+  s.len = len;
+  s.pages = {K->page_table, K->page_table ? K->page_size : 0, K->page_table ? K->pages_per_seq : 0};
+  s.S_cap = S_cap;
+  s.ctx = ctx;
+  const int64_t tiles = (ctx + kTile - 1) / kTile;
+  s.per = (tiles + splits - 1) / splits * kTile;
+  s.splits = splits;
+  s.slot0 = slot0;
+  return s;
+}
+
 }  // namespace
 
-// Layouts whose prefix the tensor-core kernel takes: 1..4 bits without QJL,
-// norms on their own alignment.
+// Layouts the tensor-core kernel takes: 1..4 bits without QJL.
 bool shared_tc_eligible(const CodecParams& PK, const CodecParams& PV) {
   return !PK.m && !PV.m && PK.bits <= 4 && PV.bits <= 4;
 }
 
-// Prefix splits: one wave of a CTA per SM, each at least a tile.
-int shared_tc_splits(int d, int B, int G, int Hkv, int64_t ctx) {
+// Splits of the prefix and of each sequence's own tokens.  One CTA per SM at a
+// time: the prefix fills one wave (at least a tile each); the own tokens are
+// split as far as the SMs that the prefix leaves idle, or a second wave, take
+// them.
+void shared_tc_splits(int d, int B, int G, int Hkv, int64_t prefix_ctx, int64_t ctx, int* n_prefix, int* n_own) {
   int tiles, NR;
   shared_rows(d, (int64_t)B * G, &tiles, &NR);
-  const int64_t most = (ctx + kTile - 1) / kTile;
-  int64_t ns = sm_count() / ((int64_t)tiles * Hkv);
-  if (ns > most) ns = most;
-  return ns < 1 ? 1 : (int)ns;
+  const int64_t sms = sm_count();
+  auto fit = [&](int64_t units, int64_t room, int64_t c) {
+    const int64_t most = (c + kTile - 1) / kTile;
+    int64_t ns = room / units;
+    if (ns > most) ns = most;
+    return (int)(ns < 1 ? 1 : ns);
+  };
+  *n_prefix = prefix_ctx > 0 ? fit((int64_t)tiles * Hkv, sms, prefix_ctx) : 0;
+  const int64_t used = (int64_t)*n_prefix * tiles * Hkv;
+  const int64_t idle = used < sms ? sms - used : 0;
+  *n_own = ctx > 0 ? fit((int64_t)B * Hkv, idle > sms / 2 ? idle : sms, ctx) : 0;
 }
 
-// Writes the partials of the prefix to slots [slot0, slot0 + n_split).
-int launch_shared_tc(const CodecParams& PK, const CodecParams& PV, const tq_kv_view* K, const tq_kv_view* V,
-                     const uint16_t* q, const int32_t* prefix_len, float* part, int B, int Hq, int Hkv, int64_t S_cap,
-                     int64_t ctx, int n_split, int slots, int slot0, float qscale, cudaStream_t st) {
+// Writes the partials of the own tokens to slots [0, n_own) and those of the
+// prefix to [n_own, n_own + n_prefix).
+int launch_shared_tc(const CodecParams& PK, const CodecParams& PV, const tq_kv_view* Kp, const tq_kv_view* Vp,
+                     int64_t P_cap, const int32_t* prefix_len, int64_t prefix_ctx, int n_prefix, const tq_kv_view* K,
+                     const tq_kv_view* V, int64_t S_cap, const int32_t* kv_len, int64_t ctx, int n_own,
+                     const uint16_t* q, float* part, int B, int Hq, int Hkv, float qscale, cudaStream_t st) {
   const WaitLimits wl = wait_limits();
   SharedArgs a{};
-  a.kc = K->codes;
-  a.ks = reinterpret_cast<const uint8_t*>(K->scales);
-  a.vc = V->codes;
-  a.vs = reinterpret_cast<const uint8_t*>(V->scales);
+  if (n_prefix) a.pre = source_of(Kp, Vp, prefix_len, P_cap, prefix_ctx, n_prefix, n_own);
+  if (n_own) a.own = source_of(K, V, kv_len, S_cap, ctx, n_own, 0);
   a.q = q;
-  a.prefix_len = prefix_len;
   a.part = part;
-  a.pages = {K->page_table, K->page_table ? K->page_size : 0, K->page_table ? K->pages_per_seq : 0};
-  a.S_cap = S_cap;
-  a.ctx = ctx;
-  const int64_t tiles_all = (ctx + kTile - 1) / kTile;
-  a.per = (tiles_all + n_split - 1) / n_split * kTile;
   a.report_ns = wl.report_ns;
   a.hard_ns = wl.hard_ns;
   a.B = B;
@@ -721,16 +904,16 @@ int launch_shared_tc(const CodecParams& PK, const CodecParams& PV, const tq_kv_v
   a.Hkv = Hkv;
   a.G = Hq / Hkv;
   while ((1 << a.lg) < a.G) ++a.lg;
-  a.slots = slots;
-  a.slot0 = slot0;
+  a.slots = n_own + n_prefix;
   a.qscale = qscale;
-  int tiles;
-  shared_rows(PK.d, (int64_t)B * a.G, &tiles, &a.NR);
-  const dim3 grid((unsigned)n_split, (unsigned)Hkv, (unsigned)tiles);
+  shared_rows(PK.d, (int64_t)B * a.G, &a.row_tiles, &a.NR);
+  const int64_t n_pre = (int64_t)n_prefix * Hkv * a.row_tiles, all = n_pre + (int64_t)n_own * Hkv * B;
+  if (all > 0x7fffffff) return TQ_ERR_UNSUPPORTED;
+  a.n_pre = (int)n_pre;
   switch (PK.d) {
-    case 64: return a.pages.table ? launch_shared<64, true>(PK, PV, a, grid, st) : launch_shared<64, false>(PK, PV, a, grid, st);
-    case 128: return a.pages.table ? launch_shared<128, true>(PK, PV, a, grid, st) : launch_shared<128, false>(PK, PV, a, grid, st);
-    default: return a.pages.table ? launch_shared<256, true>(PK, PV, a, grid, st) : launch_shared<256, false>(PK, PV, a, grid, st);
+    case 64: return launch_shared<64>(PK, PV, a, (unsigned)all, st);
+    case 128: return launch_shared<128>(PK, PV, a, (unsigned)all, st);
+    default: return launch_shared<256>(PK, PV, a, (unsigned)all, st);
   }
 }
 
