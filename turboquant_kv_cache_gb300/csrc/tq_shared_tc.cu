@@ -26,8 +26,9 @@
 // one sequence, its G rows and a slice of its tokens.  Prefix and own CTAs
 // are one launch.
 //
-// Warps: 0-7 softmax (warps 0-3 rows [0, NR/2), 4-7 the rest), which also
-// rotate the queries, 8 issues S, 9 issues O, 10-25 decode.  A decoder thread
+// Warps: 0-7 softmax (warps 0-3 rows [0, NR/2), 4-7 the rest), 8 issues S, 9
+// issues O, 12-27 decode; softmax and decoder warps rotate the queries while
+// the first loads are in flight.  A decoder thread
 // takes one 32-code group (two at head_dim 256) of the K tile and of the V
 // tile, its packed words loaded a tile ahead; at head_dim 64 half of the
 // decoder warps take K, half V.  Handoffs are mbarriers:
@@ -41,6 +42,8 @@
 // TMEM.
 #include <cuda_runtime.h>
 #include <math.h>
+
+#include <atomic>
 
 #include "tq_device.cuh"
 #include "tq_lut.cuh"
@@ -58,8 +61,13 @@ constexpr int kTile = 128;          // tokens per tile (MMA M of S^T)
 constexpr int kSoftWarps = 8;
 constexpr int kDecWarps = 16;
 constexpr int kDecThreads = 32 * kDecWarps;
-constexpr int kDec0 = 32 * (kSoftWarps + 2);          // first decoder thread
-constexpr int kThreadsSh = kDec0 + kDecThreads;       // 832
+constexpr int kDec0 = 32 * (kSoftWarps + 4);          // first decoder thread (whole warpgroups)
+constexpr int kThreadsSh = kDec0 + kDecThreads;       // 896
+// registers a thread: at launch, then the softmax warps' and the others'
+// (shares of the launch's: 256 * 104 + 640 * 56 <= 896 * 72)
+constexpr int kLaunchRegs = 72, kSoftRegs = 104, kOtherRegs = 56;
+static_assert(32 * kSoftWarps * kSoftRegs + (kThreadsSh - 32 * kSoftWarps) * kOtherRegs <= kThreadsSh * kLaunchRegs,
+              "the register split fits the launch's");
 // log2 units a score may pass its row's reference by: p stays below 2^12, far
 // inside fp16, and sums of p * v inside fp32
 constexpr float kLazySh = 12.0f;
@@ -159,8 +167,8 @@ __device__ __forceinline__ bool bar_done(uint32_t bar, uint32_t parity) {
 // sleep between polls: a handoff of this kernel is due within a microsecond);
 // past report_ns of wall time it sets `late` and goes on, past hard_ns, or
 // once the CTA has given up, it returns false.
-__device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, uint64_t report_ns, uint64_t hard_ns,
-                                           volatile int* abort, int* late) {
+__device__ __forceinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, uint64_t report_ns, uint64_t hard_ns,
+                                           volatile int& abort, int& late) {
   const uint64_t t0 = global_ns();
   for (;;) {
     uint32_t done;
@@ -170,10 +178,10 @@ __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, uint64
         : "r"(bar), "r"(parity), "r"(1000000u)
         : "memory");
     const uint64_t el = global_ns() - t0;
-    if (el > report_ns) *late = 1;
+    if (el > report_ns) late = 1;
     if (__all_sync(kFull, done)) return true;
-    if (__any_sync(kFull, el > hard_ns || *abort)) {
-      *abort = 1;
+    if (__any_sync(kFull, el > hard_ns || abort)) {
+      abort = 1;
       return false;
     }
   }
@@ -328,7 +336,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
     if (__all_sync(kFull, bar_done(bar, parity))) return true;
     int late = 0;
-    const bool ok = bar_wait_slow(bar, parity, a.report_ns, a.hard_ns, &s_abort, &late);
+    const bool ok = bar_wait_slow(bar, parity, a.report_ns, a.hard_ns, s_abort, late);
     if (late) s_late = 1;
     return ok;
   };
@@ -337,7 +345,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     s_abort = 0;
     s_late = 0;
     constexpr int kSide = C::SIDE / 32;   // decoder warps that fill one side
-    bar_init(q_full, kSoftWarps);
+    bar_init(q_full, kSoftWarps + kDecWarps);
     bar_init(kfull, kSide);
     bar_init(kfree, 1);
 #pragma unroll
@@ -367,8 +375,81 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
   fence_after();
   const uint32_t tmem = tmem_base;
 
-  if (warp >= kSoftWarps + 2) {
+  // Q^ = H D q per K block, times softmax_scale * log2 e, by the softmax and
+  // decoder warps (w of 24): a warp takes two rows at a time, a lane the D/32
+  // consecutive values from E*lane on.  Loops are kept rolled: a CTA runs this
+  // once, and straight-line code would be fetched from a cold cache.
+  auto rotate_queries = [&](int w) {
+    constexpr int E = D / 32, QW = kSoftWarps + kDecWarps;
+    const float qn = PK.inv_sqrt_blk * a.qscale;
+    const uint32_t sb = PK.sign_bits[E * lane >> 5] >> (E * lane & 31);
+#pragma unroll 1
+    for (int r0 = 2 * w; r0 < NR; r0 += 2 * QW) {
+      uint32_t u[2][E / 2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int rr = row0 + r0 + x, b = rr >> a.lg, h = kvh * a.G + (rr & (a.G - 1));
+        const uint16_t* qr = a.q + ((int64_t)b * a.Hq + h) * D + E * lane;
+        const bool in = r0 + x < rows;
+        if constexpr (E == 8) {
+          const uint4 q = in ? *reinterpret_cast<const uint4*>(qr) : make_uint4(0u, 0u, 0u, 0u);
+          u[x][0] = q.x; u[x][1] = q.y; u[x][2] = q.z; u[x][3] = q.w;
+        } else if constexpr (E == 4) {
+          const uint2 q = in ? *reinterpret_cast<const uint2*>(qr) : make_uint2(0u, 0u);
+          u[x][0] = q.x; u[x][1] = q.y;
+        } else {
+          u[x][0] = in ? *reinterpret_cast<const uint32_t*>(qr) : 0u;
+        }
+      }
+#pragma unroll 1
+      for (int x = 0; x < 2; ++x) {
+        float v[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const uint32_t q = x ? u[1][e / 2] : u[0][e / 2];
+          v[e] = flip(h2f((uint16_t)(q >> (16 * (e & 1)))) * qn, (sb >> e) & 1u);
+        }
+#pragma unroll
+        for (int hs = 1; hs < E; hs <<= 1)
+          if (hs < PK.blk) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+              if ((e & hs) == 0) {
+                const float p = v[e], q = v[e + hs];
+                v[e] = p + q;
+                v[e + hs] = p - q;
+              }
+          }
+#pragma unroll 1
+        for (int hs = E; hs < PK.blk; hs <<= 1) {
+          const int lo = hs / E;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const float p = __shfl_xor_sync(kFull, v[e], lo);
+            v[e] = (lane & lo) ? (p - v[e]) : (v[e] + p);
+          }
+        }
+        const uint32_t dst = aQ + cm_off(r0 + x, E * lane, D);
+        uint32_t o[E / 2];
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) o[e] = pack2(v[2 * e], v[2 * e + 1]);
+        if constexpr (E == 8) {
+          sts16b(dst, o[0], o[1], o[2], o[3]);
+        } else if constexpr (E == 4) {
+          asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(dst), "r"(o[0]), "r"(o[1]) : "memory");
+        } else {
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(o[0]) : "memory");
+        }
+      }
+    }
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) arrive(q_full);
+  };
+
+  if (warp >= kDec0 / 32) {
     // ================= decoders
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
     const int dt = tid - kDec0;
     const int st = C::SPLIT ? dt % C::SIDE : dt;    // thread within its side
     const bool do_k = !C::SPLIT || dt < C::SIDE, do_v = !C::SPLIT || dt >= C::SIDE;
@@ -377,7 +458,9 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     // move on by a tile; paged: page and place in it of each.
     constexpr int kStep = C::SIDE / C::G8;
     static_assert(C::N == 1 || kStep % 8 == 0, "a thread's groups have one number");
-    const int tok0 = 8 * (st / (8 * C::G8)) + (st & 7), grp = (st >> 3) % C::G8;
+    // a group's number turns with its token, so that the eight lanes of one
+    // access hit different banks whatever the records' pitch
+    const int tok0 = 8 * (st / (8 * C::G8)) + (st & 7), grp = ((st >> 3) + (C::G8 == 8 ? st : st >> 1)) % C::G8;
     const uint32_t odd = grp & 1;
     const int kbits = PK.bits, vbits = PV.bits;
     const bool paged = src.pages.table != nullptr;
@@ -461,6 +544,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     if (do_k) load_k(0);
     if (do_v) load_v(0);
     pages_on();
+    if (n_tiles > 0) rotate_queries(warp - kDec0 / 32 + kSoftWarps);
     for (int t = 0; t < n_tiles; ++t) {
       const int vb = t % NV, at = t * kTile;
       pages_of(at + kTile);
@@ -494,6 +578,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     }
   } else if (warp == kSoftWarps) {
     // ================= S^T(t) = K^(t) Q^
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
     const uint32_t idesc = (1u << 4) | ((uint32_t)(NR >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
     const uint64_t dq = sdesc(aQ, 128, kKGroup), dk = sdesc(aK, 128, kKGroup);
     bool ok = n_tiles > 0 && wait(q_full, 0);
@@ -512,6 +597,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     commit_elect(drained);
   } else if (warp == kSoftWarps + 1) {
     // ================= O^T += V^(t)^T P(t)^T
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
     const uint32_t idesc = (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(NR >> 3) << 17) |
                            ((uint32_t)(128 >> 4) << 24);
     const uint32_t pg = (uint32_t)(NR >> 3) * 128;   // bytes of 8 tokens of P
@@ -535,83 +621,11 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     }
     __syncwarp();
     commit_elect(drained);
+  } else if (warp >= kSoftWarps) {   // fills its warpgroup
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
   } else {
-    // ================= queries: Q^ = H D q per K block, times softmax_scale *
-    // log2 e; a warp per row, a lane the D/32 consecutive values from E*lane
-    // on, four rows in flight
-    if (n_tiles > 0) {
-      constexpr int E = D / 32, RB = 4;
-      const float qn = PK.inv_sqrt_blk * a.qscale;
-      for (int r0 = warp * RB; r0 < NR; r0 += kSoftWarps * RB) {
-        uint32_t u[RB][E / 2];
-#pragma unroll
-        for (int x = 0; x < RB; ++x) {
-          const int r = r0 + x;
-#pragma unroll
-          for (int e = 0; e < E / 2; ++e) u[x][e] = 0u;
-          if (r >= rows) continue;
-          const int rr = row0 + r, b = rr >> a.lg, h = kvh * a.G + (rr & (a.G - 1));
-          const uint16_t* qr = a.q + ((int64_t)b * a.Hq + h) * D + E * lane;
-          if constexpr (E == 8) {
-            const uint4 w = *reinterpret_cast<const uint4*>(qr);
-            u[x][0] = w.x; u[x][1] = w.y; u[x][2] = w.z; u[x][3] = w.w;
-          } else if constexpr (E == 4) {
-            const uint2 w = *reinterpret_cast<const uint2*>(qr);
-            u[x][0] = w.x; u[x][1] = w.y;
-          } else {
-            u[x][0] = *reinterpret_cast<const uint32_t*>(qr);
-          }
-        }
-        float v[RB][E];
-#pragma unroll
-        for (int x = 0; x < RB; ++x)
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const int i = E * lane + e;
-            v[x][e] = flip(h2f((uint16_t)(u[x][e / 2] >> (16 * (e & 1)))), (PK.sign_bits[i >> 5] >> (i & 31)) & 1u);
-          }
-#pragma unroll
-        for (int hs = 1; hs < E; hs <<= 1) {
-          if (hs >= PK.blk) break;
-#pragma unroll
-          for (int x = 0; x < RB; ++x)
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-              if ((e & hs) == 0) {
-                const float p = v[x][e], q = v[x][e + hs];
-                v[x][e] = p + q;
-                v[x][e + hs] = p - q;
-              }
-        }
-        for (int hs = E; hs < PK.blk; hs <<= 1) {
-          const int lo = hs / E;
-#pragma unroll
-          for (int x = 0; x < RB; ++x)
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-              const float p = __shfl_xor_sync(kFull, v[x][e], lo);
-              v[x][e] = (lane & lo) ? (p - v[x][e]) : (v[x][e] + p);
-            }
-        }
-#pragma unroll
-        for (int x = 0; x < RB; ++x) {
-          const uint32_t dst = aQ + cm_off(r0 + x, E * lane, D);
-          uint32_t o[E / 2];
-#pragma unroll
-          for (int e = 0; e < E / 2; ++e) o[e] = pack2(v[x][2 * e] * qn, v[x][2 * e + 1] * qn);
-          if constexpr (E == 8) {
-            sts16b(dst, o[0], o[1], o[2], o[3]);
-          } else if constexpr (E == 4) {
-            asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(dst), "r"(o[0]), "r"(o[1]) : "memory");
-          } else {
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(o[0]) : "memory");
-          }
-        }
-      }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) arrive(q_full);
-    }
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs));
+    if (n_tiles > 0) rotate_queries(warp);
     // ================= softmax: thread = token (TMEM lane) x half of the rows
     const int quarter = warp & 3, half = warp >> 2, bid = 1 + half;
     const int nc = NR / 2, col0 = half * nc;
@@ -636,12 +650,15 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
       // largest s - m.  A token past the slice has p = 0.
       auto emit = [&]() {
         float mx = -INFINITY;
+        uint32_t vv[2][16];
+        TQ_LD16(sS, vv[0]);
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
           if (16 * i >= nc) break;
-          uint32_t v[16], o[8];
-          TQ_LD16(sS + 16 * i, v);
+          uint32_t o[8];
+          uint32_t* v = vv[i & 1];
           ld_wait();
+          if (16 * (i + 1) < nc) TQ_LD16(sS + 16 * (i + 1), vv[(i + 1) & 1]);   // in flight during this chunk
 #pragma unroll
           for (int j = 0; j < 16; j += 4) {
             const float4 m = *reinterpret_cast<const float4*>(&s_m[col0 + 16 * i + j]);
@@ -803,7 +820,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
       int late = 0;
       s_abort = 0;   // the others have left: wait for the products themselves
       __syncwarp();
-      if (!bar_wait_slow(drained, 0, a.report_ns, a.hard_ns, &s_abort, &late) || late) s_late = 1;
+      if (!bar_wait_slow(drained, 0, a.report_ns, a.hard_ns, s_abort, late) || late) s_late = 1;
     }
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(tcols) : "memory");
     if (lane == 0 && (s_abort || s_late)) atomicCAS(&g_shared_status, 0, (int)TQ_ERR_TIMEOUT);
@@ -818,16 +835,19 @@ size_t shared_smem(int NR) {
 
 template <int D>
 int launch_shared(const CodecParams& PK, const CodecParams& PV, const SharedArgs& a, unsigned grid, cudaStream_t st) {
-  auto kern = shared_prefix_kernel<D>;
   const size_t sm = shared_smem<D>(a.n_pre ? a.NR : 32);
-  static bool attr_set[64] = {};
+  auto kern = shared_prefix_kernel<D>;
+  // once per device; a build with fewer registers than the split shares out
+  // would wait for them without end, so it is refused
+  static std::atomic<bool> ready[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return TQ_ERR_CUDA;
-  if (!attr_set[dev]) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared_smem<D>(ShCfg<D>::MAXR)) !=
-        cudaSuccess)
+  if (!ready[dev].load(std::memory_order_acquire)) {
+    cudaFuncAttributes fa;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared_smem<D>(ShCfg<D>::MAXR)) ||
+        cudaFuncGetAttributes(&fa, kern) || fa.numRegs < kLaunchRegs)
       return TQ_ERR_CUDA;
-    attr_set[dev] = true;
+    ready[dev].store(true, std::memory_order_release);
   }
   kern<<<grid, kThreadsSh, sm, st>>>(PK, PV, a);
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
