@@ -63,11 +63,7 @@ constexpr int kDecWarps = 16;
 constexpr int kDecThreads = 32 * kDecWarps;
 constexpr int kDec0 = 32 * (kSoftWarps + 4);          // first decoder thread (whole warpgroups)
 constexpr int kThreadsSh = kDec0 + kDecThreads;       // 896
-// registers a thread: at launch, then the softmax warps' and the others'
-// (shares of the launch's: 256 * 104 + 640 * 56 <= 896 * 72)
-constexpr int kLaunchRegs = 72, kSoftRegs = 104, kOtherRegs = 56;
-static_assert(32 * kSoftWarps * kSoftRegs + (kThreadsSh - 32 * kSoftWarps) * kOtherRegs <= kThreadsSh * kLaunchRegs,
-              "the register split fits the launch's");
+constexpr int kLaunchRegs = 72;     // registers a thread at launch (896 threads of 65536)
 // log2 units a score may pass its row's reference by: p stays below 2^12, far
 // inside fp16, and sums of p * v inside fp32
 constexpr float kLazySh = 12.0f;
@@ -80,12 +76,17 @@ struct ShCfg {
   static constexpr int NV = D == 256 ? 1 : 2;          // buffers of V (one of K)
   static constexpr int DV = D < 128 ? 128 : D;         // V tile width: whole M tiles of 128
   static constexpr int OT = DV / 128;                  // M tiles of O^T
-  static constexpr int MAXR = D == 256 ? 96 : 128;     // rows of a CTA, by shared memory
+  static constexpr int MAXR = D == 256 ? 64 : 128;     // rows of a CTA, by shared memory and registers
   static constexpr uint32_t KB = kTile * D * 2, VB = kTile * DV * 2;
   static constexpr int G8 = D / 32;                    // 32-code groups per token
   static constexpr bool SPLIT = D == 64;               // K and V on half of the decoder warps each
   static constexpr int SIDE = SPLIT ? kDecThreads / 2 : kDecThreads;   // threads on one side
   static constexpr int N = kTile * G8 / SIDE;          // groups per thread and side
+  // registers of the softmax warps and of the others after the split: shares
+  // of the launch's (a decoder thread of two groups needs the more)
+  static constexpr int SOFT = N > 1 ? 88 : 104, OTHER = N > 1 ? 64 : 56;
+  static_assert(32 * kSoftWarps * SOFT + (kThreadsSh - 32 * kSoftWarps) * OTHER <= kThreadsSh * kLaunchRegs,
+                "the register split fits the launch's");
   static_assert(N * SIDE == kTile * G8, "every decoder thread has the same number of groups");
 };
 
@@ -208,28 +209,42 @@ struct Group {
   uint32_t sc;
 };
 
-__device__ __forceinline__ void load_group_g(int bits, const uint8_t* c, uint32_t odd, const uint8_t* s, Group& g) {
-  switch (bits) {
-    case 4:
+// The loads of a thread's N groups of one side: c[k], s[k] where in[k].  One
+// branch on the bit width around all of them, so that no load waits at a join
+// for an earlier one.  3 bits: 12 bytes, 8-byte aligned for even groups and 4
+// bytes past that for odd ones, so the 16 bytes around them (an even group is
+// never a row's last, so they are inside the row).
+template <int BITS, int N>
+__device__ __forceinline__ void load_groups_b(const bool* in, const uint8_t* const* c, uint32_t odd,
+                                              const uint8_t* const* s, Group* g) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    if (!in[k]) continue;
+    if (BITS == 4) {
       asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(g.w[0]), "=r"(g.w[1]), "=r"(g.w[2]), "=r"(g.w[3])
-                   : "l"(c));
-      break;
-    case 3: {
-      // 12 bytes, 8-byte aligned for even groups and 4 bytes past that for
-      // odd ones: the 16 bytes around them (an even group is never a row's
-      // last, so they are inside the row)
-      const uint8_t* c8 = c - (odd ? 4 : 0);
-      asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(g.w[0]), "=r"(g.w[1]) : "l"(c8));
-      asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(g.w[2]), "=r"(g.w[3]) : "l"(c8 + 8));
-      break;
+                   : "=r"(g[k].w[0]), "=r"(g[k].w[1]), "=r"(g[k].w[2]), "=r"(g[k].w[3])
+                   : "l"(c[k]));
+    } else if (BITS == 3) {
+      const uint8_t* c8 = c[k] - (odd ? 4 : 0);
+      asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(g[k].w[0]), "=r"(g[k].w[1]) : "l"(c8));
+      asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(g[k].w[2]), "=r"(g[k].w[3]) : "l"(c8 + 8));
+    } else if (BITS == 2) {
+      asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(g[k].w[0]), "=r"(g[k].w[1]) : "l"(c[k]));
+    } else {
+      asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(g[k].w[0]) : "l"(c[k]));
     }
-    case 2:
-      asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(g.w[0]), "=r"(g.w[1]) : "l"(c));
-      break;
-    default: asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(g.w[0]) : "l"(c)); break;
+    asm volatile("ld.global.nc.u16 %0, [%1];" : "=r"(g[k].sc) : "l"(s[k]));
   }
-  asm volatile("ld.global.nc.u16 %0, [%1];" : "=r"(g.sc) : "l"(s));
+}
+template <int N>
+__device__ __forceinline__ void load_groups(int bits, const bool* in, const uint8_t* const* c, uint32_t odd,
+                                            const uint8_t* const* s, Group* g) {
+  switch (bits) {
+    case 4: load_groups_b<4, N>(in, c, odd, s, g); break;
+    case 3: load_groups_b<3, N>(in, c, odd, s, g); break;
+    case 2: load_groups_b<2, N>(in, c, odd, s, g); break;
+    default: load_groups_b<1, N>(in, c, odd, s, g); break;
+  }
 }
 
 // Four fp16x2 registers of a nibble word of 4-bit codes.  The codebook is
@@ -449,7 +464,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
 
   if (warp >= kDec0 / 32) {
     // ================= decoders
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::OTHER));
     const int dt = tid - kDec0;
     const int st = C::SPLIT ? dt % C::SIDE : dt;    // thread within its side
     const bool do_k = !C::SPLIT || dt < C::SIDE, do_v = !C::SPLIT || dt >= C::SIDE;
@@ -487,36 +502,46 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
       kn += tok0 * knb;
       vn += tok0 * vnb;
     }
-    Group gk[C::N], gv[C::N];
-    int32_t pgk[C::N];   // page of the next tile's tokens (paged)
+    Group gk[C::N] = {}, gv[C::N] = {};
+    int32_t pgk[C::N] = {};   // page of the next tile's tokens (paged)
     // loads of one side of the tile whose tokens begin `at` tokens into the slice
     auto load_k = [&](int at) {
+      bool in[C::N];
+      const uint8_t *c[C::N], *n[C::N];
 #pragma unroll
       for (int k = 0; k < C::N; ++k) {
-        if (tok0 + k * kStep + at >= n_tok) continue;
+        in[k] = tok0 + k * kStep + at < n_tok;
         if (paged) {
           const int64_t r = ((int64_t)pgk[k] * a.Hkv + kvh) * psize + off[k];
-          load_group_g(kbits, kc + r * kwb + kw, odd, ks + r * knb + kn, gk[k]);
+          c[k] = kc + r * kwb + kw;
+          n[k] = ks + r * knb + kn;
         } else {
-          load_group_g(kbits, kc + (kw + k * kStep * kwb), odd, ks + (kn + k * kStep * knb), gk[k]);
+          c[k] = kc + (kw + k * kStep * kwb);
+          n[k] = ks + (kn + k * kStep * knb);
         }
       }
+      load_groups<C::N>(kbits, in, c, odd, n, gk);
       if (!paged) {
         kw += kTile * kwb;
         kn += kTile * knb;
       }
     };
     auto load_v = [&](int at) {
+      bool in[C::N];
+      const uint8_t *c[C::N], *n[C::N];
 #pragma unroll
       for (int k = 0; k < C::N; ++k) {
-        if (tok0 + k * kStep + at >= n_tok) continue;
+        in[k] = tok0 + k * kStep + at < n_tok;
         if (paged) {
           const int64_t r = ((int64_t)pgk[k] * a.Hkv + kvh) * psize + off[k];
-          load_group_g(vbits, vc + r * vwb + vw, odd, vs + r * vnb + vn, gv[k]);
+          c[k] = vc + r * vwb + vw;
+          n[k] = vs + r * vnb + vn;
         } else {
-          load_group_g(vbits, vc + (vw + k * kStep * vwb), odd, vs + (vn + k * kStep * vnb), gv[k]);
+          c[k] = vc + (vw + k * kStep * vwb);
+          n[k] = vs + (vn + k * kStep * vnb);
         }
       }
+      load_groups<C::N>(vbits, in, c, odd, n, gv);
       if (!paged) {
         vw += kTile * vwb;
         vn += kTile * vnb;
@@ -578,7 +603,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     }
   } else if (warp == kSoftWarps) {
     // ================= S^T(t) = K^(t) Q^
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::OTHER));
     const uint32_t idesc = (1u << 4) | ((uint32_t)(NR >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
     const uint64_t dq = sdesc(aQ, 128, kKGroup), dk = sdesc(aK, 128, kKGroup);
     bool ok = n_tiles > 0 && wait(q_full, 0);
@@ -597,7 +622,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     commit_elect(drained);
   } else if (warp == kSoftWarps + 1) {
     // ================= O^T += V^(t)^T P(t)^T
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::OTHER));
     const uint32_t idesc = (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(NR >> 3) << 17) |
                            ((uint32_t)(128 >> 4) << 24);
     const uint32_t pg = (uint32_t)(NR >> 3) * 128;   // bytes of 8 tokens of P
@@ -622,9 +647,9 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     __syncwarp();
     commit_elect(drained);
   } else if (warp >= kSoftWarps) {   // fills its warpgroup
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::OTHER));
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(C::SOFT));
     if (n_tiles > 0) rotate_queries(warp);
     // ================= softmax: thread = token (TMEM lane) x half of the rows
     const int quarter = warp & 3, half = warp >> 2, bid = 1 + half;
