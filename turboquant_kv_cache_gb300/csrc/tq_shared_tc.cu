@@ -209,42 +209,16 @@ struct Group {
   uint32_t sc;
 };
 
-// The loads of a thread's N groups of one side: c[k], s[k] where in[k].  One
-// branch on the bit width around all of them, so that no load waits at a join
-// for an earlier one.  3 bits: 12 bytes, 8-byte aligned for even groups and 4
-// bytes past that for odd ones, so the 16 bytes around them (an even group is
-// never a row's last, so they are inside the row).
-template <int BITS, int N>
-__device__ __forceinline__ void load_groups_b(const bool* in, const uint8_t* const* c, uint32_t odd,
-                                              const uint8_t* const* s, Group* g) {
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    if (!in[k]) continue;
-    if (BITS == 4) {
-      asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(g[k].w[0]), "=r"(g[k].w[1]), "=r"(g[k].w[2]), "=r"(g[k].w[3])
-                   : "l"(c[k]));
-    } else if (BITS == 3) {
-      const uint8_t* c8 = c[k] - (odd ? 4 : 0);
-      asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(g[k].w[0]), "=r"(g[k].w[1]) : "l"(c8));
-      asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(g[k].w[2]), "=r"(g[k].w[3]) : "l"(c8 + 8));
-    } else if (BITS == 2) {
-      asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(g[k].w[0]), "=r"(g[k].w[1]) : "l"(c[k]));
-    } else {
-      asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(g[k].w[0]) : "l"(c[k]));
-    }
-    asm volatile("ld.global.nc.u16 %0, [%1];" : "=r"(g[k].sc) : "l"(s[k]));
-  }
-}
-template <int N>
-__device__ __forceinline__ void load_groups(int bits, const bool* in, const uint8_t* const* c, uint32_t odd,
-                                            const uint8_t* const* s, Group* g) {
-  switch (bits) {
-    case 4: load_groups_b<4, N>(in, c, odd, s, g); break;
-    case 3: load_groups_b<3, N>(in, c, odd, s, g); break;
-    case 2: load_groups_b<2, N>(in, c, odd, s, g); break;
-    default: load_groups_b<1, N>(in, c, odd, s, g); break;
-  }
+// A group's packed words as the 8-byte word at or 4 bytes before it and, past
+// two bits, the next one: the same two loads whatever the bit width, with no
+// branch or predicate, so that no load is waited for at a join.  Groups of
+// 4 * bits bytes come in pairs that start on 8 bytes (d / 32 is even), so both
+// words lie in the record.  1 and 3 bits: an odd group starts with the second
+// 4-byte word (`shifted`).
+__device__ __forceinline__ void load_group_g(const uint8_t* c8, int next, const uint8_t* s, Group& g) {
+  asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(g.w[0]), "=r"(g.w[1]) : "l"(c8));
+  asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(g.w[2]), "=r"(g.w[3]) : "l"(c8 + next));
+  asm volatile("ld.global.nc.u16 %0, [%1];" : "=r"(g.sc) : "l"(s));
 }
 
 // Four fp16x2 registers of a nibble word of 4-bit codes.  The codebook is
@@ -269,11 +243,11 @@ __device__ __forceinline__ void lut8_sym(uint32_t n, const Tab& T, uint32_t* o) 
 // 16-byte chunks, one per core matrix.  Each (token, block) table holds the
 // fp32 products of centroids and norm, rounded once to fp16.
 template <int BITS>
-__device__ __forceinline__ void decode_group_b(const Group& g, uint32_t odd, const float* cent, uint32_t dst) {
+__device__ __forceinline__ void decode_group_b(const Group& g, bool shifted, const float* cent, uint32_t dst) {
   uint32_t n[4];
-  if (BITS == 3) {
-    const uint32_t w3[3] = {odd ? g.w[1] : g.w[0], odd ? g.w[2] : g.w[1], odd ? g.w[3] : g.w[2]};
-    chunk_words<3>(w3, n);
+  if (BITS & 1) {
+    const uint32_t w3[3] = {shifted ? g.w[1] : g.w[0], shifted ? g.w[2] : g.w[1], shifted ? g.w[3] : g.w[2]};
+    chunk_words<BITS>(w3, n);
   } else {
     chunk_words<BITS>(g.w, n);
   }
@@ -287,7 +261,7 @@ __device__ __forceinline__ void decode_group_b(const Group& g, uint32_t odd, con
   }
 }
 
-__device__ __forceinline__ void decode_group(int bits, const Group& g, uint32_t odd, const float* cent, bool live,
+__device__ __forceinline__ void decode_group(int bits, const Group& g, bool odd, const float* cent, bool live,
                                              uint32_t dst) {
   if (!live) {   // past the slice: zero rows (their p is zero too, but 0 * NaN is not)
 #pragma unroll
@@ -465,141 +439,99 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
   if (warp >= kDec0 / 32) {
     // ================= decoders
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::OTHER));
-    const int dt = tid - kDec0;
-    const int st = C::SPLIT ? dt % C::SIDE : dt;    // thread within its side
-    const bool do_k = !C::SPLIT || dt < C::SIDE, do_v = !C::SPLIT || dt >= C::SIDE;
-    // the thread's groups: number grp of the tokens tok0 and, at head_dim 256,
-    // kStep tokens on.  Contiguous: byte offsets into the CTA's slice that
-    // move on by a tile; paged: page and place in it of each.
-    constexpr int kStep = C::SIDE / C::G8;
-    static_assert(C::N == 1 || kStep % 8 == 0, "a thread's groups have one number");
-    // a group's number turns with its token, so that the eight lanes of one
-    // access hit different banks whatever the records' pitch
-    const int tok0 = 8 * (st / (8 * C::G8)) + (st & 7), grp = ((st >> 3) + (C::G8 == 8 ? st : st >> 1)) % C::G8;
-    const uint32_t odd = grp & 1;
-    const int kbits = PK.bits, vbits = PV.bits;
-    const bool paged = src.pages.table != nullptr;
-    const uint32_t kwb = PK.code_bytes, vwb = PV.code_bytes, knb = 2 * PK.nb, vnb = 2 * PV.nb;
-    uint32_t kw = grp * 4 * kbits, kn = 32 * grp / PK.blk * 2, vw = grp * 4 * vbits, vn = 32 * grp / PV.blk * 2;
-    const int64_t rec0 = paged ? 0 : ((int64_t)seq * a.Hkv + kvh) * src.S_cap + t_lo;
-    const uint8_t *kc = src.kc + rec0 * kwb, *ks = src.ks + rec0 * knb, *vc = src.vc + rec0 * vwb,
-                  *vs = src.vs + rec0 * vnb;
-    const int32_t* table = paged ? src.pages.table + (int64_t)seq * src.pages.pages_per_seq : nullptr;
-    const int psize = src.pages.page_size;
-    int32_t page[C::N], off[C::N];
+    if (n_tiles > 0) {
+      const int dt = tid - kDec0;
+      const int st = C::SPLIT ? dt % C::SIDE : dt;    // thread within its side
+      const bool do_k = !C::SPLIT || dt < C::SIDE, do_v = !C::SPLIT || dt >= C::SIDE;
+      // the thread's groups: number grp of the tokens tok0 and, at head_dim
+      // 256, kStep tokens on.  A group's number turns with its token, so that
+      // the eight lanes of one access hit different banks whatever the
+      // records' pitch.
+      constexpr int kStep = C::SIDE / C::G8;
+      static_assert(C::N == 1 || kStep % 8 == 0, "a thread's groups have one number");
+      const int tok0 = 8 * (st / (8 * C::G8)) + (st & 7), grp = ((st >> 3) + (C::G8 == 8 ? st : st >> 1)) % C::G8;
+      const bool odd = grp & 1;
+      const int kbits = PK.bits, vbits = PV.bits;
+      const bool paged = src.pages.table != nullptr;
+      const uint32_t kwb = PK.code_bytes, vwb = PV.code_bytes, knb = 2 * PK.nb, vnb = 2 * PV.nb;
+      const uint32_t kw0 = grp * 4 * kbits - ((kbits & 1) && odd ? 4 : 0), kn0 = 32 * grp / PK.blk * 2;
+      const uint32_t vw0 = grp * 4 * vbits - ((vbits & 1) && odd ? 4 : 0), vn0 = 32 * grp / PV.blk * 2;
+      const int knext = kbits > 2 ? 8 : 0, vnext = vbits > 2 ? 8 : 0;
+      const int64_t rec0 = paged ? 0 : ((int64_t)seq * a.Hkv + kvh) * src.S_cap + t_lo;
+      const uint8_t *kc = src.kc + rec0 * kwb + kw0, *ks = src.ks + rec0 * knb + kn0;
+      const uint8_t *vc = src.vc + rec0 * vwb + vw0, *vs = src.vs + rec0 * vnb + vn0;
+      const int32_t* table = paged ? src.pages.table + (int64_t)seq * src.pages.pages_per_seq : nullptr;
+      const int psize = src.pages.page_size;
+      const int last_page = paged ? (int)((t_lo + n_tok - 1) / psize) : 0;
+      // record (contiguous: token) of each group in the tile to be loaded; a
+      // token past the slice takes the last one's place (paged: some record
+      // of the last page), and its values are not used
+      int32_t page[C::N], off[C::N];
+      int64_t rec[C::N];
 #pragma unroll
-    for (int k = 0; k < C::N; ++k) {
-      page[k] = off[k] = 0;
-      if (paged) {
+      for (int k = 0; k < C::N; ++k) {
         const int64_t t = t_lo + tok0 + k * kStep;
-        page[k] = (int32_t)(t / psize);
-        off[k] = (int32_t)(t - (int64_t)page[k] * psize);
+        page[k] = paged ? (int)(t / psize) : 0;
+        off[k] = paged ? (int)(t - (int64_t)page[k] * psize) : 0;
       }
-    }
-    if (!paged) {
-      kw += tok0 * kwb;
-      vw += tok0 * vwb;
-      kn += tok0 * knb;
-      vn += tok0 * vnb;
-    }
-    Group gk[C::N] = {}, gv[C::N] = {};
-    int32_t pgk[C::N] = {};   // page of the next tile's tokens (paged)
-    // loads of one side of the tile whose tokens begin `at` tokens into the slice
-    auto load_k = [&](int at) {
-      bool in[C::N];
-      const uint8_t *c[C::N], *n[C::N];
+      auto place = [&](int at) {   // the records of the tile `at` tokens into the slice
 #pragma unroll
-      for (int k = 0; k < C::N; ++k) {
-        in[k] = tok0 + k * kStep + at < n_tok;
-        if (paged) {
-          const int64_t r = ((int64_t)pgk[k] * a.Hkv + kvh) * psize + off[k];
-          c[k] = kc + r * kwb + kw;
-          n[k] = ks + r * knb + kn;
-        } else {
-          c[k] = kc + (kw + k * kStep * kwb);
-          n[k] = ks + (kn + k * kStep * knb);
+        for (int k = 0; k < C::N; ++k) {
+          if (paged) {
+            rec[k] = ((int64_t)table[min(page[k], last_page)] * a.Hkv + kvh) * psize + off[k];
+            off[k] += kTile;
+            while (off[k] >= psize) {
+              off[k] -= psize;
+              ++page[k];
+            }
+          } else {
+            rec[k] = min(at + tok0 + k * kStep, n_tok - 1);
+          }
+        }
+      };
+      Group gk[C::N], gv[C::N];
+      auto load_k = [&]() {
+#pragma unroll
+        for (int k = 0; k < C::N; ++k) load_group_g(kc + rec[k] * kwb, knext, ks + rec[k] * knb, gk[k]);
+      };
+      auto load_v = [&]() {
+#pragma unroll
+        for (int k = 0; k < C::N; ++k) load_group_g(vc + rec[k] * vwb, vnext, vs + rec[k] * vnb, gv[k]);
+      };
+      place(0);
+      load_k();
+      load_v();
+      rotate_queries(warp - kDec0 / 32 + kSoftWarps);
+      for (int t = 0; t < n_tiles; ++t) {
+        const int vb = t % NV, at = t * kTile;
+        place(at + kTile);
+        if (do_k) {
+          if (t >= 1) wait(kfree, (uint32_t)(t - 1) & 1);
+          if (!s_abort) {
+#pragma unroll
+            for (int k = 0; k < C::N; ++k)
+              decode_group(kbits, gk[k], odd, PK.centroids, at + tok0 + k * kStep < n_tok,
+                           aK + cm_off(tok0 + k * kStep, 32 * grp, D));
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) arrive(kfull);
+          load_k();
+        }
+        if (do_v) {
+          if (t >= NV) wait(vfree + 8 * vb, (uint32_t)(t / NV - 1) & 1);
+          if (!s_abort) {
+#pragma unroll
+            for (int k = 0; k < C::N; ++k)
+              decode_group(vbits, gv[k], odd, PV.centroids, at + tok0 + k * kStep < n_tok,
+                           aV + vb * C::VB + cm_off(tok0 + k * kStep, 32 * grp, C::DV));
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) arrive(vfull + 8 * vb);
+          load_v();
         }
       }
-      load_groups<C::N>(kbits, in, c, odd, n, gk);
-      if (!paged) {
-        kw += kTile * kwb;
-        kn += kTile * knb;
-      }
-    };
-    auto load_v = [&](int at) {
-      bool in[C::N];
-      const uint8_t *c[C::N], *n[C::N];
-#pragma unroll
-      for (int k = 0; k < C::N; ++k) {
-        in[k] = tok0 + k * kStep + at < n_tok;
-        if (paged) {
-          const int64_t r = ((int64_t)pgk[k] * a.Hkv + kvh) * psize + off[k];
-          c[k] = vc + r * vwb + vw;
-          n[k] = vs + r * vnb + vn;
-        } else {
-          c[k] = vc + (vw + k * kStep * vwb);
-          n[k] = vs + (vn + k * kStep * vnb);
-        }
-      }
-      load_groups<C::N>(vbits, in, c, odd, n, gv);
-      if (!paged) {
-        vw += kTile * vwb;
-        vn += kTile * vnb;
-      }
-    };
-    // the pages of a tile's tokens: read before its loads, moved on after them
-    auto pages_of = [&](int at) {
-      if (!paged) return;
-#pragma unroll
-      for (int k = 0; k < C::N; ++k)
-        if (tok0 + k * kStep + at < n_tok) pgk[k] = table[page[k]];
-    };
-    auto pages_on = [&]() {
-      if (!paged) return;
-#pragma unroll
-      for (int k = 0; k < C::N; ++k) {
-        off[k] += kTile;
-        while (off[k] >= psize) {
-          off[k] -= psize;
-          ++page[k];
-        }
-      }
-    };
-    pages_of(0);
-    if (do_k) load_k(0);
-    if (do_v) load_v(0);
-    pages_on();
-    if (n_tiles > 0) rotate_queries(warp - kDec0 / 32 + kSoftWarps);
-    for (int t = 0; t < n_tiles; ++t) {
-      const int vb = t % NV, at = t * kTile;
-      pages_of(at + kTile);
-      if (do_k) {
-        if (t >= 1) wait(kfree, (uint32_t)(t - 1) & 1);
-        if (!s_abort) {
-#pragma unroll
-          for (int k = 0; k < C::N; ++k)
-            decode_group(kbits, gk[k], odd, PK.centroids, at + tok0 + k * kStep < n_tok,
-                         aK + cm_off(tok0 + k * kStep, 32 * grp, D));
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) arrive(kfull);
-        if (t + 1 < n_tiles) load_k(at + kTile);
-      }
-      if (do_v) {
-        if (t >= NV) wait(vfree + 8 * vb, (uint32_t)(t / NV - 1) & 1);
-        if (!s_abort) {
-#pragma unroll
-          for (int k = 0; k < C::N; ++k)
-            decode_group(vbits, gv[k], odd, PV.centroids, at + tok0 + k * kStep < n_tok,
-                         aV + vb * C::VB + cm_off(tok0 + k * kStep, 32 * grp, C::DV));
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) arrive(vfull + 8 * vb);
-        if (t + 1 < n_tiles) load_v(at + kTile);
-      }
-      pages_on();
     }
   } else if (warp == kSoftWarps) {
     // ================= S^T(t) = K^(t) Q^
