@@ -14,9 +14,8 @@
 // work and the softmax cost what the rows there are cost (a multiple of 32),
 // not the 128 of a row-per-lane tile.  A softmax thread has one token's p for
 // half of the rows; the sums l over tokens come from the same rounded p that
-// multiplies V, by mma.sync: with a packed register of two rows as its B
-// operand (every lane another token) and a 0/1 matrix A that sends the
-// register's halves to their rows, four products sum 16 rows over a warp.
+// multiplies V: two warps read P back as mma.sync operands and multiply it by
+// a matrix of ones, in fp32.
 // The reference m of a row only moves when a score passes it by more than
 // 2^12 (the first tile always does): the common step needs no maximum over
 // tokens, only one barrier vote; the rare one takes the maxima and scales O
@@ -27,7 +26,7 @@
 // are one launch.
 //
 // Warps: 0-7 softmax (warps 0-3 rows [0, NR/2), 4-7 the rest), 8 issues S, 9
-// issues O, 12-27 decode; softmax and decoder warps rotate the queries while
+// issues O, 10 and 11 sum half of the rows each, 12-27 decode; softmax and decoder warps rotate the queries while
 // the first loads are in flight.  A decoder thread
 // takes one 32-code group (two at head_dim 256) of the K tile and of the V
 // tile, its packed words loaded a tile ahead; at head_dim 64 half of the
@@ -36,7 +35,7 @@
 //   kfull/kfree   K^(t) is decoded / S(t) is done with it (one buffer)
 //   vfull/vfree[b] the same for V and O (two buffers; one at head_dim 256)
 //   s_full[i]     S(t), t & 1 = i, is in TMEM    s_free[i] it has been read
-//   p_full[i]     P(t) is written                o_done[i] O += V(t) P(t) is done
+//   p_full[i]     P(t) is written                o_done[i] O += V(t) P(t) and l are done
 // Every wait is bounded at two levels, as in tq_tc.cuh; a CTA that gives up
 // stops decoding and issuing, waits for the products in flight and frees its
 // TMEM.
@@ -194,13 +193,24 @@ __device__ __forceinline__ float warp_max_f(float x) {
   return y;
 }
 
-// D += A B, one row of ones and zeros of A per row of D (see the sums l)
-__device__ __forceinline__ void hmma_sum(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
+// D += ones B for a 16 x 8 block of B (every row of D: the sums of its columns)
+__device__ __forceinline__ void hmma_sum(float* d, uint32_t b0, uint32_t b1) {
+  const uint32_t one = 0x3C003C00u;
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%4,%4,%4}, {%5,%6}, {%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      : "r"(one), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t* v, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 
 // The packed words and norm of one 32-code group, loaded a tile ahead.
@@ -290,7 +300,8 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
   __shared__ int s_late;
   __shared__ __align__(16) float s_m[C::MAXR];      // the rows' softmax references
   __shared__ float s_al[C::MAXR];
-  __shared__ float s_wm[4][C::MAXR];                // maxima, at the end sums, by TMEM lane quarter
+  __shared__ float s_wm[4][C::MAXR];                // maxima by TMEM lane quarter (rare path)
+  __shared__ __align__(8) float s_l[C::MAXR];                    // the rows' sums of p
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // a prefix CTA: split fastest, then KV head, then row tile; behind them a
@@ -342,7 +353,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
       bar_init(s_full + 8 * i, 1);
       bar_init(s_free + 8 * i, kSoftWarps);
       bar_init(p_full + 8 * i, kSoftWarps);
-      bar_init(o_done + 8 * i, 1);
+      bar_init(o_done + 8 * i, 3);   // the product's commit and the two summing warps
     }
     bar_init(drained, 2);
 #pragma unroll
@@ -358,77 +369,81 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
   }
-  if (tid < NR) s_m[tid] = -INFINITY;
+  if (tid < NR) {
+    s_m[tid] = -INFINITY;
+    s_l[tid] = 0.f;
+  }
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = tmem_base;
 
   // Q^ = H D q per K block, times softmax_scale * log2 e, by the softmax and
-  // decoder warps (w of 24): a warp takes two rows at a time, a lane the D/32
-  // consecutive values from E*lane on.  Loops are kept rolled: a CTA runs this
-  // once, and straight-line code would be fetched from a cold cache.
+  // decoder warps (w of 24): a warp per row, a lane the D/32 consecutive
+  // values from E*lane on, the next row's load in flight.  Loops are kept
+  // rolled: a CTA runs this once, and straight-line code would be fetched
+  // from a cold cache.
   auto rotate_queries = [&](int w) {
     constexpr int E = D / 32, QW = kSoftWarps + kDecWarps;
     const float qn = PK.inv_sqrt_blk * a.qscale;
     const uint32_t sb = PK.sign_bits[E * lane >> 5] >> (E * lane & 31);
-#pragma unroll 1
-    for (int r0 = 2 * w; r0 < NR; r0 += 2 * QW) {
-      uint32_t u[2][E / 2];
+    uint32_t next[E / 2];
+    auto fetch = [&](int r) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int rr = row0 + r0 + x, b = rr >> a.lg, h = kvh * a.G + (rr & (a.G - 1));
+      for (int e = 0; e < E / 2; ++e) next[e] = 0u;
+      if (r < rows) {
+        const int rr = row0 + r, b = rr >> a.lg, h = kvh * a.G + (rr & (a.G - 1));
         const uint16_t* qr = a.q + ((int64_t)b * a.Hq + h) * D + E * lane;
-        const bool in = r0 + x < rows;
         if constexpr (E == 8) {
-          const uint4 q = in ? *reinterpret_cast<const uint4*>(qr) : make_uint4(0u, 0u, 0u, 0u);
-          u[x][0] = q.x; u[x][1] = q.y; u[x][2] = q.z; u[x][3] = q.w;
+          const uint4 q = *reinterpret_cast<const uint4*>(qr);
+          next[0] = q.x; next[1] = q.y; next[2] = q.z; next[3] = q.w;
         } else if constexpr (E == 4) {
-          const uint2 q = in ? *reinterpret_cast<const uint2*>(qr) : make_uint2(0u, 0u);
-          u[x][0] = q.x; u[x][1] = q.y;
+          const uint2 q = *reinterpret_cast<const uint2*>(qr);
+          next[0] = q.x; next[1] = q.y;
         } else {
-          u[x][0] = in ? *reinterpret_cast<const uint32_t*>(qr) : 0u;
+          next[0] = *reinterpret_cast<const uint32_t*>(qr);
         }
       }
+    };
+    fetch(w);
 #pragma unroll 1
-      for (int x = 0; x < 2; ++x) {
-        float v[E];
+    for (int r = w; r < NR; r += QW) {
+      float v[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&next[e / 2]));
+        v[e] = flip((e & 1 ? f.y : f.x) * qn, (sb >> e) & 1u);
+      }
+      fetch(r + QW);
+#pragma unroll
+      for (int hs = 1; hs < E; hs <<= 1) {   // blocks are 32 values at least
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if ((e & hs) == 0) {
+            const float p = v[e], q = v[e + hs];
+            v[e] = p + q;
+            v[e + hs] = p - q;
+          }
+      }
+#pragma unroll 1
+      for (int hs = E; hs < PK.blk; hs <<= 1) {
+        const int lo = hs / E;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          const uint32_t q = x ? u[1][e / 2] : u[0][e / 2];
-          v[e] = flip(h2f((uint16_t)(q >> (16 * (e & 1)))) * qn, (sb >> e) & 1u);
+          const float p = __shfl_xor_sync(kFull, v[e], lo);
+          v[e] = (lane & lo) ? (p - v[e]) : (v[e] + p);
         }
+      }
+      const uint32_t dst = aQ + cm_off(r, E * lane, D);
+      uint32_t o[E / 2];
 #pragma unroll
-        for (int hs = 1; hs < E; hs <<= 1)
-          if (hs < PK.blk) {
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-              if ((e & hs) == 0) {
-                const float p = v[e], q = v[e + hs];
-                v[e] = p + q;
-                v[e + hs] = p - q;
-              }
-          }
-#pragma unroll 1
-        for (int hs = E; hs < PK.blk; hs <<= 1) {
-          const int lo = hs / E;
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const float p = __shfl_xor_sync(kFull, v[e], lo);
-            v[e] = (lane & lo) ? (p - v[e]) : (v[e] + p);
-          }
-        }
-        const uint32_t dst = aQ + cm_off(r0 + x, E * lane, D);
-        uint32_t o[E / 2];
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) o[e] = pack2(v[2 * e], v[2 * e + 1]);
-        if constexpr (E == 8) {
-          sts16b(dst, o[0], o[1], o[2], o[3]);
-        } else if constexpr (E == 4) {
-          asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(dst), "r"(o[0]), "r"(o[1]) : "memory");
-        } else {
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(o[0]) : "memory");
-        }
+      for (int e = 0; e < E / 2; ++e) o[e] = pack2(v[2 * e], v[2 * e + 1]);
+      if constexpr (E == 8) {
+        sts16b(dst, o[0], o[1], o[2], o[3]);
+      } else if constexpr (E == 4) {
+        asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(dst), "r"(o[0]), "r"(o[1]) : "memory");
+      } else {
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(o[0]) : "memory");
       }
     }
     fence_async_smem();
@@ -578,36 +593,61 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     }
     __syncwarp();
     commit_elect(drained);
-  } else if (warp >= kSoftWarps) {   // fills its warpgroup
+  } else if (warp >= kSoftWarps) {
+    // ================= l += ones P(t)^T: rows [0, NR/2) or the rest, 8 at a time
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::OTHER));
+    const int nc = NR / 2, col0 = (warp - kSoftWarps - 2) * nc;
+    // lane i's row of the four 8 x 8 matrices of 32 tokens: token i, 8 rows
+    const uint32_t row = cm_off(lane, col0, NR);
+    const uint32_t step = (uint32_t)(NR >> 3) * 512;   // 32 tokens on
+    for (int t = 0; t < n_tiles; ++t) {
+      const int pb = t & 1;
+      if (!wait(p_full + 8 * pb, (uint32_t)(t >> 1) & 1)) break;
+      __syncwarp();
+      for (int c = 0; c < nc; c += 16) {   // two blocks of 8 rows, four chains of products
+        float d[2][2][4] = {};
+        const uint32_t at = aP + pb * pbytes + row + (uint32_t)(c >> 3) * 128;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            uint32_t b[4];
+            ldsm4_trans(b, at + k * step + x * 128);
+            hmma_sum(d[x][0], b[0], b[1]);
+            hmma_sum(d[x][1], b[2], b[3]);
+          }
+        if (lane < 4) {   // columns 2 lane, 2 lane + 1 of each block
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float2* l = reinterpret_cast<float2*>(&s_l[col0 + c + 8 * x + 2 * lane]);
+            const float2 o = *l;
+            *l = make_float2(o.x + (d[x][0][0] + d[x][1][0]), o.y + (d[x][0][1] + d[x][1][1]));
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) arrive(o_done + 8 * pb);
+    }
   } else {
+    // ================= softmax: thread = token (TMEM lane) x half of the rows
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(C::SOFT));
     if (n_tiles > 0) rotate_queries(warp);
-    // ================= softmax: thread = token (TMEM lane) x half of the rows
     const int quarter = warp & 3, half = warp >> 2, bid = 1 + half;
     const int nc = NR / 2, col0 = half * nc;
     const int tk = 32 * quarter + lane;
     const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
     const uint32_t pdst0 = aP + cm_off(tk, col0, NR);
-    // the sums' A operand: row g of ones at even (odd) k of the first or
-    // second register, for the columns 4i + 0 .. 3 of product i
-    const int g = lane >> 2;
-    const uint32_t ev = (g & 1) ? 0x3C000000u : 0x00003C00u;
-    const uint32_t x0 = (g >> 1) == 0 ? ev : 0u, y0 = (g >> 1) == 1 ? ev : 0u;
-    const uint32_t x1 = (g >> 1) == 2 ? ev : 0u, y1 = (g >> 1) == 3 ? ev : 0u;
     constexpr int NCH = C::MAXR / 32;       // column chunks of 16
-    float lsum[NCH][4], lnew[NCH][4];
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) lsum[i][0] = lsum[i][1] = lsum[i][2] = lsum[i][3] = 0.f;
+    const uint32_t kOver = 0x6C006C00u;     // 2^12 twice in fp16
+    static_assert(kLazySh == 12.0f, "kOver is 2^kLazySh");
     for (int t = 0; t < n_tiles; ++t) {
-      const bool live = t * kTile + tk < n_tok;
       const uint32_t sS = lanes + (t & 1) * NR + col0;
       const uint32_t pdst = pdst0 + (t & 1) * pbytes;
-      // p of every column from its score, to P and the sums; returns the
-      // largest s - m.  A token past the slice has p = 0.
+      const bool whole = (t + 1) * kTile <= n_tok, live = t * kTile + tk < n_tok;
+      // p of every column from its score, to P; returns whether one passes
+      // 2^kLazySh.  A token past the slice has p = 0.
       auto emit = [&]() {
-        float mx = -INFINITY;
-        uint32_t vv[2][16];
+        uint32_t vv[2][16], mx = 0u;
         TQ_LD16(sS, vv[0]);
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
@@ -619,41 +659,33 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
 #pragma unroll
           for (int j = 0; j < 16; j += 4) {
             const float4 m = *reinterpret_cast<const float4*>(&s_m[col0 + 16 * i + j]);
-            const float e0 = __uint_as_float(v[j]) - m.x, e1 = __uint_as_float(v[j + 1]) - m.y;
-            const float e2 = __uint_as_float(v[j + 2]) - m.z, e3 = __uint_as_float(v[j + 3]) - m.w;
-            mx = fmaxf(mx, fmaxf(fmaxf(e0, e1), fmaxf(e2, e3)));
-            o[j / 2] = pack2(ex2s(e0), ex2s(e1));
-            o[j / 2 + 1] = pack2(ex2s(e2), ex2s(e3));
+            o[j / 2] = pack2(ex2s(__uint_as_float(v[j]) - m.x), ex2s(__uint_as_float(v[j + 1]) - m.y));
+            o[j / 2 + 1] = pack2(ex2s(__uint_as_float(v[j + 2]) - m.z), ex2s(__uint_as_float(v[j + 3]) - m.w));
           }
-          if (!live) {
-            mx = -INFINITY;
+          if (!whole) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = 0u;
+            for (int j = 0; j < 8; ++j) o[j] = live ? o[j] : 0u;
           }
-          __syncwarp();
+          mx = hmax2(mx, hmax2(hmax2(hmax2(o[0], o[1]), hmax2(o[2], o[3])), hmax2(hmax2(o[4], o[5]), hmax2(o[6], o[7]))));
           sts16b(pdst + 256 * i, o[0], o[1], o[2], o[3]);
           sts16b(pdst + 256 * i + 128, o[4], o[5], o[6], o[7]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) lnew[i][j] = lsum[i][j];
-          hmma_sum(lnew[i], x0, 0u, y0, 0u, o[0], o[1]);
-          hmma_sum(lnew[i], x1, 0u, y1, 0u, o[2], o[3]);
-          hmma_sum(lnew[i], 0u, x0, 0u, y0, o[4], o[5]);
-          hmma_sum(lnew[i], 0u, x1, 0u, y1, o[6], o[7]);
         }
-        return mx;
+        return hmax2(mx, kOver) != kOver;
       };
       wait(s_full + 8 * (t & 1), (uint32_t)(t >> 1) & 1);
       if (t >= 2) wait(o_done + 8 * (t & 1), (uint32_t)((t >> 1) - 1) & 1);   // P(t - 2) has been read
       fence_after();
+      __syncwarp();
       bool moved = t == 0;
-      if (!moved) moved = half_any(bid, emit() > kLazySh);
+      if (!moved) moved = half_any(bid, emit());
       if (moved) {
         // some row's reference moves (the first tile sets them): its maximum
         // over the tile, O and l scaled, P written again
         if (t >= 1) {
-          wait(o_done + 8 * ((t - 1) & 1), (uint32_t)((t - 1) >> 1) & 1);   // O stands still
+          wait(o_done + 8 * ((t - 1) & 1), (uint32_t)((t - 1) >> 1) & 1);   // O and l stand still
           fence_after();
         }
+        __syncwarp();
         for (int c = 0; c < nc; c += 16) {
           uint32_t v[16];
           TQ_LD16(sS + c, v);
@@ -671,20 +703,13 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
           const int r = col0 + (tid & 127);
           const float x = fmaxf(fmaxf(s_wm[0][r], s_wm[1][r]), fmaxf(s_wm[2][r], s_wm[3][r]));
           const float mo = s_m[r], mn = x > mo + kLazySh || mo == -INFINITY ? x : mo;
+          const float al = mo == -INFINITY ? 0.f : ex2s(mo - mn);
           s_m[r] = mn;
-          s_al[r] = mo == -INFINITY ? 0.f : ex2s(mo - mn);
+          s_al[r] = al;
+          s_l[r] *= al;
         }
         half_sync(bid);
         if (t >= 1) {
-#pragma unroll
-          for (int i = 0; i < NCH; ++i) {
-            if (16 * i >= nc) break;
-            const float a0 = s_al[col0 + 16 * i + g], a1 = s_al[col0 + 16 * i + 8 + g];
-            lsum[i][0] *= a0;
-            lsum[i][1] *= a0;
-            lsum[i][2] *= a1;
-            lsum[i][3] *= a1;
-          }
 #pragma unroll 1
           for (int m = 0; m < OT; ++m) {
 #pragma unroll 1
@@ -702,28 +727,12 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
         }
         emit();
       }
-#pragma unroll
-      for (int i = 0; i < NCH; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) lsum[i][j] = lnew[i][j];
       fence_async_smem();
       fence_before();
       __syncwarp();
       if (lane == 0) {
         arrive(p_full + 8 * (t & 1));
         arrive(s_free + 8 * (t & 1));
-      }
-    }
-    // the rows' sums over this warp's tokens
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      if (16 * i >= nc) break;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float x = lsum[i][2 * e] + lsum[i][2 * e + 1];
-        x += __shfl_xor_sync(kFull, x, 1);
-        x += __shfl_xor_sync(kFull, x, 2);
-        if ((lane & 3) == 0) s_wm[quarter][col0 + 16 * i + 8 * e + g] = x;
       }
     }
   }
@@ -756,7 +765,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
           if (m == 0 && quarter == 0 && lane == j) {
             const int r = c + j;
             dst[0] = ok ? s_m[r] : -INFINITY;
-            dst[1] = ok ? (s_wm[0][r] + s_wm[1][r]) + (s_wm[2][r] + s_wm[3][r]) : 0.f;
+            dst[1] = ok ? s_l[r] : 0.f;
           }
         }
         ++hh;
