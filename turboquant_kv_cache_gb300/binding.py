@@ -107,38 +107,46 @@ def make_layout(head_dim, block, bits, qjl_m=0, norm_correct=0, sign_seed=1, cod
 
 
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else None
+    return t.data_ptr() if t is not None else None
+
+
+# the current stream's handle without building a Stream object (3 us of host
+# time a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 class _on:
-    """Makes a tensor's device current for the calls inside (free when it is
-    the current one already)."""
+    """Makes a tensor's device current for the calls inside."""
 
-    def __init__(self, t):
-        self.dev = t.device.index
-        self.prev = None
+    def __init__(self, dev):
+        self.dev = dev
 
     def __enter__(self):
-        cur = torch.cuda.current_device()
-        if self.dev is not None and self.dev != cur:
-            self.prev = cur
-            torch.cuda.set_device(self.dev)
+        self.prev = torch.cuda.current_device()
+        torch.cuda.set_device(self.dev)
 
     def __exit__(self, *exc):
-        if self.prev is not None:
-            torch.cuda.set_device(self.prev)
+        torch.cuda.set_device(self.prev)
 
 
-def _i32(t, n, name, like):
-    """Checks an int32 tensor of n values (or None) on like's device."""
-    if t is not None and (t.dtype != torch.int32 or t.numel() != n or t.device != like.device or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} values on {like.device}")
+def _is(t, dtype, shape, dev):
+    """Whether t is a contiguous tensor of this type and shape on CUDA device dev."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+
+
+def _i32(t, n, name, dev):
+    """Checks a contiguous int32 tensor of n values (or None) on device dev."""
+    if t is not None and not (t.dtype is torch.int32 and t.numel() == n and t.get_device() == dev
+                              and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} values on the call's CUDA device")
 
 
 def _check(st, where):
@@ -281,13 +289,18 @@ class PackedKV:
         return self.lead_shape[2]
 
     def view(self):
+        """The C view of the cache, kept between calls while its arrays stay
+        where they are."""
         pt = self.page_table
-        return tq_kv_view(self.codes.data_ptr(), self.scales.data_ptr(),
-                          self.qjl.data_ptr() if self.qjl is not None else None,
-                          self.rnorm.data_ptr() if self.rnorm is not None else None,
-                          self.S.data_ptr() if self.S is not None else None, self.layout,
-                          pt.data_ptr() if pt is not None else None,
-                          self.lead_shape[2] if pt is not None else 0, self._table_stride())
+        at = (self.codes.data_ptr(), self.scales.data_ptr(), self.qjl.data_ptr() if self.qjl is not None else None,
+              self.rnorm.data_ptr() if self.rnorm is not None else None,
+              self.S.data_ptr() if self.S is not None else None, pt.data_ptr() if pt is not None else None)
+        kept = getattr(self, "_view", None)
+        if kept is None or kept[0] != at:
+            v = tq_kv_view(*at[:5], self.layout, at[5], self.lead_shape[2] if pt is not None else 0,
+                           self._table_stride())
+            self._view = kept = (at, v)
+        return kept[1]
 
     def _table_stride(self):
         """Entries between two rows of the table (its width unless it is part of a wider one)."""
@@ -460,37 +473,41 @@ def tq_decode_attn_shared(Kp, Vp, K, V, q, prefix_ctx=None, prefix_len=None, ctx
     None when there are none yet).  prefix_len: int32 CUDA tensor of one
     value, kv_len: int32 CUDA tensor [B]; prefix_ctx and ctx bound them."""
     lib = _load()
-    if q.dim() != 3 or q.dtype != torch.float16 or not q.is_contiguous():
-        raise ValueError("q must be a contiguous fp16 tensor [B, Hq, head_dim]")
+    dev = q.get_device()
+    if q.dim() != 3 or not _is(q, torch.float16, q.shape, dev) or dev < 0:
+        raise ValueError("q must be a contiguous fp16 CUDA tensor [B, Hq, head_dim]")
+    if dev != torch.cuda.current_device():
+        with _on(dev):
+            return tq_decode_attn_shared(Kp, Vp, K, V, q, prefix_ctx, prefix_len, ctx, kv_len, softmax_scale, n_split,
+                                         workspace, out, stream)
     B, Hq, d = q.shape
     Hkv, P_cap = _cache_for(Kp, Vp, 1)
     prefix_ctx = P_cap if prefix_ctx is None else prefix_ctx
-    S_cap = 0
+    S_cap, kv, vv = 0, None, None
+    caches = (Kp, Vp)
     if K is not None and V is not None:
         heads, S_cap = _cache_for(K, V, B)
         if heads != Hkv:
             raise ValueError("prefix and own caches must hold the same heads")
+        kv, vv = ctypes.byref(K.view()), ctypes.byref(V.view())
+        caches = (Kp, Vp, K, V)
     ctx = S_cap if ctx is None else ctx
-    for c in (Kp, Vp, K, V):
-        if c is not None and (c.layout.head_dim != d or c.codes.device != q.device):
+    for c in caches:
+        if c.layout.head_dim != d or c.codes.get_device() != dev:
             raise ValueError("caches must have q's head_dim and device")
-    _i32(prefix_len, 1, "prefix_len", q)
-    _i32(kv_len, B, "kv_len", q)
-    with _on(q):
-        if workspace is None:
-            need = tq_decode_shared_workspace_bytes(B, Hq, Hkv, d, prefix_ctx, ctx, n_split)
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-        if out is None:
-            out = torch.empty_like(q)
-        elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or out.device != q.device:
-            raise ValueError("out must be a contiguous tensor like q")
-        kp, vp = Kp.view(), Vp.view()
-        kv, vv = (K.view(), V.view()) if K is not None and V is not None else (None, None)
-        st = lib.tq_decode_attn_shared(ctypes.byref(kp), ctypes.byref(vp), P_cap, _ptr(prefix_len), prefix_ctx,
-                                       ctypes.byref(kv) if kv else None, ctypes.byref(vv) if vv else None, _ptr(q), B,
-                                       Hq, Hkv, S_cap, _ptr(kv_len), ctx, float(softmax_scale), _ptr(out),
-                                       _ptr(workspace), workspace.numel() * workspace.element_size(), n_split,
-                                       _stream(stream))
+    _i32(prefix_len, 1, "prefix_len", dev)
+    _i32(kv_len, B, "kv_len", dev)
+    if workspace is None:
+        need = tq_decode_shared_workspace_bytes(B, Hq, Hkv, d, prefix_ctx, ctx, n_split)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    if out is None:
+        out = torch.empty_like(q)
+    elif not _is(out, torch.float16, q.shape, dev):
+        raise ValueError("out must be a contiguous tensor like q")
+    st = lib.tq_decode_attn_shared(ctypes.byref(Kp.view()), ctypes.byref(Vp.view()), P_cap, _ptr(prefix_len), prefix_ctx,
+                                   kv, vv, q.data_ptr(), B, Hq, Hkv, S_cap, _ptr(kv_len), ctx, softmax_scale,
+                                   out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                   n_split, _stream(stream))
     _check(st, "tq_decode_attn_shared")
     return out
 
@@ -507,41 +524,49 @@ def tq_qkv_norm_rope(qkv, Hq, Hkv, head_dim, q_weight=None, k_weight=None, eps=1
     start as zeros when new_len is given."""
     lib = _load()
     d = head_dim
-    if qkv.dim() != 3 or qkv.shape[2] != (Hq + 2 * Hkv) * d or qkv.stride(2) != 1:
-        raise ValueError("qkv must be [B, T, (Hq + 2 Hkv) head_dim] with a contiguous last dimension")
-    B, T, _ = qkv.shape
-    row = qkv.stride(1) if T > 1 else (qkv.stride(0) if B > 1 else qkv.shape[2])
-    if T > 1 and B > 1 and qkv.stride(0) != T * row:
+    dev = qkv.get_device()
+    if qkv.dim() != 3 or qkv.shape[2] != (Hq + 2 * Hkv) * d or qkv.stride(2) != 1 or dev < 0:
+        raise ValueError("qkv must be a CUDA tensor [B, T, (Hq + 2 Hkv) head_dim] with a contiguous last dimension")
+    if dev != torch.cuda.current_device():
+        with _on(dev):
+            return tq_qkv_norm_rope(qkv, Hq, Hkv, d, q_weight, k_weight, eps, rope, interleaved, pos, new_len, slot,
+                                    q_out, k_out, v_out, stream)
+    B, T, row = qkv.shape
+    sb, st, _ = qkv.stride()
+    if T > 1 and B > 1 and sb != T * st:
         qkv = qkv.contiguous()
-        row = qkv.shape[2]
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and (w.dtype != torch.float32 or tuple(w.shape) != (d,) or not w.is_contiguous()
-                              or w.device != qkv.device):
-            raise ValueError(f"{name} must be a contiguous fp32 tensor [head_dim] on qkv's device")
-    if rope is not None and (rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous()
-                             or rope.device != qkv.device):
-        raise ValueError("rope must be a contiguous fp32 tensor [n_pos, rot_dim] on qkv's device")
-    _i32(pos, B, "pos", qkv)
-    _i32(new_len, B, "new_len", qkv)
-    _i32(slot, B, "slot", qkv)
-    new = torch.empty if new_len is None and pos is None and slot is None else torch.zeros
-    if q_out is None:
-        q_out = new((B, Hq, T, d), dtype=torch.float16, device=qkv.device)
-    if k_out is None:
-        k_out = new((B, Hkv, T, d), dtype=torch.float16, device=qkv.device)
-    if v_out is None:
-        v_out = new(tuple(k_out.shape), dtype=torch.float16, device=qkv.device)
+    elif T > 1:
+        row = st
+    elif B > 1:
+        row = sb
+    f32, f16 = torch.float32, torch.float16
+    for w in (q_weight, k_weight):
+        if w is not None and not _is(w, f32, (d,), dev):
+            raise ValueError("norm weights must be contiguous fp32 tensors [head_dim] on qkv's device")
+    n_pos, rot = 0, 0
+    if rope is not None:
+        if rope.dim() != 2 or not _is(rope, f32, rope.shape, dev):
+            raise ValueError("rope must be a contiguous fp32 tensor [n_pos, rot_dim] on qkv's device")
+        n_pos, rot = rope.shape
+    _i32(pos, B, "pos", dev)
+    _i32(new_len, B, "new_len", dev)
+    _i32(slot, B, "slot", dev)
+    if q_out is None or k_out is None or v_out is None:
+        new = torch.empty if new_len is None and pos is None and slot is None else torch.zeros
+        if q_out is None:
+            q_out = new((B, Hq, T, d), dtype=f16, device=qkv.device)
+        if k_out is None:
+            k_out = new((B, Hkv, T, d), dtype=f16, device=qkv.device)
+        if v_out is None:
+            v_out = new(tuple(k_out.shape), dtype=f16, device=qkv.device)
     cap = k_out.shape[2] if k_out.dim() == 4 else -1
-    for o, shape in ((q_out, (B, Hq, T, d)), (k_out, (B, Hkv, cap, d)), (v_out, (B, Hkv, cap, d))):
-        if (o.dtype != torch.float16 or tuple(o.shape) != shape or not o.is_contiguous()
-                or o.device != qkv.device):
-            raise ValueError("outputs must be contiguous fp16 tensors [B, Hq, T, d], [B, Hkv, cap, d] on qkv's device")
-    n_pos, rot = rope.shape if rope is not None else (0, 0)
-    with _on(qkv):
-        st = lib.tq_qkv_norm_rope(_ptr(qkv), _dtype_code(qkv.dtype), B, T, Hq, Hkv, d, row, _ptr(q_weight),
-                                  _ptr(k_weight), float(eps), _ptr(rope), n_pos, rot, 1 if interleaved else 0,
-                                  _ptr(pos), _ptr(new_len), _ptr(q_out), _ptr(k_out), _ptr(v_out), cap, _ptr(slot),
-                                  _stream(stream))
+    kv_shape = (B, Hkv, cap, d)
+    if not (_is(q_out, f16, (B, Hq, T, d), dev) and _is(k_out, f16, kv_shape, dev) and _is(v_out, f16, kv_shape, dev)):
+        raise ValueError("outputs must be contiguous fp16 tensors [B, Hq, T, d], [B, Hkv, cap, d] on qkv's device")
+    st = lib.tq_qkv_norm_rope(qkv.data_ptr(), _dtype_code(qkv.dtype), B, T, Hq, Hkv, d, row, _ptr(q_weight),
+                              _ptr(k_weight), eps, _ptr(rope), n_pos, rot, 1 if interleaved else 0, _ptr(pos),
+                              _ptr(new_len), q_out.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), cap, _ptr(slot),
+                              _stream(stream))
     _check(st, "tq_qkv_norm_rope")
     return q_out, k_out, v_out
 
@@ -563,6 +588,9 @@ class PagePool:
         if n_pages.shape[0] != page_table.shape[0]:
             raise ValueError("n_pages must have an entry for every row of page_table")
         self.page_table, self.n_pages, self.ref, self.page_size = page_table, n_pages, ref, page_size
+        self.dev = ref.get_device()
+        if self.dev < 0:
+            raise ValueError("a page pool lies on a CUDA device")
         self.caches = tuple(caches)
         self.heads = self.caches[0].lead_shape[1] if self.caches else 0
         for c in self.caches:
@@ -570,6 +598,7 @@ class PagePool:
                 raise ValueError("caches must have lead shape [num_pages, Hkv, page_size] on the pool's device")
         self.struct = tq_page_pool(page_table.data_ptr(), n_pages.data_ptr(), ref.data_ptr(), page_table.shape[0],
                                    page_table.shape[1], ref.shape[0], page_size)
+        self.ref_struct = ctypes.byref(self.struct)
         self.views = (tq_kv_view * max(1, len(self.caches)))(*[c.view() for c in self.caches])
 
     @classmethod
@@ -590,7 +619,8 @@ def _pool_call(pool, n, workspace, result):
                                 dtype=torch.uint8, device=pool.ref.device)
     if result is None:
         result = torch.empty(4, dtype=torch.int32, device=pool.ref.device)
-    _i32(result, 4, "result", pool.ref)
+    else:
+        _i32(result, 4, "result", pool.dev)
     return workspace, result
 
 
@@ -601,14 +631,18 @@ def tq_pages_fork(pool, parent, child, share_len, new_len, workspace=None, resul
     tensors of one length.  Returns the result tensor {status, pages taken,
     pages copied, 0}: status 0 done, > 0 pages missing, -1 an entry is not
     valid; unless it is 0 nothing has changed."""
-    n = child.numel()
-    for t, name in ((parent, "parent"), (child, "child"), (share_len, "share_len"), (new_len, "new_len")):
-        _i32(t, n, name, pool.ref)
-    with _on(pool.ref):
-        workspace, result = _pool_call(pool, n, workspace, result)
-        st = _load().tq_pages_fork(ctypes.byref(pool.struct), pool.views, len(pool.caches), pool.heads, _ptr(parent),
-                                   _ptr(child), _ptr(share_len), _ptr(new_len), n, _ptr(result), _ptr(workspace),
-                                   workspace.numel() * workspace.element_size(), _stream(stream))
+    n, dev = child.numel(), pool.dev
+    _i32(parent, n, "parent", dev)
+    _i32(child, n, "child", dev)
+    _i32(share_len, n, "share_len", dev)
+    _i32(new_len, n, "new_len", dev)
+    if dev != torch.cuda.current_device():
+        with _on(dev):
+            return tq_pages_fork(pool, parent, child, share_len, new_len, workspace, result, stream)
+    workspace, result = _pool_call(pool, n, workspace, result)
+    st = _load().tq_pages_fork(pool.ref_struct, pool.views, len(pool.caches), pool.heads, _ptr(parent), _ptr(child),
+                               _ptr(share_len), _ptr(new_len), n, result.data_ptr(), workspace.data_ptr(),
+                               workspace.numel() * workspace.element_size(), _stream(stream))
     _check(st, "tq_pages_fork")
     return result
 
@@ -616,22 +650,25 @@ def tq_pages_fork(pool, parent, child, share_len, new_len, workspace=None, resul
 def tq_pages_free(pool, seqs, keep_len=None, stream=None):
     """The sequences named (int32 CUDA tensor) give up their pages, or those
     behind their first keep_len tokens."""
-    n = seqs.numel()
-    _i32(seqs, n, "seqs", pool.ref)
-    _i32(keep_len, n, "keep_len", pool.ref)
-    with _on(pool.ref):
-        st = _load().tq_pages_free(ctypes.byref(pool.struct), _ptr(seqs), _ptr(keep_len), n, _stream(stream))
+    n, dev = seqs.numel(), pool.dev
+    _i32(seqs, n, "seqs", dev)
+    _i32(keep_len, n, "keep_len", dev)
+    if dev != torch.cuda.current_device():
+        with _on(dev):
+            return tq_pages_free(pool, seqs, keep_len, stream)
+    st = _load().tq_pages_free(pool.ref_struct, seqs.data_ptr(), _ptr(keep_len), n, _stream(stream))
     _check(st, "tq_pages_free")
 
 
 def tq_pages_compact(pool, workspace=None, result=None, stream=None):
     """Moves the pages in use to the front of the pool in all of its caches.
     Returns the result tensor {0, pages in use, pages moved, 0}."""
-    with _on(pool.ref):
-        workspace, result = _pool_call(pool, 0, workspace, result)
-        st = _load().tq_pages_compact(ctypes.byref(pool.struct), pool.views, len(pool.caches), pool.heads,
-                                      _ptr(result), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                      _stream(stream))
+    if pool.dev != torch.cuda.current_device():
+        with _on(pool.dev):
+            return tq_pages_compact(pool, workspace, result, stream)
+    workspace, result = _pool_call(pool, 0, workspace, result)
+    st = _load().tq_pages_compact(pool.ref_struct, pool.views, len(pool.caches), pool.heads, result.data_ptr(),
+                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream))
     _check(st, "tq_pages_compact")
     return result
 

@@ -19,7 +19,7 @@
 namespace tq {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 
 struct RopeArgs {
   const void* x;
@@ -38,16 +38,27 @@ struct RopeArgs {
   float eps;
 };
 
+// 8 values of a row as they lie in memory, and as floats
 template <bool F32>
-__device__ __forceinline__ void load8(const void* x, int64_t at, float* v) {
+struct Raw {
+  uint4 u[F32 ? 2 : 1];
+};
+template <bool F32>
+__device__ __forceinline__ Raw<F32> load8(const void* x, int64_t at) {
+  Raw<F32> r;
+  const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x) + at * (F32 ? 4 : 2));
+  r.u[0] = __ldcs(p);
+  if constexpr (F32) r.u[1] = __ldcs(p + 1);
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ void floats(const Raw<F32>& r, float* v) {
   if constexpr (F32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
-    const float4 a = p[0], b = p[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    const uint32_t w[8] = {r.u[0].x, r.u[0].y, r.u[0].z, r.u[0].w, r.u[1].x, r.u[1].y, r.u[1].z, r.u[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
   } else {
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const uint32_t w[4] = {r.u[0].x, r.u[0].y, r.u[0].z, r.u[0].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
@@ -57,106 +68,142 @@ __device__ __forceinline__ void load8(const void* x, int64_t at, float* v) {
   }
 }
 
-__device__ __forceinline__ void load4(const float* p, float* v) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+template <int N>
+__device__ __forceinline__ void load_floats(const float* p, float* v) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p + i));
+    v[i] = a.x; v[i + 1] = a.y; v[i + 2] = a.z; v[i + 3] = a.w;
+  }
 }
 
 // NEXT: rotated pairs are neighbours (2i, 2i+1); otherwise (i, i + rot/2).
-// Grid: x = token rows b*T + j, y = groups of kThreads / (D/8) heads.
-template <int D, bool F32, bool NEXT>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeArgs a) {
+// Grid: x = token rows b*T + j, y = runs of R heads for each of the block's
+// kThreads / (D/8) thread groups: a group has R rows of one token in flight
+// and reads the token's cosines and sines once for all of them.
+template <int D, bool F32, bool NEXT, int R>
+__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int TPR = D / 8;              // threads per row
-  constexpr int HPB = kThreads / TPR;     // heads per block
+  constexpr int HPB = kThreads / TPR;     // groups per block
   const int64_t tok = blockIdx.x;
-  const int b = (int)(tok / a.T), j = (int)(tok - (int64_t)b * a.T);
-  if (a.new_len && j >= a.new_len[b]) return;
-  const int64_t p = (a.pos ? (int64_t)a.pos[b] : 0) + j;
-  if (a.rot && (p < 0 || p >= a.n_pos)) return;   // no such row of the table: the token is left out
-  const int h = blockIdx.y * HPB + threadIdx.x / TPR;
-  const int H = a.Hq + 2 * a.Hkv;
   const int sub = threadIdx.x % TPR, e0 = 8 * sub;
-  const bool live = h < H;
-  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (live) load8<F32>(a.x, tok * a.row_stride + (int64_t)h * D + e0, v);
-  const bool turned = live && h < a.Hq + a.Hkv;   // queries and keys
-  const float* w = h < a.Hq ? a.wq : a.wk;
-  float ss = 0.f;
+  const int h0 = blockIdx.y * (HPB * R) + threadIdx.x / TPR;   // heads h0, h0 + HPB, ...
+  const int H = a.Hq + 2 * a.Hkv, HT = a.Hq + a.Hkv;           // all, and those with a position
+  Raw<F32> raw[R];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
-#pragma unroll
-  for (int o = 1; o < TPR; o <<= 1) ss += __shfl_xor_sync(kFull, ss, o);
-  if (turned && w) {
-    const float r = rsqrtf(ss * (1.f / D) + a.eps);
-    float wv[8];
-    load4(w + e0, wv);
-    load4(w + e0 + 4, wv + 4);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = v[i] * r * wv[i];
+  for (int i = 0; i < R; ++i)
+    raw[i] = load8<F32>(a.x, tok * a.row_stride + (int64_t)min(h0 + i * HPB, H - 1) * D + e0);
+  const int b = (int)(tok / a.T), j = (int)(tok - (int64_t)b * a.T);
+  const int n_new = a.new_len ? a.new_len[b] : a.T;
+  const int64_t p = (a.pos ? (int64_t)a.pos[b] : 0) + j;
+  const int64_t at = (a.slot ? (int64_t)a.slot[b] : 0) + j;
+  if (j >= n_new) return;
+  if (a.rot && (p < 0 || p >= a.n_pos)) return;   // no such row of the table: the token is left out
+  // the thread's cosines and sines: of its values' pairs
+  constexpr int NC = NEXT ? 4 : 8;
+  float c[NC], s[NC];
+  const int half = a.rot / 2;
+  const bool in = e0 < a.rot, lower = e0 < half;
+  if (in) {
+    const float* row = a.rope + p * a.rot + (NEXT ? e0 / 2 : (lower ? e0 : e0 - half));
+    load_floats<NC>(row, c);
+    load_floats<NC>(row + half, s);
   }
-  if (a.rot) {
-    const int half = a.rot / 2;
-    const float* row = a.rope + p * a.rot;
-    if constexpr (NEXT) {
-      if (turned && e0 < a.rot) {
-        float c[4], s[4];
-        load4(row + e0 / 2, c);
-        load4(row + half + e0 / 2, s);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x = v[2 * i], y = v[2 * i + 1];
-          v[2 * i] = x * c[i] - y * s[i];
-          v[2 * i + 1] = y * c[i] + x * s[i];
+  for (int i = 0; i < R; ++i) {
+    const int h = h0 + i * HPB;
+    float v[8];
+    floats<F32>(raw[i], v);
+    const float* w = h < a.Hq ? a.wq : a.wk;
+    float ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) ss = fmaf(v[k], v[k], ss);
+#pragma unroll
+    for (int o = 1; o < TPR; o <<= 1) ss += __shfl_xor_sync(kFull, ss, o);
+    if (h < HT && w) {
+      const float r = rsqrtf(ss * (1.f / D) + a.eps);
+      float wv[8];
+      load_floats<8>(w + e0, wv);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = v[k] * r * wv[k];
+    }
+    if (a.rot) {
+      if constexpr (NEXT) {
+        if (h < HT && in) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float x = v[2 * k], y = v[2 * k + 1];
+            v[2 * k] = x * c[k] - y * s[k];
+            v[2 * k + 1] = y * c[k] + x * s[k];
+          }
+        }
+      } else {
+        // the other value of each pair is `half` further or back: rot is a
+        // multiple of 16, so it is one other lane's same place
+        const int lane = threadIdx.x & 31;
+        const int other = in ? (lower ? lane + half / 8 : lane - half / 8) : lane;
+        float o[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] = __shfl_sync(kFull, v[k], other);
+        if (h < HT && in) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = lower ? v[k] * c[k] - o[k] * s[k] : v[k] * c[k] + o[k] * s[k];
         }
       }
+    }
+    if (h >= H) continue;
+    uint16_t* dst;
+    if (h < a.Hq) {
+      dst = a.q + (((int64_t)b * a.Hq + h) * a.T + j) * D;
     } else {
-      // the other value of each pair is `half` further or back: rot is a
-      // multiple of 16, so it is one other lane's same place
-      const bool lower = e0 < half, in = e0 < a.rot;
-      const int lane = threadIdx.x & 31;
-      const int other = in ? (lower ? lane + half / 8 : lane - half / 8) : lane;
-      float o[8];
+      if (at < 0 || at >= a.kv_cap) continue;
+      const int kv = h - a.Hq;
+      dst = kv < a.Hkv ? a.k + (((int64_t)b * a.Hkv + kv) * a.kv_cap + at) * D
+                       : a.v + (((int64_t)b * a.Hkv + kv - a.Hkv) * a.kv_cap + at) * D;
+    }
+    uint32_t o[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(kFull, v[i], other);
-      if (turned && in) {
-        const int at = lower ? e0 : e0 - half;
-        float c[8], s[8];
-        load4(row + at, c);
-        load4(row + at + 4, c + 4);
-        load4(row + half + at, s);
-        load4(row + half + at + 4, s + 4);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = lower ? v[i] * c[i] - o[i] * s[i] : v[i] * c[i] + o[i] * s[i];
+    for (int k = 0; k < 4; ++k) o[k] = (uint32_t)f2h(v[2 * k]) | ((uint32_t)f2h(v[2 * k + 1]) << 16);
+    *reinterpret_cast<uint4*>(dst + e0) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+template <int D, bool F32, bool NEXT>
+void launch_rows(const RopeArgs& a, int64_t tokens, cudaStream_t st) {
+  constexpr int HPB = kThreads / (D / 8);
+  const int H = a.Hq + 2 * a.Hkv;
+  // Rows per thread group: one while the blocks of one row each do not fill
+  // the GPU (latency counts), else the number from 2 to 4 that leaves the
+  // fewest groups without a head
+  const int64_t blocks = tokens * ((H + HPB - 1) / HPB);
+  int R = 1;
+  if (blocks > 152 * 8) {
+    int best = 1 << 30;
+    for (int r = 4; r >= 2; --r) {
+      const int idle = (H + HPB * r - 1) / (HPB * r) * (HPB * r) - H;
+      if (idle < best) {
+        best = idle;
+        R = r;
       }
     }
   }
-  if (!live) return;
-  uint16_t* dst;
-  if (h < a.Hq) {
-    dst = a.q + (((int64_t)b * a.Hq + h) * a.T + j) * D;
-  } else {
-    const int64_t at = (a.slot ? (int64_t)a.slot[b] : 0) + j;
-    if (at < 0 || at >= a.kv_cap) return;
-    const int kv = h - a.Hq;
-    dst = kv < a.Hkv ? a.k + (((int64_t)b * a.Hkv + kv) * a.kv_cap + at) * D
-                     : a.v + (((int64_t)b * a.Hkv + kv - a.Hkv) * a.kv_cap + at) * D;
+  const dim3 grid((unsigned)tokens, (unsigned)((H + HPB * R - 1) / (HPB * R)));
+  switch (R) {
+    case 1: norm_rope_kernel<D, F32, NEXT, 1><<<grid, kThreads, 0, st>>>(a); break;
+    case 2: norm_rope_kernel<D, F32, NEXT, 2><<<grid, kThreads, 0, st>>>(a); break;
+    case 3: norm_rope_kernel<D, F32, NEXT, 3><<<grid, kThreads, 0, st>>>(a); break;
+    default: norm_rope_kernel<D, F32, NEXT, 4><<<grid, kThreads, 0, st>>>(a); break;
   }
-  uint32_t o[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = (uint32_t)f2h(v[2 * i]) | ((uint32_t)f2h(v[2 * i + 1]) << 16);
-  *reinterpret_cast<uint4*>(dst + e0) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 template <int D>
 void launch(const RopeArgs& a, bool f32, bool next, int64_t tokens, cudaStream_t st) {
-  constexpr int HPB = kThreads / (D / 8);
-  const dim3 grid((unsigned)tokens, (unsigned)((a.Hq + 2 * a.Hkv + HPB - 1) / HPB));
   if (f32) {
-    if (next) norm_rope_kernel<D, true, true><<<grid, kThreads, 0, st>>>(a);
-    else norm_rope_kernel<D, true, false><<<grid, kThreads, 0, st>>>(a);
+    if (next) launch_rows<D, true, true>(a, tokens, st);
+    else launch_rows<D, true, false>(a, tokens, st);
   } else {
-    if (next) norm_rope_kernel<D, false, true><<<grid, kThreads, 0, st>>>(a);
-    else norm_rope_kernel<D, false, false><<<grid, kThreads, 0, st>>>(a);
+    if (next) launch_rows<D, false, true>(a, tokens, st);
+    else launch_rows<D, false, false>(a, tokens, st);
   }
 }
 
