@@ -10,13 +10,17 @@
 // result does not depend on the order in which blocks run.  Reference counts
 // change by atomic adds, which commute.
 //
-// Steps (each a launch; the pool's counts are read once):
+// Steps, each a launch that the next one's set-up overlaps:
 //   count   free pages of every chunk of kChunk pages
 //   plan    one block: prefix sum over the chunks; for a fork also the checks
 //           of every entry, the pages it needs and their prefix sum
 //   assign  chunks deal their free pages by rank (fork), or list holes and
 //           pages to move by rank (compact)
-//   move    page contents, tables and counts
+//   rename  tables and counts follow (compact)
+//   move    page contents
+// A small pool's call is bound by its launches (2 us each on the GPU, 3 on the
+// host), so there one block does everything but the move: a fork of 4 entries
+// over 512 pages is two launches instead of four.
 #include <cuda_runtime.h>
 
 #include "tq_device.cuh"
@@ -27,8 +31,9 @@ namespace {
 constexpr int kChunk = 1024;          // pages per block of count and assign
 constexpr int kThreads = 256;
 constexpr int kPlanThreads = 1024;
+constexpr int kSmallPages = 16384;    // pages, and table entries that a call may touch, that one block takes
 constexpr int kMaxArrays = 128;       // cache arrays one move launch takes
-constexpr int kPiece = 8192;          // bytes one block copies at a time
+constexpr int kPiece = 16384;         // bytes one block copies at a time: four 16-byte loads in flight a thread
 constexpr int kMaxPerSeq = 1 << 20;   // pages of a sequence: kPlanThreads of them sum below 2^31
 constexpr int kMaxPages = 1 << 28;    // pages of a pool
 constexpr int kManyPages = 1 << 29;   // more than any pool has
@@ -108,9 +113,16 @@ __device__ __forceinline__ int block_scan(int v, int* s_part, int* total) {
   return s_part[w] + x - v;
 }
 
+// Kernels of one call in a row: a kernel may start when the one before it
+// has, and waits here until that one has ended and its writes are visible.
+__device__ __forceinline__ void chain_begin() {
+  asm volatile("griddepcontrol.launch_dependents;\ngriddepcontrol.wait;\n" ::: "memory");
+}
+
 __device__ __forceinline__ int free_at(const int32_t* ref, int p, int n) { return p < n && ref[p] == 0 ? 1 : 0; }
 
 __global__ void __launch_bounds__(kThreads) pages_count_kernel(const int32_t* __restrict__ ref, int num_pages, Work w) {
+  chain_begin();
   __shared__ int s_part[33];
   int c = 0;
   for (int i = threadIdx.x; i < kChunk; i += kThreads) c += free_at(ref, blockIdx.x * kChunk + i, num_pages);
@@ -191,11 +203,12 @@ __device__ Entry read_entry(const ForkArgs& a, int i) {
   return e;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) pages_fork_plan_kernel(const ForkArgs a, int chunks) {
-  __shared__ int s_part[33];
-  const Work w = a.w;
+// Checks every entry and sums up what they need, given the free pages; takes
+// the sequences' new page counts over when all is well (and returns that).
+// One block of kPlanThreads.
+__device__ bool plan_entries(const ForkArgs& a, int n_free, int* s_part) {
+  const Work& w = a.w;
   const tq_page_pool& p = a.pool;
-  const int n_free = scan_chunks(w, chunks, s_part);
   for (int i = threadIdx.x; i < p.n_seqs; i += kPlanThreads) w.mark[i] = 0;
   __syncthreads();
   int bad = 0;
@@ -256,11 +269,70 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_plan_kernel(const For
       a.result[3] = 0;
     }
   }
+  __syncthreads();
+  return ok;
+}
+
+// The r-th fresh page, `page`, goes to the entry whose pages hold rank r.
+__device__ void deal(const ForkArgs& a, int r, int page) {
+  const Work& w = a.w;
+  int lo = 0, hi = a.n;   // the last entry with off <= r
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (w.off[mid] <= r) lo = mid; else hi = mid;
+  }
+  const int t = r - w.off[lo], cow = w.cow[lo];
+  const int idx = cow >= 0 ? (t == 0 ? cow : w.first[lo] + t - 1) : w.first[lo] + t;
+  a.pool.page_table[(int64_t)a.child[lo] * a.pool.pages_per_seq + idx] = page;
+  a.pool.ref[page] = 1;
+  if (t == 0) w.dst[lo] = page;   // the copy of a part-filled page goes to the first fresh page
+}
+
+// Entry i shares its parent's full pages: the pages from k0 on, `step` apart.
+__device__ void share(const ForkArgs& a, int i, int k0, int step) {
+  const tq_page_pool& p = a.pool;
+  const int parent = a.parent[i], child = a.child[i];
+  if (parent < 0 || parent == child) return;
+  const int full = a.w.first[i];
+  const int32_t* from = p.page_table + (int64_t)parent * p.pages_per_seq;
+  int32_t* to = p.page_table + (int64_t)child * p.pages_per_seq;
+  for (int k = k0; k < full; k += step) {
+    const int page = from[k];
+    to[k] = page;
+    if (page >= 0 && page < p.num_pages) atomicAdd(&p.ref[page], 1);
+  }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) pages_fork_plan_kernel(const ForkArgs a, int chunks) {
+  chain_begin();
+  __shared__ int s_part[33];
+  plan_entries(a, scan_chunks(a.w, chunks, s_part), s_part);
+}
+
+// A small pool's fork: count, plan and assign in one block, a thread taking
+// `per` consecutive pages.
+__global__ void __launch_bounds__(kPlanThreads) pages_fork_small_kernel(const ForkArgs a, int per) {
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");   // first of its call: nothing to wait for
+  __shared__ int s_part[33];
+  const int p0 = threadIdx.x * per, p1 = min(p0 + per, a.pool.num_pages);
+  int c = 0, n_free;
+  uint32_t free_bits = 0;   // per <= 16
+  for (int p = p0; p < p1; ++p) {
+    const int f = a.pool.ref[p] == 0 ? 1 : 0;
+    c += f;
+    free_bits |= (uint32_t)f << (p - p0);
+  }
+  int r = block_scan(c, s_part, &n_free);
+  if (!plan_entries(a, n_free, s_part)) return;
+  const int need = a.w.off[a.n];
+  for (; free_bits && r < need; ++r, free_bits &= free_bits - 1) deal(a, r, p0 + __ffs(free_bits) - 1);
+  for (int i = threadIdx.x >> 5; i < a.n; i += kPlanThreads / 32) share(a, i, threadIdx.x & 31, 32);
 }
 
 // Blocks [0, chunks): deal the chunk's free pages.  Blocks behind: entry
 // blockIdx.x - chunks shares its parent's full pages.
 __global__ void __launch_bounds__(kThreads) pages_fork_assign_kernel(const ForkArgs a, int chunks) {
+  chain_begin();
   __shared__ int s_part[33];
   const Work w = a.w;
   const tq_page_pool& p = a.pool;
@@ -280,36 +352,11 @@ __global__ void __launch_bounds__(kThreads) pages_fork_assign_kernel(const ForkA
     for (int k = 0; k < PER; ++k) {
       if (!f[k]) continue;
       if (r >= need) break;
-      // the entry whose fresh pages hold rank r: the last with off <= r
-      int lo = 0, hi = a.n;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (w.off[mid] <= r) lo = mid; else hi = mid;
-      }
-      int t = r - w.off[lo];
-      const int cow = w.cow[lo];
-      int idx;
-      if (cow >= 0) idx = t == 0 ? cow : w.first[lo] + t - 1;
-      else idx = w.first[lo] + t;
-      p.page_table[(int64_t)a.child[lo] * p.pages_per_seq + idx] = p0 + k;
-      p.ref[p0 + k] = 1;
-      // the copy of a part-filled page goes to the first fresh page
-      if (t == 0) w.dst[lo] = p0 + k;
-      ++r;
+      deal(a, r++, p0 + k);
     }
     return;
   }
-  const int i = blockIdx.x - chunks;
-  const int parent = a.parent[i], child = a.child[i];
-  if (parent < 0 || parent == child) return;
-  const int full = w.first[i];
-  const int32_t* from = p.page_table + (int64_t)parent * p.pages_per_seq;
-  int32_t* to = p.page_table + (int64_t)child * p.pages_per_seq;
-  for (int k = threadIdx.x; k < full; k += kThreads) {
-    const int page = from[k];
-    to[k] = page;
-    if (page >= 0 && page < p.num_pages) atomicAdd(&p.ref[page], 1);
-  }
+  share(a, blockIdx.x - chunks, threadIdx.x, kThreads);
 }
 
 // The caches' arrays as runs of bytes per page.
@@ -325,6 +372,7 @@ struct Arrays {
 // the counts of the n_drop pages that a fork's entries replaced.
 __global__ void __launch_bounds__(kThreads) pages_move_kernel(Work w, const __grid_constant__ Arrays a,
                                                               int32_t* ref, int num_pages, int n_drop) {
+  chain_begin();
   const int moves = w.head->moves;
   if (blockIdx.x == 0 && moves) {
     for (int i = threadIdx.x; i < n_drop; i += kThreads) {
@@ -349,7 +397,14 @@ __global__ void __launch_bounds__(kThreads) pages_move_kernel(Work w, const __gr
     const int n16 = (int)(imin64(kPiece, bytes - at) / 16);
     const uint4* s = reinterpret_cast<const uint4*>(a.base[lo] + src * bytes + at);
     uint4* d = reinterpret_cast<uint4*>(a.base[lo] + dst * bytes + at);
-    for (int k = threadIdx.x; k < n16; k += kThreads) d[k] = s[k];
+    constexpr int U = kPiece / 16 / kThreads;
+    uint4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (threadIdx.x + u * kThreads < n16) v[u] = __ldcs(s + threadIdx.x + u * kThreads);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (threadIdx.x + u * kThreads < n16) d[threadIdx.x + u * kThreads] = v[u];
   }
 }
 
@@ -360,6 +415,7 @@ struct CompactArgs {
 };
 
 __global__ void __launch_bounds__(kPlanThreads) pages_compact_plan_kernel(const CompactArgs a, int chunks) {
+  chain_begin();
   __shared__ int s_part[33];
   const int n_free = scan_chunks(a.w, chunks, s_part);
   const int n_live = a.pool.num_pages - n_free;
@@ -384,49 +440,11 @@ __global__ void __launch_bounds__(kPlanThreads) pages_compact_plan_kernel(const 
   }
 }
 
-// Lists the holes before n_live and the live pages behind it, by rank.
-__global__ void __launch_bounds__(kThreads) pages_compact_list_kernel(const CompactArgs a) {
-  __shared__ int s_part[33];
-  const Work w = a.w;
-  const int n_live = w.head->n_live, moves = w.head->moves;
-  if (!moves) return;
-  constexpr int PER = kChunk / kThreads;
-  const int p0 = blockIdx.x * kChunk + threadIdx.x * PER;
-  int f[PER], c = 0;
-#pragma unroll
-  for (int k = 0; k < PER; ++k) c += f[k] = free_at(a.pool.ref, p0 + k, a.pool.num_pages);
-  int total;
-  int before = w.chunk[blockIdx.x] + block_scan(c, s_part, &total);   // free pages before p0
-#pragma unroll
-  for (int k = 0; k < PER; ++k) {
-    const int page = p0 + k;
-    if (page >= a.pool.num_pages) break;
-    if (f[k]) {
-      if (page < n_live) {
-        if (before < moves) w.dst[before] = page;
-      } else {
-        w.rank[page] = -1;
-      }
-      ++before;
-    } else if (page >= n_live) {
-      // live pages before it, less those before n_live
-      const int r = page - before - (n_live - moves);
-      if (r >= 0 && r < moves) {
-        w.src[r] = page;
-        w.rank[page] = r;
-      }
-    }
-  }
-}
-
-// Tables and counts after the lists are there: a warp per sequence renames
-// its pages, and the counts move with the pages.
-__global__ void __launch_bounds__(kThreads) pages_compact_rename_kernel(const CompactArgs a) {
-  const Work w = a.w;
+// Tables and counts after the lists are there: `lanes` threads (a warp per
+// sequence) rename the pages, and the counts move with the pages.
+__device__ void rename(const CompactArgs& a, int n_live, int moves, int64_t tid, int64_t step) {
+  const Work& w = a.w;
   const tq_page_pool& p = a.pool;
-  const int n_live = w.head->n_live, moves = w.head->moves;
-  if (!moves) return;
-  const int64_t tid = (int64_t)blockIdx.x * kThreads + threadIdx.x, step = (int64_t)gridDim.x * kThreads;
   for (int64_t r = tid; r < moves; r += step) {
     p.ref[w.dst[r]] = p.ref[w.src[r]];
     p.ref[w.src[r]] = 0;
@@ -442,6 +460,85 @@ __global__ void __launch_bounds__(kThreads) pages_compact_rename_kernel(const Co
       if (r >= 0) row[j] = w.dst[r];
     }
   }
+}
+
+// Page `page` in the lists of holes before n_live and of pages to move, by
+// rank; `before`: the free pages before it.
+__device__ void list_page(const Work& w, int page, bool is_free, int before, int n_live, int moves) {
+  if (is_free) {
+    if (page >= n_live) w.rank[page] = -1;
+    else if (before < moves) w.dst[before] = page;
+  } else if (page >= n_live) {
+    const int r = page - before - (n_live - moves);   // live pages before it, less those before n_live
+    if (r >= 0 && r < moves) {
+      w.src[r] = page;
+      w.rank[page] = r;
+    }
+  }
+}
+
+// A small pool's compaction but for the copies, in one block.
+__global__ void __launch_bounds__(kPlanThreads) pages_compact_small_kernel(const CompactArgs a, int per) {
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");   // first of its call: nothing to wait for
+  __shared__ int s_part[33];
+  const int n = a.pool.num_pages, p0 = min(threadIdx.x * per, n), p1 = min(p0 + per, n);
+  int c = 0, n_free, moves;
+  uint32_t free_bits = 0;   // per <= 16
+  for (int p = p0; p < p1; ++p) {
+    const int f = a.pool.ref[p] == 0 ? 1 : 0;
+    c += f;
+    free_bits |= (uint32_t)f << (p - p0);
+  }
+  int before = block_scan(c, s_part, &n_free);
+  const int n_live = n - n_free, in = min(max(n_live - p0, 0), 31);
+  block_scan(__popc(free_bits & ((1u << in) - 1)), s_part, &moves);   // holes
+  for (int p = p0; p < p1; ++p) {
+    const bool f = (free_bits >> (p - p0)) & 1u;
+    list_page(a.w, p, f, before, n_live, moves);
+    before += f;
+  }
+  if (threadIdx.x == 0) {
+    a.w.head->ok = 1;
+    a.w.head->n_live = n_live;
+    a.w.head->moves = moves;
+    if (a.result) {
+      a.result[0] = 0;
+      a.result[1] = n_live;
+      a.result[2] = moves;
+      a.result[3] = 0;
+    }
+  }
+  __syncthreads();
+  if (moves) rename(a, n_live, moves, threadIdx.x, kPlanThreads);
+}
+
+// Lists the holes before n_live and the live pages behind it, by rank.
+__global__ void __launch_bounds__(kThreads) pages_compact_list_kernel(const CompactArgs a) {
+  chain_begin();
+  __shared__ int s_part[33];
+  const Work w = a.w;
+  const int n_live = w.head->n_live, moves = w.head->moves;
+  if (!moves) return;
+  constexpr int PER = kChunk / kThreads;
+  const int p0 = blockIdx.x * kChunk + threadIdx.x * PER;
+  int f[PER], c = 0;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) c += f[k] = free_at(a.pool.ref, p0 + k, a.pool.num_pages);
+  int total;
+  int before = w.chunk[blockIdx.x] + block_scan(c, s_part, &total);   // free pages before p0
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    if (p0 + k >= a.pool.num_pages) break;
+    list_page(w, p0 + k, f[k] != 0, before, n_live, moves);
+    before += f[k];
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) pages_compact_rename_kernel(const CompactArgs a) {
+  chain_begin();
+  const int moves = a.w.head->moves;
+  if (moves)
+    rename(a, a.w.head->n_live, moves, (int64_t)blockIdx.x * kThreads + threadIdx.x, (int64_t)gridDim.x * kThreads);
 }
 
 // A block per sequence named.
@@ -464,6 +561,22 @@ __global__ void __launch_bounds__(kThreads) pages_free_kernel(const tq_page_pool
     const int page = row[j];
     if (page >= 0 && page < p.num_pages) atomicSub(&p.ref[page], 1);
   }
+}
+
+// Launches a kernel of a call; chained: its set-up overlaps the kernel before
+// it, which it waits for itself (chain_begin).
+template <class... P, class... A>
+bool launch(void (*kern)(P...), int64_t blocks, int threads, bool chained, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = chained ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess;
 }
 
 int check_pool(const tq_page_pool* p) {
@@ -492,11 +605,11 @@ int check_caches(const tq_kv_view* caches, int n_caches, int Hkv, int page_size)
 int launch_moves(const tq_kv_view* caches, int n_caches, int Hkv, const tq_page_pool& p, const Work& w, int64_t most,
                  int n_drop, cudaStream_t st) {
   Arrays a{};
-  bool launched = false;
+  bool launched = false, ok = true;
   auto flush = [&]() {
     const int64_t items = most * a.pieces;
     const int64_t grid = items < 1 ? 1 : (items > 152 * 8 ? 152 * 8 : items);
-    pages_move_kernel<<<(unsigned)grid, kThreads, 0, st>>>(w, a, p.ref, p.num_pages, launched ? 0 : n_drop);
+    ok = ok && launch(pages_move_kernel, grid, kThreads, true, st, w, a, p.ref, p.num_pages, launched ? 0 : n_drop);
     launched = true;
     a.n = a.pieces = 0;
   };
@@ -519,7 +632,7 @@ int launch_moves(const tq_kv_view* caches, int n_caches, int Hkv, const tq_page_
     }
   }
   if (a.n || (!launched && n_drop)) flush();
-  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+  return ok && cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
 }  // namespace
@@ -549,13 +662,17 @@ extern "C" int tq_pages_fork(const tq_page_pool* pool, const tq_kv_view* caches,
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const tq::ForkArgs a{*pool, parent, child, share_len, new_len, result, n, w};
   const int chunks = (pool->num_pages + tq::kChunk - 1) / tq::kChunk;
-  tq::pages_count_kernel<<<chunks, tq::kThreads, 0, s>>>(pool->ref, pool->num_pages, w);
-  tq::pages_fork_plan_kernel<<<1, tq::kPlanThreads, 0, s>>>(a, chunks);
-  if (n) {
-    tq::pages_fork_assign_kernel<<<chunks + n, tq::kThreads, 0, s>>>(a, chunks);
-    if (cudaGetLastError() != cudaSuccess) return TQ_ERR_CUDA;
-    return tq::launch_moves(caches, n_caches, Hkv, *pool, w, n, n, s);
+  bool ok;
+  if (pool->num_pages <= tq::kSmallPages && (int64_t)n * pool->pages_per_seq <= tq::kSmallPages) {
+    const int per = (pool->num_pages + tq::kPlanThreads - 1) / tq::kPlanThreads;
+    ok = tq::launch(tq::pages_fork_small_kernel, 1, tq::kPlanThreads, false, s, a, per);
+  } else {
+    ok = tq::launch(tq::pages_count_kernel, chunks, tq::kThreads, false, s, pool->ref, pool->num_pages, w) &&
+         tq::launch(tq::pages_fork_plan_kernel, 1, tq::kPlanThreads, true, s, a, chunks) &&
+         (!n || tq::launch(tq::pages_fork_assign_kernel, chunks + n, tq::kThreads, true, s, a, chunks));
   }
+  if (!ok) return TQ_ERR_CUDA;
+  if (n) return tq::launch_moves(caches, n_caches, Hkv, *pool, w, n, n, s);
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
@@ -583,12 +700,18 @@ extern "C" int tq_pages_compact(const tq_page_pool* pool, const tq_kv_view* cach
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const tq::CompactArgs a{*pool, result, w};
   const int chunks = (pool->num_pages + tq::kChunk - 1) / tq::kChunk;
-  tq::pages_count_kernel<<<chunks, tq::kThreads, 0, s>>>(pool->ref, pool->num_pages, w);
-  tq::pages_compact_plan_kernel<<<1, tq::kPlanThreads, 0, s>>>(a, chunks);
-  tq::pages_compact_list_kernel<<<chunks, tq::kThreads, 0, s>>>(a);
-  const int64_t work = pool->num_pages > (int64_t)pool->n_seqs * 32 ? pool->num_pages : (int64_t)pool->n_seqs * 32;
-  const int64_t blocks = (work + tq::kThreads - 1) / tq::kThreads;
-  tq::pages_compact_rename_kernel<<<(unsigned)(blocks > 1216 ? 1216 : blocks), tq::kThreads, 0, s>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return TQ_ERR_CUDA;
+  bool ok;
+  if (pool->num_pages <= tq::kSmallPages && (int64_t)pool->n_seqs * pool->pages_per_seq <= tq::kSmallPages) {
+    const int per = (pool->num_pages + tq::kPlanThreads - 1) / tq::kPlanThreads;
+    ok = tq::launch(tq::pages_compact_small_kernel, 1, tq::kPlanThreads, false, s, a, per);
+  } else {
+    const int64_t work = pool->num_pages > (int64_t)pool->n_seqs * 32 ? pool->num_pages : (int64_t)pool->n_seqs * 32;
+    const int64_t blocks = (work + tq::kThreads - 1) / tq::kThreads;
+    ok = tq::launch(tq::pages_count_kernel, chunks, tq::kThreads, false, s, pool->ref, pool->num_pages, w) &&
+         tq::launch(tq::pages_compact_plan_kernel, 1, tq::kPlanThreads, true, s, a, chunks) &&
+         tq::launch(tq::pages_compact_list_kernel, chunks, tq::kThreads, true, s, a) &&
+         tq::launch(tq::pages_compact_rename_kernel, blocks > 1216 ? 1216 : blocks, tq::kThreads, true, s, a);
+  }
+  if (!ok) return TQ_ERR_CUDA;
   return tq::launch_moves(caches, n_caches, Hkv, *pool, w, pool->num_pages / 2 + 1, 0, s);
 }

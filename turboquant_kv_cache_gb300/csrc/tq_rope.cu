@@ -19,7 +19,7 @@
 namespace tq {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 64;
 
 struct RopeArgs {
   const void* x;
@@ -34,6 +34,7 @@ struct RopeArgs {
   uint16_t* k;
   uint16_t* v;
   int64_t n_pos, kv_cap;
+  int64_t tokens;          // B * T
   int T, Hq, Hkv, rot;
   float eps;
 };
@@ -78,40 +79,42 @@ __device__ __forceinline__ void load_floats(const float* p, float* v) {
 }
 
 // NEXT: rotated pairs are neighbours (2i, 2i+1); otherwise (i, i + rot/2).
-// Grid: x = token rows b*T + j, y = runs of R heads for each of the block's
-// kThreads / (D/8) thread groups: a group has R rows of one token in flight
-// and reads the token's cosines and sines once for all of them.
+// A block's kThreads / (D/8) thread groups take consecutive token rows b*T + j
+// (grid x) and the same R heads (grid y): a group has R rows of one token in
+// flight, contiguous in the input, and reads the token's cosines and sines
+// once for all of them; the block's outputs of a head are one run.
 template <int D, bool F32, bool NEXT, int R>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int TPR = D / 8;              // threads per row
   constexpr int HPB = kThreads / TPR;     // groups per block
-  const int64_t tok = blockIdx.x;
   const int sub = threadIdx.x % TPR, e0 = 8 * sub;
-  const int h0 = blockIdx.y * (HPB * R) + threadIdx.x / TPR;   // heads h0, h0 + HPB, ...
-  const int H = a.Hq + 2 * a.Hkv, HT = a.Hq + a.Hkv;           // all, and those with a position
+  const int64_t tok_at = (int64_t)blockIdx.x * HPB + threadIdx.x / TPR, tok = imin64(tok_at, a.tokens - 1);
+  const int h0 = blockIdx.y * R;
+  const int H = a.Hq + 2 * a.Hkv, HT = a.Hq + a.Hkv;   // all heads, and those with a position
   Raw<F32> raw[R];
 #pragma unroll
   for (int i = 0; i < R; ++i)
-    raw[i] = load8<F32>(a.x, tok * a.row_stride + (int64_t)min(h0 + i * HPB, H - 1) * D + e0);
+    raw[i] = load8<F32>(a.x, tok * a.row_stride + (int64_t)min(h0 + i, H - 1) * D + e0);
   const int b = (int)(tok / a.T), j = (int)(tok - (int64_t)b * a.T);
   const int n_new = a.new_len ? a.new_len[b] : a.T;
   const int64_t p = (a.pos ? (int64_t)a.pos[b] : 0) + j;
   const int64_t at = (a.slot ? (int64_t)a.slot[b] : 0) + j;
-  if (j >= n_new) return;
-  if (a.rot && (p < 0 || p >= a.n_pos)) return;   // no such row of the table: the token is left out
+  // a token behind its batch's length, or whose position has no row in the
+  // table, is left out (its lanes stay for the shuffles of their warp)
+  const bool ok = tok_at < a.tokens && j < n_new && (!a.rot || (p >= 0 && p < a.n_pos));
   // the thread's cosines and sines: of its values' pairs
   constexpr int NC = NEXT ? 4 : 8;
   float c[NC], s[NC];
   const int half = a.rot / 2;
   const bool in = e0 < a.rot, lower = e0 < half;
-  if (in) {
+  if (in && ok) {
     const float* row = a.rope + p * a.rot + (NEXT ? e0 / 2 : (lower ? e0 : e0 - half));
     load_floats<NC>(row, c);
     load_floats<NC>(row + half, s);
   }
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const int h = h0 + i * HPB;
+    const int h = h0 + i;
     float v[8];
     floats<F32>(raw[i], v);
     const float* w = h < a.Hq ? a.wq : a.wk;
@@ -151,7 +154,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
         }
       }
     }
-    if (h >= H) continue;
+    if (h >= H || !ok) continue;
     uint16_t* dst;
     if (h < a.Hq) {
       dst = a.q + (((int64_t)b * a.Hq + h) * a.T + j) * D;
@@ -172,22 +175,22 @@ template <int D, bool F32, bool NEXT>
 void launch_rows(const RopeArgs& a, int64_t tokens, cudaStream_t st) {
   constexpr int HPB = kThreads / (D / 8);
   const int H = a.Hq + 2 * a.Hkv;
-  // Rows per thread group: one while the blocks of one row each do not fill
-  // the GPU (latency counts), else the number from 2 to 4 that leaves the
-  // fewest groups without a head
-  const int64_t blocks = tokens * ((H + HPB - 1) / HPB);
+  // Rows per thread group: one while that does not fill the GPU (latency
+  // counts), else the number from 4 down to 2 that leaves the fewest without
+  // a head
+  const int64_t blocks = (tokens + HPB - 1) / HPB;
   int R = 1;
-  if (blocks > 152 * 8) {
+  if (blocks * H > 152 * 16) {
     int best = 1 << 30;
     for (int r = 4; r >= 2; --r) {
-      const int idle = (H + HPB * r - 1) / (HPB * r) * (HPB * r) - H;
+      const int idle = (H + r - 1) / r * r - H;
       if (idle < best) {
         best = idle;
         R = r;
       }
     }
   }
-  const dim3 grid((unsigned)tokens, (unsigned)((H + HPB * R - 1) / (HPB * R)));
+  const dim3 grid((unsigned)blocks, (unsigned)((H + R - 1) / R));
   switch (R) {
     case 1: norm_rope_kernel<D, F32, NEXT, 1><<<grid, kThreads, 0, st>>>(a); break;
     case 2: norm_rope_kernel<D, F32, NEXT, 2><<<grid, kThreads, 0, st>>>(a); break;
@@ -232,7 +235,7 @@ extern "C" int tq_qkv_norm_rope(const void* qkv, tq_dtype x_dtype, int B, int T,
       !tq::aligned16(rope))
     return TQ_ERR_ALIGN;
   const tq::RopeArgs a{qkv, row_stride, q_weight, k_weight, rope, pos, new_len, slot, q_out, k_out, v_out,
-                       n_pos, kv_cap, T, Hq, Hkv, rot_dim, eps};
+                       n_pos, kv_cap, (int64_t)B * T, T, Hq, Hkv, rot_dim, eps};
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int64_t tokens = (int64_t)B * T;
   switch (head_dim) {
