@@ -17,9 +17,9 @@
 // multiplies V: two warps read P back as mma.sync operands and multiply it by
 // a matrix of ones, in fp32.
 // The reference m of a row only moves when a score passes it by more than
-// 2^12 (the first tile always does): the common step needs no maximum over
-// tokens, only one barrier vote; the rare one takes the maxima and scales O
-// and l.
+// 2^12 (it starts as the largest of 32 scores): the common step needs no
+// maximum over tokens, only one barrier vote; the rare one takes the maxima
+// and scales O and l.
 //
 // The sequences' own tokens are the same work with other rows: a CTA then has
 // one sequence, its G rows and a slice of its tokens.  Prefix and own CTAs
@@ -100,13 +100,27 @@ struct Source {
   int64_t S_cap, ctx;
   int64_t per;                 // tokens per split (multiple of kTile)
   int splits, slot0;
+  uint32_t div_mul, div_shift;   // unit / splits (FastDiv)
 };
+
+// n / d for n < 2^31 by a multiplication (d >= 1)
+struct FastDiv {
+  uint32_t mul, shift;   // mul 0: d is 1
+};
+FastDiv fast_div(uint32_t d) {
+  if (d <= 1) return {0u, 0u};
+  uint32_t l = 1;
+  while (l < 31 && (1u << l) < d) ++l;   // 2^(l-1) < d <= 2^l
+  return {(uint32_t)((((uint64_t)1 << (31 + l)) + d - 1) / d), l - 1};
+}
+__device__ __forceinline__ uint32_t div_by(uint32_t n, FastDiv f) { return f.mul ? __umulhi(n, f.mul) >> f.shift : n; }
 
 struct SharedArgs {
   Source pre, own;
   const uint16_t* q;
   float* part;                 // [B*Hq][slots][D + 4]
   uint64_t report_ns, hard_ns;
+  FastDiv by_heads;            // unit / Hkv
   int B, Hq, Hkv, G, lg, slots;   // G = 1 << lg
   int NR;                      // rows of a prefix CTA (multiple of 32)
   int row_tiles;               // prefix CTAs along the rows
@@ -114,6 +128,10 @@ struct SharedArgs {
   float qscale;
 };
 
+#define TQ_LD4(taddr, v)                                                                       \
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];\n"                 \
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])                               \
+               : "r"(taddr))
 #define TQ_LD16(taddr, v)                                                                                          \
   asm volatile(                                                                                                    \
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"    \
@@ -301,6 +319,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
   __shared__ __align__(16) float s_m[C::MAXR];      // the rows' softmax references
   __shared__ float s_al[C::MAXR];
   __shared__ float s_wm[4][C::MAXR];                // maxima by TMEM lane quarter (rare path)
+  __shared__ int64_t s_dst[C::MAXR];                // where the rows' partials go
   __shared__ __align__(8) float s_l[C::MAXR];                    // the rows' sums of p
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -308,8 +327,9 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
   // sequence's own: split, KV head, sequence
   const bool pre = (int)blockIdx.x < a.n_pre;
   const Source& src = pre ? a.pre : a.own;
-  const int unit = pre ? blockIdx.x : blockIdx.x - a.n_pre;
-  const int split = unit % src.splits, kvh = unit / src.splits % a.Hkv, grp_z = unit / src.splits / a.Hkv;
+  const uint32_t unit = pre ? blockIdx.x : blockIdx.x - a.n_pre;
+  const uint32_t unit_h = div_by(unit, {src.div_mul, src.div_shift}), unit_z = div_by(unit_h, a.by_heads);
+  const int split = unit - unit_h * src.splits, kvh = unit_h - unit_z * a.Hkv, grp_z = unit_z;
   const int NR = pre ? a.NR : 32;
   const int row0 = pre ? grp_z * a.NR : grp_z * a.G;
   const int rows = pre ? min(NR, a.B * a.G - row0) : a.G;
@@ -341,7 +361,13 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     return ok;
   };
 
-  if (tid == 0) {
+  // ---- before the CTA's first barrier: each role's own preparations
+  if (warp == kSoftWarps) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(su32(&tmem_base)),
+                 "r"(tcols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+  } else if (tid == 32 * (kSoftWarps + 1)) {
     s_abort = 0;
     s_late = 0;
     constexpr int kSide = C::SIDE / 32;   // decoder warps that fill one side
@@ -362,50 +388,47 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
       bar_init(vfree + 8 * i, 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
-  }
-  if (warp == kSoftWarps) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(su32(&tmem_base)),
-                 "r"(tcols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
-  }
-  if (tid < NR) {
+  } else if (tid < NR) {
+    const int r = row0 + tid;
     s_m[tid] = -INFINITY;
     s_l[tid] = 0.f;
+    s_dst[tid] = (((int64_t)(r >> a.lg) * a.Hq + kvh * a.G + (r & (a.G - 1))) * a.slots + slot) * (D + 4);
   }
-  fence_before();
-  __syncthreads();
-  fence_after();
-  const uint32_t tmem = tmem_base;
+  uint32_t tmem;
+  auto begin = [&]() {   // every warp, once
+    fence_before();
+    asm volatile("bar.sync 0;\n" ::: "memory");
+    fence_after();
+    tmem = tmem_base;
+  };
 
   // Q^ = H D q per K block, times softmax_scale * log2 e, by the softmax and
   // decoder warps (w of 24): a warp per row, a lane the D/32 consecutive
   // values from E*lane on, the next row's load in flight.  Loops are kept
   // rolled: a CTA runs this once, and straight-line code would be fetched
   // from a cold cache.
-  auto rotate_queries = [&](int w) {
-    constexpr int E = D / 32, QW = kSoftWarps + kDecWarps;
+  constexpr int E = D / 32, QW = kSoftWarps + kDecWarps;
+  uint32_t next[E / 2];
+  auto fetch_query = [&](int r) {
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) next[e] = 0u;
+    if (r < rows) {
+      const int rr = row0 + r, b = rr >> a.lg, h = kvh * a.G + (rr & (a.G - 1));
+      const uint16_t* qr = a.q + ((int64_t)b * a.Hq + h) * D + E * lane;
+      if constexpr (E == 8) {
+        const uint4 q = *reinterpret_cast<const uint4*>(qr);
+        next[0] = q.x; next[1] = q.y; next[2] = q.z; next[3] = q.w;
+      } else if constexpr (E == 4) {
+        const uint2 q = *reinterpret_cast<const uint2*>(qr);
+        next[0] = q.x; next[1] = q.y;
+      } else {
+        next[0] = *reinterpret_cast<const uint32_t*>(qr);
+      }
+    }
+  };
+  auto rotate_queries = [&](int w) {   // after fetch_query(w)
     const float qn = PK.inv_sqrt_blk * a.qscale;
     const uint32_t sb = PK.sign_bits[E * lane >> 5] >> (E * lane & 31);
-    uint32_t next[E / 2];
-    auto fetch = [&](int r) {
-#pragma unroll
-      for (int e = 0; e < E / 2; ++e) next[e] = 0u;
-      if (r < rows) {
-        const int rr = row0 + r, b = rr >> a.lg, h = kvh * a.G + (rr & (a.G - 1));
-        const uint16_t* qr = a.q + ((int64_t)b * a.Hq + h) * D + E * lane;
-        if constexpr (E == 8) {
-          const uint4 q = *reinterpret_cast<const uint4*>(qr);
-          next[0] = q.x; next[1] = q.y; next[2] = q.z; next[3] = q.w;
-        } else if constexpr (E == 4) {
-          const uint2 q = *reinterpret_cast<const uint2*>(qr);
-          next[0] = q.x; next[1] = q.y;
-        } else {
-          next[0] = *reinterpret_cast<const uint32_t*>(qr);
-        }
-      }
-    };
-    fetch(w);
 #pragma unroll 1
     for (int r = w; r < NR; r += QW) {
       float v[E];
@@ -414,7 +437,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&next[e / 2]));
         v[e] = flip((e & 1 ? f.y : f.x) * qn, (sb >> e) & 1u);
       }
-      fetch(r + QW);
+      fetch_query(r + QW);
 #pragma unroll
       for (int hs = 1; hs < E; hs <<= 1) {   // blocks are 32 values at least
 #pragma unroll
@@ -454,7 +477,9 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
   if (warp >= kDec0 / 32) {
     // ================= decoders
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::OTHER));
-    if (n_tiles > 0) {
+    if (n_tiles == 0) {
+      begin();
+    } else {
       const int dt = tid - kDec0;
       const int st = C::SPLIT ? dt % C::SIDE : dt;    // thread within its side
       const bool do_k = !C::SPLIT || dt < C::SIDE, do_v = !C::SPLIT || dt >= C::SIDE;
@@ -476,8 +501,8 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
       const uint8_t *kc = src.kc + rec0 * kwb + kw0, *ks = src.ks + rec0 * knb + kn0;
       const uint8_t *vc = src.vc + rec0 * vwb + vw0, *vs = src.vs + rec0 * vnb + vn0;
       const int32_t* table = paged ? src.pages.table + (int64_t)seq * src.pages.pages_per_seq : nullptr;
-      const int psize = src.pages.page_size;
-      const int last_page = paged ? (int)((t_lo + n_tok - 1) / psize) : 0;
+      const uint32_t psize = src.pages.page_size;
+      const int last_page = paged ? ((uint32_t)t_lo + n_tok - 1) / psize : 0;
       // record (contiguous: token) of each group in the tile to be loaded; a
       // token past the slice takes the last one's place (paged: some record
       // of the last page), and its values are not used
@@ -485,9 +510,9 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
       int64_t rec[C::N];
 #pragma unroll
       for (int k = 0; k < C::N; ++k) {
-        const int64_t t = t_lo + tok0 + k * kStep;
-        page[k] = paged ? (int)(t / psize) : 0;
-        off[k] = paged ? (int)(t - (int64_t)page[k] * psize) : 0;
+        const uint32_t t = (uint32_t)t_lo + tok0 + k * kStep;
+        page[k] = paged ? t / psize : 0;
+        off[k] = paged ? t - page[k] * psize : 0;
       }
       auto place = [&](int at) {   // the records of the tile `at` tokens into the slice
 #pragma unroll
@@ -495,7 +520,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
           if (paged) {
             rec[k] = ((int64_t)table[min(page[k], last_page)] * a.Hkv + kvh) * psize + off[k];
             off[k] += kTile;
-            while (off[k] >= psize) {
+            while ((uint32_t)off[k] >= psize) {
               off[k] -= psize;
               ++page[k];
             }
@@ -516,6 +541,8 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
       place(0);
       load_k();
       load_v();
+      fetch_query(warp - kDec0 / 32 + kSoftWarps);
+      begin();
       rotate_queries(warp - kDec0 / 32 + kSoftWarps);
       for (int t = 0; t < n_tiles; ++t) {
         const int vb = t % NV, at = t * kTile;
@@ -551,6 +578,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
   } else if (warp == kSoftWarps) {
     // ================= S^T(t) = K^(t) Q^
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::OTHER));
+    begin();
     const uint32_t idesc = (1u << 4) | ((uint32_t)(NR >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
     const uint64_t dq = sdesc(aQ, 128, kKGroup), dk = sdesc(aK, 128, kKGroup);
     bool ok = n_tiles > 0 && wait(q_full, 0);
@@ -570,6 +598,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
   } else if (warp == kSoftWarps + 1) {
     // ================= O^T += V^(t)^T P(t)^T
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::OTHER));
+    begin();
     const uint32_t idesc = (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(NR >> 3) << 17) |
                            ((uint32_t)(128 >> 4) << 24);
     const uint32_t pg = (uint32_t)(NR >> 3) * 128;   // bytes of 8 tokens of P
@@ -596,6 +625,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
   } else if (warp >= kSoftWarps) {
     // ================= l += ones P(t)^T: rows [0, NR/2) or the rest, 8 at a time
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::OTHER));
+    begin();
     const int nc = NR / 2, col0 = (warp - kSoftWarps - 2) * nc;
     // lane i's row of the four 8 x 8 matrices of 32 tokens: token i, 8 rows
     const uint32_t row = cm_off(lane, col0, NR);
@@ -631,6 +661,8 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
   } else {
     // ================= softmax: thread = token (TMEM lane) x half of the rows
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(C::SOFT));
+    if (n_tiles > 0) fetch_query(warp);
+    begin();
     if (n_tiles > 0) rotate_queries(warp);
     const int quarter = warp & 3, half = warp >> 2, bid = 1 + half;
     const int nc = NR / 2, col0 = half * nc;
@@ -676,11 +708,26 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
       if (t >= 2) wait(o_done + 8 * (t & 1), (uint32_t)((t >> 1) - 1) & 1);   // P(t - 2) has been read
       fence_after();
       __syncwarp();
-      bool moved = t == 0;
-      if (!moved) moved = half_any(bid, emit());
-      if (moved) {
-        // some row's reference moves (the first tile sets them): its maximum
-        // over the tile, O and l scaled, P written again
+      if (t == 0) {
+        // the first references: a row's largest score over 32 tokens, each
+        // quarter's tokens for a quarter of the rows
+        for (int c = 4 * quarter; c < nc; c += 16) {
+          uint32_t v[4];
+          TQ_LD4(sS + c, v);
+          ld_wait();
+          float mine = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float x = warp_max_f(live ? __uint_as_float(v[j]) : -INFINITY);
+            if (lane == j) mine = x;
+          }
+          if (lane < 4) s_m[col0 + c + lane] = mine;
+        }
+        half_sync(bid);
+      }
+      if (half_any(bid, emit())) {
+        // some row's reference moves: its maximum over the tile, O and l
+        // scaled, P written again
         if (t >= 1) {
           wait(o_done + 8 * ((t - 1) & 1), (uint32_t)((t - 1) >> 1) & 1);   // O and l stand still
           fence_after();
@@ -747,35 +794,24 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
   if (warp < 24) {
     const int quarter = warp & 3;
     const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
-    const int64_t rstep = (int64_t)a.slots * (D + 4);
     for (int w = warp >> 2; w < OT * (NR / 16); w += 6) {
-      const int m = w % OT, c = w / OT * 16;
+      const int m = OT > 1 ? w % OT : 0, c = w / OT * 16;
       uint32_t v[16];
       if (ok) {
         TQ_LD16(lanes + cO + m * NR + c, v);
         ld_wait();
       }
       const int dim = 128 * m + 32 * quarter + lane;
-      int hh = (row0 + c) & (a.G - 1);
-      float* dst = a.part + ((int64_t)((row0 + c) >> a.lg) * a.Hq + kvh * a.G + hh) * rstep + (int64_t)slot * (D + 4);
+      float* base = a.part + 2 + dim;
+      if (dim < D) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        if (c + j < rows) {
-          if (dim < D) dst[2 + dim] = ok ? __uint_as_float(v[j]) : 0.f;
-          if (m == 0 && quarter == 0 && lane == j) {
-            const int r = c + j;
-            dst[0] = ok ? s_m[r] : -INFINITY;
-            dst[1] = ok ? s_l[r] : 0.f;
-          }
-        }
-        ++hh;
-        dst += rstep;
-        if (hh == a.G) {   // the next sequence's first head
-          hh = 0;
-          dst += (int64_t)(a.Hq - a.G) * rstep;
-        }
+        for (int j = 0; j < 16; ++j)
+          if (c + j < rows) base[s_dst[c + j]] = ok ? __uint_as_float(v[j]) : 0.f;
       }
     }
+  } else {
+    for (int r = tid - 24 * 32; r < rows; r += kThreadsSh - 24 * 32)
+      *reinterpret_cast<float2*>(a.part + s_dst[r]) = make_float2(ok ? s_m[r] : -INFINITY, ok ? s_l[r] : 0.f);
   }
   fence_before();
   __syncthreads();
@@ -840,6 +876,9 @@ Source source_of(const tq_kv_view* K, const tq_kv_view* V, const int32_t* len, i
   const int64_t tiles = (ctx + kTile - 1) / kTile;
   s.per = (tiles + splits - 1) / splits * kTile;
   s.splits = splits;
+  const FastDiv f = fast_div((uint32_t)splits);
+  s.div_mul = f.mul;
+  s.div_shift = f.shift;
   s.slot0 = slot0;
   return s;
 }
@@ -888,13 +927,15 @@ int launch_shared_tc(const CodecParams& PK, const CodecParams& PV, const tq_kv_v
   a.B = B;
   a.Hq = Hq;
   a.Hkv = Hkv;
+  a.by_heads = fast_div((uint32_t)Hkv);
   a.G = Hq / Hkv;
   while ((1 << a.lg) < a.G) ++a.lg;
   a.slots = n_own + n_prefix;
   a.qscale = qscale;
   shared_rows(PK.d, (int64_t)B * a.G, &a.row_tiles, &a.NR);
   const int64_t n_pre = (int64_t)n_prefix * Hkv * a.row_tiles, all = n_pre + (int64_t)n_own * Hkv * B;
-  if (all > 0x7fffffff) return TQ_ERR_UNSUPPORTED;
+  // 32-bit units and token numbers
+  if (all > 0x7fffffff || prefix_ctx > 0x7fffff00 || ctx > 0x7fffff00) return TQ_ERR_UNSUPPORTED;
   a.n_pre = (int)n_pre;
   switch (PK.d) {
     case 64: return launch_shared<64>(PK, PV, a, (unsigned)all, st);
