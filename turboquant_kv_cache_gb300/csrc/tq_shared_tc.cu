@@ -249,6 +249,13 @@ __device__ __forceinline__ void load_group_g(const uint8_t* c8, int next, const 
   asm volatile("ld.global.nc.u16 %0, [%1];" : "=r"(g.sc) : "l"(s));
 }
 
+// Keeps what is computed from a group behind this point: otherwise the first
+// steps of its decode are scheduled right after its loads, a tile too early,
+// and wait for them there.
+__device__ __forceinline__ void pin(Group& g) {
+  asm volatile("" : "+r"(g.w[0]), "+r"(g.w[1]), "+r"(g.w[2]), "+r"(g.w[3]), "+r"(g.sc));
+}
+
 // Four fp16x2 registers of a nibble word of 4-bit codes.  The codebook is
 // symmetric, c(15 - k) = -c(k): the upper eight levels in the byte tables, a
 // lower code looked up as 15 - k and its sign bit set in the high byte.
@@ -267,40 +274,45 @@ __device__ __forceinline__ void lut8_sym(uint32_t n, const Tab& T, uint32_t* o) 
   }
 }
 
-// One group's 32 values (centroid * norm, fp16) to the core-matrix tile: four
-// 16-byte chunks, one per core matrix.  Each (token, block) table holds the
-// fp32 products of centroids and norm, rounded once to fp16.
-template <int BITS>
-__device__ __forceinline__ void decode_group_b(const Group& g, bool shifted, const float* cent, uint32_t dst) {
-  uint32_t n[4];
-  if (BITS & 1) {
-    const uint32_t w3[3] = {shifted ? g.w[1] : g.w[0], shifted ? g.w[2] : g.w[1], shifted ? g.w[3] : g.w[2]};
-    chunk_words<BITS>(w3, n);
-  } else {
-    chunk_words<BITS>(g.w, n);
-  }
-  const Tab T = make_tab_f32<BITS == 4 ? 3 : BITS>(BITS == 4 ? cent + 8 : cent, h2f((uint16_t)g.sc));
+// A thread's N groups, 32 values each (centroid * norm, fp16), to the
+// core-matrix tile: four 16-byte chunks, one per core matrix.  Each (token,
+// block) table holds the fp32 products of centroids and norm, rounded once to
+// fp16.  A token past the slice (not live) takes norm 0: zero rows, since 0 * p
+// must be 0.  One branch on the bit width around all groups, so that their
+// instructions interleave.
+template <int BITS, int N>
+__device__ __forceinline__ void decode_groups_b(const Group* g, bool shifted, const float* cent, const bool* live,
+                                                uint32_t dst, uint32_t step) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    uint32_t o[4];
-    if (BITS == 4) lut8_sym(n[c], T, o);
-    else lut8<BITS>(n[c], T, o);
-    sts16b(dst + 128 * c, o[0], o[1], o[2], o[3]);
+  for (int k = 0; k < N; ++k) {
+    uint32_t n[4];
+    if (BITS & 1) {
+      const uint32_t w3[3] = {shifted ? g[k].w[1] : g[k].w[0], shifted ? g[k].w[2] : g[k].w[1],
+                              shifted ? g[k].w[3] : g[k].w[2]};
+      chunk_words<BITS>(w3, n);
+    } else {
+      chunk_words<BITS>(g[k].w, n);
+    }
+    const float norm = live[k] ? h2f((uint16_t)g[k].sc) : 0.f;
+    const Tab T = make_tab_f32<BITS == 4 ? 3 : BITS>(BITS == 4 ? cent + 8 : cent, norm);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t o[4];
+      if (BITS == 4) lut8_sym(n[c], T, o);
+      else lut8<BITS>(n[c], T, o);
+      sts16b(dst + k * step + 128 * c, o[0], o[1], o[2], o[3]);
+    }
   }
 }
 
-__device__ __forceinline__ void decode_group(int bits, const Group& g, bool odd, const float* cent, bool live,
-                                             uint32_t dst) {
-  if (!live) {   // past the slice: zero rows (their p is zero too, but 0 * NaN is not)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) sts16b(dst + 128 * c, 0u, 0u, 0u, 0u);
-    return;
-  }
+template <int N>
+__device__ __forceinline__ void decode_groups(int bits, const Group* g, bool odd, const float* cent, const bool* live,
+                                              uint32_t dst, uint32_t step) {
   switch (bits) {
-    case 4: decode_group_b<4>(g, odd, cent, dst); break;
-    case 3: decode_group_b<3>(g, odd, cent, dst); break;
-    case 2: decode_group_b<2>(g, odd, cent, dst); break;
-    default: decode_group_b<1>(g, odd, cent, dst); break;
+    case 4: decode_groups_b<4, N>(g, odd, cent, live, dst, step); break;
+    case 3: decode_groups_b<3, N>(g, odd, cent, live, dst, step); break;
+    case 2: decode_groups_b<2, N>(g, odd, cent, live, dst, step); break;
+    default: decode_groups_b<1, N>(g, odd, cent, live, dst, step); break;
   }
 }
 
@@ -538,23 +550,25 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
 #pragma unroll
         for (int k = 0; k < C::N; ++k) load_group_g(vc + rec[k] * vwb, vnext, vs + rec[k] * vnb, gv[k]);
       };
+      fetch_query(warp - kDec0 / 32 + kSoftWarps);
       place(0);
       load_k();
       load_v();
-      fetch_query(warp - kDec0 / 32 + kSoftWarps);
       begin();
       rotate_queries(warp - kDec0 / 32 + kSoftWarps);
       for (int t = 0; t < n_tiles; ++t) {
         const int vb = t % NV, at = t * kTile;
+        bool live[C::N];
+#pragma unroll
+        for (int k = 0; k < C::N; ++k) live[k] = at + tok0 + k * kStep < n_tok;
         place(at + kTile);
         if (do_k) {
           if (t >= 1) wait(kfree, (uint32_t)(t - 1) & 1);
-          if (!s_abort) {
 #pragma unroll
-            for (int k = 0; k < C::N; ++k)
-              decode_group(kbits, gk[k], odd, PK.centroids, at + tok0 + k * kStep < n_tok,
-                           aK + cm_off(tok0 + k * kStep, 32 * grp, D));
-          }
+          for (int k = 0; k < C::N; ++k) pin(gk[k]);
+          if (!s_abort)
+            decode_groups<C::N>(kbits, gk, odd, PK.centroids, live, aK + cm_off(tok0, 32 * grp, D),
+                                cm_off(kStep, 0, D));
           fence_async_smem();
           __syncwarp();
           if (lane == 0) arrive(kfull);
@@ -562,12 +576,11 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
         }
         if (do_v) {
           if (t >= NV) wait(vfree + 8 * vb, (uint32_t)(t / NV - 1) & 1);
-          if (!s_abort) {
 #pragma unroll
-            for (int k = 0; k < C::N; ++k)
-              decode_group(vbits, gv[k], odd, PV.centroids, at + tok0 + k * kStep < n_tok,
-                           aV + vb * C::VB + cm_off(tok0 + k * kStep, 32 * grp, C::DV));
-          }
+          for (int k = 0; k < C::N; ++k) pin(gv[k]);
+          if (!s_abort)
+            decode_groups<C::N>(vbits, gv, odd, PV.centroids, live, aV + vb * C::VB + cm_off(tok0, 32 * grp, C::DV),
+                                cm_off(kStep, 0, C::DV));
           fence_async_smem();
           __syncwarp();
           if (lane == 0) arrive(vfull + 8 * vb);
