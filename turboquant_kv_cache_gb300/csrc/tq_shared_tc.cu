@@ -32,7 +32,9 @@
 // tile, its packed words loaded a tile ahead; at head_dim 64 half of the
 // decoder warps take K, half V.  Handoffs are mbarriers:
 //   q_full        Q^ is written
-//   kfull/kfree   K^(t) is decoded / S(t) is done with it (one buffer)
+//   kfull/kfree[b] K^(t) is decoded / S(t) is done with it (two buffers; one
+//                 where a CTA of head_dim 256 has more than 32 rows: with one,
+//                 decode and S take turns)
 //   vfull/vfree[b] the same for V and O (two buffers; one at head_dim 256)
 //   s_full[i]     S(t), t & 1 = i, is in TMEM    s_free[i] it has been read
 //   p_full[i]     P(t) is written                o_done[i] O += V(t) P(t) and l are done
@@ -72,7 +74,8 @@ __device__ int g_shared_status;
 
 template <int D>
 struct ShCfg {
-  static constexpr int NV = D == 256 ? 1 : 2;          // buffers of V (one of K)
+  static constexpr int NV = D == 256 ? 1 : 2;          // buffers of V
+  __host__ __device__ static constexpr int nk(int NR) { return D == 256 && NR > 32 ? 1 : 2; }   // buffers of K
   static constexpr int DV = D < 128 ? 128 : D;         // V tile width: whole M tiles of 128
   static constexpr int OT = DV / 128;                  // M tiles of O^T
   static constexpr int MAXR = D == 256 ? 64 : 128;     // rows of a CTA, by shared memory and registers
@@ -324,13 +327,12 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
   constexpr uint32_t kKGroup = (D / 8) * 128;       // bytes of 8 tokens of K, 8 rows of Q
   constexpr uint32_t kVGroup = (C::DV / 8) * 128;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t bars[2 * NV + 12];
+  __shared__ __align__(8) uint64_t bars[2 * NV + 14];
   __shared__ uint32_t tmem_base;
   __shared__ volatile int s_abort;
   __shared__ int s_late;
   __shared__ __align__(16) float s_m[C::MAXR];      // the rows' softmax references
   __shared__ float s_al[C::MAXR];
-  __shared__ float s_wm[4][C::MAXR];                // maxima by TMEM lane quarter (rare path)
   __shared__ int64_t s_dst[C::MAXR];                // where the rows' partials go
   __shared__ __align__(8) float s_l[C::MAXR];                    // the rows' sums of p
 
@@ -355,11 +357,12 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
   const int n_tiles = (n_tok + kTile - 1) / kTile;
 
   // K, V buffers, Q^, two P buffers
+  const int nk = C::nk(NR);
   const uint32_t pbytes = (uint32_t)NR * kTile * 2;
-  const uint32_t aK = su32(smem), aV = aK + C::KB, aQ = aV + NV * C::VB, aP = aQ + (uint32_t)NR * D * 2;
+  const uint32_t aK = su32(smem), aV = aK + nk * C::KB, aQ = aV + NV * C::VB, aP = aQ + (uint32_t)NR * D * 2;
   const uint32_t b0 = su32(&bars[0]);
-  const uint32_t q_full = b0, kfull = b0 + 8, kfree = b0 + 16, s_full = b0 + 24, s_free = b0 + 40, p_full = b0 + 56,
-                 o_done = b0 + 72, drained = b0 + 88, vfull = b0 + 96, vfree = vfull + 8 * NV;
+  const uint32_t q_full = b0, kfull = b0 + 8, kfree = b0 + 24, s_full = b0 + 40, s_free = b0 + 56, p_full = b0 + 72,
+                 o_done = b0 + 88, drained = b0 + 104, vfull = b0 + 112, vfree = vfull + 8 * NV;
   // TMEM columns: S twice, then O
   const uint32_t cO = 2u * NR;
   const uint32_t tused = cO + (uint32_t)OT * NR;
@@ -384,10 +387,10 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     s_late = 0;
     constexpr int kSide = C::SIDE / 32;   // decoder warps that fill one side
     bar_init(q_full, kSoftWarps + kDecWarps);
-    bar_init(kfull, kSide);
-    bar_init(kfree, 1);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      bar_init(kfull + 8 * i, kSide);
+      bar_init(kfree + 8 * i, 1);
       bar_init(s_full + 8 * i, 1);
       bar_init(s_free + 8 * i, kSoftWarps);
       bar_init(p_full + 8 * i, kSoftWarps);
@@ -519,7 +522,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
       // token past the slice takes the last one's place (paged: some record
       // of the last page), and its values are not used
       int32_t page[C::N], off[C::N];
-      int64_t rec[C::N];
+      int64_t rec[C::N], recv[C::N];   // of the next K and the next V loads
 #pragma unroll
       for (int k = 0; k < C::N; ++k) {
         const uint32_t t = (uint32_t)t_lo + tok0 + k * kStep;
@@ -548,33 +551,51 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
       };
       auto load_v = [&]() {
 #pragma unroll
-        for (int k = 0; k < C::N; ++k) load_group_g(vc + rec[k] * vwb, vnext, vs + rec[k] * vnb, gv[k]);
+        for (int k = 0; k < C::N; ++k) load_group_g(vc + recv[k] * vwb, vnext, vs + recv[k] * vnb, gv[k]);
       };
       fetch_query(warp - kDec0 / 32 + kSoftWarps);
+      auto next_place = [&](int at) {
+#pragma unroll
+        for (int k = 0; k < C::N; ++k) recv[k] = rec[k];
+        place(at);
+      };
       place(0);
       load_k();
+      next_place(kTile);
       load_v();
       begin();
       rotate_queries(warp - kDec0 / 32 + kSoftWarps);
-      for (int t = 0; t < n_tiles; ++t) {
-        const int vb = t % NV, at = t * kTile;
-        bool live[C::N];
+      auto live_at = [&](int at, bool* live) {
 #pragma unroll
         for (int k = 0; k < C::N; ++k) live[k] = at + tok0 + k * kStep < n_tok;
-        place(at + kTile);
-        if (do_k) {
-          if (t >= 1) wait(kfree, (uint32_t)(t - 1) & 1);
+      };
+      auto do_tile_k = [&](int t) {
+        const int kb = nk == 2 ? t & 1 : 0;
+        bool live[C::N];
+        live_at(t * kTile, live);
+        if (t >= nk) wait(kfree + 8 * kb, (uint32_t)((nk == 2 ? t >> 1 : t) - 1) & 1);
 #pragma unroll
-          for (int k = 0; k < C::N; ++k) pin(gk[k]);
-          if (!s_abort)
-            decode_groups<C::N>(kbits, gk, odd, PK.centroids, live, aK + cm_off(tok0, 32 * grp, D),
-                                cm_off(kStep, 0, D));
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) arrive(kfull);
-          load_k();
+        for (int k = 0; k < C::N; ++k) pin(gk[k]);
+        if (!s_abort)
+          decode_groups<C::N>(kbits, gk, odd, PK.centroids, live, aK + kb * C::KB + cm_off(tok0, 32 * grp, D),
+                              cm_off(kStep, 0, D));
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive(kfull + 8 * kb);
+        load_k();
+      };
+      // K runs a tile ahead of V: V(t) waits for O(t - NV), and what the
+      // softmax of the next tile needs must not queue behind that
+      if (do_k) do_tile_k(0);
+      for (int t = 0; t < n_tiles; ++t) {
+        if (t + 1 < n_tiles) {
+          next_place((t + 2) * kTile);
+          if (do_k) do_tile_k(t + 1);
         }
         if (do_v) {
+          const int vb = t % NV;
+          bool live[C::N];
+          live_at(t * kTile, live);
           if (t >= NV) wait(vfree + 8 * vb, (uint32_t)(t / NV - 1) & 1);
 #pragma unroll
           for (int k = 0; k < C::N; ++k) pin(gv[k]);
@@ -593,18 +614,20 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::OTHER));
     begin();
     const uint32_t idesc = (1u << 4) | ((uint32_t)(NR >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
-    const uint64_t dq = sdesc(aQ, 128, kKGroup), dk = sdesc(aK, 128, kKGroup);
+    const uint64_t dq = sdesc(aQ, 128, kKGroup);
     bool ok = n_tiles > 0 && wait(q_full, 0);
     for (int t = 0; t < n_tiles && ok; ++t) {
-      ok = wait(kfull, (uint32_t)t & 1) && (t < 2 || wait(s_free + 8 * (t & 1), (uint32_t)((t >> 1) - 1) & 1));
+      const int kb = nk == 2 ? t & 1 : 0;
+      ok = wait(kfull + 8 * kb, (uint32_t)(nk == 2 ? t >> 1 : t) & 1) && (t < 2 || wait(s_free + 8 * (t & 1), (uint32_t)((t >> 1) - 1) & 1));
       if (!ok) break;
       fence_after();
       __syncwarp();
+      const uint64_t dk = sdesc(aK + kb * C::KB, 128, kKGroup);
 #pragma unroll
       for (int s = 0; s < D / 16; ++s)
         mma_ss_elect(tmem + (t & 1) * NR, dk + (uint64_t)(16 * s), dq + (uint64_t)(16 * s), idesc, s > 0);
       commit_elect(s_full + 8 * (t & 1));
-      commit_elect(kfree);
+      commit_elect(kfree + 8 * kb);
     }
     __syncwarp();
     commit_elect(drained);
@@ -746,6 +769,9 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
           fence_after();
         }
         __syncwarp();
+        // the maxima by TMEM lane quarter, in this half's part of the first
+        // eight tokens of P(t), which is written again below
+        float* wm = reinterpret_cast<float*>(smem + (aP - aK) + (t & 1) * pbytes + (col0 >> 3) * 128);
         for (int c = 0; c < nc; c += 16) {
           uint32_t v[16];
           TQ_LD16(sS + c, v);
@@ -756,12 +782,12 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
             const float x = warp_max_f(live ? __uint_as_float(v[j]) : -INFINITY);
             if (lane == j) mine = x;
           }
-          if (lane < 16) s_wm[quarter][col0 + c + lane] = mine;
+          if (lane < 16) wm[quarter * nc + c + lane] = mine;
         }
         half_sync(bid);
         if ((tid & 127) < nc) {
-          const int r = col0 + (tid & 127);
-          const float x = fmaxf(fmaxf(s_wm[0][r], s_wm[1][r]), fmaxf(s_wm[2][r], s_wm[3][r]));
+          const int i = tid & 127, r = col0 + i;
+          const float x = fmaxf(fmaxf(wm[i], wm[nc + i]), fmaxf(wm[2 * nc + i], wm[3 * nc + i]));
           const float mo = s_m[r], mn = x > mo + kLazySh || mo == -INFINITY ? x : mo;
           const float al = mo == -INFINITY ? 0.f : ex2s(mo - mn);
           s_m[r] = mn;
@@ -845,12 +871,14 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
 template <int D>
 size_t shared_smem(int NR) {
   using C = ShCfg<D>;
-  return (size_t)C::KB + (size_t)C::NV * C::VB + (size_t)NR * D * 2 + (size_t)2 * NR * kTile * 2;
+  return (size_t)C::nk(NR) * C::KB + (size_t)C::NV * C::VB + (size_t)NR * D * 2 + (size_t)2 * NR * kTile * 2;
 }
 
 template <int D>
 int launch_shared(const CodecParams& PK, const CodecParams& PV, const SharedArgs& a, unsigned grid, cudaStream_t st) {
-  const size_t sm = shared_smem<D>(a.n_pre ? a.NR : 32);
+  // the own tokens' CTAs have 32 rows
+  size_t sm = a.n_pre ? shared_smem<D>(a.NR) : 0;
+  if (a.own.splits && shared_smem<D>(32) > sm) sm = shared_smem<D>(32);
   auto kern = shared_prefix_kernel<D>;
   // once per device; a build with fewer registers than the split shares out
   // would wait for them without end, so it is refused
@@ -858,8 +886,10 @@ int launch_shared(const CodecParams& PK, const CodecParams& PV, const SharedArgs
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return TQ_ERR_CUDA;
   if (!ready[dev].load(std::memory_order_acquire)) {
+    size_t most = 0;
+    for (int r = 32; r <= ShCfg<D>::MAXR; r += 32) most = shared_smem<D>(r) > most ? shared_smem<D>(r) : most;
     cudaFuncAttributes fa;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared_smem<D>(ShCfg<D>::MAXR)) ||
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) ||
         cudaFuncGetAttributes(&fa, kern) || fa.numRegs < kLaunchRegs)
       return TQ_ERR_CUDA;
     ready[dev].store(true, std::memory_order_release);
