@@ -141,6 +141,23 @@ def test_own_split_counts(tqlib, n_split):
     assert (out.double() - ref).abs().max().item() < ATTN_ATOL
 
 
+@pytest.mark.parametrize("d,kbits,vbits,block", [(64, 4, 4, 64), (64, 1, 2, 32), (128, 3, 3, 32), (128, 4, 1, 128),
+                                                 (256, 4, 3, 32), (256, 2, 4, 256)])
+@pytest.mark.parametrize("ctx", [383, 385, 512, 513, 640, 641, 767, 1408])
+def test_slices_of_many_tiles(tqlib, d, kbits, vbits, block, ctx):
+    """Own tokens and prefix in one part each, over tile counts from three up,
+    and the same output again."""
+    from turboquant_kv_cache_gb300 import binding as tb
+    Kp, Vp, K, V, q = _inputs(tb, d, (block, kbits, 0, 0), (block, vbits, 0, 0), 40, 8, 2, 1409, 1409, seed=51)
+    one = tb.tq_decode_attn_shared(Kp, Vp, K, V, q, prefix_ctx=0, ctx=ctx, n_split=1)
+    two = tb.tq_decode_attn_shared(Kp, Vp, K, V, q, prefix_ctx=0, ctx=ctx, n_split=1)
+    assert torch.equal(one, two)
+    pick = [0, 17, 39]   # sequences checked
+    ref = _reference(tb, Kp, Vp, 0, *(tb.PackedKV.of(c.layout, c.codes[pick], c.scales[pick]) for c in (K, V)),
+                     [ctx] * 3, q[pick])
+    assert (one[pick].double() - ref).abs().max().item() < ATTN_ATOL
+
+
 def test_oracle_bytes(tqlib):
     """The oracle's own packed bytes and its decoded vectors."""
     from turboquant_kv_cache_gb300 import binding as tb

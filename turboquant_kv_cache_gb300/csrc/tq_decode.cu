@@ -1001,7 +1001,8 @@ int check_cache_pair(const tq_kv_view* K, const tq_kv_view* V, const CodecParams
   if (PK.m && (!K->qjl_bits || !K->qjl_rnorm || !K->S)) return TQ_ERR_ARG;
   if (PV.m && (!V->qjl_bits || !V->qjl_rnorm || !V->S)) return TQ_ERR_ARG;
   if (check_paging(K, S_cap) != TQ_OK || !same_paging(K, V)) return TQ_ERR_ARG;
-  return aligned16(K->codes) && aligned16(V->codes) ? TQ_OK : TQ_ERR_ALIGN;
+  return aligned16(K->codes) && aligned16(V->codes) && aligned16(K->scales) && aligned16(V->scales) ? TQ_OK
+                                                                                                   : TQ_ERR_ALIGN;
 }
 
 bool same_layout(const tq_layout& a, const tq_layout& b) {

@@ -32,9 +32,7 @@
 // tile, its packed words loaded a tile ahead; at head_dim 64 half of the
 // decoder warps take K, half V.  Handoffs are mbarriers:
 //   q_full        Q^ is written
-//   kfull/kfree[b] K^(t) is decoded / S(t) is done with it (two buffers; one
-//                 where a CTA of head_dim 256 has more than 32 rows: with one,
-//                 decode and S take turns)
+//   kfull/kfree   K^(t) is decoded / S(t) is done with it (one buffer)
 //   vfull/vfree[b] the same for V and O (two buffers; one at head_dim 256)
 //   s_full[i]     S(t), t & 1 = i, is in TMEM    s_free[i] it has been read
 //   p_full[i]     P(t) is written                o_done[i] O += V(t) P(t) and l are done
@@ -74,8 +72,9 @@ __device__ int g_shared_status;
 
 template <int D>
 struct ShCfg {
-  static constexpr int NV = D == 256 ? 1 : 2;          // buffers of V
-  __host__ __device__ static constexpr int nk(int NR) { return D == 256 && NR > 32 ? 1 : 2; }   // buffers of K
+  static constexpr int NV = D == 256 ? 1 : 2;          // buffers of V (one of K)
+  // buffers of P: two, one where shared memory holds no more
+  __host__ __device__ static constexpr int np(int NR) { return D == 256 && NR > 32 ? 1 : 2; }
   static constexpr int DV = D < 128 ? 128 : D;         // V tile width: whole M tiles of 128
   static constexpr int OT = DV / 128;                  // M tiles of O^T
   static constexpr int MAXR = D == 256 ? 64 : 128;     // rows of a CTA, by shared memory and registers
@@ -102,7 +101,7 @@ struct Source {
   PageMap pages;
   int64_t S_cap, ctx;
   int64_t per;                 // tokens per split (multiple of kTile)
-  int splits, slot0;
+  int splits, slot0, seqs;     // seqs: sequences of the cache
   uint32_t div_mul, div_shift;   // unit / splits (FastDiv)
 };
 
@@ -234,29 +233,61 @@ __device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// The packed words and norm of one 32-code group, loaded a tile ahead.
+// The packed words and norm of one 32-code group.
 struct Group {
   uint32_t w[4];
   uint32_t sc;
 };
 
-// A group's packed words as the 8-byte word at or 4 bytes before it and, past
-// two bits, the next one: the same two loads whatever the bit width, with no
-// branch or predicate, so that no load is waited for at a join.  Groups of
-// 4 * bits bytes come in pairs that start on 8 bytes (d / 32 is even), so both
-// words lie in the record.  1 and 3 bits: an odd group starts with the second
-// 4-byte word (`shifted`).
-__device__ __forceinline__ void load_group_g(const uint8_t* c8, int next, const uint8_t* s, Group& g) {
-  asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(g.w[0]), "=r"(g.w[1]) : "l"(c8));
-  asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(g.w[2]), "=r"(g.w[3]) : "l"(c8 + next));
-  asm volatile("ld.global.nc.u16 %0, [%1];" : "=r"(g.sc) : "l"(s));
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+  if (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Keeps what is computed from a group behind this point: otherwise the first
-// steps of its decode are scheduled right after its loads, a tile too early,
-// and wait for them there.
-__device__ __forceinline__ void pin(Group& g) {
-  asm volatile("" : "+r"(g.w[0]), "+r"(g.w[1]), "+r"(g.w[2]), "+r"(g.w[3]), "+r"(g.sc));
+// Copies a group's words to its thread's 16-byte slot.  3 bits: 12 bytes,
+// 8-byte aligned for even groups and 4 bytes past that for odd ones (c is 4
+// bytes before those), so the 16 bytes around them (an even group is never a
+// row's last, so they are inside the row).
+__device__ __forceinline__ void copy_words(int bits, uint32_t dst, const uint8_t* c) {
+  switch (bits) {
+    case 4: cp_async<16>(dst, c); break;
+    case 3:
+      cp_async<8>(dst, c);
+      cp_async<8>(dst + 8, c + 8);
+      break;
+    case 2: cp_async<8>(dst, c); break;
+    default: cp_async<4>(dst, c); break;
+  }
+}
+// Copies the 4-byte word that holds a norm (an array of norms is 4-byte
+// aligned; where its last norm is the first half of a word that the array does
+// not fill, the norm alone, by register).
+__device__ __forceinline__ void copy_norm(uint32_t dst, const uint8_t* s, bool last) {
+  if (!last) {
+    cp_async<4>(dst, reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(s) & ~(uintptr_t)3));
+  } else {
+    const uint32_t v = *reinterpret_cast<const uint16_t*>(s);
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(v) : "memory");
+  }
+}
+// A thread's group from its slots, `shift` 16 where the norm is the word's
+// second half.
+__device__ __forceinline__ Group read_group(uint32_t words, uint32_t norm, uint32_t shift) {
+  Group g;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(g.w[0]), "=r"(g.w[1]), "=r"(g.w[2]), "=r"(g.w[3])
+               : "r"(words)
+               : "memory");
+  g.sc = lds32(norm) >> shift;
+  return g;
 }
 
 // Four fp16x2 registers of a nibble word of 4-bit codes.  The codebook is
@@ -289,7 +320,7 @@ __device__ __forceinline__ void decode_groups_b(const Group* g, bool shifted, co
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     uint32_t n[4];
-    if (BITS & 1) {
+    if (BITS == 3) {
       const uint32_t w3[3] = {shifted ? g[k].w[1] : g[k].w[0], shifted ? g[k].w[2] : g[k].w[1],
                               shifted ? g[k].w[3] : g[k].w[2]};
       chunk_words<BITS>(w3, n);
@@ -327,7 +358,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
   constexpr uint32_t kKGroup = (D / 8) * 128;       // bytes of 8 tokens of K, 8 rows of Q
   constexpr uint32_t kVGroup = (C::DV / 8) * 128;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t bars[2 * NV + 14];
+  __shared__ __align__(8) uint64_t bars[2 * NV + 12];
   __shared__ uint32_t tmem_base;
   __shared__ volatile int s_abort;
   __shared__ int s_late;
@@ -356,13 +387,14 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
   const int n_tok = t_hi > t_lo ? (int)(t_hi - t_lo) : 0;
   const int n_tiles = (n_tok + kTile - 1) / kTile;
 
-  // K, V buffers, Q^, two P buffers
-  const int nk = C::nk(NR);
+  // K, V buffers, Q^, two P buffers, the decoder threads' packed words and norms
+  const int np = C::np(NR);
   const uint32_t pbytes = (uint32_t)NR * kTile * 2;
-  const uint32_t aK = su32(smem), aV = aK + nk * C::KB, aQ = aV + NV * C::VB, aP = aQ + (uint32_t)NR * D * 2;
+  const uint32_t aK = su32(smem), aV = aK + C::KB, aQ = aV + NV * C::VB, aP = aQ + (uint32_t)NR * D * 2,
+                 aW = aP + np * pbytes;
   const uint32_t b0 = su32(&bars[0]);
-  const uint32_t q_full = b0, kfull = b0 + 8, kfree = b0 + 24, s_full = b0 + 40, s_free = b0 + 56, p_full = b0 + 72,
-                 o_done = b0 + 88, drained = b0 + 104, vfull = b0 + 112, vfree = vfull + 8 * NV;
+  const uint32_t q_full = b0, kfull = b0 + 8, kfree = b0 + 16, s_full = b0 + 24, s_free = b0 + 40, p_full = b0 + 56,
+                 o_done = b0 + 72, drained = b0 + 88, vfull = b0 + 96, vfree = vfull + 8 * NV;
   // TMEM columns: S twice, then O
   const uint32_t cO = 2u * NR;
   const uint32_t tused = cO + (uint32_t)OT * NR;
@@ -387,10 +419,10 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     s_late = 0;
     constexpr int kSide = C::SIDE / 32;   // decoder warps that fill one side
     bar_init(q_full, kSoftWarps + kDecWarps);
+    bar_init(kfull, kSide);
+    bar_init(kfree, 1);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      bar_init(kfull + 8 * i, kSide);
-      bar_init(kfree + 8 * i, 1);
       bar_init(s_full + 8 * i, 1);
       bar_init(s_free + 8 * i, kSoftWarps);
       bar_init(p_full + 8 * i, kSoftWarps);
@@ -509,9 +541,8 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
       const int kbits = PK.bits, vbits = PV.bits;
       const bool paged = src.pages.table != nullptr;
       const uint32_t kwb = PK.code_bytes, vwb = PV.code_bytes, knb = 2 * PK.nb, vnb = 2 * PV.nb;
-      const uint32_t kw0 = grp * 4 * kbits - ((kbits & 1) && odd ? 4 : 0), kn0 = 32 * grp / PK.blk * 2;
-      const uint32_t vw0 = grp * 4 * vbits - ((vbits & 1) && odd ? 4 : 0), vn0 = 32 * grp / PV.blk * 2;
-      const int knext = kbits > 2 ? 8 : 0, vnext = vbits > 2 ? 8 : 0;
+      const uint32_t kw0 = grp * 4 * kbits - (kbits == 3 && odd ? 4 : 0), kn0 = 32 * grp / PK.blk * 2;
+      const uint32_t vw0 = grp * 4 * vbits - (vbits == 3 && odd ? 4 : 0), vn0 = 32 * grp / PV.blk * 2;
       const int64_t rec0 = paged ? 0 : ((int64_t)seq * a.Hkv + kvh) * src.S_cap + t_lo;
       const uint8_t *kc = src.kc + rec0 * kwb + kw0, *ks = src.ks + rec0 * knb + kn0;
       const uint8_t *vc = src.vc + rec0 * vwb + vw0, *vs = src.vs + rec0 * vnb + vn0;
@@ -544,14 +575,36 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
           }
         }
       };
-      Group gk[C::N], gv[C::N];
+      // slots: words (16 bytes a group) of K, of V, then norms (4 bytes)
+      constexpr uint32_t kSlots = kTile * C::G8;
+      const uint32_t kslot = aW + 16 * st, vslot = kslot + 16 * kSlots;
+      const uint32_t knslot = aW + 32 * kSlots + 4 * st, vnslot = knslot + 4 * kSlots;
+      // the caches' last record, where its norm does not fill a word: paged
+      // caches and records of two norms always do
+      const int64_t end = (int64_t)src.seqs * a.Hkv * src.S_cap;
+      const bool ragged = !paged && (end & 1);
+      const int64_t last_rec = end - 1 - rec0;
+      const uint32_t kcut = ragged && PK.nb == 1 ? 1 : 0, vcut = ragged && PV.nb == 1 ? 1 : 0;
+      uint32_t kshift[C::N], vshift[C::N];   // of the copies in flight
       auto load_k = [&]() {
 #pragma unroll
-        for (int k = 0; k < C::N; ++k) load_group_g(kc + rec[k] * kwb, knext, ks + rec[k] * knb, gk[k]);
+        for (int k = 0; k < C::N; ++k) {
+          const uint8_t* n = ks + rec[k] * knb;
+          copy_words(kbits, kslot + k * 16 * C::SIDE, kc + rec[k] * kwb);
+          copy_norm(knslot + k * 4 * C::SIDE, n, kcut && rec[k] == last_rec);
+          kshift[k] = (uint32_t)(reinterpret_cast<uintptr_t>(n) & 2) * 8;
+        }
+        cp_commit();
       };
       auto load_v = [&]() {
 #pragma unroll
-        for (int k = 0; k < C::N; ++k) load_group_g(vc + recv[k] * vwb, vnext, vs + recv[k] * vnb, gv[k]);
+        for (int k = 0; k < C::N; ++k) {
+          const uint8_t* n = vs + recv[k] * vnb;
+          copy_words(vbits, vslot + k * 16 * C::SIDE, vc + recv[k] * vwb);
+          copy_norm(vnslot + k * 4 * C::SIDE, n, vcut && recv[k] == last_rec);
+          vshift[k] = (uint32_t)(reinterpret_cast<uintptr_t>(n) & 2) * 8;
+        }
+        cp_commit();
       };
       fetch_query(warp - kDec0 / 32 + kSoftWarps);
       auto next_place = [&](int at) {
@@ -560,9 +613,9 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
         place(at);
       };
       place(0);
-      load_k();
+      if (do_k) load_k();
       next_place(kTile);
-      load_v();
+      if (do_v) load_v();
       begin();
       rotate_queries(warp - kDec0 / 32 + kSoftWarps);
       auto live_at = [&](int at, bool* live) {
@@ -570,64 +623,71 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
         for (int k = 0; k < C::N; ++k) live[k] = at + tok0 + k * kStep < n_tok;
       };
       auto do_tile_k = [&](int t) {
-        const int kb = nk == 2 ? t & 1 : 0;
         bool live[C::N];
         live_at(t * kTile, live);
-        if (t >= nk) wait(kfree + 8 * kb, (uint32_t)((nk == 2 ? t >> 1 : t) - 1) & 1);
+        if (t >= 1) wait(kfree, (uint32_t)(t - 1) & 1);
+        if (C::SPLIT || t == 1) cp_wait<0>();
+        else cp_wait<1>();   // all but V's latest
+        Group g[C::N];
 #pragma unroll
-        for (int k = 0; k < C::N; ++k) pin(gk[k]);
+        for (int k = 0; k < C::N; ++k) g[k] = read_group(kslot + k * 16 * C::SIDE, knslot + k * 4 * C::SIDE, kshift[k]);
         if (!s_abort)
-          decode_groups<C::N>(kbits, gk, odd, PK.centroids, live, aK + kb * C::KB + cm_off(tok0, 32 * grp, D),
-                              cm_off(kStep, 0, D));
+          decode_groups<C::N>(kbits, g, odd, PK.centroids, live, aK + cm_off(tok0, 32 * grp, D), cm_off(kStep, 0, D));
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) arrive(kfull + 8 * kb);
+        if (lane == 0) arrive(kfull);
         load_k();
       };
-      // K runs a tile ahead of V: V(t) waits for O(t - NV), and what the
-      // softmax of the next tile needs must not queue behind that
+      // In a long slice K runs a tile ahead of V: V(t) waits for O(t - NV),
+      // and what the next tile's softmax needs must not queue behind that.
+      // (The first two K tiles then follow each other, and the second one's
+      // words are waited for: not worth it for a few tiles.)
+      const bool ahead = n_tiles > 4;
       if (do_k) do_tile_k(0);
       for (int t = 0; t < n_tiles; ++t) {
-        if (t + 1 < n_tiles) {
-          next_place((t + 2) * kTile);
-          if (do_k) do_tile_k(t + 1);
-        }
+        next_place((t + 2) * kTile);
+        if (ahead && do_k && t + 1 < n_tiles) do_tile_k(t + 1);
         if (do_v) {
           const int vb = t % NV;
           bool live[C::N];
           live_at(t * kTile, live);
           if (t >= NV) wait(vfree + 8 * vb, (uint32_t)(t / NV - 1) & 1);
+          // all but K's latest, which there is none of behind the last K tile
+          if (C::SPLIT || (ahead && t + 1 == n_tiles)) cp_wait<0>();
+          else cp_wait<1>();
+          Group g[C::N];
 #pragma unroll
-          for (int k = 0; k < C::N; ++k) pin(gv[k]);
+          for (int k = 0; k < C::N; ++k)
+            g[k] = read_group(vslot + k * 16 * C::SIDE, vnslot + k * 4 * C::SIDE, vshift[k]);
           if (!s_abort)
-            decode_groups<C::N>(vbits, gv, odd, PV.centroids, live, aV + vb * C::VB + cm_off(tok0, 32 * grp, C::DV),
+            decode_groups<C::N>(vbits, g, odd, PV.centroids, live, aV + vb * C::VB + cm_off(tok0, 32 * grp, C::DV),
                                 cm_off(kStep, 0, C::DV));
           fence_async_smem();
           __syncwarp();
           if (lane == 0) arrive(vfull + 8 * vb);
           load_v();
         }
+        if (!ahead && do_k && t + 1 < n_tiles) do_tile_k(t + 1);
       }
+      cp_wait<0>();
     }
   } else if (warp == kSoftWarps) {
     // ================= S^T(t) = K^(t) Q^
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::OTHER));
     begin();
     const uint32_t idesc = (1u << 4) | ((uint32_t)(NR >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
-    const uint64_t dq = sdesc(aQ, 128, kKGroup);
+    const uint64_t dq = sdesc(aQ, 128, kKGroup), dk = sdesc(aK, 128, kKGroup);
     bool ok = n_tiles > 0 && wait(q_full, 0);
     for (int t = 0; t < n_tiles && ok; ++t) {
-      const int kb = nk == 2 ? t & 1 : 0;
-      ok = wait(kfull + 8 * kb, (uint32_t)(nk == 2 ? t >> 1 : t) & 1) && (t < 2 || wait(s_free + 8 * (t & 1), (uint32_t)((t >> 1) - 1) & 1));
+      ok = wait(kfull, (uint32_t)t & 1) && (t < 2 || wait(s_free + 8 * (t & 1), (uint32_t)((t >> 1) - 1) & 1));
       if (!ok) break;
       fence_after();
       __syncwarp();
-      const uint64_t dk = sdesc(aK + kb * C::KB, 128, kKGroup);
 #pragma unroll
       for (int s = 0; s < D / 16; ++s)
         mma_ss_elect(tmem + (t & 1) * NR, dk + (uint64_t)(16 * s), dq + (uint64_t)(16 * s), idesc, s > 0);
       commit_elect(s_full + 8 * (t & 1));
-      commit_elect(kfree + 8 * kb);
+      commit_elect(kfree);
     }
     __syncwarp();
     commit_elect(drained);
@@ -644,7 +704,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
       if (!wait(p_full + 8 * pb, (uint32_t)(t >> 1) & 1)) break;
       fence_after();
       __syncwarp();
-      const uint64_t dp = sdesc(aP + pb * pbytes, pg, 128);
+      const uint64_t dp = sdesc(aP + (np == 2 ? pb : 0) * pbytes, pg, 128);
 #pragma unroll
       for (int m = 0; m < OT; ++m) {
         const uint64_t dv = sdesc(aV + vb * C::VB + m * 16 * 128, kVGroup, 128);
@@ -672,7 +732,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
       __syncwarp();
       for (int c = 0; c < nc; c += 16) {   // two blocks of 8 rows, four chains of products
         float d[2][2][4] = {};
-        const uint32_t at = aP + pb * pbytes + row + (uint32_t)(c >> 3) * 128;
+        const uint32_t at = aP + (np == 2 ? pb : 0) * pbytes + row + (uint32_t)(c >> 3) * 128;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -710,7 +770,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     static_assert(kLazySh == 12.0f, "kOver is 2^kLazySh");
     for (int t = 0; t < n_tiles; ++t) {
       const uint32_t sS = lanes + (t & 1) * NR + col0;
-      const uint32_t pdst = pdst0 + (t & 1) * pbytes;
+      const uint32_t poff = np == 2 ? (t & 1) * pbytes : 0, pdst = pdst0 + poff;
       const bool whole = (t + 1) * kTile <= n_tok, live = t * kTile + tk < n_tok;
       // p of every column from its score, to P; returns whether one passes
       // 2^kLazySh.  A token past the slice has p = 0.
@@ -741,7 +801,10 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
         return hmax2(mx, kOver) != kOver;
       };
       wait(s_full + 8 * (t & 1), (uint32_t)(t >> 1) & 1);
-      if (t >= 2) wait(o_done + 8 * (t & 1), (uint32_t)((t >> 1) - 1) & 1);   // P(t - 2) has been read
+      if (t >= np) {   // P(t - np) has been read
+        const int u = t - np;
+        wait(o_done + 8 * (u & 1), (uint32_t)(u >> 1) & 1);
+      }
       fence_after();
       __syncwarp();
       if (t == 0) {
@@ -771,7 +834,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
         __syncwarp();
         // the maxima by TMEM lane quarter, in this half's part of the first
         // eight tokens of P(t), which is written again below
-        float* wm = reinterpret_cast<float*>(smem + (aP - aK) + (t & 1) * pbytes + (col0 >> 3) * 128);
+        float* wm = reinterpret_cast<float*>(smem + (aP - aK) + poff + (col0 >> 3) * 128);
         for (int c = 0; c < nc; c += 16) {
           uint32_t v[16];
           TQ_LD16(sS + c, v);
@@ -871,7 +934,8 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
 template <int D>
 size_t shared_smem(int NR) {
   using C = ShCfg<D>;
-  return (size_t)C::nk(NR) * C::KB + (size_t)C::NV * C::VB + (size_t)NR * D * 2 + (size_t)2 * NR * kTile * 2;
+  return (size_t)C::KB + (size_t)C::NV * C::VB + (size_t)NR * D * 2 + (size_t)C::np(NR) * NR * kTile * 2 +
+         (size_t)kTile * C::G8 * 2 * 20;   // a slot of 16 + 4 bytes per group of K and V
 }
 
 template <int D>
@@ -906,7 +970,7 @@ void shared_rows(int d, int64_t R, int* tiles, int* NR) {
 }
 
 Source source_of(const tq_kv_view* K, const tq_kv_view* V, const int32_t* len, int64_t S_cap, int64_t ctx, int splits,
-                 int slot0) {
+                 int slot0, int seqs) {
   Source s{};
   s.kc = K->codes;
   s.ks = reinterpret_cast<const uint8_t*>(K->scales);
@@ -923,6 +987,7 @@ Source source_of(const tq_kv_view* K, const tq_kv_view* V, const int32_t* len, i
   s.div_mul = f.mul;
   s.div_shift = f.shift;
   s.slot0 = slot0;
+  s.seqs = seqs;
   return s;
 }
 
@@ -961,8 +1026,8 @@ int launch_shared_tc(const CodecParams& PK, const CodecParams& PV, const tq_kv_v
                      const uint16_t* q, float* part, int B, int Hq, int Hkv, float qscale, cudaStream_t st) {
   const WaitLimits wl = wait_limits();
   SharedArgs a{};
-  if (n_prefix) a.pre = source_of(Kp, Vp, prefix_len, P_cap, prefix_ctx, n_prefix, n_own);
-  if (n_own) a.own = source_of(K, V, kv_len, S_cap, ctx, n_own, 0);
+  if (n_prefix) a.pre = source_of(Kp, Vp, prefix_len, P_cap, prefix_ctx, n_prefix, n_own, 1);
+  if (n_own) a.own = source_of(K, V, kv_len, S_cap, ctx, n_own, 0, B);
   a.q = q;
   a.part = part;
   a.report_ns = wl.report_ns;
