@@ -32,8 +32,8 @@
 // tile, its packed words loaded a tile ahead; at head_dim 64 half of the
 // decoder warps take K, half V.  Handoffs are mbarriers:
 //   q_full        Q^ is written
-//   kfull/kfree   K^(t) is decoded / S(t) is done with it (one buffer)
-//   vfull/vfree[b] the same for V and O (two buffers; one at head_dim 256)
+//   kfull/kfree[b], vfull/vfree[b]  K^(t) (V^(t)) is decoded / S(t) (O(t)) is
+//                 done with it (two buffers each; one at head_dim 256)
 //   s_full[i]     S(t), t & 1 = i, is in TMEM    s_free[i] it has been read
 //   p_full[i]     P(t) is written                o_done[i] O += V(t) P(t) and l are done
 // Every wait is bounded at two levels, as in tq_tc.cuh; a CTA that gives up
@@ -72,9 +72,7 @@ __device__ int g_shared_status;
 
 template <int D>
 struct ShCfg {
-  static constexpr int NV = D == 256 ? 1 : 2;          // buffers of V (one of K)
-  // buffers of P: two, one where shared memory holds no more
-  __host__ __device__ static constexpr int np(int NR) { return D == 256 && NR > 32 ? 1 : 2; }
+  static constexpr int NB = D == 256 ? 1 : 2;          // buffers of K and of V
   static constexpr int DV = D < 128 ? 128 : D;         // V tile width: whole M tiles of 128
   static constexpr int OT = DV / 128;                  // M tiles of O^T
   static constexpr int MAXR = D == 256 ? 64 : 128;     // rows of a CTA, by shared memory and registers
@@ -101,7 +99,7 @@ struct Source {
   PageMap pages;
   int64_t S_cap, ctx;
   int64_t per;                 // tokens per split (multiple of kTile)
-  int splits, slot0, seqs;     // seqs: sequences of the cache
+  int splits, slot0;
   uint32_t div_mul, div_shift;   // unit / splits (FastDiv)
 };
 
@@ -233,61 +231,29 @@ __device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// The packed words and norm of one 32-code group.
+// The packed words and norm of one 32-code group, loaded a tile ahead.
 struct Group {
   uint32_t w[4];
   uint32_t sc;
 };
 
-template <int BYTES>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
-  if (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// A group's packed words as the 8-byte word at or 4 bytes before it and, past
+// two bits, the next one: the same two loads whatever the bit width, with no
+// branch or predicate, so that no load is waited for at a join.  Groups of
+// 4 * bits bytes come in pairs that start on 8 bytes (d / 32 is even), so both
+// words lie in the record.  1 and 3 bits: an odd group starts with the second
+// 4-byte word (`shifted`).
+__device__ __forceinline__ void load_group_g(const uint8_t* c8, int next, const uint8_t* s, Group& g) {
+  asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(g.w[0]), "=r"(g.w[1]) : "l"(c8));
+  asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(g.w[2]), "=r"(g.w[3]) : "l"(c8 + next));
+  asm volatile("ld.global.nc.u16 %0, [%1];" : "=r"(g.sc) : "l"(s));
 }
 
-// Copies a group's words to its thread's 16-byte slot.  3 bits: 12 bytes,
-// 8-byte aligned for even groups and 4 bytes past that for odd ones (c is 4
-// bytes before those), so the 16 bytes around them (an even group is never a
-// row's last, so they are inside the row).
-__device__ __forceinline__ void copy_words(int bits, uint32_t dst, const uint8_t* c) {
-  switch (bits) {
-    case 4: cp_async<16>(dst, c); break;
-    case 3:
-      cp_async<8>(dst, c);
-      cp_async<8>(dst + 8, c + 8);
-      break;
-    case 2: cp_async<8>(dst, c); break;
-    default: cp_async<4>(dst, c); break;
-  }
-}
-// Copies the 4-byte word that holds a norm (an array of norms is 4-byte
-// aligned; where its last norm is the first half of a word that the array does
-// not fill, the norm alone, by register).
-__device__ __forceinline__ void copy_norm(uint32_t dst, const uint8_t* s, bool last) {
-  if (!last) {
-    cp_async<4>(dst, reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(s) & ~(uintptr_t)3));
-  } else {
-    const uint32_t v = *reinterpret_cast<const uint16_t*>(s);
-    asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(v) : "memory");
-  }
-}
-// A thread's group from its slots, `shift` 16 where the norm is the word's
-// second half.
-__device__ __forceinline__ Group read_group(uint32_t words, uint32_t norm, uint32_t shift) {
-  Group g;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(g.w[0]), "=r"(g.w[1]), "=r"(g.w[2]), "=r"(g.w[3])
-               : "r"(words)
-               : "memory");
-  g.sc = lds32(norm) >> shift;
-  return g;
+// Keeps what is computed from a group behind this point: otherwise the first
+// steps of its decode are scheduled right after its loads, a tile too early,
+// and wait for them there.
+__device__ __forceinline__ void pin(Group& g) {
+  asm volatile("" : "+r"(g.w[0]), "+r"(g.w[1]), "+r"(g.w[2]), "+r"(g.w[3]), "+r"(g.sc));
 }
 
 // Four fp16x2 registers of a nibble word of 4-bit codes.  The codebook is
@@ -320,7 +286,7 @@ __device__ __forceinline__ void decode_groups_b(const Group* g, bool shifted, co
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     uint32_t n[4];
-    if (BITS == 3) {
+    if (BITS & 1) {
       const uint32_t w3[3] = {shifted ? g[k].w[1] : g[k].w[0], shifted ? g[k].w[2] : g[k].w[1],
                               shifted ? g[k].w[3] : g[k].w[2]};
       chunk_words<BITS>(w3, n);
@@ -354,11 +320,11 @@ template <int D>
 __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const CodecParams PK, const CodecParams PV,
                                                                       const __grid_constant__ SharedArgs a) {
   using C = ShCfg<D>;
-  constexpr int NV = C::NV, OT = C::OT;
+  constexpr int NB = C::NB, OT = C::OT;
   constexpr uint32_t kKGroup = (D / 8) * 128;       // bytes of 8 tokens of K, 8 rows of Q
   constexpr uint32_t kVGroup = (C::DV / 8) * 128;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t bars[2 * NV + 12];
+  __shared__ __align__(8) uint64_t bars[4 * NB + 10];
   __shared__ uint32_t tmem_base;
   __shared__ volatile int s_abort;
   __shared__ int s_late;
@@ -387,14 +353,12 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
   const int n_tok = t_hi > t_lo ? (int)(t_hi - t_lo) : 0;
   const int n_tiles = (n_tok + kTile - 1) / kTile;
 
-  // K, V buffers, Q^, two P buffers, the decoder threads' packed words and norms
-  const int np = C::np(NR);
+  // K, V buffers, Q^, two P buffers
   const uint32_t pbytes = (uint32_t)NR * kTile * 2;
-  const uint32_t aK = su32(smem), aV = aK + C::KB, aQ = aV + NV * C::VB, aP = aQ + (uint32_t)NR * D * 2,
-                 aW = aP + np * pbytes;
+  const uint32_t aK = su32(smem), aV = aK + NB * C::KB, aQ = aV + NB * C::VB, aP = aQ + (uint32_t)NR * D * 2;
   const uint32_t b0 = su32(&bars[0]);
-  const uint32_t q_full = b0, kfull = b0 + 8, kfree = b0 + 16, s_full = b0 + 24, s_free = b0 + 40, p_full = b0 + 56,
-                 o_done = b0 + 72, drained = b0 + 88, vfull = b0 + 96, vfree = vfull + 8 * NV;
+  const uint32_t q_full = b0, s_full = b0 + 8, s_free = b0 + 24, p_full = b0 + 40, o_done = b0 + 56, drained = b0 + 72,
+                 kfull = b0 + 80, kfree = kfull + 8 * NB, vfull = kfree + 8 * NB, vfree = vfull + 8 * NB;
   // TMEM columns: S twice, then O
   const uint32_t cO = 2u * NR;
   const uint32_t tused = cO + (uint32_t)OT * NR;
@@ -419,8 +383,6 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     s_late = 0;
     constexpr int kSide = C::SIDE / 32;   // decoder warps that fill one side
     bar_init(q_full, kSoftWarps + kDecWarps);
-    bar_init(kfull, kSide);
-    bar_init(kfree, 1);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       bar_init(s_full + 8 * i, 1);
@@ -430,7 +392,9 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     }
     bar_init(drained, 2);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
+    for (int i = 0; i < NB; ++i) {
+      bar_init(kfull + 8 * i, kSide);
+      bar_init(kfree + 8 * i, 1);
       bar_init(vfull + 8 * i, kSide);
       bar_init(vfree + 8 * i, 1);
     }
@@ -541,8 +505,9 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
       const int kbits = PK.bits, vbits = PV.bits;
       const bool paged = src.pages.table != nullptr;
       const uint32_t kwb = PK.code_bytes, vwb = PV.code_bytes, knb = 2 * PK.nb, vnb = 2 * PV.nb;
-      const uint32_t kw0 = grp * 4 * kbits - (kbits == 3 && odd ? 4 : 0), kn0 = 32 * grp / PK.blk * 2;
-      const uint32_t vw0 = grp * 4 * vbits - (vbits == 3 && odd ? 4 : 0), vn0 = 32 * grp / PV.blk * 2;
+      const uint32_t kw0 = grp * 4 * kbits - ((kbits & 1) && odd ? 4 : 0), kn0 = 32 * grp / PK.blk * 2;
+      const uint32_t vw0 = grp * 4 * vbits - ((vbits & 1) && odd ? 4 : 0), vn0 = 32 * grp / PV.blk * 2;
+      const int knext = kbits > 2 ? 8 : 0, vnext = vbits > 2 ? 8 : 0;
       const int64_t rec0 = paged ? 0 : ((int64_t)seq * a.Hkv + kvh) * src.S_cap + t_lo;
       const uint8_t *kc = src.kc + rec0 * kwb + kw0, *ks = src.ks + rec0 * knb + kn0;
       const uint8_t *vc = src.vc + rec0 * vwb + vw0, *vs = src.vs + rec0 * vnb + vn0;
@@ -553,7 +518,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
       // token past the slice takes the last one's place (paged: some record
       // of the last page), and its values are not used
       int32_t page[C::N], off[C::N];
-      int64_t rec[C::N], recv[C::N];   // of the next K and the next V loads
+      int64_t rec[C::N];
 #pragma unroll
       for (int k = 0; k < C::N; ++k) {
         const uint32_t t = (uint32_t)t_lo + tok0 + k * kStep;
@@ -575,119 +540,72 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
           }
         }
       };
-      // slots: words (16 bytes a group) of K, of V, then norms (4 bytes)
-      constexpr uint32_t kSlots = kTile * C::G8;
-      const uint32_t kslot = aW + 16 * st, vslot = kslot + 16 * kSlots;
-      const uint32_t knslot = aW + 32 * kSlots + 4 * st, vnslot = knslot + 4 * kSlots;
-      // the caches' last record, where its norm does not fill a word: paged
-      // caches and records of two norms always do
-      const int64_t end = (int64_t)src.seqs * a.Hkv * src.S_cap;
-      const bool ragged = !paged && (end & 1);
-      const int64_t last_rec = end - 1 - rec0;
-      const uint32_t kcut = ragged && PK.nb == 1 ? 1 : 0, vcut = ragged && PV.nb == 1 ? 1 : 0;
-      uint32_t kshift[C::N], vshift[C::N];   // of the copies in flight
+      Group gk[C::N], gv[C::N];
       auto load_k = [&]() {
 #pragma unroll
-        for (int k = 0; k < C::N; ++k) {
-          const uint8_t* n = ks + rec[k] * knb;
-          copy_words(kbits, kslot + k * 16 * C::SIDE, kc + rec[k] * kwb);
-          copy_norm(knslot + k * 4 * C::SIDE, n, kcut && rec[k] == last_rec);
-          kshift[k] = (uint32_t)(reinterpret_cast<uintptr_t>(n) & 2) * 8;
-        }
-        cp_commit();
+        for (int k = 0; k < C::N; ++k) load_group_g(kc + rec[k] * kwb, knext, ks + rec[k] * knb, gk[k]);
       };
       auto load_v = [&]() {
 #pragma unroll
-        for (int k = 0; k < C::N; ++k) {
-          const uint8_t* n = vs + recv[k] * vnb;
-          copy_words(vbits, vslot + k * 16 * C::SIDE, vc + recv[k] * vwb);
-          copy_norm(vnslot + k * 4 * C::SIDE, n, vcut && recv[k] == last_rec);
-          vshift[k] = (uint32_t)(reinterpret_cast<uintptr_t>(n) & 2) * 8;
-        }
-        cp_commit();
+        for (int k = 0; k < C::N; ++k) load_group_g(vc + rec[k] * vwb, vnext, vs + rec[k] * vnb, gv[k]);
       };
       fetch_query(warp - kDec0 / 32 + kSoftWarps);
-      auto next_place = [&](int at) {
-#pragma unroll
-        for (int k = 0; k < C::N; ++k) recv[k] = rec[k];
-        place(at);
-      };
       place(0);
-      if (do_k) load_k();
-      next_place(kTile);
-      if (do_v) load_v();
+      load_k();
+      load_v();
       begin();
       rotate_queries(warp - kDec0 / 32 + kSoftWarps);
-      auto live_at = [&](int at, bool* live) {
+      for (int t = 0; t < n_tiles; ++t) {
+        const int bf = t % NB, at = t * kTile;
+        bool live[C::N];
 #pragma unroll
         for (int k = 0; k < C::N; ++k) live[k] = at + tok0 + k * kStep < n_tok;
-      };
-      auto do_tile_k = [&](int t) {
-        bool live[C::N];
-        live_at(t * kTile, live);
-        if (t >= 1) wait(kfree, (uint32_t)(t - 1) & 1);
-        if (C::SPLIT || t == 1) cp_wait<0>();
-        else cp_wait<1>();   // all but V's latest
-        Group g[C::N];
+        place(at + kTile);
+        if (do_k) {
+          if (t >= NB) wait(kfree + 8 * bf, (uint32_t)(t / NB - 1) & 1);
 #pragma unroll
-        for (int k = 0; k < C::N; ++k) g[k] = read_group(kslot + k * 16 * C::SIDE, knslot + k * 4 * C::SIDE, kshift[k]);
-        if (!s_abort)
-          decode_groups<C::N>(kbits, g, odd, PK.centroids, live, aK + cm_off(tok0, 32 * grp, D), cm_off(kStep, 0, D));
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) arrive(kfull);
-        load_k();
-      };
-      // In a long slice K runs a tile ahead of V: V(t) waits for O(t - NV),
-      // and what the next tile's softmax needs must not queue behind that.
-      // (The first two K tiles then follow each other, and the second one's
-      // words are waited for: not worth it for a few tiles.)
-      const bool ahead = n_tiles > 4;
-      if (do_k) do_tile_k(0);
-      for (int t = 0; t < n_tiles; ++t) {
-        next_place((t + 2) * kTile);
-        if (ahead && do_k && t + 1 < n_tiles) do_tile_k(t + 1);
-        if (do_v) {
-          const int vb = t % NV;
-          bool live[C::N];
-          live_at(t * kTile, live);
-          if (t >= NV) wait(vfree + 8 * vb, (uint32_t)(t / NV - 1) & 1);
-          // all but K's latest, which there is none of behind the last K tile
-          if (C::SPLIT || (ahead && t + 1 == n_tiles)) cp_wait<0>();
-          else cp_wait<1>();
-          Group g[C::N];
-#pragma unroll
-          for (int k = 0; k < C::N; ++k)
-            g[k] = read_group(vslot + k * 16 * C::SIDE, vnslot + k * 4 * C::SIDE, vshift[k]);
+          for (int k = 0; k < C::N; ++k) pin(gk[k]);
           if (!s_abort)
-            decode_groups<C::N>(vbits, g, odd, PV.centroids, live, aV + vb * C::VB + cm_off(tok0, 32 * grp, C::DV),
+            decode_groups<C::N>(kbits, gk, odd, PK.centroids, live, aK + bf * C::KB + cm_off(tok0, 32 * grp, D),
+                                cm_off(kStep, 0, D));
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) arrive(kfull + 8 * bf);
+          load_k();
+        }
+        if (do_v) {
+          if (t >= NB) wait(vfree + 8 * bf, (uint32_t)(t / NB - 1) & 1);
+#pragma unroll
+          for (int k = 0; k < C::N; ++k) pin(gv[k]);
+          if (!s_abort)
+            decode_groups<C::N>(vbits, gv, odd, PV.centroids, live, aV + bf * C::VB + cm_off(tok0, 32 * grp, C::DV),
                                 cm_off(kStep, 0, C::DV));
           fence_async_smem();
           __syncwarp();
-          if (lane == 0) arrive(vfull + 8 * vb);
+          if (lane == 0) arrive(vfull + 8 * bf);
           load_v();
         }
-        if (!ahead && do_k && t + 1 < n_tiles) do_tile_k(t + 1);
       }
-      cp_wait<0>();
     }
   } else if (warp == kSoftWarps) {
     // ================= S^T(t) = K^(t) Q^
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::OTHER));
     begin();
     const uint32_t idesc = (1u << 4) | ((uint32_t)(NR >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
-    const uint64_t dq = sdesc(aQ, 128, kKGroup), dk = sdesc(aK, 128, kKGroup);
+    const uint64_t dq = sdesc(aQ, 128, kKGroup);
     bool ok = n_tiles > 0 && wait(q_full, 0);
     for (int t = 0; t < n_tiles && ok; ++t) {
-      ok = wait(kfull, (uint32_t)t & 1) && (t < 2 || wait(s_free + 8 * (t & 1), (uint32_t)((t >> 1) - 1) & 1));
+      const int bf = t % NB;
+      ok = wait(kfull + 8 * bf, (uint32_t)(t / NB) & 1) && (t < 2 || wait(s_free + 8 * (t & 1), (uint32_t)((t >> 1) - 1) & 1));
       if (!ok) break;
       fence_after();
       __syncwarp();
+      const uint64_t dk = sdesc(aK + bf * C::KB, 128, kKGroup);
 #pragma unroll
       for (int s = 0; s < D / 16; ++s)
         mma_ss_elect(tmem + (t & 1) * NR, dk + (uint64_t)(16 * s), dq + (uint64_t)(16 * s), idesc, s > 0);
       commit_elect(s_full + 8 * (t & 1));
-      commit_elect(kfree);
+      commit_elect(kfree + 8 * bf);
     }
     __syncwarp();
     commit_elect(drained);
@@ -699,12 +617,12 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
                            ((uint32_t)(128 >> 4) << 24);
     const uint32_t pg = (uint32_t)(NR >> 3) * 128;   // bytes of 8 tokens of P
     for (int t = 0; t < n_tiles; ++t) {
-      const int vb = t % NV, pb = t & 1;
-      if (!wait(vfull + 8 * vb, (uint32_t)(t / NV) & 1)) break;
+      const int vb = t % NB, pb = t & 1;
+      if (!wait(vfull + 8 * vb, (uint32_t)(t / NB) & 1)) break;
       if (!wait(p_full + 8 * pb, (uint32_t)(t >> 1) & 1)) break;
       fence_after();
       __syncwarp();
-      const uint64_t dp = sdesc(aP + (np == 2 ? pb : 0) * pbytes, pg, 128);
+      const uint64_t dp = sdesc(aP + pb * pbytes, pg, 128);
 #pragma unroll
       for (int m = 0; m < OT; ++m) {
         const uint64_t dv = sdesc(aV + vb * C::VB + m * 16 * 128, kVGroup, 128);
@@ -732,7 +650,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
       __syncwarp();
       for (int c = 0; c < nc; c += 16) {   // two blocks of 8 rows, four chains of products
         float d[2][2][4] = {};
-        const uint32_t at = aP + (np == 2 ? pb : 0) * pbytes + row + (uint32_t)(c >> 3) * 128;
+        const uint32_t at = aP + pb * pbytes + row + (uint32_t)(c >> 3) * 128;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -770,7 +688,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     static_assert(kLazySh == 12.0f, "kOver is 2^kLazySh");
     for (int t = 0; t < n_tiles; ++t) {
       const uint32_t sS = lanes + (t & 1) * NR + col0;
-      const uint32_t poff = np == 2 ? (t & 1) * pbytes : 0, pdst = pdst0 + poff;
+      const uint32_t pdst = pdst0 + (t & 1) * pbytes;
       const bool whole = (t + 1) * kTile <= n_tok, live = t * kTile + tk < n_tok;
       // p of every column from its score, to P; returns whether one passes
       // 2^kLazySh.  A token past the slice has p = 0.
@@ -801,10 +719,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
         return hmax2(mx, kOver) != kOver;
       };
       wait(s_full + 8 * (t & 1), (uint32_t)(t >> 1) & 1);
-      if (t >= np) {   // P(t - np) has been read
-        const int u = t - np;
-        wait(o_done + 8 * (u & 1), (uint32_t)(u >> 1) & 1);
-      }
+      if (t >= 2) wait(o_done + 8 * (t & 1), (uint32_t)((t >> 1) - 1) & 1);   // P(t - 2) has been read
       fence_after();
       __syncwarp();
       if (t == 0) {
@@ -834,7 +749,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
         __syncwarp();
         // the maxima by TMEM lane quarter, in this half's part of the first
         // eight tokens of P(t), which is written again below
-        float* wm = reinterpret_cast<float*>(smem + (aP - aK) + poff + (col0 >> 3) * 128);
+        float* wm = reinterpret_cast<float*>(smem + (aP - aK) + (t & 1) * pbytes + (col0 >> 3) * 128);
         for (int c = 0; c < nc; c += 16) {
           uint32_t v[16];
           TQ_LD16(sS + c, v);
@@ -934,15 +849,12 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
 template <int D>
 size_t shared_smem(int NR) {
   using C = ShCfg<D>;
-  return (size_t)C::KB + (size_t)C::NV * C::VB + (size_t)NR * D * 2 + (size_t)C::np(NR) * NR * kTile * 2 +
-         (size_t)kTile * C::G8 * 2 * 20;   // a slot of 16 + 4 bytes per group of K and V
+  return (size_t)C::NB * (C::KB + C::VB) + (size_t)NR * D * 2 + (size_t)2 * NR * kTile * 2;
 }
 
 template <int D>
 int launch_shared(const CodecParams& PK, const CodecParams& PV, const SharedArgs& a, unsigned grid, cudaStream_t st) {
-  // the own tokens' CTAs have 32 rows
-  size_t sm = a.n_pre ? shared_smem<D>(a.NR) : 0;
-  if (a.own.splits && shared_smem<D>(32) > sm) sm = shared_smem<D>(32);
+  const size_t sm = shared_smem<D>(a.n_pre ? a.NR : 32);
   auto kern = shared_prefix_kernel<D>;
   // once per device; a build with fewer registers than the split shares out
   // would wait for them without end, so it is refused
@@ -950,10 +862,8 @@ int launch_shared(const CodecParams& PK, const CodecParams& PV, const SharedArgs
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return TQ_ERR_CUDA;
   if (!ready[dev].load(std::memory_order_acquire)) {
-    size_t most = 0;
-    for (int r = 32; r <= ShCfg<D>::MAXR; r += 32) most = shared_smem<D>(r) > most ? shared_smem<D>(r) : most;
     cudaFuncAttributes fa;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) ||
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared_smem<D>(ShCfg<D>::MAXR)) ||
         cudaFuncGetAttributes(&fa, kern) || fa.numRegs < kLaunchRegs)
       return TQ_ERR_CUDA;
     ready[dev].store(true, std::memory_order_release);
@@ -970,7 +880,7 @@ void shared_rows(int d, int64_t R, int* tiles, int* NR) {
 }
 
 Source source_of(const tq_kv_view* K, const tq_kv_view* V, const int32_t* len, int64_t S_cap, int64_t ctx, int splits,
-                 int slot0, int seqs) {
+                 int slot0) {
   Source s{};
   s.kc = K->codes;
   s.ks = reinterpret_cast<const uint8_t*>(K->scales);
@@ -987,7 +897,6 @@ Source source_of(const tq_kv_view* K, const tq_kv_view* V, const int32_t* len, i
   s.div_mul = f.mul;
   s.div_shift = f.shift;
   s.slot0 = slot0;
-  s.seqs = seqs;
   return s;
 }
 
@@ -1026,8 +935,8 @@ int launch_shared_tc(const CodecParams& PK, const CodecParams& PV, const tq_kv_v
                      const uint16_t* q, float* part, int B, int Hq, int Hkv, float qscale, cudaStream_t st) {
   const WaitLimits wl = wait_limits();
   SharedArgs a{};
-  if (n_prefix) a.pre = source_of(Kp, Vp, prefix_len, P_cap, prefix_ctx, n_prefix, n_own, 1);
-  if (n_own) a.own = source_of(K, V, kv_len, S_cap, ctx, n_own, 0, B);
+  if (n_prefix) a.pre = source_of(Kp, Vp, prefix_len, P_cap, prefix_ctx, n_prefix, n_own);
+  if (n_own) a.own = source_of(K, V, kv_len, S_cap, ctx, n_own, 0);
   a.q = q;
   a.part = part;
   a.report_ns = wl.report_ns;
