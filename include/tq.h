@@ -396,7 +396,8 @@ int tq_decode_attn_shared(const tq_kv_view* Kp, const tq_kv_view* Vp, int64_t P_
                           int Hq, int Hkv, int64_t S_cap, const int32_t* kv_len, int64_t ctx, float softmax_scale,
                           uint16_t* out, void* workspace, size_t workspace_bytes, int n_split, void* stream);
 
-/* Workspace bytes for tq_decode_attn_shared with these sizes (host). */
+/* Workspace bytes for tq_decode_attn_shared with these sizes, and with these
+ * and a shorter prefix_ctx or ctx (host). */
 int tq_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int head_dim, int64_t prefix_ctx, int64_t ctx,
                                      int n_split, size_t* bytes);
 
@@ -502,7 +503,8 @@ int tq_pages_compact(const tq_page_pool* pool, const tq_kv_view* caches, int n_c
 int tq_pages_workspace_bytes(int n_seqs, int num_pages, int n, size_t* bytes);
 
 /* ---- Device-side waits and status ----------------------------------------
- * The tensor-core prefill (tq_prefill_attn) and the fast quantiser
+ * The tensor-core prefill (tq_prefill_attn), the shared-prefix decode
+ * (tq_decode_attn_shared, 1..4 bits without QJL) and the fast quantiser
  * (tq_quantize_kv / tq_append_kv with fp16 input, block 32 or 64, 2-4 bits,
  * no QJL) hand work between the warps of a CTA through mbarriers, and every
  * such wait is bounded.  A wait longer than the wait limit records
@@ -510,10 +512,11 @@ int tq_pages_workspace_bytes(int n_seqs, int num_pages, int n, size_t* bytes);
  * goes on waiting, so the launch still completes and its outputs are valid;
  * a call returns before its kernels run, so this is the only way a caller
  * learns of it.  A wait longer than the hard bound (2 s, or the limit if
- * larger) stops its CTA: the fast quantiser first waits for every load and
- * product it has in flight, then stops with its outputs incomplete; the
- * prefill stops without that drain (a device that has stopped making
- * progress).  Either way the status word says TQ_ERR_TIMEOUT. */
+ * larger) stops its CTA: the fast quantiser and the shared-prefix decode
+ * first wait for every load and product they have in flight, then stop with
+ * their outputs incomplete; the prefill stops without that drain (a device
+ * that has stopped making progress).  Either way the status word says
+ * TQ_ERR_TIMEOUT. */
 
 /* Sets the wait limit, in nanoseconds, for launches issued after the call
  * (process-wide, all devices); 0 restores the default of 2 s.  Always

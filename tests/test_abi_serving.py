@@ -58,6 +58,20 @@ def test_shared_workspace_query(tqlib):
     assert tqlib.tq_decode_shared_workspace_bytes(8, 32, 8, 128, 1, 1, 0, None) == ARG
 
 
+@pytest.mark.parametrize("B,Hq,Hkv,d", [(1, 1, 1, 64), (7, 16, 8, 64), (4, 32, 8, 128), (8, 16, 4, 256), (64, 8, 1, 128)])
+def test_shared_workspace_serves_shorter_lengths(tqlib, B, Hq, Hkv, d):
+    def need(P, S):
+        nb = ctypes.c_size_t()
+        assert tqlib.tq_decode_shared_workspace_bytes(B, Hq, Hkv, d, P, S, 0, ctypes.byref(nb)) == 0
+        return nb.value
+
+    lengths = [0, 1, 128, 129, 500, 2000, 9000, 40000, 200000]
+    for S in lengths:
+        for a, b in zip(lengths, lengths[1:]):
+            assert need(a, S) <= need(b, S)
+            assert need(S, a) <= need(S, b)
+
+
 def _rows(lib, x=P16, dt=0, B=1, T=2, Hq=8, Hkv=2, d=128, stride=None, wq=P16, wk=P16, eps=1e-6, rope=P16, n_pos=10,
           rot=128, inter=0, q=P16, k=P16, v=P16, cap=2):
     stride = (Hq + 2 * Hkv) * d if stride is None else stride

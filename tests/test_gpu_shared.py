@@ -282,3 +282,41 @@ def test_binding_refusals(tqlib):
         tb.tq_decode_attn_shared(Kp, Vp, K, V, q, out=torch.empty(2, 8, 64, dtype=torch.float16, device="cuda"))
     with pytest.raises(tb.TQError):
         tb.tq_decode_attn_shared(Kp, Vp, K, V, q, prefix_ctx=65)
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,d,short", [(7, 16, 8, 64, (300, 200)), (2, 8, 2, 128, (1, 9)), (4, 4, 1, 256, (1500, 0))])
+def test_workspace_of_longer_lengths(tqlib, B, Hq, Hkv, d, short):
+    """A workspace for the longest lengths serves shorter ones, with the same results."""
+    from turboquant_kv_cache_gb300 import binding as tb
+    L = (32, 3, 0, 0)
+    Kp, Vp, K, V, q = _inputs(tb, d, L, L, B, Hq, Hkv, 2048, 512)
+    ws = torch.empty(tb.tq_decode_shared_workspace_bytes(B, Hq, Hkv, d, 2048, 512), dtype=torch.uint8, device="cuda")
+    for P, S in [(2048, 512), short, (0, 512), (2048, 0)]:
+        got = tb.tq_decode_attn_shared(Kp, Vp, K, V, q, prefix_ctx=P, ctx=S, workspace=ws)
+        assert torch.equal(got, tb.tq_decode_attn_shared(Kp, Vp, K, V, q, prefix_ctx=P, ctx=S))
+        ref = _reference(tb, Kp, Vp, P, K, V, [S] * B, q)
+        assert (got.double() - ref).abs().max().item() < ATTN_ATOL
+
+
+def test_reports_timeout_and_stays_exact(tqlib):
+    """A wait limit far below any real wait (1 ns): TQ_ERR_TIMEOUT in the
+    device status, the output that of an ordinary launch."""
+    from turboquant_kv_cache_gb300 import binding as tb
+    L = (32, 3, 0, 0)
+    Kp, Vp, K, V, q = _inputs(tb, 128, L, L, 8, 32, 8, 4096, 256)
+    run = lambda: tb.tq_decode_attn_shared(Kp, Vp, K, V, q, prefix_ctx=4000, ctx=250)  # noqa: E731
+    torch.cuda.synchronize()
+    tb.tq_set_wait_limit_ns(0)
+    tb.tq_device_status(clear=True)
+    try:
+        ref = run()
+        assert tb.tq_device_status(clear=True) == 0
+        tb.tq_set_wait_limit_ns(1)
+        got = run()
+        assert tb.tq_device_status(clear=True) == -6
+        assert torch.equal(got, ref)
+    finally:
+        tb.tq_set_wait_limit_ns(0)
+        tb.tq_device_status(clear=True)
+    assert torch.equal(run(), ref)
+    assert tb.tq_device_status() == 0

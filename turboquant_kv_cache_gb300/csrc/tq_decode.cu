@@ -35,6 +35,7 @@ int launch_decode_tc(const CodecParams& PK, const CodecParams& PV, const tq_kv_v
 size_t decode_ws_bytes(int B, int Hq, int d, int n_split);
 bool shared_tc_eligible(const CodecParams& PK, const CodecParams& PV);
 void shared_tc_splits(int d, int B, int G, int Hkv, int64_t prefix_ctx, int64_t ctx, int* n_prefix, int* n_own);
+void shared_tc_most_splits(int d, int B, int G, int Hkv, int64_t prefix_ctx, int64_t ctx, int* n_prefix, int* n_own);
 int launch_shared_tc(const CodecParams& PK, const CodecParams& PV, const tq_kv_view* Kp, const tq_kv_view* Vp,
                      int64_t P_cap, const int32_t* prefix_len, int64_t prefix_ctx, int n_prefix, const tq_kv_view* K,
                      const tq_kv_view* V, int64_t S_cap, const int32_t* kv_len, int64_t ctx, int n_own,
@@ -1231,7 +1232,7 @@ extern "C" int tq_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int head
   if (!bytes) return TQ_ERR_ARG;
   // the layout decides which kernel runs: the most parts of either
   int tcp = 0, tco = 0;
-  tq::shared_tc_splits(head_dim, B, Hq / Hkv, Hkv, prefix_ctx, ctx, &tcp, &tco);
+  tq::shared_tc_most_splits(head_dim, B, Hq / Hkv, Hkv, prefix_ctx, ctx, &tcp, &tco);
   if (prefix_ctx > 0) np = tq::decode_auto_splits(B, Hkv, prefix_ctx);
   if (tcp > np) np = tcp;
   if (!n_split && tco > ns) ns = tco;

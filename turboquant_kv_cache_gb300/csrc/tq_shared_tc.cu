@@ -907,24 +907,59 @@ bool shared_tc_eligible(const CodecParams& PK, const CodecParams& PV) {
   return !PK.m && !PV.m && PK.bits <= 4 && PV.bits <= 4;
 }
 
-// Splits of the prefix and of each sequence's own tokens.  One CTA per SM at a
-// time: the prefix fills one wave (at least a tile each); the own tokens are
-// split as far as the SMs that the prefix leaves idle, or a second wave, take
-// them.
+// Splits of the prefix and of each sequence's own tokens.  An SM holds one CTA
+// at a time and a CTA's start and end cost about two tiles (kSetup), so there
+// are two ways.  One wave: every CTA on an SM of its own, with the fewest
+// tiles at which they all have one.  Or the prefix over all SMs and the own
+// tokens in waves behind it, which is shorter when there is much prefix or
+// there are many sequences.
+// 7 sequences of 333 tokens, 2011 shared ones, 8 KV heads at head_dim 64: one
+// wave of 3 tiles 10.6 us, two of 1 and 2 tiles 15.6 us.  8 sequences of 256 and
+// 131072 shared ones, 4 KV heads at head_dim 256: one wave of 35 tiles 93.6 us,
+// two of 27 and 1 tiles 82.6 us.
 void shared_tc_splits(int d, int B, int G, int Hkv, int64_t prefix_ctx, int64_t ctx, int* n_prefix, int* n_own) {
-  int tiles, NR;
-  shared_rows(d, (int64_t)B * G, &tiles, &NR);
-  const int64_t sms = sm_count();
-  auto fit = [&](int64_t units, int64_t room, int64_t c) {
-    const int64_t most = (c + kTile - 1) / kTile;
-    int64_t ns = room / units;
-    if (ns > most) ns = most;
-    return (int)(ns < 1 ? 1 : ns);
+  constexpr int64_t kSetup = 2;
+  int row_tiles, NR;
+  shared_rows(d, (int64_t)B * G, &row_tiles, &NR);
+  const int64_t sms = sm_count(), up = (int64_t)row_tiles * Hkv, uo = (int64_t)B * Hkv;
+  const int64_t tp = (prefix_ctx + kTile - 1) / kTile, to = (ctx + kTile - 1) / kTile;
+  auto parts = [](int64_t tiles, int64_t most) { return most > 0 ? (tiles + most - 1) / most : 0; };
+  auto waves = [&](int64_t units, int64_t ns, int64_t tiles) {
+    return ns > 0 ? parts(units * ns, sms) * (parts(tiles, ns) + kSetup) : 0;
   };
-  *n_prefix = prefix_ctx > 0 ? fit((int64_t)tiles * Hkv, sms, prefix_ctx) : 0;
-  const int64_t used = (int64_t)*n_prefix * tiles * Hkv;
-  const int64_t idle = used < sms ? sms - used : 0;
-  *n_own = ctx > 0 ? fit((int64_t)B * Hkv, idle > sms / 2 ? idle : sms, ctx) : 0;
+  // the prefix over all SMs, then the own tokens
+  const int64_t np = tp > 0 ? imin64(tp, up < sms ? sms / up : 1) : 0;
+  int64_t no = to > 0 ? 1 : 0;
+  for (int64_t n = 2; n <= imin64(to, 64) && uo * n <= 2 * sms; ++n)
+    if (waves(uo, n, to) < waves(uo, no, to)) no = n;
+  const int64_t two = waves(up, np, tp) + waves(uo, no, to);
+  *n_prefix = (int)np;
+  *n_own = (int)no;
+  // one wave of CTAs of at most `most` tiles
+  auto fits = [&](int64_t most) { return up * parts(tp, most) + uo * parts(to, most) <= sms; };
+  int64_t lo = 1, hi = tp > to ? tp : to;
+  if (hi < 1 || !fits(hi)) return;
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) / 2;
+    if (fits(mid)) hi = mid;
+    else lo = mid + 1;
+  }
+  if (lo + kSetup > two) return;
+  *n_prefix = (int)parts(tp, lo);
+  *n_own = (int)parts(to, lo);
+}
+
+// At least the splits above, and no fewer for longer lengths: a workspace for
+// the longest lengths serves shorter ones.
+void shared_tc_most_splits(int d, int B, int G, int Hkv, int64_t prefix_ctx, int64_t ctx, int* n_prefix, int* n_own) {
+  int row_tiles, NR;
+  shared_rows(d, (int64_t)B * G, &row_tiles, &NR);
+  const int64_t sms = sm_count(), up = (int64_t)row_tiles * Hkv, uo = (int64_t)B * Hkv;
+  auto most = [&](int64_t tokens, int64_t ctas, int64_t units) {
+    return (int)imin64((tokens + kTile - 1) / kTile, ctas > units ? ctas / units : 1);
+  };
+  *n_prefix = most(prefix_ctx, sms, up);
+  *n_own = most(ctx, 2 * sms, uo);
 }
 
 // Writes the partials of the own tokens to slots [0, n_own) and those of the
