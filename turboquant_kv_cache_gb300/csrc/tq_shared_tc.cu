@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
   constexpr uint32_t kKGroup = (D / 8) * 128;       // bytes of 8 tokens of K, 8 rows of Q
   constexpr uint32_t kVGroup = (C::DV / 8) * 128;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t bars[4 * NB + 10];
+  __shared__ __align__(8) uint64_t bars[3 * NB + 8];
   __shared__ uint32_t tmem_base;
   __shared__ volatile int s_abort;
   __shared__ int s_late;
@@ -357,8 +357,8 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
   const uint32_t pbytes = (uint32_t)NR * kTile * 2;
   const uint32_t aK = su32(smem), aV = aK + NB * C::KB, aQ = aV + NB * C::VB, aP = aQ + (uint32_t)NR * D * 2;
   const uint32_t b0 = su32(&bars[0]);
-  const uint32_t q_full = b0, s_full = b0 + 8, s_free = b0 + 24, p_full = b0 + 40, o_done = b0 + 56, drained = b0 + 72,
-                 kfull = b0 + 80, kfree = kfull + 8 * NB, vfull = kfree + 8 * NB, vfree = vfull + 8 * NB;
+  const uint32_t q_full = b0, s_full = b0 + 8, p_full = b0 + 24, o_done = b0 + 40, drained = b0 + 56,
+                 kfull = b0 + 64, vfull = kfull + 8 * NB, vfree = vfull + 8 * NB;
   // TMEM columns: S twice, then O
   const uint32_t cO = 2u * NR;
   const uint32_t tused = cO + (uint32_t)OT * NR;
@@ -382,11 +382,10 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     s_abort = 0;
     s_late = 0;
     constexpr int kSide = C::SIDE / 32;   // decoder warps that fill one side
-    bar_init(q_full, kSoftWarps + kDecWarps);
+    bar_init(q_full, kSoftWarps);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       bar_init(s_full + 8 * i, 1);
-      bar_init(s_free + 8 * i, kSoftWarps);
       bar_init(p_full + 8 * i, kSoftWarps);
       bar_init(o_done + 8 * i, 3);   // the product's commit and the two summing warps
     }
@@ -394,7 +393,6 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
       bar_init(kfull + 8 * i, kSide);
-      bar_init(kfree + 8 * i, 1);
       bar_init(vfull + 8 * i, kSide);
       bar_init(vfree + 8 * i, 1);
     }
@@ -413,46 +411,41 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     tmem = tmem_base;
   };
 
-  // Q^ = H D q per K block, times softmax_scale * log2 e, by the softmax and
-  // decoder warps (w of 24): a warp per row, a lane the D/32 consecutive
-  // values from E*lane on, the next row's load in flight.  Loops are kept
-  // rolled: a CTA runs this once, and straight-line code would be fetched
-  // from a cold cache.
-  constexpr int E = D / 32, QW = kSoftWarps + kDecWarps;
-  uint32_t next[E / 2];
-  auto fetch_query = [&](int r) {
+  // Q^ = H D q per K block, times softmax_scale * log2 e, by the softmax warps:
+  // a lane has 32 values of one row, a warp QR = 1024 / D rows at a time, the
+  // rows on consecutive lanes, so that eight lanes write one core matrix.
+  constexpr int QL = D / 32, QR = 32 / QL;
+  uint4 qv[4];
+  auto fetch_query = [&](int i) {   // rows [QR * i, QR * (i + 1))
+    const int r = QR * i + lane % QR;
 #pragma unroll
-    for (int e = 0; e < E / 2; ++e) next[e] = 0u;
+    for (int e = 0; e < 4; ++e) qv[e] = make_uint4(0u, 0u, 0u, 0u);
     if (r < rows) {
       const int rr = row0 + r, b = rr >> a.lg, h = kvh * a.G + (rr & (a.G - 1));
-      const uint16_t* qr = a.q + ((int64_t)b * a.Hq + h) * D + E * lane;
-      if constexpr (E == 8) {
-        const uint4 q = *reinterpret_cast<const uint4*>(qr);
-        next[0] = q.x; next[1] = q.y; next[2] = q.z; next[3] = q.w;
-      } else if constexpr (E == 4) {
-        const uint2 q = *reinterpret_cast<const uint2*>(qr);
-        next[0] = q.x; next[1] = q.y;
-      } else {
-        next[0] = *reinterpret_cast<const uint32_t*>(qr);
-      }
+      const uint4* qr = reinterpret_cast<const uint4*>(a.q + ((int64_t)b * a.Hq + h) * D + 32 * (lane / QR));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) qv[e] = qr[e];
     }
   };
   auto rotate_queries = [&](int w) {   // after fetch_query(w)
     const float qn = PK.inv_sqrt_blk * a.qscale;
-    const uint32_t sb = PK.sign_bits[E * lane >> 5] >> (E * lane & 31);
+    const uint32_t sb = PK.sign_bits[lane / QR];
 #pragma unroll 1
-    for (int r = w; r < NR; r += QW) {
-      float v[E];
+    for (int i = w; QR * i < NR; i += kSoftWarps) {
+      float v[32];
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&next[e / 2]));
-        v[e] = flip((e & 1 ? f.y : f.x) * qn, (sb >> e) & 1u);
+      for (int e = 0; e < 32; e += 2) {
+        const uint4& x = qv[e >> 3];
+        const uint32_t u = (e & 6) == 0 ? x.x : (e & 6) == 2 ? x.y : (e & 6) == 4 ? x.z : x.w;
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
+        v[e] = flip(f.x * qn, (sb >> e) & 1u);
+        v[e + 1] = flip(f.y * qn, (sb >> (e + 1)) & 1u);
       }
-      fetch_query(r + QW);
+      fetch_query(i + kSoftWarps);
 #pragma unroll
-      for (int hs = 1; hs < E; hs <<= 1) {   // blocks are 32 values at least
+      for (int hs = 1; hs < 32; hs <<= 1) {   // blocks are 32 values at least
 #pragma unroll
-        for (int e = 0; e < E; ++e)
+        for (int e = 0; e < 32; ++e)
           if ((e & hs) == 0) {
             const float p = v[e], q = v[e + hs];
             v[e] = p + q;
@@ -460,25 +453,19 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
           }
       }
 #pragma unroll 1
-      for (int hs = E; hs < PK.blk; hs <<= 1) {
-        const int lo = hs / E;
+      for (int hs = 32; hs < PK.blk; hs <<= 1) {
+        const int lo = hs / 32 * QR;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
+        for (int e = 0; e < 32; ++e) {
           const float p = __shfl_xor_sync(kFull, v[e], lo);
           v[e] = (lane & lo) ? (p - v[e]) : (v[e] + p);
         }
       }
-      const uint32_t dst = aQ + cm_off(r, E * lane, D);
-      uint32_t o[E / 2];
+      const uint32_t dst = aQ + cm_off(QR * i + lane % QR, 32 * (lane / QR), D);
 #pragma unroll
-      for (int e = 0; e < E / 2; ++e) o[e] = pack2(v[2 * e], v[2 * e + 1]);
-      if constexpr (E == 8) {
-        sts16b(dst, o[0], o[1], o[2], o[3]);
-      } else if constexpr (E == 4) {
-        asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(dst), "r"(o[0]), "r"(o[1]) : "memory");
-      } else {
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(o[0]) : "memory");
-      }
+      for (int c = 0; c < 4; ++c)
+        sts16b(dst + 128 * c, pack2(v[8 * c], v[8 * c + 1]), pack2(v[8 * c + 2], v[8 * c + 3]),
+               pack2(v[8 * c + 4], v[8 * c + 5]), pack2(v[8 * c + 6], v[8 * c + 7]));
     }
     fence_async_smem();
     __syncwarp();
@@ -549,20 +536,17 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
 #pragma unroll
         for (int k = 0; k < C::N; ++k) load_group_g(vc + rec[k] * vwb, vnext, vs + rec[k] * vnb, gv[k]);
       };
-      fetch_query(warp - kDec0 / 32 + kSoftWarps);
       place(0);
       load_k();
       load_v();
       begin();
-      rotate_queries(warp - kDec0 / 32 + kSoftWarps);
       for (int t = 0; t < n_tiles; ++t) {
         const int bf = t % NB, at = t * kTile;
         bool live[C::N];
 #pragma unroll
         for (int k = 0; k < C::N; ++k) live[k] = at + tok0 + k * kStep < n_tok;
-        place(at + kTile);
         if (do_k) {
-          if (t >= NB) wait(kfree + 8 * bf, (uint32_t)(t / NB - 1) & 1);
+          if (t >= NB) wait(s_full + 8 * ((t - NB) & 1), (uint32_t)((t - NB) >> 1) & 1);   // S(t - NB) is done
 #pragma unroll
           for (int k = 0; k < C::N; ++k) pin(gk[k]);
           if (!s_abort)
@@ -571,6 +555,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
           fence_async_smem();
           __syncwarp();
           if (lane == 0) arrive(kfull + 8 * bf);
+          place(at + kTile);
           load_k();
         }
         if (do_v) {
@@ -583,6 +568,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
           fence_async_smem();
           __syncwarp();
           if (lane == 0) arrive(vfull + 8 * bf);
+          if (C::SPLIT) place(at + kTile);
           load_v();
         }
       }
@@ -596,7 +582,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     bool ok = n_tiles > 0 && wait(q_full, 0);
     for (int t = 0; t < n_tiles && ok; ++t) {
       const int bf = t % NB;
-      ok = wait(kfull + 8 * bf, (uint32_t)(t / NB) & 1) && (t < 2 || wait(s_free + 8 * (t & 1), (uint32_t)((t >> 1) - 1) & 1));
+      ok = wait(kfull + 8 * bf, (uint32_t)(t / NB) & 1) && (t < 2 || wait(p_full + 8 * (t & 1), (uint32_t)((t >> 1) - 1) & 1));
       if (!ok) break;
       fence_after();
       __syncwarp();
@@ -605,7 +591,6 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
       for (int s = 0; s < D / 16; ++s)
         mma_ss_elect(tmem + (t & 1) * NR, dk + (uint64_t)(16 * s), dq + (uint64_t)(16 * s), idesc, s > 0);
       commit_elect(s_full + 8 * (t & 1));
-      commit_elect(kfree + 8 * bf);
     }
     __syncwarp();
     commit_elect(drained);
@@ -794,10 +779,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
       fence_async_smem();
       fence_before();
       __syncwarp();
-      if (lane == 0) {
-        arrive(p_full + 8 * (t & 1));
-        arrive(s_free + 8 * (t & 1));
-      }
+      if (lane == 0) arrive(p_full + 8 * (t & 1));
     }
   }
   // the next kernel may be scheduled; it waits for this grid before it ends
@@ -914,9 +896,9 @@ bool shared_tc_eligible(const CodecParams& PK, const CodecParams& PV) {
 // tokens in waves behind it, which is shorter when there is much prefix or
 // there are many sequences.
 // 7 sequences of 333 tokens, 2011 shared ones, 8 KV heads at head_dim 64: one
-// wave of 3 tiles 10.6 us, two of 1 and 2 tiles 15.6 us.  8 sequences of 256 and
-// 131072 shared ones, 4 KV heads at head_dim 256: one wave of 35 tiles 93.6 us,
-// two of 27 and 1 tiles 82.6 us.
+// wave of 3 tiles @@ us, two of 1 and 2 tiles 15.6 us.  8 sequences of 256 and
+// 131072 shared ones, 4 KV heads at head_dim 256: one wave of 35 tiles @@ us,
+// two of 27 and 1 tiles 82.8 us.
 void shared_tc_splits(int d, int B, int G, int Hkv, int64_t prefix_ctx, int64_t ctx, int* n_prefix, int* n_own) {
   constexpr int64_t kSetup = 2;
   int row_tiles, NR;
