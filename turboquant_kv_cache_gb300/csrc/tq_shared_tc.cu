@@ -1,10 +1,15 @@
-// Attention of many queries over one shared packed prefix on the tensor cores
-// (tcgen05, TMEM accumulators): the prefix part of tq_decode_attn_shared.
+// Attention of a batch over one shared packed prefix and each sequence's own
+// tokens on the tensor cores (tcgen05, TMEM accumulators): tq_decode_attn_shared
+// for 1..4 bits without QJL.
 //
 // Rows: the B sequences' queries of one KV head, R = B*G rows (sequence b,
-// head h -> row b*G + h), all of which attend to the same tokens.  A CTA owns
-// a tile of up to NR rows, one KV head and a slice of the prefix, which it
+// head h -> row b*G + h), all of which attend to the same prefix.  A prefix CTA
+// owns a tile of up to NR rows, one KV head and a slice of the prefix, which it
 // walks in tiles of 128 tokens; its codes are decoded once for all its rows.
+// The sequences' own tokens are the same work with other rows: a CTA then has
+// one sequence, its G rows and a slice of its tokens.  Both kinds are one
+// launch; every CTA writes a partial (m, l, O) per row, and the combine kernel
+// joins a row's partials and turns O out of the rotated domain.
 //
 //   S^T [128 tokens x NR]  = K^ (A, smem, K-major) . Q^ (B, smem, K-major)
 //   P^T                    = exp2(S^T - m), fp16, to shared memory
@@ -12,33 +17,56 @@
 //
 // Tokens are on the 128 TMEM lanes and rows on the columns, so the tensor
 // work and the softmax cost what the rows there are cost (a multiple of 32),
-// not the 128 of a row-per-lane tile.  A softmax thread has one token's p for
-// half of the rows; the sums l over tokens come from the same rounded p that
-// multiplies V: two warps read P back as mma.sync operands and multiply it by
-// a matrix of ones, in fp32.
+// not the 128 of a row-per-lane tile.  (Rows on the lanes with Q^ and P in
+// TMEM reads less shared memory, but one thread then has 64 tokens of a row in
+// sequence: 53.5 us against 52.2 us for 128 rows over 32768 tokens, 28.6
+// against 26.1 us for 16.)  A softmax thread has one token's p for half of the
+// rows; the sums l over tokens come from the same rounded p that multiplies V:
+// two warps read P back as mma.sync operands and multiply it by a matrix of
+// ones, in fp32.
 // The reference m of a row only moves when a score passes it by more than
 // 2^12 (it starts as the largest of 32 scores): the common step needs no
 // maximum over tokens, only one barrier vote; the rare one takes the maxima
 // and scales O and l.
 //
-// The sequences' own tokens are the same work with other rows: a CTA then has
-// one sequence, its G rows and a slice of its tokens.  Prefix and own CTAs
-// are one launch.
+// Roundings.  Scores, m, l and O are fp32.  Q^, K^ and V^ are rounded once to
+// fp16 (half a step, 2^-11 relative to each value) and p once (2^-11): the
+// tensor cores' operands, the same as the prefill's.  Their errors are
+// independent over d values and over the tokens, so an output is off by a few
+// 1e-4 of its scale.  p below 2^-25 of the reference is dropped; a slice holds
+// 2^-25 per token of that at most, 2^-12 of a softmax over 8192 such tokens.
 //
-// Warps: 0-7 softmax (warps 0-3 rows [0, NR/2), 4-7 the rest), 8 issues S, 9
-// issues O, 10 and 11 sum half of the rows each, 12-27 decode; softmax and decoder warps rotate the queries while
-// the first loads are in flight.  A decoder thread
+// Warps: 0-7 softmax (warps 0-3 rows [0, NR/2), 4-7 the rest), which also
+// rotate the queries while the first loads are in flight, 8 issues S, 9 issues
+// O, 10 and 11 sum half of the rows each, 12-27 decode.  A decoder thread
 // takes one 32-code group (two at head_dim 256) of the K tile and of the V
 // tile, its packed words loaded a tile ahead; at head_dim 64 half of the
 // decoder warps take K, half V.  Handoffs are mbarriers:
-//   q_full        Q^ is written
-//   kfull/kfree[b], vfull/vfree[b]  K^(t) (V^(t)) is decoded / S(t) (O(t)) is
-//                 done with it (two buffers each; one at head_dim 256)
-//   s_full[i]     S(t), t & 1 = i, is in TMEM    s_free[i] it has been read
-//   p_full[i]     P(t) is written                o_done[i] O += V(t) P(t) and l are done
+//   q_full      Q^ is written
+//   kfull[b]    K^(t) is decoded; its buffer is free when S(t) is done
+//   vfull[b]/vfree[b]  V^(t) is decoded / O(t) is done with it
+//               (two buffers of each; one at head_dim 256)
+//   s_full[i]   S(t), t & 1 = i, is in TMEM
+//   p_full[i]   P(t) is written and S(t) has been read
+//   o_done[i]   O += V(t) P(t) and l are done
 // Every wait is bounded at two levels, as in tq_tc.cuh; a CTA that gives up
 // stops decoding and issuing, waits for the products in flight and frees its
 // TMEM.
+//
+// Measured (GB300; graph replays of the call, the combine in it).  128 rows
+// over 32768 shared tokens and 512 own ones of 32 sequences, 8 KV heads,
+// head_dim 128, 3 bits: 52.2 us for 40.9 MB of cache and 17.2 GFLOP (floors
+// 6.1 and 8.8 us).  16 rows in 32 over 131072 shared tokens, 4 KV heads,
+// head_dim 256, 4 and 3 bits: 78.4 us for 136 MB (floor 20.3 us).  Neither the
+// memory nor the tensor cores bound it but the decode and the softmax on the
+// way between them: at 128 rows a tile takes 3400 cycles, of which 2400 the
+// softmax's exponentials, with issue slots 55 % and the shared-memory pipe
+// 49 % busy over the kernel (the products' operand reads on top); at head_dim
+// 256 it takes 4750, of which 2900 a decoder's two sides.  Sixteen softmax and
+// eight decoder warps: 57.9 us against 54.7 before the query rotation's
+// change.  Packed words through shared memory by asynchronous copies of 16
+// bytes a thread 62.8, by bulk copies 69.3.  Two CTAs of half the size on an
+// SM for 32 rows: as fast per tile (1.5 us against 1.4).
 #include <cuda_runtime.h>
 #include <math.h>
 
