@@ -420,8 +420,8 @@ int tq_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int head_dim, int64
  *   pos        device int32 [B] or NULL (0): token j of batch b has position
  *              pos[b] + j.  With a rotation, tokens whose position is outside
  *              [0, n_pos) are left out: nothing of theirs is written
- *   new_len    device int32 [B] or NULL: batch b has new_len[b] tokens, and
- *              what lies behind them is neither read nor written
+ *   new_len    device int32 [B] or NULL: batch b has new_len[b] tokens; the
+ *              rows behind them may hold anything and leave nothing behind
  *   q_out      device fp16 [B, Hq, T, head_dim]
  *   k_out, v_out, kv_cap, slot
  *              device fp16 [B, Hkv, kv_cap, head_dim]; token j of batch b goes

@@ -150,3 +150,23 @@ def test_page_workspace_query(tqlib):
     assert tqlib.tq_pages_workspace_bytes(4, 0, 3, ctypes.byref(nb)) == ARG
     assert tqlib.tq_pages_workspace_bytes(4, 32, -1, ctypes.byref(nb)) == ARG
     assert tqlib.tq_pages_workspace_bytes(4, 32, 3, None) == ARG
+
+
+def test_view_follows_the_table(tqlib):
+    """The kept C view is built anew when the table is another one of the same
+    storage, or the arrays are others."""
+    import torch
+    L = tb.make_layout(128, 32, 3)
+    codes = torch.zeros(16, 2, 32, 48, dtype=torch.uint8)
+    scales = torch.zeros(16, 2, 32, 4, dtype=torch.float16)
+    table = torch.zeros(16, dtype=torch.int32)
+    c = tb.PackedKV.of(L, codes, scales, page_table=table.view(2, 8))
+    assert (c.view().pages_per_seq, c.view().page_size) == (8, 32)
+    c.page_table = table.view(4, 4)
+    assert c.view().pages_per_seq == 4
+    c.page_table = table.view(2, 8)[:, :4]
+    assert c.view().pages_per_seq == 8 and c.capacity == 128
+    c.page_table = None
+    assert c.view().pages_per_seq == 0 and not c.view().page_table
+    c.codes = codes.clone()
+    assert c.view().codes == c.codes.data_ptr()

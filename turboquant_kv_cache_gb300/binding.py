@@ -115,12 +115,24 @@ def _ptr(t):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+# the current device without the check that CUDA has been initialised (a CUDA
+# tensor is at hand where it is used)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream(stream):
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:
         return _raw_stream(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
+
+
+def _stream_on(stream, dev):
+    """The same where dev is the current device."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
 
 
 class _on:
@@ -147,6 +159,11 @@ def _i32(t, n, name, dev):
     if t is not None and not (t.dtype is torch.int32 and t.numel() == n and t.get_device() == dev
                               and t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous int32 tensor of {n} values on the call's CUDA device")
+
+
+def _check_workspace(w, dev):
+    if w.get_device() != dev or not w.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the call's CUDA device")
 
 
 def _check(st, where):
@@ -227,6 +244,8 @@ class PackedKV:
     [B, pages_per_seq] (paged: token t of batch b is row t % page_size of
     page page_table[b, t // page_size])."""
 
+    _view = None
+
     def __init__(self, layout, lead_shape, device="cuda", S=None, page_table=None):
         cb, ns, qb = tq_layout_sizes(layout)
         self.layout = layout
@@ -292,13 +311,15 @@ class PackedKV:
         """The C view of the cache, kept between calls while its arrays stay
         where they are."""
         pt = self.page_table
-        at = (self.codes.data_ptr(), self.scales.data_ptr(), self.qjl.data_ptr() if self.qjl is not None else None,
-              self.rnorm.data_ptr() if self.rnorm is not None else None,
-              self.S.data_ptr() if self.S is not None else None, pt.data_ptr() if pt is not None else None)
-        kept = getattr(self, "_view", None)
+        if self.qjl is None and self.S is None:
+            at = (self.codes.data_ptr(), self.scales.data_ptr(), None, None, None)
+        else:
+            at = (self.codes.data_ptr(), self.scales.data_ptr(), _ptr(self.qjl), _ptr(self.rnorm), _ptr(self.S))
+        if pt is not None:
+            at += (pt.data_ptr(), self.lead_shape[2], self._table_stride())
+        kept = self._view
         if kept is None or kept[0] != at:
-            v = tq_kv_view(*at[:5], self.layout, at[5], self.lead_shape[2] if pt is not None else 0,
-                           self._table_stride())
+            v = tq_kv_view(*at[:5], self.layout, *(at[5:] or (None, 0, 0)))
             self._view = kept = (at, v)
         return kept[1]
 
@@ -375,6 +396,10 @@ def tq_dequantize_kv(packed, out_dtype=torch.float16, stream=None, out=None):
 
 def _cache_for(K, V, B):
     """Heads and S_cap of a K/V cache pair read by B sequences."""
+    if K.page_table is None and V.page_table is None:
+        k, v = K.lead_shape, V.lead_shape
+        if len(k) == 3 and k[0] >= B and k[1:] == v[1:] and v[0] >= B:
+            return k[1], k[2]
     if K.batch < B or V.batch < B or (K.heads, K.capacity) != (V.heads, V.capacity):
         raise ValueError("K and V caches must hold the same heads and slots for at least B sequences")
     return K.heads, K.capacity
@@ -472,43 +497,51 @@ def tq_decode_attn_shared(Kp, Vp, K, V, q, prefix_ctx=None, prefix_len=None, ctx
     sequence's own tokens behind it (K, V: caches as in tq_decode_attn, or
     None when there are none yet).  prefix_len: int32 CUDA tensor of one
     value, kv_len: int32 CUDA tensor [B]; prefix_ctx and ctx bound them."""
-    lib = _load()
-    dev = q.get_device()
-    if q.dim() != 3 or not _is(q, torch.float16, q.shape, dev) or dev < 0:
+    dev, shape = q.get_device(), q.shape
+    if len(shape) != 3 or dev < 0 or q.dtype is not torch.float16 or not q.is_contiguous():
         raise ValueError("q must be a contiguous fp16 CUDA tensor [B, Hq, head_dim]")
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         with _on(dev):
             return tq_decode_attn_shared(Kp, Vp, K, V, q, prefix_ctx, prefix_len, ctx, kv_len, softmax_scale, n_split,
                                          workspace, out, stream)
-    B, Hq, d = q.shape
+    B, Hq, d = shape
     Hkv, P_cap = _cache_for(Kp, Vp, 1)
-    prefix_ctx = P_cap if prefix_ctx is None else prefix_ctx
-    S_cap, kv, vv = 0, None, None
-    caches = (Kp, Vp)
+    if prefix_ctx is None:
+        prefix_ctx = P_cap
     if K is not None and V is not None:
         heads, S_cap = _cache_for(K, V, B)
         if heads != Hkv:
             raise ValueError("prefix and own caches must hold the same heads")
-        kv, vv = ctypes.byref(K.view()), ctypes.byref(V.view())
-        caches = (Kp, Vp, K, V)
-    ctx = S_cap if ctx is None else ctx
-    for c in caches:
-        if c.layout.head_dim != d or c.codes.get_device() != dev:
+        if K.codes.get_device() != dev or V.codes.get_device() != dev:
             raise ValueError("caches must have q's head_dim and device")
-    _i32(prefix_len, 1, "prefix_len", dev)
-    _i32(kv_len, B, "kv_len", dev)
+        kv, vv = ctypes.byref(K.view()), ctypes.byref(V.view())
+    else:
+        S_cap = 0
+        kv = vv = None
+    if ctx is None:
+        ctx = S_cap
+    # the call itself checks that all layouts agree
+    if Kp.layout.head_dim != d or Kp.codes.get_device() != dev or Vp.codes.get_device() != dev:
+        raise ValueError("caches must have q's head_dim and device")
+    if prefix_len is not None:
+        _i32(prefix_len, 1, "prefix_len", dev)
+    if kv_len is not None:
+        _i32(kv_len, B, "kv_len", dev)
     if workspace is None:
         need = tq_decode_shared_workspace_bytes(B, Hq, Hkv, d, prefix_ctx, ctx, n_split)
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    else:
+        _check_workspace(workspace, dev)
     if out is None:
         out = torch.empty_like(q)
-    elif not _is(out, torch.float16, q.shape, dev):
+    elif not _is(out, torch.float16, shape, dev):
         raise ValueError("out must be a contiguous tensor like q")
-    st = lib.tq_decode_attn_shared(ctypes.byref(Kp.view()), ctypes.byref(Vp.view()), P_cap, _ptr(prefix_len), prefix_ctx,
-                                   kv, vv, q.data_ptr(), B, Hq, Hkv, S_cap, _ptr(kv_len), ctx, softmax_scale,
-                                   out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                   n_split, _stream(stream))
-    _check(st, "tq_decode_attn_shared")
+    st = _load().tq_decode_attn_shared(ctypes.byref(Kp.view()), ctypes.byref(Vp.view()), P_cap, _ptr(prefix_len),
+                                       prefix_ctx, kv, vv, q.data_ptr(), B, Hq, Hkv, S_cap, _ptr(kv_len), ctx, softmax_scale,
+                                       out.data_ptr(), workspace.data_ptr(), workspace.nbytes, n_split,
+                                       _stream_on(stream, dev))
+    if st:
+        _check(st, "tq_decode_attn_shared")
     return out
 
 
@@ -522,52 +555,63 @@ def tq_qkv_norm_rope(qkv, Hq, Hkv, head_dim, q_weight=None, k_weight=None, eps=1
     default to new arrays of cap = T (cap: their third dimension).  In an
     output that is given, what no token goes to is left as it was; new ones
     start as zeros when new_len is given."""
-    lib = _load()
     d = head_dim
-    dev = qkv.get_device()
-    if qkv.dim() != 3 or qkv.shape[2] != (Hq + 2 * Hkv) * d or qkv.stride(2) != 1 or dev < 0:
+    dev, shape = qkv.get_device(), qkv.shape
+    if len(shape) != 3 or shape[2] != (Hq + 2 * Hkv) * d or dev < 0:
         raise ValueError("qkv must be a CUDA tensor [B, T, (Hq + 2 Hkv) head_dim] with a contiguous last dimension")
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         with _on(dev):
             return tq_qkv_norm_rope(qkv, Hq, Hkv, d, q_weight, k_weight, eps, rope, interleaved, pos, new_len, slot,
                                     q_out, k_out, v_out, stream)
-    B, T, row = qkv.shape
-    sb, st, _ = qkv.stride()
-    if T > 1 and B > 1 and sb != T * st:
-        qkv = qkv.contiguous()
-    elif T > 1:
-        row = st
-    elif B > 1:
-        row = sb
+    B, T, row = shape
+    if not qkv.is_contiguous():
+        sb, st, one = qkv.stride()
+        if one != 1:
+            raise ValueError("qkv must be a CUDA tensor [B, T, (Hq + 2 Hkv) head_dim] with a contiguous last dimension")
+        if T > 1 and B > 1 and sb != T * st:
+            qkv = qkv.contiguous()
+        elif T > 1:
+            row = st
+        elif B > 1:
+            row = sb
     f32, f16 = torch.float32, torch.float16
-    for w in (q_weight, k_weight):
-        if w is not None and not _is(w, f32, (d,), dev):
+    if q_weight is not None:
+        if not _is(q_weight, f32, (d,), dev):
             raise ValueError("norm weights must be contiguous fp32 tensors [head_dim] on qkv's device")
-    n_pos, rot = 0, 0
+    if k_weight is not None:
+        if not _is(k_weight, f32, (d,), dev):
+            raise ValueError("norm weights must be contiguous fp32 tensors [head_dim] on qkv's device")
+    n_pos = rot = 0
     if rope is not None:
-        if rope.dim() != 2 or not _is(rope, f32, rope.shape, dev):
+        table = rope.shape
+        if len(table) != 2 or rope.dtype is not f32 or rope.get_device() != dev or not rope.is_contiguous():
             raise ValueError("rope must be a contiguous fp32 tensor [n_pos, rot_dim] on qkv's device")
-        n_pos, rot = rope.shape
-    _i32(pos, B, "pos", dev)
-    _i32(new_len, B, "new_len", dev)
-    _i32(slot, B, "slot", dev)
+        n_pos, rot = table
+    fresh = torch.empty if new_len is None and pos is None and slot is None else torch.zeros
+    if pos is not None:
+        _i32(pos, B, "pos", dev)
+    if new_len is not None:
+        _i32(new_len, B, "new_len", dev)
+    if slot is not None:
+        _i32(slot, B, "slot", dev)
     if q_out is None or k_out is None or v_out is None:
-        new = torch.empty if new_len is None and pos is None and slot is None else torch.zeros
         if q_out is None:
-            q_out = new((B, Hq, T, d), dtype=f16, device=qkv.device)
+            q_out = fresh((B, Hq, T, d), dtype=f16, device=qkv.device)
         if k_out is None:
-            k_out = new((B, Hkv, T, d), dtype=f16, device=qkv.device)
+            k_out = fresh((B, Hkv, T, d), dtype=f16, device=qkv.device)
         if v_out is None:
-            v_out = new(tuple(k_out.shape), dtype=f16, device=qkv.device)
-    cap = k_out.shape[2] if k_out.dim() == 4 else -1
-    kv_shape = (B, Hkv, cap, d)
-    if not (_is(q_out, f16, (B, Hq, T, d), dev) and _is(k_out, f16, kv_shape, dev) and _is(v_out, f16, kv_shape, dev)):
+            v_out = fresh(tuple(k_out.shape), dtype=f16, device=qkv.device)
+    kv_shape = k_out.shape
+    cap = kv_shape[2] if len(kv_shape) == 4 else -1
+    if (kv_shape != (B, Hkv, cap, d) or not _is(q_out, f16, (B, Hq, T, d), dev) or not _is(k_out, f16, kv_shape, dev)
+            or not _is(v_out, f16, kv_shape, dev)):
         raise ValueError("outputs must be contiguous fp16 tensors [B, Hq, T, d], [B, Hkv, cap, d] on qkv's device")
-    st = lib.tq_qkv_norm_rope(qkv.data_ptr(), _dtype_code(qkv.dtype), B, T, Hq, Hkv, d, row, _ptr(q_weight),
-                              _ptr(k_weight), eps, _ptr(rope), n_pos, rot, 1 if interleaved else 0, _ptr(pos),
-                              _ptr(new_len), q_out.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), cap, _ptr(slot),
-                              _stream(stream))
-    _check(st, "tq_qkv_norm_rope")
+    st = _load().tq_qkv_norm_rope(qkv.data_ptr(), _dtype_code(qkv.dtype), B, T, Hq, Hkv, d, row, _ptr(q_weight),
+                                  _ptr(k_weight), eps, _ptr(rope), n_pos, rot, 1 if interleaved else 0, _ptr(pos),
+                                  _ptr(new_len), q_out.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), cap, _ptr(slot),
+                                  _stream_on(stream, dev))
+    if st:
+        _check(st, "tq_qkv_norm_rope")
     return q_out, k_out, v_out
 
 
@@ -617,6 +661,8 @@ def _pool_call(pool, n, workspace, result):
     if workspace is None:
         workspace = torch.empty(tq_pages_workspace_bytes(pool.n_pages.shape[0], pool.ref.shape[0], n),
                                 dtype=torch.uint8, device=pool.ref.device)
+    else:
+        _check_workspace(workspace, pool.dev)
     if result is None:
         result = torch.empty(4, dtype=torch.int32, device=pool.ref.device)
     else:
@@ -636,14 +682,15 @@ def tq_pages_fork(pool, parent, child, share_len, new_len, workspace=None, resul
     _i32(child, n, "child", dev)
     _i32(share_len, n, "share_len", dev)
     _i32(new_len, n, "new_len", dev)
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         with _on(dev):
             return tq_pages_fork(pool, parent, child, share_len, new_len, workspace, result, stream)
     workspace, result = _pool_call(pool, n, workspace, result)
-    st = _load().tq_pages_fork(pool.ref_struct, pool.views, len(pool.caches), pool.heads, _ptr(parent), _ptr(child),
-                               _ptr(share_len), _ptr(new_len), n, result.data_ptr(), workspace.data_ptr(),
-                               workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(st, "tq_pages_fork")
+    st = _load().tq_pages_fork(pool.ref_struct, pool.views, len(pool.caches), pool.heads, parent.data_ptr(),
+                               child.data_ptr(), share_len.data_ptr(), new_len.data_ptr(), n, result.data_ptr(), workspace.data_ptr(),
+                               workspace.nbytes, _stream_on(stream, pool.dev))
+    if st:
+        _check(st, "tq_pages_fork")
     return result
 
 
@@ -653,23 +700,25 @@ def tq_pages_free(pool, seqs, keep_len=None, stream=None):
     n, dev = seqs.numel(), pool.dev
     _i32(seqs, n, "seqs", dev)
     _i32(keep_len, n, "keep_len", dev)
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         with _on(dev):
             return tq_pages_free(pool, seqs, keep_len, stream)
-    st = _load().tq_pages_free(pool.ref_struct, seqs.data_ptr(), _ptr(keep_len), n, _stream(stream))
-    _check(st, "tq_pages_free")
+    st = _load().tq_pages_free(pool.ref_struct, seqs.data_ptr(), _ptr(keep_len), n, _stream_on(stream, pool.dev))
+    if st:
+        _check(st, "tq_pages_free")
 
 
 def tq_pages_compact(pool, workspace=None, result=None, stream=None):
     """Moves the pages in use to the front of the pool in all of its caches.
     Returns the result tensor {0, pages in use, pages moved, 0}."""
-    if pool.dev != torch.cuda.current_device():
+    if pool.dev != _current_device():
         with _on(pool.dev):
             return tq_pages_compact(pool, workspace, result, stream)
     workspace, result = _pool_call(pool, 0, workspace, result)
     st = _load().tq_pages_compact(pool.ref_struct, pool.views, len(pool.caches), pool.heads, result.data_ptr(),
-                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(st, "tq_pages_compact")
+                                  workspace.data_ptr(), workspace.nbytes, _stream_on(stream, pool.dev))
+    if st:
+        _check(st, "tq_pages_compact")
     return result
 
 

@@ -1038,8 +1038,8 @@ int decode_shared_impl(const tq_kv_view* Kp, const tq_kv_view* Vp, int64_t P_cap
   CodecParams PK, PV;
   int st = make_params(&Kp->layout, &PK);
   if (st != TQ_OK) return st;
-  st = make_params(&Vp->layout, &PV);
-  if (st != TQ_OK) return st;
+  if (same_layout(Kp->layout, Vp->layout)) PV = PK;
+  else if ((st = make_params(&Vp->layout, &PV)) != TQ_OK) return st;
   if (PK.d != PV.d || PV.m > kMaxQjlV || PV.bits > 4 || (PK.bits > 4 && PV.m)) return TQ_ERR_UNSUPPORTED;
   Codebook8 cbk;
   if (PK.bits == 8 && make_codebook8(&Kp->layout, &cbk) != TQ_OK) return TQ_ERR_UNSUPPORTED;
