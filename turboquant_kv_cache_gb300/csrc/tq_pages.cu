@@ -21,6 +21,13 @@
 // A small pool's call is bound by its launches (2 us each on the GPU, 3 on the
 // host), so there one block does everything but the move: a fork of 4 entries
 // over 512 pages is two launches instead of four.
+//
+// Bound: launches, and for large pools the copies, which read and write every
+// moved byte once.  Measured in graph replays, with the call that frees pages
+// and a reset of the books before each: 3 freed, 4 forked and 4 grown over 512
+// pages of 28 KB 10.7 us; 60, 150 and 40 over 2000 pages in 64 arrays (134 MB
+// moved, 20 us at a copy's rate) 36.8 us; 512 pages compacted 8.8 us, 2500 in
+// 64 arrays (557 MB, 83 us) 107.5 us.
 #include <cuda_runtime.h>
 
 #include "tq_device.cuh"
