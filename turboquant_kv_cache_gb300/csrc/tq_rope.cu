@@ -8,15 +8,18 @@
 // in fp32 whatever the input's type, rounded to fp16 once at the end.  Value
 // rows are only converted.
 //
-// Mapping: a thread owns 8 consecutive values of a row, d/8 threads a row, so
-// a row is one coalesced read and write of 16 bytes a thread; the sum of
-// squares is a shuffle reduction and a half-split pair's other value comes by
-// shuffle from the lane that owns it.
+// Mapping: a thread owns 16 values of a row, 8 of the rotated lower half and
+// the 8 that they are paired with, or 16 consecutive ones behind the rotated
+// part: no value crosses threads but for the sum of squares, a shuffle
+// reduction over the row's d/16 threads.  A row is read and written in pieces
+// of 16 bytes a thread.  (8 consecutive values a thread and the pair's other
+// value by shuffle: 153 us against 132 for 32768 tokens; the shuffles, and the
+// weights read anew for every row, kept the load/store pipe 75 % busy.)
 //
 // Bound: memory once there are many tokens, since a row is read and written
 // once and nothing else is (822 MB for 32768 tokens of 48 heads, head_dim 128,
-// fp16: 153 us, 5.4 TB/s, 80 % of a copy's rate); for a few tokens the launch
-// (8 tokens 1.95 us in a graph, 15 tokens of fp32 rows at head_dim 256 2.0).
+// fp16: 132 us, 6.2 TB/s, 93 % of a copy's rate); for a few tokens the launch
+// (8 tokens 2.1 us in a graph, 15 tokens of fp32 rows at head_dim 256 2.2).
 #include <cuda_runtime.h>
 
 #include "tq_device.cuh"
@@ -84,22 +87,30 @@ __device__ __forceinline__ void load_floats(const float* p, float* v) {
 }
 
 // NEXT: rotated pairs are neighbours (2i, 2i+1); otherwise (i, i + rot/2).
-// A block's kThreads / (D/8) thread groups take consecutive token rows b*T + j
+// A block's kThreads / (D/16) thread groups take consecutive token rows b*T + j
 // (grid x) and the same R heads (grid y): a group has R rows of one token in
 // flight, contiguous in the input, and reads the token's cosines and sines
-// once for all of them; the block's outputs of a head are one run.
+// once for all of them, and the weights once for heads of one kind; the
+// block's outputs of a head are one run.
 template <int D, bool F32, bool NEXT, int R>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ RopeArgs a) {
-  constexpr int TPR = D / 8;              // threads per row
+  constexpr int TPR = D / 16;             // threads per row
   constexpr int HPB = kThreads / TPR;     // groups per block
-  const int sub = threadIdx.x % TPR, e0 = 8 * sub;
+  // the thread's chunks of 8 values: one of the rotated lower half and its
+  // counterpart of the upper half, or two neighbours behind the rotated part
+  const int sub = threadIdx.x % TPR, lows = a.rot / 16;
+  const bool in = sub < lows;
+  const int e0 = in ? 8 * sub : 16 * sub, e1 = in ? e0 + a.rot / 2 : e0 + 8;
   const int64_t tok_at = (int64_t)blockIdx.x * HPB + threadIdx.x / TPR, tok = imin64(tok_at, a.tokens - 1);
   const int h0 = blockIdx.y * R;
   const int H = a.Hq + 2 * a.Hkv, HT = a.Hq + a.Hkv;   // all heads, and those with a position
-  Raw<F32> raw[R];
+  Raw<F32> raw[R][2];
 #pragma unroll
-  for (int i = 0; i < R; ++i)
-    raw[i] = load8<F32>(a.x, tok * a.row_stride + (int64_t)min(h0 + i, H - 1) * D + e0);
+  for (int i = 0; i < R; ++i) {
+    const int64_t row = tok * a.row_stride + (int64_t)min(h0 + i, H - 1) * D;
+    raw[i][0] = load8<F32>(a.x, row + e0);
+    raw[i][1] = load8<F32>(a.x, row + e1);
+  }
   const int b = (int)(tok / a.T), j = (int)(tok - (int64_t)b * a.T);
   const int n_new = a.new_len ? a.new_len[b] : a.T;
   const int64_t p = (a.pos ? (int64_t)a.pos[b] : 0) + j;
@@ -107,56 +118,57 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
   // a token behind its batch's length, or whose position has no row in the
   // table, is left out (its lanes stay for the shuffles of their warp)
   const bool ok = tok_at < a.tokens && j < n_new && (!a.rot || (p >= 0 && p < a.n_pos));
-  // the thread's cosines and sines: of its values' pairs
-  constexpr int NC = NEXT ? 4 : 8;
-  float c[NC], s[NC];
-  const int half = a.rot / 2;
-  const bool in = e0 < a.rot, lower = e0 < half;
+  // cosines and sines of the thread's pairs: (e0 + k, e1 + k), or four
+  // neighbouring pairs of each chunk
+  float c[8], s[8];
   if (in && ok) {
-    const float* row = a.rope + p * a.rot + (NEXT ? e0 / 2 : (lower ? e0 : e0 - half));
-    load_floats<NC>(row, c);
-    load_floats<NC>(row + half, s);
+    const float* row = a.rope + p * a.rot;
+    const int half = a.rot / 2;
+    if constexpr (NEXT) {
+      load_floats<4>(row + e0 / 2, c);
+      load_floats<4>(row + e1 / 2, c + 4);
+      load_floats<4>(row + half + e0 / 2, s);
+      load_floats<4>(row + half + e1 / 2, s + 4);
+    } else {
+      load_floats<8>(row + e0, c);
+      load_floats<8>(row + half + e0, s);
+    }
   }
+  const float* have = nullptr;   // the weights in wv
+  float wv[16];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int h = h0 + i;
-    float v[8];
-    floats<F32>(raw[i], v);
-    const float* w = h < a.Hq ? a.wq : a.wk;
-    float ss = 0.f;
+    const float* w = h < a.Hq ? a.wq : (h < HT ? a.wk : nullptr);
+    float v[16];
+    floats<F32>(raw[i][0], v);
+    floats<F32>(raw[i][1], v + 8);
+    if (w) {   // the same for the whole block
+      if (w != have) {
+        load_floats<8>(w + e0, wv);
+        load_floats<8>(w + e1, wv + 8);
+        have = w;
+      }
+      float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) ss = fmaf(v[k], v[k], ss);
+      for (int k = 0; k < 8; ++k) {
+        s0 = fmaf(v[k], v[k], s0);
+        s1 = fmaf(v[8 + k], v[8 + k], s1);
+      }
+      float ss = s0 + s1;
 #pragma unroll
-    for (int o = 1; o < TPR; o <<= 1) ss += __shfl_xor_sync(kFull, ss, o);
-    if (h < HT && w) {
+      for (int o = 1; o < TPR; o <<= 1) ss += __shfl_xor_sync(kFull, ss, o);
       const float r = rsqrtf(ss * (1.f / D) + a.eps);
-      float wv[8];
-      load_floats<8>(w + e0, wv);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = v[k] * r * wv[k];
+      for (int k = 0; k < 16; ++k) v[k] = v[k] * r * wv[k];
     }
-    if (a.rot) {
-      if constexpr (NEXT) {
-        if (h < HT && in) {
+    if (in && h < HT) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float x = v[2 * k], y = v[2 * k + 1];
-            v[2 * k] = x * c[k] - y * s[k];
-            v[2 * k + 1] = y * c[k] + x * s[k];
-          }
-        }
-      } else {
-        // the other value of each pair is `half` further or back: rot is a
-        // multiple of 16, so it is one other lane's same place
-        const int lane = threadIdx.x & 31;
-        const int other = in ? (lower ? lane + half / 8 : lane - half / 8) : lane;
-        float o[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) o[k] = __shfl_sync(kFull, v[k], other);
-        if (h < HT && in) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = lower ? v[k] * c[k] - o[k] * s[k] : v[k] * c[k] + o[k] * s[k];
-        }
+      for (int k = 0; k < 8; ++k) {
+        const int x = NEXT ? 2 * k : k, y = NEXT ? 2 * k + 1 : k + 8;
+        const float vx = v[x], vy = v[y];
+        v[x] = vx * c[k] - vy * s[k];
+        v[y] = vy * c[k] + vx * s[k];
       }
     }
     if (h >= H || !ok) continue;
@@ -169,22 +181,28 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
       dst = kv < a.Hkv ? a.k + (((int64_t)b * a.Hkv + kv) * a.kv_cap + at) * D
                        : a.v + (((int64_t)b * a.Hkv + kv - a.Hkv) * a.kv_cap + at) * D;
     }
-    uint32_t o[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) o[k] = (uint32_t)f2h(v[2 * k]) | ((uint32_t)f2h(v[2 * k + 1]) << 16);
-    *reinterpret_cast<uint4*>(dst + e0) = make_uint4(o[0], o[1], o[2], o[3]);
+    for (int x = 0; x < 2; ++x) {
+      uint32_t o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const __half2 y = __floats2half2_rn(v[8 * x + 2 * k], v[8 * x + 2 * k + 1]);
+        o[k] = *reinterpret_cast<const uint32_t*>(&y);
+      }
+      *reinterpret_cast<uint4*>(dst + (x ? e1 : e0)) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
   }
 }
 
 template <int D, bool F32, bool NEXT>
 void launch_rows(const RopeArgs& a, int64_t tokens, cudaStream_t st) {
-  constexpr int HPB = kThreads / (D / 8);
+  constexpr int HPB = kThreads / (D / 16);
   const int H = a.Hq + 2 * a.Hkv;
   // Rows per thread group: one while that does not fill the GPU (latency
   // counts), else the number from 4 down to 2 that leaves the fewest without
   // a head: several rows in flight and the cosines and sines read once for
-  // them.  8 tokens of 48 heads: 1 row 1.95 us, 2 rows 2.25, 4 rows 2.8;
-  // 32768 tokens: 1 row 239 us, 2 rows 176, 4 rows 153.
+  // them.  8 tokens of 48 heads: 1 or 2 rows 2.2 us, 4 rows 2.5; 32768 tokens:
+  // 1 row 151 us, 2 rows 136, 3 rows 141, 4 rows 132.
   const int64_t blocks = (tokens + HPB - 1) / HPB;
   int R = 1;
   if (blocks * H > 152 * 16) {
