@@ -217,7 +217,8 @@ def test_free_twice_out_of_range_and_longer_than_held(tqlib):
 
 @pytest.mark.parametrize("n_seqs,pps,num_pages,page,steps", [(9, 7, 40, 32, 60), (64, 40, 1500, 64, 25),
                                                               (300, 12, 2049, 32, 20), (1300, 5, 5000, 32, 6),
-                                                              (40, 30, 17000, 32, 8), (420, 48, 2500, 32, 8)])
+                                                              (40, 30, 17000, 32, 8), (420, 48, 2500, 32, 8),
+                                                              (1300, 90, 6000, 32, 4)])
 def test_random_runs(tqlib, n_seqs, pps, num_pages, page, steps):
     """Random steps of a scheduler, more sequences and pages than a block
     takes at once, until the pool is short; pools on both sides of the size

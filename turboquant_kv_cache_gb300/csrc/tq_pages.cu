@@ -20,13 +20,14 @@
 //   move    page contents
 // A small pool's call is bound by its launches (2 us each on the GPU, 3 on the
 // host), so there one block does everything but the move: a fork of 4 entries
-// over 512 pages is two launches instead of four.
+// over 512 pages is two launches instead of four, and so is one of 190 entries
+// of up to 128 pages over 2000 pages (with the copies 32.3 us against 36.8).
 //
 // Bound: launches, and for large pools the copies, which read and write every
 // moved byte once.  Measured in graph replays, with the call that frees pages
 // and a reset of the books before each: 3 freed, 4 forked and 4 grown over 512
-// pages of 28 KB 10.7 us; 60, 150 and 40 over 2000 pages in 64 arrays (134 MB
-// moved, 20 us at a copy's rate) 36.8 us; 512 pages compacted 8.8 us, 2500 in
+// pages of 28 KB 11.0 us; 60, 150 and 40 over 2000 pages in 64 arrays (134 MB
+// moved, 20 us at a copy's rate) 32.3 us; 512 pages compacted 8.8 us, 2500 in
 // 64 arrays (557 MB, 83 us) 107.5 us.
 #include <cuda_runtime.h>
 
@@ -38,7 +39,8 @@ namespace {
 constexpr int kChunk = 1024;          // pages per block of count and assign
 constexpr int kThreads = 256;
 constexpr int kPlanThreads = 1024;
-constexpr int kSmallPages = 16384;    // pages, and table entries that a call may touch, that one block takes
+constexpr int kSmallPages = 16384;    // pages that one block takes (16 a thread)
+constexpr int kSmallEntries = 32768;  // table entries a call may touch that one block takes
 constexpr int kMaxArrays = 128;       // cache arrays one move launch takes
 constexpr int kPiece = 16384;         // bytes one block copies at a time: four 16-byte loads in flight a thread
 constexpr int kMaxPerSeq = 1 << 20;   // pages of a sequence: kPlanThreads of them sum below 2^31
@@ -670,7 +672,7 @@ extern "C" int tq_pages_fork(const tq_page_pool* pool, const tq_kv_view* caches,
   const tq::ForkArgs a{*pool, parent, child, share_len, new_len, result, n, w};
   const int chunks = (pool->num_pages + tq::kChunk - 1) / tq::kChunk;
   bool ok;
-  if (pool->num_pages <= tq::kSmallPages && (int64_t)n * pool->pages_per_seq <= tq::kSmallPages) {
+  if (pool->num_pages <= tq::kSmallPages && (int64_t)n * pool->pages_per_seq <= tq::kSmallEntries) {
     const int per = (pool->num_pages + tq::kPlanThreads - 1) / tq::kPlanThreads;
     ok = tq::launch(tq::pages_fork_small_kernel, 1, tq::kPlanThreads, false, s, a, per);
   } else {
@@ -708,7 +710,7 @@ extern "C" int tq_pages_compact(const tq_page_pool* pool, const tq_kv_view* cach
   const tq::CompactArgs a{*pool, result, w};
   const int chunks = (pool->num_pages + tq::kChunk - 1) / tq::kChunk;
   bool ok;
-  if (pool->num_pages <= tq::kSmallPages && (int64_t)pool->n_seqs * pool->pages_per_seq <= tq::kSmallPages) {
+  if (pool->num_pages <= tq::kSmallPages && (int64_t)pool->n_seqs * pool->pages_per_seq <= tq::kSmallEntries) {
     const int per = (pool->num_pages + tq::kPlanThreads - 1) / tq::kPlanThreads;
     ok = tq::launch(tq::pages_compact_small_kernel, 1, tq::kPlanThreads, false, s, a, per);
   } else {
