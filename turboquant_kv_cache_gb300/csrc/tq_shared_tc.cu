@@ -55,9 +55,9 @@
 //
 // Measured (GB300; graph replays of the call, the combine in it).  128 rows
 // over 32768 shared tokens and 512 own ones of 32 sequences, 8 KV heads,
-// head_dim 128, 3 bits: 52.2 us for 40.9 MB of cache and 17.2 GFLOP (floors
+// head_dim 128, 3 bits: 52.1 us for 40.9 MB of cache and 17.2 GFLOP (floors
 // 6.1 and 8.8 us).  16 rows in 32 over 131072 shared tokens, 4 KV heads,
-// head_dim 256, 4 and 3 bits: 78.4 us for 136 MB (floor 20.3 us).  Neither the
+// head_dim 256, 4 and 3 bits: 77.1 us for 136 MB (floor 20.3 us).  Neither the
 // memory nor the tensor cores bound it but the decode and the softmax on the
 // way between them: at 128 rows a tile takes 3400 cycles, of which 2400 the
 // softmax's exponentials, with issue slots 55 % and the shared-memory pipe
@@ -381,6 +381,11 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
   const int n_tok = t_hi > t_lo ? (int)(t_hi - t_lo) : 0;
   const int n_tiles = (n_tok + kTile - 1) / kTile;
 
+  // P(t) is written once O(t - 2) and l are done with its buffer: up to 64 rows
+  // S(t) is issued only then, so that a softmax warp has one wait a tile (16
+  // rows, head_dim 256: 77.0 us against 78.7); past them the sums take longer
+  // and the softmax waits itself (128 rows: 52.5 us against 54.2)
+  const bool s_waits = NR <= 64;
   // K, V buffers, Q^, two P buffers
   const uint32_t pbytes = (uint32_t)NR * kTile * 2;
   const uint32_t aK = su32(smem), aV = aK + NB * C::KB, aQ = aV + NB * C::VB, aP = aQ + (uint32_t)NR * D * 2;
@@ -465,9 +470,10 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
       for (int e = 0; e < 32; e += 2) {
         const uint4& x = qv[e >> 3];
         const uint32_t u = (e & 6) == 0 ? x.x : (e & 6) == 2 ? x.y : (e & 6) == 4 ? x.z : x.w;
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
-        v[e] = flip(f.x * qn, (sb >> e) & 1u);
-        v[e + 1] = flip(f.y * qn, (sb >> (e + 1)) & 1u);
+        const uint32_t us = u ^ ((sb >> e & 1u) << 15 | (sb >> (e + 1) & 1u) << 31);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&us));
+        v[e] = f.x * qn;
+        v[e + 1] = f.y * qn;
       }
       fetch_query(i + kSoftWarps);
 #pragma unroll
@@ -610,7 +616,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     bool ok = n_tiles > 0 && wait(q_full, 0);
     for (int t = 0; t < n_tiles && ok; ++t) {
       const int bf = t % NB;
-      ok = wait(kfull + 8 * bf, (uint32_t)(t / NB) & 1) && (t < 2 || wait(p_full + 8 * (t & 1), (uint32_t)((t >> 1) - 1) & 1));
+      ok = wait(kfull + 8 * bf, (uint32_t)(t / NB) & 1) && (t < 2 || wait((s_waits ? o_done : p_full) + 8 * (t & 1), (uint32_t)((t >> 1) - 1) & 1));
       if (!ok) break;
       fence_after();
       __syncwarp();
@@ -732,7 +738,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
         return hmax2(mx, kOver) != kOver;
       };
       wait(s_full + 8 * (t & 1), (uint32_t)(t >> 1) & 1);
-      if (t >= 2) wait(o_done + 8 * (t & 1), (uint32_t)((t >> 1) - 1) & 1);   // P(t - 2) has been read
+      if (!s_waits && t >= 2) wait(o_done + 8 * (t & 1), (uint32_t)((t >> 1) - 1) & 1);
       fence_after();
       __syncwarp();
       if (t == 0) {
@@ -924,8 +930,8 @@ bool shared_tc_eligible(const CodecParams& PK, const CodecParams& PV) {
 // tokens in waves behind it, which is shorter when there is much prefix or
 // there are many sequences.
 // 7 sequences of 333 tokens, 2011 shared ones, 8 KV heads at head_dim 64: one
-// wave of 3 tiles @@ us, two of 1 and 2 tiles 15.6 us.  8 sequences of 256 and
-// 131072 shared ones, 4 KV heads at head_dim 256: one wave of 35 tiles @@ us,
+// wave of 3 tiles 10.6 us, two of 1 and 2 tiles 15.6 us.  8 sequences of 256 and
+// 131072 shared ones, 4 KV heads at head_dim 256: one wave of 35 tiles 93.6 us,
 // two of 27 and 1 tiles 82.8 us.
 void shared_tc_splits(int d, int B, int G, int Hkv, int64_t prefix_ctx, int64_t ctx, int* n_prefix, int* n_own) {
   constexpr int64_t kSetup = 2;
