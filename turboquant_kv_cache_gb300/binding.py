@@ -316,10 +316,11 @@ class PackedKV:
         else:
             at = (self.codes.data_ptr(), self.scales.data_ptr(), _ptr(self.qjl), _ptr(self.rnorm), _ptr(self.S))
         if pt is not None:
-            at += (pt.data_ptr(), self.lead_shape[2], self._table_stride())
+            at += (pt.data_ptr(), self.lead_shape[2], pt.shape, pt.stride())
         kept = self._view
         if kept is None or kept[0] != at:
-            v = tq_kv_view(*at[:5], self.layout, *(at[5:] or (None, 0, 0)))
+            paging = (None, 0, 0) if pt is None else (at[5], at[6], self._table_stride())
+            v = tq_kv_view(*at[:5], self.layout, *paging)
             self._view = kept = (at, v)
         return kept[1]
 
@@ -396,9 +397,13 @@ def tq_dequantize_kv(packed, out_dtype=torch.float16, stream=None, out=None):
 
 def _cache_for(K, V, B):
     """Heads and S_cap of a K/V cache pair read by B sequences."""
-    if K.page_table is None and V.page_table is None:
-        k, v = K.lead_shape, V.lead_shape
-        if len(k) == 3 and k[0] >= B and k[1:] == v[1:] and v[0] >= B:
+    k, v, table = K.lead_shape, V.lead_shape, K.page_table
+    if table is V.page_table and len(k) == 3 and k[1:] == v[1:]:   # the usual pair
+        if table is not None:
+            n, pages = table.shape
+            if n >= B:
+                return k[1], pages * k[2]
+        elif k[0] >= B and v[0] >= B:
             return k[1], k[2]
     if K.batch < B or V.batch < B or (K.heads, K.capacity) != (V.heads, V.capacity):
         raise ValueError("K and V caches must hold the same heads and slots for at least B sequences")
