@@ -320,3 +320,43 @@ def test_reports_timeout_and_stays_exact(tqlib):
         tb.tq_device_status(clear=True)
     assert torch.equal(run(), ref)
     assert tb.tq_device_status() == 0
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_offsets_past_32_bits(tqlib, paged):
+    """A prefix and own tokens that lie more than 2^32 bytes into their
+    arrays give what the same records give in small arrays."""
+    from turboquant_kv_cache_gb300 import binding as tb
+    d, B, Hq, Hkv, P, S = 256, 2, 8, 4, 700, 90
+    Kp, Vp, K, V, q = _inputs(tb, d, (32, 4, 0, 0), (32, 3, 0, 0), B, Hq, Hkv, P, S)
+    want = tb.tq_decode_attn_shared(Kp, Vp, K, V, q)
+
+    def far(c, table):
+        n = c.lead_shape[0]
+        if paged:   # pages of 32 tokens at the end of a pool of 2^33 bytes of codes (K) and less
+            page, pps = 32, -(-c.lead_shape[2] // 32)
+            pool = (1 << 33) // (Hkv * page * 128) + n * pps
+            lead = (pool, Hkv, page)
+        else:       # heads 2^31 bytes apart and more
+            lead = (n, Hkv, (1 << 31) // 96 + 1)
+        codes = torch.empty(lead + c.codes.shape[3:], dtype=torch.uint8, device="cuda")
+        scales = torch.empty(lead + c.scales.shape[3:], dtype=torch.float16, device="cuda")
+        for src, dst in ((c.codes, codes), (c.scales, scales)):
+            for b in range(n):
+                if not paged:
+                    dst[b, :, :c.lead_shape[2]] = src[b]
+                    continue
+                for j in range(pps):
+                    part = src[b, :, 32 * j:32 * j + 32]
+                    dst[pool - n * pps + b * pps + j, :, :part.shape[1]] = part
+        if paged and table is None:
+            table = (torch.arange(n * pps, dtype=torch.int32, device="cuda") + (pool - n * pps)).view(n, pps)
+        return tb.PackedKV.of(c.layout, codes, scales, page_table=table)
+
+    Kp2 = far(Kp, None)
+    Vp2 = far(Vp, Kp2.page_table)
+    assert torch.equal(tb.tq_decode_attn_shared(Kp2, Vp2, K, V, q, prefix_ctx=P), want)
+    del Kp2, Vp2
+    K2 = far(K, None)
+    V2 = far(V, K2.page_table)
+    assert torch.equal(tb.tq_decode_attn_shared(Kp, Vp, K2, V2, q, ctx=S), want)
