@@ -506,190 +506,191 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     if (lane == 0) arrive(q_full);
   };
 
-  if (warp >= kDec0 / 32) {
-    // ================= decoders
+  if (warp >= kSoftWarps) {
+    // whole warpgroups (4 warps) execute one instruction each
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::OTHER));
-    if (n_tiles == 0) {
-      begin();
-    } else {
-      const int dt = tid - kDec0;
-      const int st = C::SPLIT ? dt % C::SIDE : dt;    // thread within its side
-      const bool do_k = !C::SPLIT || dt < C::SIDE, do_v = !C::SPLIT || dt >= C::SIDE;
-      // the thread's groups: number grp of the tokens tok0 and, at head_dim
-      // 256, kStep tokens on.  A group's number turns with its token, so that
-      // the eight lanes of one access hit different banks whatever the
-      // records' pitch.
-      constexpr int kStep = C::SIDE / C::G8;
-      static_assert(C::N == 1 || kStep % 8 == 0, "a thread's groups have one number");
-      const int tok0 = 8 * (st / (8 * C::G8)) + (st & 7), grp = ((st >> 3) + (C::G8 == 8 ? st : st >> 1)) % C::G8;
-      const bool odd = grp & 1;
-      const int kbits = PK.bits, vbits = PV.bits;
-      const bool paged = src.pages.table != nullptr;
-      const uint32_t kwb = PK.code_bytes, vwb = PV.code_bytes, knb = 2 * PK.nb, vnb = 2 * PV.nb;
-      const uint32_t kw0 = grp * 4 * kbits - ((kbits & 1) && odd ? 4 : 0), kn0 = 32 * grp / PK.blk * 2;
-      const uint32_t vw0 = grp * 4 * vbits - ((vbits & 1) && odd ? 4 : 0), vn0 = 32 * grp / PV.blk * 2;
-      const int knext = kbits > 2 ? 8 : 0, vnext = vbits > 2 ? 8 : 0;
-      const int64_t rec0 = paged ? 0 : ((int64_t)seq * a.Hkv + kvh) * src.S_cap + t_lo;
-      const uint8_t *kc = src.kc + rec0 * kwb + kw0, *ks = src.ks + rec0 * knb + kn0;
-      const uint8_t *vc = src.vc + rec0 * vwb + vw0, *vs = src.vs + rec0 * vnb + vn0;
-      const int32_t* table = paged ? src.pages.table + (int64_t)seq * src.pages.pages_per_seq : nullptr;
-      const uint32_t psize = src.pages.page_size;
-      const int last_page = paged ? ((uint32_t)t_lo + n_tok - 1) / psize : 0;
-      // record (contiguous: token) of each group in the tile to be loaded; a
-      // token past the slice takes the last one's place (paged: some record
-      // of the last page), and its values are not used
-      int32_t page[C::N], off[C::N];
-      int64_t rec[C::N];
-#pragma unroll
-      for (int k = 0; k < C::N; ++k) {
-        const uint32_t t = (uint32_t)t_lo + tok0 + k * kStep;
-        page[k] = paged ? t / psize : 0;
-        off[k] = paged ? t - page[k] * psize : 0;
-      }
-      auto place = [&](int at) {   // the records of the tile `at` tokens into the slice
+    if (warp >= kDec0 / 32) {
+      // ================= decoders
+      if (n_tiles == 0) {
+        begin();
+      } else {
+        const int dt = tid - kDec0;
+        const int st = C::SPLIT ? dt % C::SIDE : dt;    // thread within its side
+        const bool do_k = !C::SPLIT || dt < C::SIDE, do_v = !C::SPLIT || dt >= C::SIDE;
+        // the thread's groups: number grp of the tokens tok0 and, at head_dim
+        // 256, kStep tokens on.  A group's number turns with its token, so that
+        // the eight lanes of one access hit different banks whatever the
+        // records' pitch.
+        constexpr int kStep = C::SIDE / C::G8;
+        static_assert(C::N == 1 || kStep % 8 == 0, "a thread's groups have one number");
+        const int tok0 = 8 * (st / (8 * C::G8)) + (st & 7), grp = ((st >> 3) + (C::G8 == 8 ? st : st >> 1)) % C::G8;
+        const bool odd = grp & 1;
+        const int kbits = PK.bits, vbits = PV.bits;
+        const bool paged = src.pages.table != nullptr;
+        const uint32_t kwb = PK.code_bytes, vwb = PV.code_bytes, knb = 2 * PK.nb, vnb = 2 * PV.nb;
+        const uint32_t kw0 = grp * 4 * kbits - ((kbits & 1) && odd ? 4 : 0), kn0 = 32 * grp / PK.blk * 2;
+        const uint32_t vw0 = grp * 4 * vbits - ((vbits & 1) && odd ? 4 : 0), vn0 = 32 * grp / PV.blk * 2;
+        const int knext = kbits > 2 ? 8 : 0, vnext = vbits > 2 ? 8 : 0;
+        const int64_t rec0 = paged ? 0 : ((int64_t)seq * a.Hkv + kvh) * src.S_cap + t_lo;
+        const uint8_t *kc = src.kc + rec0 * kwb + kw0, *ks = src.ks + rec0 * knb + kn0;
+        const uint8_t *vc = src.vc + rec0 * vwb + vw0, *vs = src.vs + rec0 * vnb + vn0;
+        const int32_t* table = paged ? src.pages.table + (int64_t)seq * src.pages.pages_per_seq : nullptr;
+        const uint32_t psize = src.pages.page_size;
+        const int last_page = paged ? ((uint32_t)t_lo + n_tok - 1) / psize : 0;
+        // record (contiguous: token) of each group in the tile to be loaded; a
+        // token past the slice takes the last one's place (paged: some record
+        // of the last page), and its values are not used
+        int32_t page[C::N], off[C::N];
+        int64_t rec[C::N];
 #pragma unroll
         for (int k = 0; k < C::N; ++k) {
-          if (paged) {
-            rec[k] = ((int64_t)table[min(page[k], last_page)] * a.Hkv + kvh) * psize + off[k];
-            off[k] += kTile;
-            while ((uint32_t)off[k] >= psize) {
-              off[k] -= psize;
-              ++page[k];
+          const uint32_t t = (uint32_t)t_lo + tok0 + k * kStep;
+          page[k] = paged ? t / psize : 0;
+          off[k] = paged ? t - page[k] * psize : 0;
+        }
+        auto place = [&](int at) {   // the records of the tile `at` tokens into the slice
+#pragma unroll
+          for (int k = 0; k < C::N; ++k) {
+            if (paged) {
+              rec[k] = ((int64_t)table[min(page[k], last_page)] * a.Hkv + kvh) * psize + off[k];
+              off[k] += kTile;
+              while ((uint32_t)off[k] >= psize) {
+                off[k] -= psize;
+                ++page[k];
+              }
+            } else {
+              rec[k] = min(at + tok0 + k * kStep, n_tok - 1);
             }
-          } else {
-            rec[k] = min(at + tok0 + k * kStep, n_tok - 1);
+          }
+        };
+        Group gk[C::N], gv[C::N];
+        auto load_k = [&]() {
+#pragma unroll
+          for (int k = 0; k < C::N; ++k) load_group_g(kc + rec[k] * kwb, knext, ks + rec[k] * knb, gk[k]);
+        };
+        auto load_v = [&]() {
+#pragma unroll
+          for (int k = 0; k < C::N; ++k) load_group_g(vc + rec[k] * vwb, vnext, vs + rec[k] * vnb, gv[k]);
+        };
+        place(0);
+        load_k();
+        load_v();
+        begin();
+        for (int t = 0; t < n_tiles; ++t) {
+          const int bf = t % NB, at = t * kTile;
+          bool live[C::N];
+#pragma unroll
+          for (int k = 0; k < C::N; ++k) live[k] = at + tok0 + k * kStep < n_tok;
+          if (do_k) {
+            if (t >= NB) wait(s_full + 8 * ((t - NB) & 1), (uint32_t)((t - NB) >> 1) & 1);   // S(t - NB) is done
+#pragma unroll
+            for (int k = 0; k < C::N; ++k) pin(gk[k]);
+            if (!s_abort)
+              decode_groups<C::N>(kbits, gk, odd, PK.centroids, live, aK + bf * C::KB + cm_off(tok0, 32 * grp, D),
+                                  cm_off(kStep, 0, D));
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive(kfull + 8 * bf);
+            place(at + kTile);
+            load_k();
+          }
+          if (do_v) {
+            if (t >= NB) wait(vfree + 8 * bf, (uint32_t)(t / NB - 1) & 1);
+#pragma unroll
+            for (int k = 0; k < C::N; ++k) pin(gv[k]);
+            if (!s_abort)
+              decode_groups<C::N>(vbits, gv, odd, PV.centroids, live, aV + bf * C::VB + cm_off(tok0, 32 * grp, C::DV),
+                                  cm_off(kStep, 0, C::DV));
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive(vfull + 8 * bf);
+            if (C::SPLIT) place(at + kTile);
+            load_v();
           }
         }
-      };
-      Group gk[C::N], gv[C::N];
-      auto load_k = [&]() {
-#pragma unroll
-        for (int k = 0; k < C::N; ++k) load_group_g(kc + rec[k] * kwb, knext, ks + rec[k] * knb, gk[k]);
-      };
-      auto load_v = [&]() {
-#pragma unroll
-        for (int k = 0; k < C::N; ++k) load_group_g(vc + rec[k] * vwb, vnext, vs + rec[k] * vnb, gv[k]);
-      };
-      place(0);
-      load_k();
-      load_v();
+      }
+    } else if (warp == kSoftWarps) {
+      // ================= S^T(t) = K^(t) Q^
       begin();
+      const uint32_t idesc = (1u << 4) | ((uint32_t)(NR >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+      const uint64_t dq = sdesc(aQ, 128, kKGroup);
+      bool ok = n_tiles > 0 && wait(q_full, 0);
+      for (int t = 0; t < n_tiles && ok; ++t) {
+        const int bf = t % NB;
+        ok = wait(kfull + 8 * bf, (uint32_t)(t / NB) & 1) &&
+             (t < 2 || wait((s_waits ? o_done : p_full) + 8 * (t & 1), (uint32_t)((t >> 1) - 1) & 1));
+        if (!ok) break;
+        fence_after();
+        __syncwarp();
+        const uint64_t dk = sdesc(aK + bf * C::KB, 128, kKGroup);
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+          mma_ss_elect(tmem + (t & 1) * NR, dk + (uint64_t)(16 * s), dq + (uint64_t)(16 * s), idesc, s > 0);
+        commit_elect(s_full + 8 * (t & 1));
+      }
+      __syncwarp();
+      commit_elect(drained);
+    } else if (warp == kSoftWarps + 1) {
+      // ================= O^T += V^(t)^T P(t)^T
+      begin();
+      const uint32_t idesc = (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(NR >> 3) << 17) |
+                             ((uint32_t)(128 >> 4) << 24);
+      const uint32_t pg = (uint32_t)(NR >> 3) * 128;   // bytes of 8 tokens of P
       for (int t = 0; t < n_tiles; ++t) {
-        const int bf = t % NB, at = t * kTile;
-        bool live[C::N];
+        const int vb = t % NB, pb = t & 1;
+        if (!wait(vfull + 8 * vb, (uint32_t)(t / NB) & 1)) break;
+        if (!wait(p_full + 8 * pb, (uint32_t)(t >> 1) & 1)) break;
+        fence_after();
+        __syncwarp();
+        const uint64_t dp = sdesc(aP + pb * pbytes, pg, 128);
 #pragma unroll
-        for (int k = 0; k < C::N; ++k) live[k] = at + tok0 + k * kStep < n_tok;
-        if (do_k) {
-          if (t >= NB) wait(s_full + 8 * ((t - NB) & 1), (uint32_t)((t - NB) >> 1) & 1);   // S(t - NB) is done
+        for (int m = 0; m < OT; ++m) {
+          const uint64_t dv = sdesc(aV + vb * C::VB + m * 16 * 128, kVGroup, 128);
 #pragma unroll
-          for (int k = 0; k < C::N; ++k) pin(gk[k]);
-          if (!s_abort)
-            decode_groups<C::N>(kbits, gk, odd, PK.centroids, live, aK + bf * C::KB + cm_off(tok0, 32 * grp, D),
-                                cm_off(kStep, 0, D));
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) arrive(kfull + 8 * bf);
-          place(at + kTile);
-          load_k();
+          for (int s = 0; s < kTile / 16; ++s)
+            mma_ss_elect(tmem + cO + m * NR, dv + (uint64_t)(s * (2 * kVGroup >> 4)),
+                         dp + (uint64_t)(s * (2 * pg >> 4)), idesc, t > 0 || s > 0);
         }
-        if (do_v) {
-          if (t >= NB) wait(vfree + 8 * bf, (uint32_t)(t / NB - 1) & 1);
-#pragma unroll
-          for (int k = 0; k < C::N; ++k) pin(gv[k]);
-          if (!s_abort)
-            decode_groups<C::N>(vbits, gv, odd, PV.centroids, live, aV + bf * C::VB + cm_off(tok0, 32 * grp, C::DV),
-                                cm_off(kStep, 0, C::DV));
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) arrive(vfull + 8 * bf);
-          if (C::SPLIT) place(at + kTile);
-          load_v();
-        }
+        commit_elect(o_done + 8 * pb);
+        commit_elect(vfree + 8 * vb);
       }
-    }
-  } else if (warp == kSoftWarps) {
-    // ================= S^T(t) = K^(t) Q^
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::OTHER));
-    begin();
-    const uint32_t idesc = (1u << 4) | ((uint32_t)(NR >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
-    const uint64_t dq = sdesc(aQ, 128, kKGroup);
-    bool ok = n_tiles > 0 && wait(q_full, 0);
-    for (int t = 0; t < n_tiles && ok; ++t) {
-      const int bf = t % NB;
-      ok = wait(kfull + 8 * bf, (uint32_t)(t / NB) & 1) && (t < 2 || wait((s_waits ? o_done : p_full) + 8 * (t & 1), (uint32_t)((t >> 1) - 1) & 1));
-      if (!ok) break;
-      fence_after();
       __syncwarp();
-      const uint64_t dk = sdesc(aK + bf * C::KB, 128, kKGroup);
+      commit_elect(drained);
+    } else {
+      // ================= l += ones P(t)^T: rows [0, NR/2) or the rest, 8 at a time
+      begin();
+      const int nc = NR / 2, col0 = (warp - kSoftWarps - 2) * nc;
+      // lane i's row of the four 8 x 8 matrices of 32 tokens: token i, 8 rows
+      const uint32_t row = cm_off(lane, col0, NR);
+      const uint32_t step = (uint32_t)(NR >> 3) * 512;   // 32 tokens on
+      for (int t = 0; t < n_tiles; ++t) {
+        const int pb = t & 1;
+        if (!wait(p_full + 8 * pb, (uint32_t)(t >> 1) & 1)) break;
+        __syncwarp();
+        for (int c = 0; c < nc; c += 16) {   // two blocks of 8 rows, four chains of products
+          float d[2][2][4] = {};
+          const uint32_t at = aP + pb * pbytes + row + (uint32_t)(c >> 3) * 128;
 #pragma unroll
-      for (int s = 0; s < D / 16; ++s)
-        mma_ss_elect(tmem + (t & 1) * NR, dk + (uint64_t)(16 * s), dq + (uint64_t)(16 * s), idesc, s > 0);
-      commit_elect(s_full + 8 * (t & 1));
-    }
-    __syncwarp();
-    commit_elect(drained);
-  } else if (warp == kSoftWarps + 1) {
-    // ================= O^T += V^(t)^T P(t)^T
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::OTHER));
-    begin();
-    const uint32_t idesc = (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(NR >> 3) << 17) |
-                           ((uint32_t)(128 >> 4) << 24);
-    const uint32_t pg = (uint32_t)(NR >> 3) * 128;   // bytes of 8 tokens of P
-    for (int t = 0; t < n_tiles; ++t) {
-      const int vb = t % NB, pb = t & 1;
-      if (!wait(vfull + 8 * vb, (uint32_t)(t / NB) & 1)) break;
-      if (!wait(p_full + 8 * pb, (uint32_t)(t >> 1) & 1)) break;
-      fence_after();
-      __syncwarp();
-      const uint64_t dp = sdesc(aP + pb * pbytes, pg, 128);
+          for (int k = 0; k < 4; ++k)
 #pragma unroll
-      for (int m = 0; m < OT; ++m) {
-        const uint64_t dv = sdesc(aV + vb * C::VB + m * 16 * 128, kVGroup, 128);
+            for (int x = 0; x < 2; ++x) {
+              uint32_t b[4];
+              ldsm4_trans(b, at + k * step + x * 128);
+              hmma_sum(d[x][0], b[0], b[1]);
+              hmma_sum(d[x][1], b[2], b[3]);
+            }
+          if (lane < 4) {   // columns 2 lane, 2 lane + 1 of each block
 #pragma unroll
-        for (int s = 0; s < kTile / 16; ++s)
-          mma_ss_elect(tmem + cO + m * NR, dv + (uint64_t)(s * (2 * kVGroup >> 4)),
-                       dp + (uint64_t)(s * (2 * pg >> 4)), idesc, t > 0 || s > 0);
-      }
-      commit_elect(o_done + 8 * pb);
-      commit_elect(vfree + 8 * vb);
-    }
-    __syncwarp();
-    commit_elect(drained);
-  } else if (warp >= kSoftWarps) {
-    // ================= l += ones P(t)^T: rows [0, NR/2) or the rest, 8 at a time
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::OTHER));
-    begin();
-    const int nc = NR / 2, col0 = (warp - kSoftWarps - 2) * nc;
-    // lane i's row of the four 8 x 8 matrices of 32 tokens: token i, 8 rows
-    const uint32_t row = cm_off(lane, col0, NR);
-    const uint32_t step = (uint32_t)(NR >> 3) * 512;   // 32 tokens on
-    for (int t = 0; t < n_tiles; ++t) {
-      const int pb = t & 1;
-      if (!wait(p_full + 8 * pb, (uint32_t)(t >> 1) & 1)) break;
-      __syncwarp();
-      for (int c = 0; c < nc; c += 16) {   // two blocks of 8 rows, four chains of products
-        float d[2][2][4] = {};
-        const uint32_t at = aP + pb * pbytes + row + (uint32_t)(c >> 3) * 128;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            uint32_t b[4];
-            ldsm4_trans(b, at + k * step + x * 128);
-            hmma_sum(d[x][0], b[0], b[1]);
-            hmma_sum(d[x][1], b[2], b[3]);
-          }
-        if (lane < 4) {   // columns 2 lane, 2 lane + 1 of each block
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            float2* l = reinterpret_cast<float2*>(&s_l[col0 + c + 8 * x + 2 * lane]);
-            const float2 o = *l;
-            *l = make_float2(o.x + (d[x][0][0] + d[x][1][0]), o.y + (d[x][0][1] + d[x][1][1]));
+            for (int x = 0; x < 2; ++x) {
+              float2* l = reinterpret_cast<float2*>(&s_l[col0 + c + 8 * x + 2 * lane]);
+              const float2 o = *l;
+              *l = make_float2(o.x + (d[x][0][0] + d[x][1][0]), o.y + (d[x][0][1] + d[x][1][1]));
+            }
           }
         }
+        __syncwarp();
+        if (lane == 0) arrive(o_done + 8 * pb);
       }
-      __syncwarp();
-      if (lane == 0) arrive(o_done + 8 * pb);
     }
   } else {
     // ================= softmax: thread = token (TMEM lane) x half of the rows
