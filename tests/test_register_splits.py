@@ -32,6 +32,7 @@ def _branches(name):
 @pytest.mark.parametrize("name,whole", [
     # conditions that hold for whole warpgroups (4 warps) only
     ("tq_shared_tc.cu", [("dec", "if (warp >= kSoftWarps) {"), ("inc", "} else {")]),
+    ("tq_prefill_tc.cu", [("dec", "if (warp >= 4) {"), ("inc", "} else {")]),
 ])
 def test_one_register_split_per_warpgroup(name, whole):
     assert _branches(name) == whole

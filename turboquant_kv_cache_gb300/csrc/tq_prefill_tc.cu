@@ -600,73 +600,74 @@ __global__ void __launch_bounds__(192 + 32 * (NK + NV), 1) prefill_ws_kernel(con
     if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
   };
 
-  if (warp >= 6) {
-    // ================= decoders: NK warps fill the K ring, NV warps the V
-    // ring.  Each thread loads its items' packed words for tile t+1 into
-    // registers before decoding tile t, so the global latency hides behind
-    // the decode.
+  if (warp >= 4) {
+    // whole warpgroups (4 warps) execute one instruction each
     if (RB) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kDecRegs));
-    // the contiguous and the paged cache get their own copy of the role, so
-    // the contiguous one keeps its single base address
-    const ContigRec crec{(int64_t)bh * a.S_cap};
-    const PagedRec prec{a.pages, a.S_cap, a.Hkv, b, kvh};
-    if (warp < 6 + NK) {
-      if (a.pages.table)
-        decoder_role<D, kNK, NB, 1>(PK, s_tabs[0], a.kc, a.ks, tid - 192, kfull, kfree, aK(0), kTileBytes, prec, t_lo,
-                                    n_tiles, rank, n_valid_of, wait_cl, s_abort);
-      else
-        decoder_role<D, kNK, NB, 1>(PK, s_tabs[0], a.kc, a.ks, tid - 192, kfull, kfree, aK(0), kTileBytes, crec, t_lo,
-                                    n_tiles, rank, n_valid_of, wait_cl, s_abort);
-    } else {
-      if (a.pages.table)
-        decoder_role<D, kNV, NB, 2>(PV, s_tabs[1], a.vc, a.vs, tid - 192 - kNK, vfull, vfree, aV(0), kTileBytes,
-                                    prec, t_lo, n_tiles, rank, n_valid_of, wait_cl, s_abort);
-      else
-        decoder_role<D, kNV, NB, 2>(PV, s_tabs[1], a.vc, a.vs, tid - 192 - kNK, vfull, vfree, aV(0), kTileBytes,
-                                    crec, t_lo, n_tiles, rank, n_valid_of, wait_cl, s_abort);
-    }
-  } else if (warp == 4) {
-    // ================= S issue: S(t) = Q^ (TMEM) K^(t)^T once K(t) is decoded
-    // and S(t-1) has been read.  The whole warp walks the schedule, one
-    // elected lane issues each MMA and commit.  S and O have a warp each, so
-    // neither stream of MMAs waits behind the other's handoffs.
-    if (RB) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kDecRegs));
-    const uint32_t idesc_s = (1u << 4) | ((uint32_t)(kTok >> 3) << 17) | ((uint32_t)(kRowsTc >> 4) << 24);
-    bool ok = n_tiles > 0 && wait(q_full, 0);
-    for (int t = 0; t < n_tiles && ok; ++t) {
-      const int kb = t % NB;
-      ok = wait_cl(kfull + 8 * kb, (uint32_t)(t / NB) & 1) && (t == 0 || wait(s_free, (uint32_t)(t - 1) & 1));
-      if (!ok) break;
-      fence_after();
-      __syncwarp();
-      // fully unrolled: back-to-back MMAs in straight-line code keep the
-      // tensor pipe fed; an issue loop with a branch per MMA does not
-      const uint64_t dk = sdesc(aK(kb), 128, kGroupBytes);   // + 16 per 16 columns of d (256 bytes)
+    if (warp >= 6) {
+      // ================= decoders: NK warps fill the K ring, NV warps the V
+      // ring.  Each thread loads its items' packed words for tile t+1 into
+      // registers before decoding tile t, so the global latency hides behind
+      // the decode.
+      // the contiguous and the paged cache get their own copy of the role, so
+      // the contiguous one keeps its single base address
+      const ContigRec crec{(int64_t)bh * a.S_cap};
+      const PagedRec prec{a.pages, a.S_cap, a.Hkv, b, kvh};
+      if (warp < 6 + NK) {
+        if (a.pages.table)
+          decoder_role<D, kNK, NB, 1>(PK, s_tabs[0], a.kc, a.ks, tid - 192, kfull, kfree, aK(0), kTileBytes, prec, t_lo,
+                                      n_tiles, rank, n_valid_of, wait_cl, s_abort);
+        else
+          decoder_role<D, kNK, NB, 1>(PK, s_tabs[0], a.kc, a.ks, tid - 192, kfull, kfree, aK(0), kTileBytes, crec, t_lo,
+                                      n_tiles, rank, n_valid_of, wait_cl, s_abort);
+      } else {
+        if (a.pages.table)
+          decoder_role<D, kNV, NB, 2>(PV, s_tabs[1], a.vc, a.vs, tid - 192 - kNK, vfull, vfree, aV(0), kTileBytes,
+                                      prec, t_lo, n_tiles, rank, n_valid_of, wait_cl, s_abort);
+        else
+          decoder_role<D, kNV, NB, 2>(PV, s_tabs[1], a.vc, a.vs, tid - 192 - kNK, vfull, vfree, aV(0), kTileBytes,
+                                      crec, t_lo, n_tiles, rank, n_valid_of, wait_cl, s_abort);
+      }
+    } else if (warp == 4) {
+      // ================= S issue: S(t) = Q^ (TMEM) K^(t)^T once K(t) is decoded
+      // and S(t-1) has been read.  The whole warp walks the schedule, one
+      // elected lane issues each MMA and commit.  S and O have a warp each, so
+      // neither stream of MMAs waits behind the other's handoffs.
+      const uint32_t idesc_s = (1u << 4) | ((uint32_t)(kTok >> 3) << 17) | ((uint32_t)(kRowsTc >> 4) << 24);
+      bool ok = n_tiles > 0 && wait(q_full, 0);
+      for (int t = 0; t < n_tiles && ok; ++t) {
+        const int kb = t % NB;
+        ok = wait_cl(kfull + 8 * kb, (uint32_t)(t / NB) & 1) && (t == 0 || wait(s_free, (uint32_t)(t - 1) & 1));
+        if (!ok) break;
+        fence_after();
+        __syncwarp();
+        // fully unrolled: back-to-back MMAs in straight-line code keep the
+        // tensor pipe fed; an issue loop with a branch per MMA does not
+        const uint64_t dk = sdesc(aK(kb), 128, kGroupBytes);   // + 16 per 16 columns of d (256 bytes)
 #pragma unroll
-      for (int s = 0; s < D / 16; ++s)
-        mma_ts_elect(tmem + kColS, tmem + kColQ + 8 * s, dk + (uint64_t)(16 * s), idesc_s, s > 0);
-      commit_elect(s_full);
-      commit_elect_pair(kfree + 8 * kb);
-    }
-  } else if (warp == 5) {
-    // ================= O issue: O += P(t) (TMEM) V^(t) once P(t) is written
-    // and V(t) decoded
-    if (RB) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kDecRegs));
-    const uint32_t idesc_o = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kRowsTc >> 4) << 24);
-    bool ok = true;
-    for (int t = 0; t < n_tiles && ok; ++t) {
-      const int vb = t % NB, pb = t & 1;
-      ok = wait(p_full + 8 * pb, (uint32_t)(t >> 1) & 1) && wait_cl(vfull + 8 * vb, (uint32_t)(t / NB) & 1);
-      if (!ok) break;
-      fence_after();
-      __syncwarp();
-      const uint64_t dv = sdesc(aV(vb), kGroupBytes, 128);   // + per 16 tokens (2 groups)
+        for (int s = 0; s < D / 16; ++s)
+          mma_ts_elect(tmem + kColS, tmem + kColQ + 8 * s, dk + (uint64_t)(16 * s), idesc_s, s > 0);
+        commit_elect(s_full);
+        commit_elect_pair(kfree + 8 * kb);
+      }
+    } else if (warp == 5) {
+      // ================= O issue: O += P(t) (TMEM) V^(t) once P(t) is written
+      // and V(t) decoded
+      const uint32_t idesc_o = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kRowsTc >> 4) << 24);
+      bool ok = true;
+      for (int t = 0; t < n_tiles && ok; ++t) {
+        const int vb = t % NB, pb = t & 1;
+        ok = wait(p_full + 8 * pb, (uint32_t)(t >> 1) & 1) && wait_cl(vfull + 8 * vb, (uint32_t)(t / NB) & 1);
+        if (!ok) break;
+        fence_after();
+        __syncwarp();
+        const uint64_t dv = sdesc(aV(vb), kGroupBytes, 128);   // + per 16 tokens (2 groups)
 #pragma unroll
-      for (int s = 0; s < kTok / 16; ++s)
-        mma_ts_elect(tmem + kColO, tmem + kColP + 32 * pb + 8 * s, dv + (uint64_t)(s * (2 * kGroupBytes >> 4)),
-                     idesc_o, (t == 0 && s == 0) ? 0 : 1);
-      commit_elect(o_done + 8 * pb);
-      commit_elect_pair(vfree + 8 * vb);
+        for (int s = 0; s < kTok / 16; ++s)
+          mma_ts_elect(tmem + kColO, tmem + kColP + 32 * pb + 8 * s, dv + (uint64_t)(s * (2 * kGroupBytes >> 4)),
+                       idesc_o, (t == 0 && s == 0) ? 0 : 1);
+        commit_elect(o_done + 8 * pb);
+        commit_elect_pair(vfree + 8 * vb);
+      }
     }
   } else {
     // ================= softmax: one row per thread
