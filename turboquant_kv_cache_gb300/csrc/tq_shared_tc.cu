@@ -24,17 +24,22 @@
 // rows; the sums l over tokens come from the same rounded p that multiplies V:
 // two warps read P back as mma.sync operands and multiply it by a matrix of
 // ones, in fp32.
-// The reference m of a row only moves when a score passes it by more than
-// 2^12 (it starts as the largest of 32 scores): the common step needs no
-// maximum over tokens, only one barrier vote; the rare one takes the maxima
-// and scales O and l.
+// The reference of a row only moves when a score passes it by more than 2^8
+// (it starts as the largest of 32 scores): the common step needs no maximum
+// over tokens, only one barrier vote; the rare one takes the maxima and scales
+// O and l.  What is kept as m lies 7 below the reference, so p is 2^7 there and
+// at most 2^15: the upper half of fp16's range for what is larger, the rest
+// for what is smaller.
 //
 // Roundings.  Scores, m, l and O are fp32.  Q^, K^ and V^ are rounded once to
 // fp16 (half a step, 2^-11 relative to each value) and p once (2^-11): the
 // tensor cores' operands, the same as the prefill's.  Their errors are
-// independent over d values and over the tokens, so an output is off by a few
-// 1e-4 of its scale.  p below 2^-25 of the reference is dropped; a slice holds
-// 2^-25 per token of that at most, 2^-12 of a softmax over 8192 such tokens.
+// independent over d values and over the tokens: with Gaussian vectors the
+// outputs are 6e-4 to 9e-4 (relative, as norms) from attention in 64 bits, of
+// which 2.1e-4 are the output's own rounding; a score of s (in e-folds) is off
+// by up to 2^-10 sum |q k|, so weights of large scores by as much.  p is kept to
+// 2^-32 of the reference's and dropped below: at most that per token, 2^-15 of a
+// softmax over a slice of 131072 tokens.
 //
 // Warps: 0-7 softmax (warps 0-3 rows [0, NR/2), 4-7 the rest), which also
 // rotate the queries while the first loads are in flight, 8 issues S, 9 issues
@@ -91,9 +96,9 @@ constexpr int kDecThreads = 32 * kDecWarps;
 constexpr int kDec0 = 32 * (kSoftWarps + 4);          // first decoder thread (whole warpgroups)
 constexpr int kThreadsSh = kDec0 + kDecThreads;       // 896
 constexpr int kLaunchRegs = 72;     // registers a thread at launch (896 threads of 65536)
-// log2 units a score may pass its row's reference by: p stays below 2^12, far
-// inside fp16, and sums of p * v inside fp32
-constexpr float kLazySh = 12.0f;
+// log2 of p at a row's reference, and the log2 units a score may pass it by: p
+// stays below 2^15, inside fp16, and sums of p * v inside fp32
+constexpr float kHeadSh = 7.0f, kLazySh = 8.0f;
 
 // first failure status of a launch since the last read (0 = none)
 __device__ int g_shared_status;
@@ -356,7 +361,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
   __shared__ uint32_t tmem_base;
   __shared__ volatile int s_abort;
   __shared__ int s_late;
-  __shared__ __align__(16) float s_m[C::MAXR];      // the rows' softmax references
+  __shared__ __align__(16) float s_m[C::MAXR];      // kHeadSh below the rows' softmax references
   __shared__ float s_al[C::MAXR];
   __shared__ int64_t s_dst[C::MAXR];                // where the rows' partials go
   __shared__ __align__(8) float s_l[C::MAXR];                    // the rows' sums of p
@@ -704,14 +709,14 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
     const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
     const uint32_t pdst0 = aP + cm_off(tk, col0, NR);
     constexpr int NCH = C::MAXR / 32;       // column chunks of 16
-    const uint32_t kOver = 0x6C006C00u;     // 2^12 twice in fp16
-    static_assert(kLazySh == 12.0f, "kOver is 2^kLazySh");
+    const uint32_t kOver = 0x78007800u;     // 2^15 twice in fp16
+    static_assert(kHeadSh + kLazySh == 15.0f, "kOver is p where the reference moves");
     for (int t = 0; t < n_tiles; ++t) {
       const uint32_t sS = lanes + (t & 1) * NR + col0;
       const uint32_t pdst = pdst0 + (t & 1) * pbytes;
       const bool whole = (t + 1) * kTile <= n_tok, live = t * kTile + tk < n_tok;
       // p of every column from its score, to P; returns whether one passes
-      // 2^kLazySh.  A token past the slice has p = 0.
+      // 2^15.  A token past the slice has p = 0.
       auto emit = [&]() {
         uint32_t vv[2][16], mx = 0u;
         TQ_LD16(sS, vv[0]);
@@ -755,7 +760,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
             const float x = warp_max_f(live ? __uint_as_float(v[j]) : -INFINITY);
             if (lane == j) mine = x;
           }
-          if (lane < 4) s_m[col0 + c + lane] = mine;
+          if (lane < 4) s_m[col0 + c + lane] = mine - kHeadSh;
         }
         half_sync(bid);
       }
@@ -786,7 +791,7 @@ __global__ void __launch_bounds__(kThreadsSh, 1) shared_prefix_kernel(const Code
         if ((tid & 127) < nc) {
           const int i = tid & 127, r = col0 + i;
           const float x = fmaxf(fmaxf(wm[i], wm[nc + i]), fmaxf(wm[2 * nc + i], wm[3 * nc + i]));
-          const float mo = s_m[r], mn = x > mo + kLazySh || mo == -INFINITY ? x : mo;
+          const float mo = s_m[r], mn = x > mo + (kHeadSh + kLazySh) || mo == -INFINITY ? x - kHeadSh : mo;
           const float al = mo == -INFINITY ? 0.f : ex2s(mo - mn);
           s_m[r] = mn;
           s_al[r] = al;
