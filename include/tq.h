@@ -465,9 +465,12 @@ typedef struct {
  *                           share_len[i] tokens fill, by reference, and gets a
  *                           copy of the page that they fill in part; the child
  *                           must hold no pages
- *   parent[i] = child[i]    the sequence grows: it keeps its pages, and where
- *                           the page that token share_len[i] goes to is also
- *                           held by others it is replaced by a copy of its own
+ *   parent[i] = child[i]    the sequence of share_len[i] tokens grows: it keeps
+ *                           its pages, but those that tokens from share_len[i]
+ *                           to new_len[i] go to and that are also held by others
+ *                           (the page of token share_len[i] even when no token
+ *                           is added) are replaced by pages of its own; the
+ *                           first of them, where it is filled in part, by a copy
  * Fresh pages are the free pages in ascending order, dealt to the entries in
  * order (an entry's by ascending position in its row).  Pages are copied in
  * all of the caches (every layer's K and V, the views' arrays as

@@ -678,8 +678,9 @@ def _pool_call(pool, n, workspace, result):
 def tq_pages_fork(pool, parent, child, share_len, new_len, workspace=None, result=None, stream=None):
     """Sequences begin (parent -1), fork (share the full pages of the parent's
     first share_len tokens, copy the part-filled one) and grow (parent equal
-    to child), so that child[i] holds pages for new_len[i] tokens.  int32 CUDA
-    tensors of one length.  Returns the result tensor {status, pages taken,
+    to child: pages that tokens from share_len on go to and that others hold
+    too are replaced), so that child[i] holds pages for new_len[i] tokens.
+    int32 CUDA tensors of one length.  Returns the result tensor {status, pages taken,
     pages copied, 0}: status 0 done, > 0 pages missing, -1 an entry is not
     valid; unless it is 0 nothing has changed."""
     n, dev = child.numel(), pool.dev

@@ -60,12 +60,12 @@ struct Work {
   int32_t* chunk;    // [chunks] free pages of each chunk, then before each
   int32_t* mark;     // [n_seqs] 1: a child of this call
   int32_t* off;      // [n + 1] fresh pages before entry i
-  int32_t* first;    // [n] first table index a fresh page goes to
-  int32_t* cow;      // [n] table index of the shared page replaced, or -1
+  int32_t* first;    // [n] first table index a fresh page goes to, behind the shared ones replaced
+  int32_t* cow;      // [n] shared pages that fresh ones replace
   int32_t* src;      // [n] or [num_pages]: page copied
   int32_t* dst;      // [n] or [num_pages]: page it is copied to
-  int32_t* drop;     // [n] page whose count falls by one, or -1
-  int32_t* rank;     // [num_pages] rank of a page that moves
+  int32_t* rank;     // [num_pages] compact: rank of a page that moves.  fork: for a fresh page, by rank, that
+                     // replaces a shared one the table index, then (from deal on) the page replaced
 };
 
 size_t carve(void* ws, int n_seqs, int num_pages, int n, Work* w) {
@@ -87,7 +87,6 @@ size_t carve(void* ws, int n_seqs, int num_pages, int n, Work* w) {
   t.cow = take(n);
   t.src = take(lists);
   t.dst = take(lists);
-  t.drop = take(n);
   t.rank = take(num_pages);
   if (w) *w = t;
   return at;
@@ -165,18 +164,23 @@ struct ForkArgs {
   Work w;
 };
 
-// What entry i of a fork takes.  ok: the entry can be done.
+// What entry i of a fork takes, but for the shared pages in [at, last) of its
+// own row that it replaces.  ok: the entry can be done.
 struct Entry {
-  int parent, child, at, first, fresh, total, cow, src, drop;
+  int parent, child, at, last, first, fresh, total, src;
   bool ok;
 };
+
+__device__ __forceinline__ bool held_by_others(const tq_page_pool& p, int page) {
+  return page >= 0 && page < p.num_pages && p.ref[page] > 1;
+}
 
 __device__ Entry read_entry(const ForkArgs& a, int i) {
   Entry e{};
   const tq_page_pool& p = a.pool;
   e.parent = a.parent[i];
   e.child = a.child[i];
-  e.cow = e.src = e.drop = -1;
+  e.src = -1;
   const int share = a.share_len[i], len = a.new_len[i];
   e.ok = e.child >= 0 && e.child < p.n_seqs && e.parent >= -1 && e.parent < p.n_seqs && share >= 0 && len >= share;
   if (!e.ok) return e;
@@ -193,23 +197,40 @@ __device__ Entry read_entry(const ForkArgs& a, int i) {
   if (grow) {
     e.first = held;
     e.fresh = e.total > held ? e.total - held : 0;
-    if (e.at < held) {
-      const int page = row[e.at];
-      if (page >= 0 && page < p.num_pages && p.ref[page] > 1) {   // shared: it would be written
-        e.cow = e.at;
-        e.drop = page;
-        ++e.fresh;
-        if (part) e.src = page;
-      }
-    }
+    // the held pages that tokens [share, len) go to: shared ones would be written
+    e.last = min(held, max(e.total, e.at + 1));
+    if (part && e.at < held && held_by_others(p, row[e.at])) e.src = row[e.at];
     if (e.total < held) e.total = held;
   } else {
     e.first = e.at;
     e.fresh = e.total - e.at;
     if (part) e.src = row[e.at];
   }
-  if (e.src >= p.num_pages || (e.src < 0 && part && !(grow && e.cow < 0))) e.ok = false;   // a table entry that is no page
+  if (!grow && part && (e.src < 0 || e.src >= p.num_pages)) e.ok = false;   // a table entry that is no page
   return e;
+}
+
+// How many of the pages [j0, j1) of sequence s others hold too; with `list`
+// their table indexes, ascending, go there.  Every lane asks for its own
+// (nothing where j0 >= j1), one range after the other by the whole warp.
+__device__ __forceinline__ int shared_pages(const tq_page_pool& p, int s, int j0, int j1, int32_t* list) {
+  const int lane = threadIdx.x & 31;
+  int n = 0;
+  for (uint32_t todo = __ballot_sync(kFull, j0 < j1); todo; todo &= todo - 1) {
+    const int l = __ffs(todo) - 1;
+    const int32_t* row = p.page_table + (int64_t)__shfl_sync(kFull, s, l) * p.pages_per_seq;
+    const int a = __shfl_sync(kFull, j0, l), b = __shfl_sync(kFull, j1, l);
+    int32_t* to = reinterpret_cast<int32_t*>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(list), l));
+    int c = 0;
+    for (int k = a; k < b; k += 32) {
+      const bool found = k + lane < b && held_by_others(p, row[k + lane]);
+      const uint32_t m = __ballot_sync(kFull, found);
+      if (found && to) to[c + __popc(m & ((1u << lane) - 1))] = k + lane;
+      c += __popc(m);
+    }
+    if (lane == l) n = c;
+  }
+  return n;
 }
 
 // Checks every entry and sums up what they need, given the free pages; takes
@@ -240,16 +261,19 @@ __device__ bool plan_entries(const ForkArgs& a, int n_free, int* s_part) {
         e.fresh = 0;
       }
     }
+    // most ranges are one page, which its own thread looks at
+    int cow = e.ok && e.last == e.at + 1 && held_by_others(p, p.page_table[(int64_t)e.child * p.pages_per_seq + e.at]);
+    const int many = shared_pages(p, e.child, e.at, e.ok && e.last > e.at + 1 ? e.last : e.at, nullptr);
+    cow += many;
     int total;
     // an entry takes at most kMaxPerSeq pages, so a block's sum fits; the
     // running sum saturates above any pool, whose size is checked against it
-    const int before = block_scan(e.fresh, s_part, &total);
+    const int before = block_scan(e.fresh + cow, s_part, &total);
     if (i < a.n) {
       w.off[i] = min(base + before, kManyPages);
       w.first[i] = e.first;
-      w.cow[i] = e.cow;
+      w.cow[i] = cow;
       w.src[i] = e.src;
-      w.drop[i] = e.drop;
       w.dst[i] = -1;
     }
     base = min(base + total, kManyPages);
@@ -260,10 +284,22 @@ __device__ bool plan_entries(const ForkArgs& a, int n_free, int* s_part) {
   block_scan(copies, s_part, &n_copies);
   const bool ok = !any_bad && base <= n_free;
   if (ok) {   // every count has been read: the sequences hold their new pages from here on
-    for (int i = threadIdx.x; i < a.n; i += kPlanThreads) {
-      const int c = a.child[i];
-      const int total = (int)(((int64_t)a.new_len[i] + p.page_size - 1) / p.page_size);
-      if (a.parent[i] != c || total > p.n_pages[c]) p.n_pages[c] = total;
+    for (int i0 = 0; i0 < a.n; i0 += kPlanThreads) {
+      const int i = i0 + threadIdx.x;
+      int c = 0, at = 0, last = 0;
+      int32_t* list = nullptr;
+      if (i < a.n) {
+        c = a.child[i];
+        const int held = p.n_pages[c];   // a sequence is one entry's child: this thread's to read and change
+        const int total = (int)(((int64_t)a.new_len[i] + p.page_size - 1) / p.page_size);
+        if (w.cow[i]) {
+          at = a.share_len[i] / p.page_size;
+          last = min(held, max(total, at + 1));
+          list = w.rank + w.off[i];
+        }
+        if (a.parent[i] != c || total > held) p.n_pages[c] = total;
+      }
+      shared_pages(p, c, at, last, list);
     }
   }
   if (threadIdx.x == 0) {
@@ -291,8 +327,14 @@ __device__ void deal(const ForkArgs& a, int r, int page) {
     if (w.off[mid] <= r) lo = mid; else hi = mid;
   }
   const int t = r - w.off[lo], cow = w.cow[lo];
-  const int idx = cow >= 0 ? (t == 0 ? cow : w.first[lo] + t - 1) : w.first[lo] + t;
-  a.pool.page_table[(int64_t)a.child[lo] * a.pool.pages_per_seq + idx] = page;
+  int32_t* row = a.pool.page_table + (int64_t)a.child[lo] * a.pool.pages_per_seq;
+  if (t < cow) {   // in a shared page's place, whose count falls once no count is read any more
+    const int idx = w.rank[r];
+    w.rank[r] = row[idx];
+    row[idx] = page;
+  } else {
+    row[w.first[lo] + t - cow] = page;
+  }
   a.pool.ref[page] = 1;
   if (t == 0) w.dst[lo] = page;   // the copy of a part-filled page goes to the first fresh page
 }
@@ -377,18 +419,12 @@ struct Arrays {
 };
 
 // Copies w.moves pages src[r] -> dst[r] (an entry of a fork without a copy
-// has src -1), one piece of one array per block and step.  Block 0 also lowers
-// the counts of the n_drop pages that a fork's entries replaced.
+// has src -1), one piece of one array per block and step.  The blocks also
+// lower the counts of the pages that a fork's n_drop entries replaced.
 __global__ void __launch_bounds__(kThreads) pages_move_kernel(Work w, const __grid_constant__ Arrays a,
                                                               int32_t* ref, int num_pages, int n_drop) {
   chain_begin();
   const int moves = w.head->moves;
-  if (blockIdx.x == 0 && moves) {
-    for (int i = threadIdx.x; i < n_drop; i += kThreads) {
-      const int page = w.drop[i];
-      if (page >= 0) atomicSub(&ref[page], 1);
-    }
-  }
   const int64_t items = (int64_t)moves * a.pieces;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
     const int r = (int)(it / a.pieces), pc = (int)(it - (int64_t)r * a.pieces);
@@ -414,6 +450,12 @@ __global__ void __launch_bounds__(kThreads) pages_move_kernel(Work w, const __gr
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (threadIdx.x + u * kThreads < n16) d[threadIdx.x + u * kThreads] = v[u];
+  }
+  if (moves) {
+    for (int i = blockIdx.x; i < n_drop; i += gridDim.x) {
+      const int cow = w.cow[i];
+      for (int t = threadIdx.x; t < cow; t += kThreads) atomicSub(&ref[w.rank[w.off[i] + t]], 1);
+    }
   }
 }
 
@@ -616,7 +658,7 @@ int launch_moves(const tq_kv_view* caches, int n_caches, int Hkv, const tq_page_
   Arrays a{};
   bool launched = false, ok = true;
   auto flush = [&]() {
-    const int64_t items = most * a.pieces;
+    const int64_t items = most * a.pieces > n_drop ? most * a.pieces : n_drop;
     const int64_t grid = items < 1 ? 1 : (items > 152 * 8 ? 152 * 8 : items);
     ok = ok && launch(pages_move_kernel, grid, kThreads, true, st, w, a, p.ref, p.num_pages, launched ? 0 : n_drop);
     launched = true;
