@@ -132,7 +132,19 @@ def _stream_on(stream, dev):
     """The same where dev is the current device."""
     if stream is None and _raw_stream is not None:
         return _raw_stream(dev)
+    if stream is not None and stream.device_index != dev:
+        raise ValueError("stream must be a stream of the call's CUDA device")
     return _stream(stream)
+
+
+def _new(stream, make, *args, **kw):
+    """A tensor that a call makes for itself or returns, made on the call's
+    stream: fills and copies are in the kernels' order, and the memory, once
+    let go, is that stream's to use again."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
 
 
 class _on:
@@ -534,11 +546,11 @@ def tq_decode_attn_shared(Kp, Vp, K, V, q, prefix_ctx=None, prefix_len=None, ctx
         _i32(kv_len, B, "kv_len", dev)
     if workspace is None:
         need = tq_decode_shared_workspace_bytes(B, Hq, Hkv, d, prefix_ctx, ctx, n_split)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _new(stream, torch.empty, max(need, 16), dtype=torch.uint8, device=q.device)
     else:
         _check_workspace(workspace, dev)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, torch.empty_like, q)
     elif not _is(out, torch.float16, shape, dev):
         raise ValueError("out must be a contiguous tensor like q")
     st = _load().tq_decode_attn_shared(ctypes.byref(Kp.view()), ctypes.byref(Vp.view()), P_cap, _ptr(prefix_len),
@@ -574,7 +586,7 @@ def tq_qkv_norm_rope(qkv, Hq, Hkv, head_dim, q_weight=None, k_weight=None, eps=1
         if one != 1:
             raise ValueError("qkv must be a CUDA tensor [B, T, (Hq + 2 Hkv) head_dim] with a contiguous last dimension")
         if T > 1 and B > 1 and sb != T * st:
-            qkv = qkv.contiguous()
+            qkv = _new(stream, qkv.contiguous)
         elif T > 1:
             row = st
         elif B > 1:
@@ -601,11 +613,11 @@ def tq_qkv_norm_rope(qkv, Hq, Hkv, head_dim, q_weight=None, k_weight=None, eps=1
         _i32(slot, B, "slot", dev)
     if q_out is None or k_out is None or v_out is None:
         if q_out is None:
-            q_out = fresh((B, Hq, T, d), dtype=f16, device=qkv.device)
+            q_out = _new(stream, fresh, (B, Hq, T, d), dtype=f16, device=qkv.device)
         if k_out is None:
-            k_out = fresh((B, Hkv, T, d), dtype=f16, device=qkv.device)
+            k_out = _new(stream, fresh, (B, Hkv, T, d), dtype=f16, device=qkv.device)
         if v_out is None:
-            v_out = fresh(tuple(k_out.shape), dtype=f16, device=qkv.device)
+            v_out = _new(stream, fresh, tuple(k_out.shape), dtype=f16, device=qkv.device)
     kv_shape = k_out.shape
     cap = kv_shape[2] if len(kv_shape) == 4 else -1
     if (kv_shape != (B, Hkv, cap, d) or not _is(q_out, f16, (B, Hq, T, d), dev) or not _is(k_out, f16, kv_shape, dev)
@@ -662,14 +674,14 @@ def tq_pages_workspace_bytes(n_seqs, num_pages, n):
     return nb.value
 
 
-def _pool_call(pool, n, workspace, result):
+def _pool_call(pool, n, workspace, result, stream):
     if workspace is None:
-        workspace = torch.empty(tq_pages_workspace_bytes(pool.n_pages.shape[0], pool.ref.shape[0], n),
-                                dtype=torch.uint8, device=pool.ref.device)
+        workspace = _new(stream, torch.empty, tq_pages_workspace_bytes(pool.n_pages.shape[0], pool.ref.shape[0], n),
+                         dtype=torch.uint8, device=pool.ref.device)
     else:
         _check_workspace(workspace, pool.dev)
     if result is None:
-        result = torch.empty(4, dtype=torch.int32, device=pool.ref.device)
+        result = _new(stream, torch.empty, 4, dtype=torch.int32, device=pool.ref.device)
     else:
         _i32(result, 4, "result", pool.dev)
     return workspace, result
@@ -691,7 +703,7 @@ def tq_pages_fork(pool, parent, child, share_len, new_len, workspace=None, resul
     if dev != _current_device():
         with _on(dev):
             return tq_pages_fork(pool, parent, child, share_len, new_len, workspace, result, stream)
-    workspace, result = _pool_call(pool, n, workspace, result)
+    workspace, result = _pool_call(pool, n, workspace, result, stream)
     st = _load().tq_pages_fork(pool.ref_struct, pool.views, len(pool.caches), pool.heads, parent.data_ptr(),
                                child.data_ptr(), share_len.data_ptr(), new_len.data_ptr(), n, result.data_ptr(), workspace.data_ptr(),
                                workspace.nbytes, _stream_on(stream, pool.dev))
@@ -720,7 +732,7 @@ def tq_pages_compact(pool, workspace=None, result=None, stream=None):
     if pool.dev != _current_device():
         with _on(pool.dev):
             return tq_pages_compact(pool, workspace, result, stream)
-    workspace, result = _pool_call(pool, 0, workspace, result)
+    workspace, result = _pool_call(pool, 0, workspace, result, stream)
     st = _load().tq_pages_compact(pool.ref_struct, pool.views, len(pool.caches), pool.heads, result.data_ptr(),
                                   workspace.data_ptr(), workspace.nbytes, _stream_on(stream, pool.dev))
     if st:
