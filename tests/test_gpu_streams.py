@@ -130,3 +130,60 @@ def test_stream_of_another_device_is_refused(tqlib):
         tb.tq_qkv_norm_rope(x.contiguous(), *sizes, q_out=outs[0], k_out=outs[1], v_out=outs[2], stream=far)
     with pytest.raises(ValueError):
         tb.tq_pages_free(tb.PagePool.new(4, 8, 40, 32), one, stream=far)
+
+
+def _codec(tb):
+    """Inputs that the calls copy before their kernels read them."""
+    L = tb.make_layout(128, 32, 3)
+    x = torch.from_numpy(inputs.gaussian((2, 40, 3, 128), 21)).cuda().transpose(1, 2)       # [2, 3, 40, 128], strided
+    pos = torch.tensor([[3, 9], [0, 9]], dtype=torch.int32, device="cuda")[:, 0]
+    q = torch.from_numpy(inputs.gaussian((2, 6, 128), 22)).cuda()
+    return L, x, pos, q
+
+
+def test_codec_on_another_stream(tqlib):
+    from turboquant_kv_cache_gb300 import binding as tb
+    L, x, pos, q = _codec(tb)
+
+    def append(s):
+        c = tb.PackedKV(L, (2, 3, 64))
+        c.codes.zero_()
+        c.scales.zero_()
+        if s is not None:
+            torch.cuda.synchronize()     # the cache is filled before the side stream has it
+            torch.cuda._sleep(40_000_000)
+        return tb.tq_append_kv(c, x, pos, stream=s)
+
+    for call in (lambda s: tb.tq_quantize_kv(L, x, stream=s), append):
+        want, got = call(None), _held_back(call)
+        assert torch.equal(got.codes, want.codes) and torch.equal(got.scales, want.scales)
+    want, got = (f(lambda s: tb.tq_polar_quantize(x, 3, stream=s)) for f in (lambda c: c(None), _held_back))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    K = tb.tq_quantize_kv(L, x)
+    # a window whose rows lie apart
+    win = torch.from_numpy(inputs.gaussian((2, 7, 3, 128), 23)).cuda().transpose(1, 2)
+    call = lambda s: tb.tq_decode_attn_window(K, K, q, win, win, stream=s)  # noqa: E731
+    assert torch.equal(_held_back(call), call(None))
+
+
+def test_what_the_other_calls_make_is_their_streams(tqlib, made):
+    from turboquant_kv_cache_gb300 import binding as tb
+    L, x, pos, q = _codec(tb)
+    K = tb.tq_quantize_kv(L, x)
+    blocks = tb.tq_to_blocks(K)
+    codes, radius = tb.tq_polar_quantize(x, 3)
+    win = torch.zeros(2, 3, 8, 128, dtype=torch.float16, device="cuda")
+    q4 = q[:, :, None].expand(-1, -1, 5, -1).contiguous()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for call in (lambda: tb.tq_quantize_kv(L, x, stream=side), lambda: tb.tq_dequantize_kv(K, stream=side),
+                 lambda: tb.tq_decode_attn(K, K, q, stream=side), lambda: tb.tq_decode_attn_static(K, K, q, stream=side),
+                 lambda: tb.tq_decode_attn_window(K, K, q, win, win, stream=side), lambda: tb.tq_to_blocks(K, stream=side),
+                 lambda: tb.tq_from_blocks(L, blocks, stream=side),
+                 lambda: tb.tq_decode_attn_blocks(L, blocks, L, blocks, q, stream=side),
+                 lambda: tb.tq_polar_quantize(x, 3, stream=side), lambda: tb.tq_polar_dequantize(codes, radius, 128, 3, stream=side),
+                 lambda: tb.tq_prefill_attn(K, K, q4, 40, stream=side)):
+        made.clear()
+        call()
+        assert made and set(made) == {side.cuda_stream}
+    torch.cuda.synchronize()

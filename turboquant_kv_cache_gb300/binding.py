@@ -357,9 +357,9 @@ def tq_quantize_kv(layout, x, S=None, out=None, stream=None):
     if x.shape[-1] != d or x.stride(-1) != 1:
         raise ValueError("x must have a contiguous last dimension of head_dim")
     lead = tuple(x.shape[:-1])
-    x2 = x.reshape(-1, d)
+    x2 = _new(stream, x.reshape, -1, d)
     if out is None:
-        out = PackedKV(layout, lead, device=x.device, S=S)
+        out = _new(stream, PackedKV, layout, lead, device=x.device, S=S)
     n = x2.shape[0]
     st = lib.tq_quantize_kv(ctypes.byref(layout), _ptr(x2), _dtype_code(x.dtype), n, x2.stride(0), _ptr(S),
                             _ptr(out.codes), _ptr(out.scales), _ptr(out.qjl), _ptr(out.rnorm), _stream(stream))
@@ -382,10 +382,11 @@ def tq_append_kv(cache, x, pos, stream=None):
         raise ValueError("cache must have leading shape [B, H, S_cap] (or be paged for B sequences) matching x")
     if pos.dtype != torch.int32 or pos.numel() != B or not pos.is_cuda:
         raise ValueError("pos must be an int32 CUDA tensor of B slot offsets")
-    x2 = x.reshape(-1, d)
+    x2 = _new(stream, x.reshape, -1, d)
+    pos = _new(stream, pos.contiguous)
     pt = cache.page_table
     st = lib.tq_append_kv(ctypes.byref(layout), _ptr(x2), _dtype_code(x.dtype), B, H, n_new, x2.stride(0),
-                          _ptr(pos.contiguous()), cache.capacity, _ptr(pt),
+                          _ptr(pos), cache.capacity, _ptr(pt),
                           cache.lead_shape[2] if pt is not None else 0, cache._table_stride(),
                           _ptr(cache.S), _ptr(cache.codes), _ptr(cache.scales), _ptr(cache.qjl), _ptr(cache.rnorm),
                           _stream(stream))
@@ -397,7 +398,7 @@ def tq_dequantize_kv(packed, out_dtype=torch.float16, stream=None, out=None):
     lib = _load()
     d = packed.layout.head_dim
     if out is None:
-        out = torch.empty(packed.lead_shape + (d,), dtype=out_dtype, device=packed.codes.device)
+        out = _new(stream, torch.empty, packed.lead_shape + (d,), dtype=out_dtype, device=packed.codes.device)
     elif out.dtype != out_dtype or out.numel() != packed.n_vec * d or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor of n_vec x head_dim elements of out_dtype")
     st = lib.tq_dequantize_kv(ctypes.byref(packed.layout), _ptr(packed.codes), _ptr(packed.scales),
@@ -432,9 +433,9 @@ def tq_decode_attn(K, V, q, ctx=None, kv_len=None, softmax_scale=0.0, n_split=0,
     ctx = S_cap if ctx is None else ctx
     need, ns = tq_decode_workspace_bytes(B, Hq, Hkv, d, ctx, n_split)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _new(stream, torch.empty, max(need, 16), dtype=torch.uint8, device=q.device)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, torch.empty_like, q)
     kv, vv = K.view(), V.view()
     st = lib.tq_decode_attn(ctypes.byref(kv), ctypes.byref(vv), _ptr(q), B, Hq, Hkv, S_cap, _ptr(kv_len), ctx,
                             float(softmax_scale), _ptr(out), _ptr(workspace), workspace.numel(), n_split,
@@ -451,7 +452,7 @@ def tq_decode_attn_static(K, V, q, ctx=None, kv_len=None, softmax_scale=0.0, n_s
     Hkv, S_cap = _cache_for(K, V, B)
     ctx = S_cap if ctx is None else ctx
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, torch.empty_like, q)
     kv, vv = K.view(), V.view()
     st = lib.tq_decode_attn_static(ctypes.byref(kv), ctypes.byref(vv), _ptr(q), B, Hq, Hkv, S_cap, _ptr(kv_len),
                                    ctx, float(softmax_scale), _ptr(out), n_split, _stream(stream))
@@ -481,16 +482,16 @@ def tq_decode_attn_window(K, V, q, k_win, v_win, ctx=None, kv_len=None, win_len=
         raise ValueError("k_win, v_win must be [B, Hkv, W_cap, head_dim]")
     if k_win.dtype != torch.float16 or v_win.dtype != torch.float16:
         raise ValueError("the window is fp16")
-    k_win, v_win = k_win.contiguous(), v_win.contiguous()
+    k_win, v_win = _new(stream, k_win.contiguous), _new(stream, v_win.contiguous)
     W_cap = k_win.shape[2]
     if win_len is not None and (win_len.dtype != torch.int32 or win_len.numel() != B or not win_len.is_cuda):
         raise ValueError("win_len must be an int32 CUDA tensor of B window lengths")
     win = W_cap if win is None else win
     need = tq_decode_window_workspace_bytes(B, Hq, Hkv, d, ctx, n_split)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _new(stream, torch.empty, max(need, 16), dtype=torch.uint8, device=q.device)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, torch.empty_like, q)
     kv, vv = K.view(), V.view()
     st = lib.tq_decode_attn_window(ctypes.byref(kv), ctypes.byref(vv), _ptr(q), B, Hq, Hkv, S_cap, _ptr(kv_len), ctx,
                                    _ptr(k_win), _ptr(v_win), W_cap, _ptr(win_len), win, float(softmax_scale),
@@ -747,7 +748,8 @@ def tq_to_blocks(pk, stream=None):
     L = pk.layout
     n = pk.scales.numel() // pk.scales.shape[-1]
     bb = 2 + 4 * L.bits
-    out = torch.empty(tuple(pk.lead_shape) + (L.head_dim // 32, bb), dtype=torch.uint8, device=pk.codes.device)
+    out = _new(stream, torch.empty, tuple(pk.lead_shape) + (L.head_dim // 32, bb), dtype=torch.uint8,
+               device=pk.codes.device)
     _check(lib.tq_to_blocks(ctypes.byref(L), _ptr(pk.codes), _ptr(pk.scales), n, _ptr(out), _stream(stream)),
            "tq_to_blocks")
     return out
@@ -771,9 +773,9 @@ def tq_decode_attn_blocks(Lk, k_blocks, Lv, v_blocks, q, ctx=None, kv_len=None, 
     ctx = S_cap if ctx is None else ctx
     need, ns = tq_decode_workspace_bytes(B, Hq, Hkv, d, ctx, n_split)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _new(stream, torch.empty, max(need, 16), dtype=torch.uint8, device=q.device)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, torch.empty_like, q)
     st = lib.tq_decode_attn_blocks(ctypes.byref(Lk), _ptr(k_blocks), ctypes.byref(Lv), _ptr(v_blocks), _ptr(q), B,
                                    Hq, Hkv, S_cap, _ptr(kv_len), ctx, float(softmax_scale), _ptr(out),
                                    _ptr(workspace), workspace.numel(), n_split, _stream(stream))
@@ -785,7 +787,7 @@ def tq_from_blocks(layout, blocks, stream=None):
     """Inverse of tq_to_blocks: a PackedKV with leading shape blocks.shape[:-2]."""
     lib = _load()
     lead = tuple(blocks.shape[:-2])
-    pk = PackedKV(layout, lead, device=blocks.device)
+    pk = _new(stream, PackedKV, layout, lead, device=blocks.device)
     n = pk.scales.numel() // pk.scales.shape[-1]
     _check(lib.tq_from_blocks(ctypes.byref(layout), _ptr(blocks), n, _ptr(pk.codes), _ptr(pk.scales),
                               _stream(stream)), "tq_from_blocks")
@@ -800,12 +802,12 @@ def tq_polar_quantize(x, bits, stream=None):
     if x.stride(-1) != 1:
         raise ValueError("x must have a contiguous last dimension")
     lead = tuple(x.shape[:-1])
-    x2 = x.reshape(-1, d)
+    x2 = _new(stream, x.reshape, -1, d)
     n = x2.shape[0]
     cb = ctypes.c_int64()
     _check(lib.tq_polar_code_bytes(d, bits, ctypes.byref(cb)), "tq_polar_code_bytes")
-    codes = torch.empty(lead + (cb.value,), dtype=torch.uint8, device=x.device)
-    radius = torch.empty(lead, dtype=torch.float16, device=x.device)
+    codes = _new(stream, torch.empty, lead + (cb.value,), dtype=torch.uint8, device=x.device)
+    radius = _new(stream, torch.empty, lead, dtype=torch.float16, device=x.device)
     st = lib.tq_polar_quantize(_ptr(x2), _dtype_code(x.dtype), n, d, x2.stride(0), bits, _ptr(codes), _ptr(radius),
                                _stream(stream))
     _check(st, "tq_polar_quantize")
@@ -817,7 +819,7 @@ def tq_polar_dequantize(codes, radius, head_dim, bits, out_dtype=torch.float16, 
     lead = tuple(radius.shape)
     n = radius.numel()
     if out is None:
-        out = torch.empty(lead + (head_dim,), dtype=out_dtype, device=codes.device)
+        out = _new(stream, torch.empty, lead + (head_dim,), dtype=out_dtype, device=codes.device)
     st = lib.tq_polar_dequantize(_ptr(codes), _ptr(radius), n, head_dim, bits, _ptr(out), _dtype_code(out.dtype),
                                  _stream(stream))
     _check(st, "tq_polar_dequantize")
@@ -831,9 +833,9 @@ def tq_prefill_attn(K, V, q, ctx, causal=True, softmax_scale=0.0, workspace=None
     Hkv, S_cap = _cache_for(K, V, B)
     need = tq_prefill_workspace_bytes(B, Hq, Hkv, d, Tq, ctx)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _new(stream, torch.empty, max(need, 16), dtype=torch.uint8, device=q.device)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, torch.empty_like, q)
     kv, vv = K.view(), V.view()
     st = lib.tq_prefill_attn(ctypes.byref(kv), ctypes.byref(vv), _ptr(q), B, Hq, Hkv, Tq, S_cap, ctx,
                              1 if causal else 0, float(softmax_scale), _ptr(out), _ptr(workspace),
