@@ -217,3 +217,27 @@ def test_binding_refusals(tqlib):
         tb.tq_qkv_norm_rope(x.bfloat16(), 3, 1, 64)
     with pytest.raises(tb.TQError):
         tb.tq_qkv_norm_rope(x, 3, 1, 64, rope=torch.zeros(8, 24, device="cuda"))
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(new_len=[7, 2]), dict(pos=[30, 5]), dict(slot=[3, -2]), dict(rows=5),
+                                dict(cap=16), dict(cap=4)])
+def test_new_outputs_are_zero_where_no_token_goes(tqlib, kw):
+    """Outputs that the call makes, over memory that held something else: a
+    rotation table of fewer rows than there are tokens leaves tokens out with
+    no other argument, and new values beside given keys have the keys' slots."""
+    from turboquant_kv_cache_gb300 import binding as tb
+    B, T, Hq, Hkv, d = 2, 9, 3, 2, 64
+    x = torch.from_numpy(inputs.gaussian((B, T, (Hq + 2 * Hkv) * d), 31)).cuda()
+    rope = torch.from_numpy(_table(kw.get("rows", 32), d)).cuda()
+    args = {n: torch.tensor(kw[n], dtype=torch.int32, device="cuda") for n in ("new_len", "pos", "slot") if n in kw}
+    cap = kw.get("cap")
+    z = lambda *s: torch.zeros(s, dtype=torch.float16, device="cuda")  # noqa: E731
+    want = tb.tq_qkv_norm_rope(x, Hq, Hkv, d, rope=rope, q_out=z(B, Hq, T, d), k_out=z(B, Hkv, cap or T, d),
+                               v_out=z(B, Hkv, cap or T, d), **args)
+    k_out = z(B, Hkv, cap, d) if cap else None
+    for h in (Hq, Hkv, Hkv):     # what the allocator hands out next
+        for n in (T, cap or T):
+            torch.full((B, h, n, d), 9.0, dtype=torch.float16, device="cuda")
+    got = tb.tq_qkv_norm_rope(x, Hq, Hkv, d, rope=rope, k_out=k_out, **args)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)

@@ -571,8 +571,8 @@ def tq_qkv_norm_rope(qkv, Hq, Hkv, head_dim, q_weight=None, k_weight=None, eps=1
     k_weight: fp32 [d] or None; rope: fp32 [n_pos, rot_dim] (cosines, then
     sines) or None; pos, new_len, slot: int32 [B] or None.  k_out and v_out
     default to new arrays of cap = T (cap: their third dimension).  In an
-    output that is given, what no token goes to is left as it was; new ones
-    start as zeros when new_len is given."""
+    output that is given, what no token goes to is left as it was; in a new
+    one it is zero."""
     d = head_dim
     dev, shape = qkv.get_device(), qkv.shape
     if len(shape) != 3 or shape[2] != (Hq + 2 * Hkv) * d or dev < 0:
@@ -605,7 +605,9 @@ def tq_qkv_norm_rope(qkv, Hq, Hkv, head_dim, q_weight=None, k_weight=None, eps=1
         if len(table) != 2 or rope.dtype is not f32 or rope.get_device() != dev or not rope.is_contiguous():
             raise ValueError("rope must be a contiguous fp32 tensor [n_pos, rot_dim] on qkv's device")
         n_pos, rot = table
-    fresh = torch.empty if new_len is None and pos is None and slot is None else torch.zeros
+    # zeros in new outputs that some token may leave out
+    whole = new_len is None and pos is None and slot is None and (rot == 0 or n_pos >= T)
+    fresh = torch.empty if whole else torch.zeros
     if pos is not None:
         _i32(pos, B, "pos", dev)
     if new_len is not None:
@@ -618,6 +620,8 @@ def tq_qkv_norm_rope(qkv, Hq, Hkv, head_dim, q_weight=None, k_weight=None, eps=1
         if k_out is None:
             k_out = _new(stream, fresh, (B, Hkv, T, d), dtype=f16, device=qkv.device)
         if v_out is None:
+            if k_out.shape[2:3] != (T,):
+                fresh = torch.zeros
             v_out = _new(stream, fresh, tuple(k_out.shape), dtype=f16, device=qkv.device)
     kv_shape = k_out.shape
     cap = kv_shape[2] if len(kv_shape) == 4 else -1
