@@ -360,3 +360,15 @@ def test_offsets_past_32_bits(tqlib, paged):
     K2 = far(K, None)
     V2 = far(V, K2.page_table)
     assert torch.equal(tb.tq_decode_attn_shared(Kp, Vp, K2, V2, q, ctx=S), want)
+
+
+def test_one_own_cache_alone_is_refused(tqlib):
+    """K without V (or V without K) is no batch without own tokens."""
+    from turboquant_kv_cache_gb300 import binding as tb
+    Kp, Vp, K, V, q = _inputs(tb, 128, (32, 3, 0, 0), (32, 3, 0, 0), 2, 8, 2, 64, 64)
+    for k, v in ((K, None), (None, V)):
+        for kw in (dict(), dict(ctx=0), dict(ctx=64)):
+            with pytest.raises(ValueError):
+                tb.tq_decode_attn_shared(Kp, Vp, k, v, q, **kw)
+    ref = _reference(tb, Kp, Vp, 64, None, None, None, q)
+    assert (tb.tq_decode_attn_shared(Kp, Vp, None, None, q).double() - ref).abs().max().item() < ATTN_ATOL

@@ -526,7 +526,9 @@ def tq_decode_attn_shared(Kp, Vp, K, V, q, prefix_ctx=None, prefix_len=None, ctx
     Hkv, P_cap = _cache_for(Kp, Vp, 1)
     if prefix_ctx is None:
         prefix_ctx = P_cap
-    if K is not None and V is not None:
+    if (K is None) != (V is None):
+        raise ValueError("K and V, the sequences' own caches, are given together or left out together")
+    if K is not None:
         heads, S_cap = _cache_for(K, V, B)
         if heads != Hkv:
             raise ValueError("prefix and own caches must hold the same heads")
