@@ -170,3 +170,20 @@ def test_view_follows_the_table(tqlib):
     assert c.view().pages_per_seq == 0 and not c.view().page_table
     c.codes = codes.clone()
     assert c.view().codes == c.codes.data_ptr()
+
+
+def test_views_are_of_now_and_the_callers_own(tqlib):
+    """A replaced or changed layout is in the next view, and a changed view is
+    nobody else's."""
+    import torch
+    L = tb.make_layout(128, 32, 3)
+    c = tb.PackedKV.of(L, torch.zeros(4, 2, 32, 48, dtype=torch.uint8), torch.zeros(4, 2, 32, 4, dtype=torch.float16))
+    v = c.view()
+    assert v.layout.sign_seed == 1
+    c.layout = tb.make_layout(128, 32, 3, sign_seed=9)
+    assert c.view().layout.sign_seed == 9 and v.layout.sign_seed == 1
+    c.layout.norm_correct = 1
+    assert c.view().layout.norm_correct == 1
+    v = c.view()
+    v.page_size, v.codes = 7, 16
+    assert (c.view().page_size, c.view().codes) == (0, c.codes.data_ptr())

@@ -256,8 +256,6 @@ class PackedKV:
     [B, pages_per_seq] (paged: token t of batch b is row t % page_size of
     page page_table[b, t // page_size])."""
 
-    _view = None
-
     def __init__(self, layout, lead_shape, device="cuda", S=None, page_table=None):
         cb, ns, qb = tq_layout_sizes(layout)
         self.layout = layout
@@ -320,21 +318,17 @@ class PackedKV:
         return self.lead_shape[2]
 
     def view(self):
-        """The C view of the cache, kept between calls while its arrays stay
-        where they are."""
-        pt = self.page_table
-        if self.qjl is None and self.S is None:
-            at = (self.codes.data_ptr(), self.scales.data_ptr(), None, None, None)
-        else:
-            at = (self.codes.data_ptr(), self.scales.data_ptr(), _ptr(self.qjl), _ptr(self.rnorm), _ptr(self.S))
-        if pt is not None:
-            at += (pt.data_ptr(), self.lead_shape[2], pt.shape, pt.stride())
-        kept = self._view
-        if kept is None or kept[0] != at:
-            paging = (None, 0, 0) if pt is None else (at[5], at[6], self._table_stride())
-            v = tq_kv_view(*at[:5], self.layout, *paging)
-            self._view = kept = (at, v)
-        return kept[1]
+        """The C view of the cache as it is now, the caller's own."""
+        v = tq_kv_view(self.codes.data_ptr(), self.scales.data_ptr())
+        v.layout = self.layout
+        if self.qjl is not None:
+            v.qjl_bits, v.qjl_rnorm = self.qjl.data_ptr(), _ptr(self.rnorm)
+        if self.S is not None:
+            v.S = self.S.data_ptr()
+        if self.page_table is not None:
+            v.page_table, v.page_size = self.page_table.data_ptr(), self.lead_shape[2]
+            v.pages_per_seq = self._table_stride()
+        return v
 
     def _table_stride(self):
         """Entries between two rows of the table (its width unless it is part of a wider one)."""
