@@ -330,3 +330,50 @@ def test_binding_refusals(tqlib):
         tb.tq_pages_fork(pool, z(5), z(5), z(5), z(5))
     with pytest.raises(ValueError):
         tb.tq_pages_free(pool, z(2), z(1))
+
+
+def test_replaced_arrays_are_followed(tqlib):
+    """The page calls work on the pool's and the caches' arrays as they are at
+    the call, and refuse what no longer fits."""
+    from turboquant_kv_cache_gb300 import binding as tb
+    L = tb.make_layout(64, 32, 4)
+    c = tb.PackedKV(L, (20, 2, 32))
+    c.codes.view(-1).copy_(torch.arange(c.codes.numel(), device="cuda") % 251)
+    c.scales.fill_(1)
+    pool = tb.PagePool.new(4, 6, 20, 32, [c])
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    fork = lambda *e: tb.tq_pages_fork(pool, *(i32(x) for x in e)).tolist()  # noqa: E731
+    assert fork(-1, 0, 0, 40) == [0, 2, 0, 0]
+    old = c.codes
+    c.codes = old.clone()
+    first = old.clone()
+    assert fork(0, 1, 40, 40) == [0, 1, 1, 0]                      # page 1 copied to page 2, in the new array
+    assert torch.equal(old, first)
+    assert torch.equal(c.codes[2], first[1]) and torch.equal(c.codes[3:], first[3:])
+    # a wider table, other books
+    was = pool.page_table, pool.n_pages, pool.ref
+    pool.page_table = torch.zeros(4, 9, dtype=torch.int32, device="cuda")
+    pool.page_table[:, :6] = was[0]
+    pool.ref, pool.n_pages = was[2].clone(), was[1].clone()
+    kept = [t.clone() for t in was]
+    assert fork(1, 1, 40, 9 * 32) == [0, 7, 0, 0] and pool.n_pages.tolist() == [2, 9, 0, 0]
+    assert all(torch.equal(a, b) for a, b in zip(was, kept))
+    tb.tq_pages_free(pool, i32(0))
+    assert tb.tq_pages_compact(pool).tolist() == [0, 9, 1, 0]
+    assert torch.equal(c.codes[1], first[9]) and torch.equal(old, first)
+    # a table of the same storage with other rows
+    pool.page_table = pool.page_table.view(-1)[:32].view(4, 8)
+    assert pool.books() and pool.struct.pages_per_seq == 8
+    # what no longer fits is refused before anything runs
+    c.codes = old[:19].contiguous()
+    for call in (lambda: fork(-1, 2, 0, 1), lambda: tb.tq_pages_compact(pool)):
+        with pytest.raises(ValueError):
+            call()
+    c.codes = old
+    pool.n_pages = pool.n_pages[:3].clone()
+    for call in (lambda: fork(-1, 2, 0, 1), lambda: tb.tq_pages_compact(pool), lambda: tb.tq_pages_free(pool, i32(0))):
+        with pytest.raises(ValueError):
+            call()
+    pool.n_pages, pool.ref = was[1].clone(), was[2].long()
+    with pytest.raises(ValueError):
+        tb.tq_pages_free(pool, i32(0))

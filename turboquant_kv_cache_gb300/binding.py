@@ -277,15 +277,7 @@ class PackedKV:
         """A PackedKV over arrays that exist already (contiguous; the lead
         shape is codes.shape[:-1]).  A table may be part of a wider one (its
         rows then lie further apart than they are long)."""
-        cb, ns, qb = tq_layout_sizes(layout)
         lead = tuple(codes.shape[:-1])
-        if qb and (qjl is None or rnorm is None):
-            raise ValueError("a layout with QJL has its sign bits and residual norms")
-        for t, dt, tail in ((codes, torch.uint8, (cb,)), (scales, torch.float16, (ns,)),
-                            (qjl if qb else None, torch.uint8, (qb,)), (rnorm if qb else None, torch.float16, ())):
-            if t is not None and (t.dtype != dt or tuple(t.shape) != lead + tail or not t.is_contiguous()
-                                  or t.device != codes.device):
-                raise ValueError("arrays must be contiguous, of one lead shape and device, as the layout has them")
         if page_table is not None and (page_table.dtype != torch.int32 or page_table.dim() != 2 or len(lead) != 3
                                        or page_table.device != codes.device or page_table.stride(1) != 1):
             raise ValueError("paged cache: lead shape [num_pages, Hkv, page_size] and an int32 page table "
@@ -293,7 +285,20 @@ class PackedKV:
         self = cls.__new__(cls)
         self.layout, self.lead_shape, self.page_table, self.S = layout, lead, page_table, S
         self.codes, self.scales, self.qjl, self.rnorm = codes, scales, qjl, rnorm
+        self.check_arrays()
         return self
+
+    def check_arrays(self):
+        """Raises ValueError where an array is not what the layout and the lead
+        shape say."""
+        cb, ns, qb = tq_layout_sizes(self.layout)
+        if qb and (self.qjl is None or self.rnorm is None):
+            raise ValueError("a layout with QJL has its sign bits and residual norms")
+        for t, dt, tail in ((self.codes, torch.uint8, (cb,)), (self.scales, torch.float16, (ns,)),
+                            (self.qjl if qb else None, torch.uint8, (qb,)), (self.rnorm if qb else None, torch.float16, ())):
+            if t is not None and (t.dtype != dt or tuple(t.shape) != self.lead_shape + tail or not t.is_contiguous()
+                                  or t.device != self.codes.device):
+                raise ValueError("arrays must be contiguous, of one lead shape and device, as the layout has them")
 
     @property
     def n_vec(self):
@@ -640,28 +645,57 @@ class PagePool:
     holds), ref int32 [num_pages] (sequences that hold each page), and the
     caches whose pages they name (PackedKV of lead shape [num_pages, Hkv,
     page_size]: every layer's K and V).  A new pool has zeros in n_pages and
-    ref (PagePool.new)."""
+    ref (PagePool.new).  The calls follow when one of these arrays is replaced
+    by another; none of them must be given another storage in place (set_,
+    resize_)."""
 
     def __init__(self, page_table, n_pages, ref, page_size, caches=()):
-        for t, dim in ((page_table, 2), (n_pages, 1), (ref, 1)):
-            if t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous() or t.device != page_table.device:
-                raise ValueError("page_table [n_seqs, pages_per_seq], n_pages [n_seqs] and ref [num_pages] must be "
-                                 "contiguous int32 tensors on one device")
-        if n_pages.shape[0] != page_table.shape[0]:
-            raise ValueError("n_pages must have an entry for every row of page_table")
         self.page_table, self.n_pages, self.ref, self.page_size = page_table, n_pages, ref, page_size
-        self.dev = ref.get_device()
-        if self.dev < 0:
-            raise ValueError("a page pool lies on a CUDA device")
         self.caches = tuple(caches)
+        self._books_of = (None, None, None, 0)
+        self.bound()
+
+    def books(self):
+        """The C struct of the table and its books, checked and built anew
+        where one of them has been replaced."""
+        was = self._books_of    # the tensors themselves: none of them is freed while the struct names it
+        if (self.page_table is not was[0] or self.n_pages is not was[1] or self.ref is not was[2]
+                or self.page_size != was[3]):
+            table, n_pages, ref = t = self.page_table, self.n_pages, self.ref
+            for x, dim in zip(t, (2, 1, 1)):
+                if x.dtype != torch.int32 or x.dim() != dim or not x.is_contiguous() or x.device != table.device:
+                    raise ValueError("page_table [n_seqs, pages_per_seq], n_pages [n_seqs] and ref [num_pages] must be "
+                                     "contiguous int32 tensors on one device")
+            if n_pages.shape[0] != table.shape[0]:
+                raise ValueError("n_pages must have an entry for every row of page_table")
+            if ref.get_device() < 0:
+                raise ValueError("a page pool lies on a CUDA device")
+            self.dev = ref.get_device()
+            self.struct = tq_page_pool(table.data_ptr(), n_pages.data_ptr(), ref.data_ptr(), table.shape[0],
+                                       table.shape[1], ref.shape[0], self.page_size)
+            self.ref_struct = ctypes.byref(self.struct)
+            self._books_of, self._caches_of = t + (self.page_size,), None
+        return self.ref_struct
+
+    def bound(self):
+        """books(), and the same for the caches' C views."""
+        struct, was = self.books(), self._caches_of
+        if was is not None and len(was) == len(self.caches):
+            for c, k in zip(self.caches, was):
+                if c.codes is not k[0] or c.scales is not k[1] or c.qjl is not k[2] or c.rnorm is not k[3]:
+                    break
+            else:
+                return struct
+        self._caches_of = None
         self.heads = self.caches[0].lead_shape[1] if self.caches else 0
+        lead = (self.ref.shape[0], self.heads, self.page_size)
         for c in self.caches:
-            if c.lead_shape != (ref.shape[0], self.heads, page_size) or c.codes.device != ref.device:
+            if c.lead_shape != lead or c.codes.device != self.ref.device:
                 raise ValueError("caches must have lead shape [num_pages, Hkv, page_size] on the pool's device")
-        self.struct = tq_page_pool(page_table.data_ptr(), n_pages.data_ptr(), ref.data_ptr(), page_table.shape[0],
-                                   page_table.shape[1], ref.shape[0], page_size)
-        self.ref_struct = ctypes.byref(self.struct)
+            c.check_arrays()
         self.views = (tq_kv_view * max(1, len(self.caches)))(*[c.view() for c in self.caches])
+        self._caches_of = [(c.codes, c.scales, c.qjl, c.rnorm) for c in self.caches]
+        return struct
 
     @classmethod
     def new(cls, n_seqs, pages_per_seq, num_pages, page_size, caches=(), device="cuda"):
@@ -696,7 +730,7 @@ def tq_pages_fork(pool, parent, child, share_len, new_len, workspace=None, resul
     int32 CUDA tensors of one length.  Returns the result tensor {status, pages taken,
     pages copied, 0}: status 0 done, > 0 pages missing, -1 an entry is not
     valid; unless it is 0 nothing has changed."""
-    n, dev = child.numel(), pool.dev
+    struct, n, dev = pool.bound(), child.numel(), pool.dev
     _i32(parent, n, "parent", dev)
     _i32(child, n, "child", dev)
     _i32(share_len, n, "share_len", dev)
@@ -705,7 +739,7 @@ def tq_pages_fork(pool, parent, child, share_len, new_len, workspace=None, resul
         with _on(dev):
             return tq_pages_fork(pool, parent, child, share_len, new_len, workspace, result, stream)
     workspace, result = _pool_call(pool, n, workspace, result, stream)
-    st = _load().tq_pages_fork(pool.ref_struct, pool.views, len(pool.caches), pool.heads, parent.data_ptr(),
+    st = _load().tq_pages_fork(struct, pool.views, len(pool.caches), pool.heads, parent.data_ptr(),
                                child.data_ptr(), share_len.data_ptr(), new_len.data_ptr(), n, result.data_ptr(), workspace.data_ptr(),
                                workspace.nbytes, _stream_on(stream, pool.dev))
     if st:
@@ -716,13 +750,13 @@ def tq_pages_fork(pool, parent, child, share_len, new_len, workspace=None, resul
 def tq_pages_free(pool, seqs, keep_len=None, stream=None):
     """The sequences named (int32 CUDA tensor) give up their pages, or those
     behind their first keep_len tokens."""
-    n, dev = seqs.numel(), pool.dev
+    struct, n, dev = pool.books(), seqs.numel(), pool.dev
     _i32(seqs, n, "seqs", dev)
     _i32(keep_len, n, "keep_len", dev)
     if dev != _current_device():
         with _on(dev):
             return tq_pages_free(pool, seqs, keep_len, stream)
-    st = _load().tq_pages_free(pool.ref_struct, seqs.data_ptr(), _ptr(keep_len), n, _stream_on(stream, pool.dev))
+    st = _load().tq_pages_free(struct, seqs.data_ptr(), _ptr(keep_len), n, _stream_on(stream, pool.dev))
     if st:
         _check(st, "tq_pages_free")
 
@@ -730,11 +764,12 @@ def tq_pages_free(pool, seqs, keep_len=None, stream=None):
 def tq_pages_compact(pool, workspace=None, result=None, stream=None):
     """Moves the pages in use to the front of the pool in all of its caches.
     Returns the result tensor {0, pages in use, pages moved, 0}."""
+    struct = pool.bound()
     if pool.dev != _current_device():
         with _on(pool.dev):
             return tq_pages_compact(pool, workspace, result, stream)
     workspace, result = _pool_call(pool, 0, workspace, result, stream)
-    st = _load().tq_pages_compact(pool.ref_struct, pool.views, len(pool.caches), pool.heads, result.data_ptr(),
+    st = _load().tq_pages_compact(struct, pool.views, len(pool.caches), pool.heads, result.data_ptr(),
                                   workspace.data_ptr(), workspace.nbytes, _stream_on(stream, pool.dev))
     if st:
         _check(st, "tq_pages_compact")
