@@ -187,3 +187,36 @@ def test_views_are_of_now_and_the_callers_own(tqlib):
     v = c.view()
     v.page_size, v.codes = 7, 16
     assert (c.view().page_size, c.view().codes) == (0, c.codes.data_ptr())
+
+
+def test_calls_see_the_cache_as_it_is(tqlib):
+    """What the C calls get equals a view of now after every kind of change,
+    and is not the struct that view() hands out."""
+    import torch
+    L = tb.make_layout(128, 128, 2, qjl_m=128)
+    cb, ns, qb = tb.tq_layout_sizes(L)
+    z = lambda dt, *s: torch.zeros(s, dtype=dt)  # noqa: E731
+    c = tb.PackedKV.of(L, z(torch.uint8, 4, 2, 32, cb), z(torch.float16, 4, 2, 32, ns), z(torch.uint8, 4, 2, 32, qb),
+                       z(torch.float16, 4, 2, 32))
+
+    def same():
+        got = c._view_ref()._obj
+        assert bytes(got) == bytes(c.view())
+        v = c.view()
+        v.codes = 16
+        assert bytes(c._view_ref()._obj) == bytes(c.view()) != bytes(v)
+
+    same()
+    for name in ("codes", "scales", "qjl", "rnorm"):
+        setattr(c, name, getattr(c, name).clone())
+        same()
+    c.S = torch.zeros(128, 128)
+    same()
+    c.layout = tb.make_layout(128, 128, 2, qjl_m=128, sign_seed=3)
+    same()
+    c.layout.norm_correct = 1
+    same()
+    table = torch.zeros(16, dtype=torch.int32)
+    for t in (table.view(2, 8), table.view(4, 4), table.view(2, 8)[:, :3], table[8:].view(1, 8), None):
+        c.page_table = t
+        same()

@@ -335,6 +335,21 @@ class PackedKV:
             v.pages_per_seq = self._table_stride()
         return v
 
+    _kept = (None, None)
+
+    def _view_ref(self):
+        """view() by reference, for a C call of this module: nobody changes it,
+        so it is kept while all that it is made of is what it was."""
+        of = self.codes.data_ptr(), self.scales.data_ptr(), bytes(self.layout)
+        pt = self.page_table
+        if pt is not None:
+            of += pt.data_ptr(), self.lead_shape[2], pt.shape, pt.stride()
+        if self.qjl is not None or self.S is not None:
+            of += _ptr(self.qjl), _ptr(self.rnorm), _ptr(self.S)
+        if of != self._kept[0]:
+            self._kept = of, ctypes.byref(self.view())
+        return self._kept[1]
+
     def _table_stride(self):
         """Entries between two rows of the table (its width unless it is part of a wider one)."""
         pt = self.page_table
@@ -435,8 +450,8 @@ def tq_decode_attn(K, V, q, ctx=None, kv_len=None, softmax_scale=0.0, n_split=0,
         workspace = _new(stream, torch.empty, max(need, 16), dtype=torch.uint8, device=q.device)
     if out is None:
         out = _new(stream, torch.empty_like, q)
-    kv, vv = K.view(), V.view()
-    st = lib.tq_decode_attn(ctypes.byref(kv), ctypes.byref(vv), _ptr(q), B, Hq, Hkv, S_cap, _ptr(kv_len), ctx,
+    kv, vv = K._view_ref(), V._view_ref()
+    st = lib.tq_decode_attn(kv, vv, _ptr(q), B, Hq, Hkv, S_cap, _ptr(kv_len), ctx,
                             float(softmax_scale), _ptr(out), _ptr(workspace), workspace.numel(), n_split,
                             _stream(stream))
     _check(st, "tq_decode_attn")
@@ -452,8 +467,8 @@ def tq_decode_attn_static(K, V, q, ctx=None, kv_len=None, softmax_scale=0.0, n_s
     ctx = S_cap if ctx is None else ctx
     if out is None:
         out = _new(stream, torch.empty_like, q)
-    kv, vv = K.view(), V.view()
-    st = lib.tq_decode_attn_static(ctypes.byref(kv), ctypes.byref(vv), _ptr(q), B, Hq, Hkv, S_cap, _ptr(kv_len),
+    kv, vv = K._view_ref(), V._view_ref()
+    st = lib.tq_decode_attn_static(kv, vv, _ptr(q), B, Hq, Hkv, S_cap, _ptr(kv_len),
                                    ctx, float(softmax_scale), _ptr(out), n_split, _stream(stream))
     _check(st, "tq_decode_attn_static")
     return out
@@ -491,8 +506,8 @@ def tq_decode_attn_window(K, V, q, k_win, v_win, ctx=None, kv_len=None, win_len=
         workspace = _new(stream, torch.empty, max(need, 16), dtype=torch.uint8, device=q.device)
     if out is None:
         out = _new(stream, torch.empty_like, q)
-    kv, vv = K.view(), V.view()
-    st = lib.tq_decode_attn_window(ctypes.byref(kv), ctypes.byref(vv), _ptr(q), B, Hq, Hkv, S_cap, _ptr(kv_len), ctx,
+    kv, vv = K._view_ref(), V._view_ref()
+    st = lib.tq_decode_attn_window(kv, vv, _ptr(q), B, Hq, Hkv, S_cap, _ptr(kv_len), ctx,
                                    _ptr(k_win), _ptr(v_win), W_cap, _ptr(win_len), win, float(softmax_scale),
                                    _ptr(out), _ptr(workspace), workspace.numel(), n_split, _stream(stream))
     _check(st, "tq_decode_attn_window")
@@ -533,7 +548,7 @@ def tq_decode_attn_shared(Kp, Vp, K, V, q, prefix_ctx=None, prefix_len=None, ctx
             raise ValueError("prefix and own caches must hold the same heads")
         if K.codes.get_device() != dev or V.codes.get_device() != dev:
             raise ValueError("caches must have q's head_dim and device")
-        kv, vv = ctypes.byref(K.view()), ctypes.byref(V.view())
+        kv, vv = K._view_ref(), V._view_ref()
     else:
         S_cap = 0
         kv = vv = None
@@ -555,7 +570,7 @@ def tq_decode_attn_shared(Kp, Vp, K, V, q, prefix_ctx=None, prefix_len=None, ctx
         out = _new(stream, torch.empty_like, q)
     elif not _is(out, torch.float16, shape, dev):
         raise ValueError("out must be a contiguous tensor like q")
-    st = _load().tq_decode_attn_shared(ctypes.byref(Kp.view()), ctypes.byref(Vp.view()), P_cap, _ptr(prefix_len),
+    st = _load().tq_decode_attn_shared(Kp._view_ref(), Vp._view_ref(), P_cap, _ptr(prefix_len),
                                        prefix_ctx, kv, vv, q.data_ptr(), B, Hq, Hkv, S_cap, _ptr(kv_len), ctx, softmax_scale,
                                        out.data_ptr(), workspace.data_ptr(), workspace.nbytes, n_split,
                                        _stream_on(stream, dev))
@@ -871,8 +886,8 @@ def tq_prefill_attn(K, V, q, ctx, causal=True, softmax_scale=0.0, workspace=None
         workspace = _new(stream, torch.empty, max(need, 16), dtype=torch.uint8, device=q.device)
     if out is None:
         out = _new(stream, torch.empty_like, q)
-    kv, vv = K.view(), V.view()
-    st = lib.tq_prefill_attn(ctypes.byref(kv), ctypes.byref(vv), _ptr(q), B, Hq, Hkv, Tq, S_cap, ctx,
+    kv, vv = K._view_ref(), V._view_ref()
+    st = lib.tq_prefill_attn(kv, vv, _ptr(q), B, Hq, Hkv, Tq, S_cap, ctx,
                              1 if causal else 0, float(softmax_scale), _ptr(out), _ptr(workspace),
                              workspace.numel(), _stream(stream))
     _check(st, "tq_prefill_attn")
