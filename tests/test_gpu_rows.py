@@ -241,3 +241,47 @@ def test_new_outputs_are_zero_where_no_token_goes(tqlib, kw):
     got = tb.tq_qkv_norm_rope(x, Hq, Hkv, d, rope=rope, k_out=k_out, **args)
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+# Thread groups that take several rows of a token: 4 rows (12 heads; 7 and 11
+# with one group's last head missing), 3 (9 heads; 5 with one missing), 2 (10
+# heads; 13 with one missing), with the borders between query, key and value
+# heads inside a group.  There are enough tokens for 2432 blocks of one row.
+GROUPS = [
+    # rows a group, B, T, Hq, Hkv, d
+    (4, 5, 401, 6, 3, 128), (4, 3, 1201, 3, 2, 128), (4, 3, 301, 5, 3, 256), (4, 4, 900, 6, 3, 64),
+    (3, 5, 451, 5, 2, 128), (3, 4, 601, 3, 1, 256), (2, 5, 401, 4, 3, 128), (2, 3, 301, 7, 3, 256),
+]
+
+
+@pytest.mark.parametrize("rows,B,T,Hq,Hkv,d", GROUPS)
+@pytest.mark.parametrize("f32,rot,inter,nq,nk", [(False, 1.0, False, True, True), (True, 0.5, True, True, True),
+                                                 (False, 0.75, True, True, False), (True, 1.0, False, False, True),
+                                                 (False, 0.0, False, True, True)])
+def test_groups_of_several_rows(tqlib, rows, B, T, Hq, Hkv, d, f32, rot, inter, nq, nk):
+    H = Hq + 2 * Hkv
+    idle = {r: -H % r for r in (4, 3, 2)}
+    assert -(-B * T // (64 // (d // 16))) * H > 152 * 16 and min(idle, key=idle.get) == rows   # the library's rule
+    test_rows_match_64_bits(tqlib, B, T, Hq, Hkv, d, f32, int(rot * d) // 16 * 16, inter, nq, nk, 2)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,f32", [(6, 3, 128, False), (5, 2, 256, True), (7, 3, 64, False)])
+def test_groups_of_several_rows_in_a_padded_batch(tqlib, Hq, Hkv, d, f32):
+    """Ragged lengths over many tokens: the tokens there are as without
+    lengths, the rest is left alone."""
+    from turboquant_kv_cache_gb300 import binding as tb
+    B, T = 6, 900
+    x = torch.from_numpy(inputs.gaussian((B, T, (Hq + 2 * Hkv) * d), 41, np.float32 if f32 else np.float16)).cuda()
+    w = torch.from_numpy(1 + 0.2 * inputs.gaussian((2, d), 42, np.float32)).cuda()
+    rope = torch.from_numpy(_table(T, d)).cuda()
+    full = tb.tq_qkv_norm_rope(x, Hq, Hkv, d, w[0], w[1], rope=rope)
+    lens = [900, 0, 1, 899, 450, 7]
+    outs = [torch.full_like(t, 9.0) for t in full]
+    pad = x.clone()
+    for b, n in enumerate(lens):
+        pad[b, n:] = float("nan")
+    tb.tq_qkv_norm_rope(pad, Hq, Hkv, d, w[0], w[1], rope=rope, new_len=torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                        q_out=outs[0], k_out=outs[1], v_out=outs[2])
+    for o, t in zip(outs, full):
+        for b, n in enumerate(lens):
+            assert torch.equal(o[b, :, :n], t[b, :, :n]) and (o[b, :, n:] == 9.0).all()
