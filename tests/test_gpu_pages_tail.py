@@ -140,3 +140,22 @@ def test_random_roll_backs(tqlib, n_seqs, pps, num_pages, page, steps):
                 p.free([s])
                 length[s] = 0
     assert replaced > steps
+
+
+@pytest.mark.parametrize("num_pages,n_seqs,pps", [(4000, 6, 2300), (8000, 6, 2300), (17000, 6, 4200), (4000, 200, 700), (9000, 1100, 20)])
+def test_long_rows_and_many_sequences(tqlib, num_pages, n_seqs, pps):
+    """Rows longer than a block takes at once, shared, rolled back over and
+    compacted; pools, entries and sequences on both sides of what one block
+    takes."""
+    from turboquant_kv_cache_gb300 import binding as tb
+    p = _pair(tb, n_seqs, pps, num_pages, 32, ("pervec_d64",))
+    held = min(pps - 3, num_pages // 2)
+    assert p.fork([(-1, 1, 0, 40), (-1, 0, 0, held * 32 - 5)])[0] == 0
+    assert p.fork([(0, c, held * 32 - 5 - c % 27, held * 32 - 5 - c % 27) for c in range(2, n_seqs)])[0] == 0
+    p.free([1])
+    p.compact()
+    assert p.fork([(2, 2, held * 16 + 3, held * 32 + 40)])[0] == 0       # half of the row replaced
+    p.free([0])
+    p.compact()
+    p.free([c for c in range(3, n_seqs)])
+    p.compact()

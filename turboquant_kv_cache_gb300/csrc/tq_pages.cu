@@ -17,17 +17,35 @@
 //   assign  chunks deal their free pages by rank (fork), or list holes and
 //           pages to move by rank (compact)
 //   rename  tables and counts follow (compact)
-//   move    page contents
+//   move    a block per entry shares the parent's pages (fork); page contents
 // A small pool's call is bound by its launches (2 us each on the GPU, 3 on the
-// host), so there one block does everything but the move: a fork of 4 entries
-// over 512 pages is two launches instead of four, and so is one of 190 entries
-// of up to 128 pages over 2000 pages (with the copies 32.3 us against 36.8).
+// host), so there one block does everything but the move, two launches instead
+// of four or five.  What bounds that block are the counts it reads, up to eight
+// a thread, and for a compaction the rows, a warp each.  Graph replays without
+// caches, one block against several:
+//   fork, children sharing whole rows    entries x pages a row   us
+//     pool of 2000                       8 x 1023        7.6     11.5
+//                                        190 x 127       9.5     14.1
+//     pool of 8192                       8 x 255        10.0     11.7
+//                                        250 x 63       12.7     13.8
+//                                        1000 x 31      16.5     16.9
+//     pool of 16384                      8 x 4095       15.9     14.9
+//                                        128 x 255      19.8     13.4
+//   compaction                           sequences x pages a row
+//     pool of 2000                       8 x 1023        5.5     10.3
+//                                        64 x 127        6.1      7.5
+//                                        160 x 127       9.3      7.7
+//                                        256 x 31        9.4      8.1
+//     pool of 4096                       64 x 127        6.4      7.9
+//     pool of 8192                       8 x 255         8.5      8.6
+//                                        64 x 127       10.6      7.8
+// so the limits are 8192 pages and 1024 entries, 4096 pages and 128 sequences.
 //
 // Bound: launches, and for large pools the copies, which read and write every
 // moved byte once.  Measured in graph replays, with the call that frees pages
 // and a reset of the books before each: 3 freed, 4 forked and 4 grown over 512
-// pages of 28 KB 11.0 us; 60, 150 and 40 over 2000 pages in 64 arrays (134 MB
-// moved, 20 us at a copy's rate) 32.3 us; 512 pages compacted 8.8 us, 2500 in
+// pages of 28 KB 11.1 us; 60, 150 and 40 over 2000 pages in 64 arrays (134 MB
+// moved, 20 us at a copy's rate) 31.1 us; 512 pages compacted 9.5 us, 2500 in
 // 64 arrays (557 MB, 83 us) 107.5 us.
 #include <cuda_runtime.h>
 
@@ -39,8 +57,10 @@ namespace {
 constexpr int kChunk = 1024;          // pages per block of count and assign
 constexpr int kThreads = 256;
 constexpr int kPlanThreads = 1024;
-constexpr int kSmallPages = 16384;    // pages that one block takes (16 a thread)
-constexpr int kSmallEntries = 32768;  // table entries a call may touch that one block takes
+// what one block takes: pages of the pool (8 or 4 a thread), entries of a fork, sequences of a compacted pool
+constexpr int kForkPages = 8192, kForkEntries = 1024;
+constexpr int kPackPages = 4096, kPackSeqs = 128;
+constexpr int kAhead = 8;             // table entries whose loads a thread has in flight
 constexpr int kMaxArrays = 128;       // cache arrays one move launch takes
 constexpr int kPiece = 16384;         // bytes one block copies at a time: four 16-byte loads in flight a thread
 constexpr int kMaxPerSeq = 1 << 20;   // pages of a sequence: kPlanThreads of them sum below 2^31
@@ -339,18 +359,27 @@ __device__ void deal(const ForkArgs& a, int r, int page) {
   if (t == 0) w.dst[lo] = page;   // the copy of a part-filled page goes to the first fresh page
 }
 
-// Entry i shares its parent's full pages: the pages from k0 on, `step` apart.
-__device__ void share(const ForkArgs& a, int i, int k0, int step) {
+// Entry i shares its parent's full pages (its first, which no entry of the
+// call changes), and the shared pages that it replaced lose it as a holder;
+// by one block.
+__device__ void share(const ForkArgs& a, int i) {
   const tq_page_pool& p = a.pool;
-  const int parent = a.parent[i], child = a.child[i];
+  const int parent = a.parent[i], child = a.child[i], cow = a.w.cow[i];
+  for (int t = threadIdx.x; t < cow; t += kThreads) atomicSub(&p.ref[a.w.rank[a.w.off[i] + t]], 1);
   if (parent < 0 || parent == child) return;
   const int full = a.w.first[i];
   const int32_t* from = p.page_table + (int64_t)parent * p.pages_per_seq;
   int32_t* to = p.page_table + (int64_t)child * p.pages_per_seq;
-  for (int k = k0; k < full; k += step) {
-    const int page = from[k];
-    to[k] = page;
-    if (page >= 0 && page < p.num_pages) atomicAdd(&p.ref[page], 1);
+  for (int k = threadIdx.x; k < full; k += kAhead * kThreads) {
+    int page[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) page[u] = k + u * kThreads < full ? from[k + u * kThreads] : 0;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (k + u * kThreads >= full) break;
+      to[k + u * kThreads] = page[u];
+      if (page[u] >= 0 && page[u] < p.num_pages) atomicAdd(&p.ref[page[u]], 1);
+    }
   }
 }
 
@@ -367,7 +396,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_small_kernel(const Fo
   __shared__ int s_part[33];
   const int p0 = threadIdx.x * per, p1 = min(p0 + per, a.pool.num_pages);
   int c = 0, n_free;
-  uint32_t free_bits = 0;   // per <= 16
+  uint32_t free_bits = 0;   // per <= 8
   for (int p = p0; p < p1; ++p) {
     const int f = a.pool.ref[p] == 0 ? 1 : 0;
     c += f;
@@ -377,37 +406,31 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_small_kernel(const Fo
   if (!plan_entries(a, n_free, s_part)) return;
   const int need = a.w.off[a.n];
   for (; free_bits && r < need; ++r, free_bits &= free_bits - 1) deal(a, r, p0 + __ffs(free_bits) - 1);
-  for (int i = threadIdx.x >> 5; i < a.n; i += kPlanThreads / 32) share(a, i, threadIdx.x & 31, 32);
 }
 
-// Blocks [0, chunks): deal the chunk's free pages.  Blocks behind: entry
-// blockIdx.x - chunks shares its parent's full pages.
-__global__ void __launch_bounds__(kThreads) pages_fork_assign_kernel(const ForkArgs a, int chunks) {
+// A block deals a chunk's free pages.
+__global__ void __launch_bounds__(kThreads) pages_fork_assign_kernel(const ForkArgs a) {
   chain_begin();
   __shared__ int s_part[33];
   const Work w = a.w;
   const tq_page_pool& p = a.pool;
   if (!w.head->ok) return;
-  if ((int)blockIdx.x < chunks) {
-    const int need = w.head->need;
-    const int base = w.chunk[blockIdx.x];
-    if (base >= need) return;
-    constexpr int PER = kChunk / kThreads;
-    const int p0 = blockIdx.x * kChunk + threadIdx.x * PER;
-    int f[PER], c = 0;
+  const int need = w.head->need;
+  const int base = w.chunk[blockIdx.x];
+  if (base >= need) return;
+  constexpr int PER = kChunk / kThreads;
+  const int p0 = blockIdx.x * kChunk + threadIdx.x * PER;
+  int f[PER], c = 0;
 #pragma unroll
-    for (int k = 0; k < PER; ++k) c += f[k] = free_at(p.ref, p0 + k, p.num_pages);
-    int total;
-    int r = base + block_scan(c, s_part, &total);
+  for (int k = 0; k < PER; ++k) c += f[k] = free_at(p.ref, p0 + k, p.num_pages);
+  int total;
+  int r = base + block_scan(c, s_part, &total);
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-      if (!f[k]) continue;
-      if (r >= need) break;
-      deal(a, r++, p0 + k);
-    }
-    return;
+  for (int k = 0; k < PER; ++k) {
+    if (!f[k]) continue;
+    if (r >= need) break;
+    deal(a, r++, p0 + k);
   }
-  share(a, blockIdx.x - chunks, threadIdx.x, kThreads);
 }
 
 // The caches' arrays as runs of bytes per page.
@@ -419,12 +442,15 @@ struct Arrays {
 };
 
 // Copies w.moves pages src[r] -> dst[r] (an entry of a fork without a copy
-// has src -1), one piece of one array per block and step.  The blocks also
-// lower the counts of the pages that a fork's n_drop entries replaced.
-__global__ void __launch_bounds__(kThreads) pages_move_kernel(Work w, const __grid_constant__ Arrays a,
-                                                              int32_t* ref, int num_pages, int n_drop) {
+// has src -1), one piece of one array per block and step.  Before that the
+// blocks do what is left of a fork's f.n entries (0: nothing), whose pages have
+// all been dealt: the counts that tell the free ones are not read any more.
+__global__ void __launch_bounds__(kThreads) pages_move_kernel(const ForkArgs f, const __grid_constant__ Arrays a) {
   chain_begin();
-  const int moves = w.head->moves;
+  const Work& w = f.w;
+  const int moves = w.head->moves, num_pages = f.pool.num_pages;
+  if (moves)
+    for (int i = blockIdx.x; i < f.n; i += gridDim.x) share(f, i);
   const int64_t items = (int64_t)moves * a.pieces;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
     const int r = (int)(it / a.pieces), pc = (int)(it - (int64_t)r * a.pieces);
@@ -450,12 +476,6 @@ __global__ void __launch_bounds__(kThreads) pages_move_kernel(Work w, const __gr
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (threadIdx.x + u * kThreads < n16) d[threadIdx.x + u * kThreads] = v[u];
-  }
-  if (moves) {
-    for (int i = blockIdx.x; i < n_drop; i += gridDim.x) {
-      const int cow = w.cow[i];
-      for (int t = threadIdx.x; t < cow; t += kThreads) atomicSub(&ref[w.rank[w.off[i] + t]], 1);
-    }
   }
 }
 
@@ -504,11 +524,17 @@ __device__ void rename(const CompactArgs& a, int n_live, int moves, int64_t tid,
   for (int64_t s = tid / 32; s < p.n_seqs; s += step / 32) {
     int32_t* row = p.page_table + s * p.pages_per_seq;
     const int held = min(p.n_pages[s], p.pages_per_seq);
-    for (int j = lane; j < held; j += 32) {
-      const int page = row[j];
-      if (page < n_live || page >= p.num_pages) continue;
-      const int r = w.rank[page];   // -1: a free page, which no table should name
-      if (r >= 0) row[j] = w.dst[r];
+    for (int j = lane; j < held; j += kAhead * 32) {
+      int x[kAhead];   // the entry's page, its rank (-1: none, or a free page, which no table should name), its new page
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) x[u] = j + u * 32 < held ? row[j + u * 32] : -1;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) x[u] = x[u] >= n_live && x[u] < p.num_pages ? w.rank[x[u]] : -1;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) x[u] = x[u] >= 0 ? w.dst[x[u]] : -1;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (x[u] >= 0) row[j + u * 32] = x[u];
     }
   }
 }
@@ -534,7 +560,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_compact_small_kernel(const
   __shared__ int s_part[33];
   const int n = a.pool.num_pages, p0 = min(threadIdx.x * per, n), p1 = min(p0 + per, n);
   int c = 0, n_free, moves;
-  uint32_t free_bits = 0;   // per <= 16
+  uint32_t free_bits = 0;   // per <= 8
   for (int p = p0; p < p1; ++p) {
     const int f = a.pool.ref[p] == 0 ? 1 : 0;
     c += f;
@@ -653,15 +679,18 @@ int check_caches(const tq_kv_view* caches, int n_caches, int Hkv, int page_size)
   return TQ_OK;
 }
 
-int launch_moves(const tq_kv_view* caches, int n_caches, int Hkv, const tq_page_pool& p, const Work& w, int64_t most,
-                 int n_drop, cudaStream_t st) {
+// f: a fork's entries, or none (n = 0) with the pool and the lists; at most
+// `most` pages are copied.
+int launch_moves(const tq_kv_view* caches, int n_caches, int Hkv, ForkArgs f, int64_t most, cudaStream_t st) {
+  const tq_page_pool& p = f.pool;
   Arrays a{};
   bool launched = false, ok = true;
   auto flush = [&]() {
-    const int64_t items = most * a.pieces > n_drop ? most * a.pieces : n_drop;
+    const int64_t items = most * a.pieces > f.n ? most * a.pieces : f.n;
     const int64_t grid = items < 1 ? 1 : (items > 152 * 8 ? 152 * 8 : items);
-    ok = ok && launch(pages_move_kernel, grid, kThreads, true, st, w, a, p.ref, p.num_pages, launched ? 0 : n_drop);
+    ok = ok && launch(pages_move_kernel, grid, kThreads, true, st, f, a);
     launched = true;
+    f.n = 0;   // the first launch has done the entries
     a.n = a.pieces = 0;
   };
   auto add = [&](const void* base, int64_t bytes) {
@@ -682,7 +711,7 @@ int launch_moves(const tq_kv_view* caches, int n_caches, int Hkv, const tq_page_
       add(c.qjl_rnorm, rows * 2);
     }
   }
-  if (a.n || (!launched && n_drop)) flush();
+  if (a.n || (!launched && f.n)) flush();
   return ok && cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
@@ -714,16 +743,16 @@ extern "C" int tq_pages_fork(const tq_page_pool* pool, const tq_kv_view* caches,
   const tq::ForkArgs a{*pool, parent, child, share_len, new_len, result, n, w};
   const int chunks = (pool->num_pages + tq::kChunk - 1) / tq::kChunk;
   bool ok;
-  if (pool->num_pages <= tq::kSmallPages && (int64_t)n * pool->pages_per_seq <= tq::kSmallEntries) {
+  if (pool->num_pages <= tq::kForkPages && n <= tq::kForkEntries) {
     const int per = (pool->num_pages + tq::kPlanThreads - 1) / tq::kPlanThreads;
     ok = tq::launch(tq::pages_fork_small_kernel, 1, tq::kPlanThreads, false, s, a, per);
   } else {
     ok = tq::launch(tq::pages_count_kernel, chunks, tq::kThreads, false, s, pool->ref, pool->num_pages, w) &&
          tq::launch(tq::pages_fork_plan_kernel, 1, tq::kPlanThreads, true, s, a, chunks) &&
-         (!n || tq::launch(tq::pages_fork_assign_kernel, chunks + n, tq::kThreads, true, s, a, chunks));
+         (!n || tq::launch(tq::pages_fork_assign_kernel, chunks, tq::kThreads, true, s, a));
   }
   if (!ok) return TQ_ERR_CUDA;
-  if (n) return tq::launch_moves(caches, n_caches, Hkv, *pool, w, n, n, s);
+  if (n) return tq::launch_moves(caches, n_caches, Hkv, a, n, s);
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
@@ -752,7 +781,7 @@ extern "C" int tq_pages_compact(const tq_page_pool* pool, const tq_kv_view* cach
   const tq::CompactArgs a{*pool, result, w};
   const int chunks = (pool->num_pages + tq::kChunk - 1) / tq::kChunk;
   bool ok;
-  if (pool->num_pages <= tq::kSmallPages && (int64_t)pool->n_seqs * pool->pages_per_seq <= tq::kSmallEntries) {
+  if (pool->num_pages <= tq::kPackPages && pool->n_seqs <= tq::kPackSeqs) {
     const int per = (pool->num_pages + tq::kPlanThreads - 1) / tq::kPlanThreads;
     ok = tq::launch(tq::pages_compact_small_kernel, 1, tq::kPlanThreads, false, s, a, per);
   } else {
@@ -764,5 +793,8 @@ extern "C" int tq_pages_compact(const tq_page_pool* pool, const tq_kv_view* cach
          tq::launch(tq::pages_compact_rename_kernel, blocks > 1216 ? 1216 : blocks, tq::kThreads, true, s, a);
   }
   if (!ok) return TQ_ERR_CUDA;
-  return tq::launch_moves(caches, n_caches, Hkv, *pool, w, pool->num_pages / 2 + 1, 0, s);
+  tq::ForkArgs none{};
+  none.pool = *pool;
+  none.w = w;
+  return tq::launch_moves(caches, n_caches, Hkv, none, pool->num_pages / 2 + 1, s);
 }
