@@ -52,6 +52,9 @@
 #include "tq_device.cuh"
 
 namespace tq {
+
+int sm_count();
+
 namespace {
 
 constexpr int kChunk = 1024;          // pages per block of count and assign
@@ -687,7 +690,7 @@ int launch_moves(const tq_kv_view* caches, int n_caches, int Hkv, ForkArgs f, in
   bool launched = false, ok = true;
   auto flush = [&]() {
     const int64_t items = most * a.pieces > f.n ? most * a.pieces : f.n;
-    const int64_t grid = items < 1 ? 1 : (items > 152 * 8 ? 152 * 8 : items);
+    const int64_t most_blocks = 8 * sm_count(), grid = items < 1 ? 1 : (items > most_blocks ? most_blocks : items);
     ok = ok && launch(pages_move_kernel, grid, kThreads, true, st, f, a);
     launched = true;
     f.n = 0;   // the first launch has done the entries
@@ -786,11 +789,12 @@ extern "C" int tq_pages_compact(const tq_page_pool* pool, const tq_kv_view* cach
     ok = tq::launch(tq::pages_compact_small_kernel, 1, tq::kPlanThreads, false, s, a, per);
   } else {
     const int64_t work = pool->num_pages > (int64_t)pool->n_seqs * 32 ? pool->num_pages : (int64_t)pool->n_seqs * 32;
-    const int64_t blocks = (work + tq::kThreads - 1) / tq::kThreads;
+    const int64_t all = (work + tq::kThreads - 1) / tq::kThreads, most = 8 * tq::sm_count();
+    const int64_t blocks = all > most ? most : all;
     ok = tq::launch(tq::pages_count_kernel, chunks, tq::kThreads, false, s, pool->ref, pool->num_pages, w) &&
          tq::launch(tq::pages_compact_plan_kernel, 1, tq::kPlanThreads, true, s, a, chunks) &&
          tq::launch(tq::pages_compact_list_kernel, chunks, tq::kThreads, true, s, a) &&
-         tq::launch(tq::pages_compact_rename_kernel, blocks > 1216 ? 1216 : blocks, tq::kThreads, true, s, a);
+         tq::launch(tq::pages_compact_rename_kernel, blocks, tq::kThreads, true, s, a);
   }
   if (!ok) return TQ_ERR_CUDA;
   tq::ForkArgs none{};

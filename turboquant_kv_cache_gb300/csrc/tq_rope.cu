@@ -25,6 +25,9 @@
 #include "tq_device.cuh"
 
 namespace tq {
+
+int sm_count();
+
 namespace {
 
 constexpr int kThreads = 64;
@@ -205,7 +208,7 @@ void launch_rows(const RopeArgs& a, int64_t tokens, cudaStream_t st) {
   // 1 row 151 us, 2 rows 136, 3 rows 141, 4 rows 132.
   const int64_t blocks = (tokens + HPB - 1) / HPB;
   int R = 1;
-  if (blocks * H > 152 * 16) {
+  if (blocks * H > 16 * sm_count()) {
     int best = 1 << 30;
     for (int r = 4; r >= 2; --r) {
       const int idle = (H + r - 1) / r * r - H;
