@@ -8,8 +8,8 @@ half a step each: 2^-11 of the value.  Then
     (Cauchy-Schwarz; a rotation keeps norms), and its weight by the factor
     exp of that;
   * p, which is also what the sum l is made of, changes its weight by 2^-11
-    more, and by 2^-32 of the reference's weight below fp16's normal range
-    (the reference's p is 2^7, fp16's smallest step 2^-24);
+    more, and by 2^-30 of the reference's weight below fp16's normal range
+    (the reference's p is 2^5, fp16's smallest step 2^-24);
   * a weight's factor e^x moves the output by w (e^x - 1) (v - out);
   * v^ moves an output component by 2^-11 sum w |v| (norms: the rotation back
     mixes a block's components);
@@ -38,7 +38,7 @@ def _attend(q, k, v, scale):
     grow = w * torch.expm1(x)
     tol = grow @ v.abs() + grow.sum(-1, keepdim=True) * out.abs()          # sum of grow |v - out|, from above
     tol = tol * x.amax(-1, keepdim=True).exp()                             # the weights' sum, which divides
-    small = k.shape[1] * 2.0 ** -32                                        # all that p's smallest steps leave out
+    small = k.shape[1] * 2.0 ** -30                                        # all that p's smallest steps leave out
     tol += small * (v.abs().amax(1, keepdim=True) + out.abs())
     tol += HALF * (w * v.norm(dim=-1)[:, None]).sum(-1, keepdim=True) + HALF * out.abs() + 2.0 ** -25
     return out, 1.01 * tol
@@ -80,10 +80,10 @@ def test_many_weights_far_below_the_largest(tqlib, d, kbits, vbits, block):
     ref = rest / (1 + rest) * v[0]
     # the first score, 25.6 in powers of two: q^ and k^ move it by 2 * 2^-11 of
     # itself (all products are squares), 0.025, so the weights by 1.8 %; p =
-    # 2^-18.6 has steps of 2^-24, half of one is 2^-6.4 = 1.2 % of it; v^,
+    # 2^-20.6 has steps of 2^-24, half of one is 2^-4.4 = 4.7 % of it; v^,
     # the output and the products of the two errors: below 0.5 %
     err = (out[0, 0].double() - ref).abs()
-    assert (err <= 0.035 * ref.abs() + 0.002 * rest * v[0].norm()).all(), (err.max().item(), ref.abs().max().item())
+    assert (err <= 0.07 * ref.abs() + 0.002 * rest * v[0].norm()).all(), (err.max().item(), ref.abs().max().item())
 
 
 def _levels(T, slice_tokens):

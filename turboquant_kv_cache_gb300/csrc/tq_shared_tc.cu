@@ -24,12 +24,14 @@
 // rows; the sums l over tokens come from the same rounded p that multiplies V:
 // two warps read P back as mma.sync operands and multiply it by a matrix of
 // ones, in fp32.
-// The reference of a row only moves when a score passes it by more than 2^8
+// The reference of a row only moves when a score passes it by more than 2^10
 // (it starts as the largest of 32 scores): the common step needs no maximum
 // over tokens, only one barrier vote; the rare one takes the maxima and scales
-// O and l.  What is kept as m lies 7 below the reference, so p is 2^7 there and
-// at most 2^15: the upper half of fp16's range for what is larger, the rest
-// for what is smaller.
+// O and l.  What is kept as m lies 5 below the reference, so p is 2^5 there and
+// at most 2^15: a part of fp16's range for what is larger, the rest for what is
+// smaller.  (7 below and moves past 2^8: where scores have twice the unit
+// deviation, 128 rows over 32768 tokens, references then move often enough to
+// cost 55.5 us against 53.4; 3 and 2^12 53.3.)
 //
 // Roundings.  Scores, m, l and O are fp32.  Q^, K^ and V^ are rounded once to
 // fp16 (half a step, 2^-11 relative to each value) and p once (2^-11): the
@@ -38,7 +40,7 @@
 // outputs are 6e-4 to 9e-4 (relative, as norms) from attention in 64 bits, of
 // which 2.1e-4 are the output's own rounding; a score of s (in e-folds) is off
 // by up to 2^-10 sum |q k|, so weights of large scores by as much.  p is kept to
-// 2^-32 of the reference's and dropped below: at most that per token, 2^-15 of a
+// 2^-30 of the reference's and dropped below: at most that per token, 2^-13 of a
 // softmax over a slice of 131072 tokens.
 //
 // Warps: 0-7 softmax (warps 0-3 rows [0, NR/2), 4-7 the rest), which also
@@ -98,7 +100,7 @@ constexpr int kThreadsSh = kDec0 + kDecThreads;       // 896
 constexpr int kLaunchRegs = 72;     // registers a thread at launch (896 threads of 65536)
 // log2 of p at a row's reference, and the log2 units a score may pass it by: p
 // stays below 2^15, inside fp16, and sums of p * v inside fp32
-constexpr float kHeadSh = 7.0f, kLazySh = 8.0f;
+constexpr float kHeadSh = 5.0f, kLazySh = 10.0f;
 
 // first failure status of a launch since the last read (0 = none)
 __device__ int g_shared_status;
