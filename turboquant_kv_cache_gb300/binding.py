@@ -2,7 +2,9 @@
 
 Argument marshalling only: every function here checks shapes, takes raw
 pointers from torch tensors, calls the C entry point of the same name on the
-caller's current CUDA stream and raises TQError on a non-zero status.  All
+caller's current CUDA stream, or on `stream` (a torch.cuda.Stream), and raises
+TQError on a non-zero status.  What a call makes for itself or returns anew is
+made on that stream and is its memory, as if it were the current one.  All
 computation happens in the library's CUDA kernels; there is no fallback.
 """
 from __future__ import annotations

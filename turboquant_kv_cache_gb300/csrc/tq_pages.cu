@@ -45,8 +45,8 @@
 // moved byte once.  Measured in graph replays, with the call that frees pages
 // and a reset of the books before each: 3 freed, 4 forked and 4 grown over 512
 // pages of 28 KB 11.1 us; 60, 150 and 40 over 2000 pages in 64 arrays (134 MB
-// moved, 20 us at a copy's rate) 31.1 us; 512 pages compacted 9.5 us, 2500 in
-// 64 arrays (557 MB, 83 us) 107.5 us.
+// moved, 20 us at a copy's rate) 31.6 us; 512 pages compacted 9.1 us, 2500 in
+// 64 arrays (557 MB, 83 us) 107.3 us.
 #include <cuda_runtime.h>
 
 #include "tq_device.cuh"

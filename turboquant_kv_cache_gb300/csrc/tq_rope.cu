@@ -18,8 +18,8 @@
 //
 // Bound: memory once there are many tokens, since a row is read and written
 // once and nothing else is (822 MB for 32768 tokens of 48 heads, head_dim 128,
-// fp16: 132 us, 6.2 TB/s, 93 % of a copy's rate); for a few tokens the launch
-// (8 tokens 2.1 us in a graph, 15 tokens of fp32 rows at head_dim 256 2.2).
+// fp16: 130.5 us, 6.3 TB/s, 94 % of a copy's rate); for a few tokens the launch
+// (8 tokens 2.4 us in a graph, 15 tokens of fp32 rows at head_dim 256 2.5).
 #include <cuda_runtime.h>
 
 #include "tq_device.cuh"

@@ -62,9 +62,9 @@
 //
 // Measured (GB300; graph replays of the call, the combine in it).  128 rows
 // over 32768 shared tokens and 512 own ones of 32 sequences, 8 KV heads,
-// head_dim 128, 3 bits: 52.1 us for 40.9 MB of cache and 17.2 GFLOP (floors
+// head_dim 128, 3 bits: 53.3 us for 40.9 MB of cache and 17.2 GFLOP (floors
 // 6.1 and 8.8 us).  16 rows in 32 over 131072 shared tokens, 4 KV heads,
-// head_dim 256, 4 and 3 bits: 77.1 us for 136 MB (floor 20.3 us).  Neither the
+// head_dim 256, 4 and 3 bits: 78.9 us for 136 MB (floor 20.3 us).  Neither the
 // memory nor the tensor cores bound it but the decode and the softmax on the
 // way between them: at 128 rows a tile takes 3400 cycles, of which 2400 the
 // softmax's exponentials, with issue slots 55 % and the shared-memory pipe
