@@ -220,3 +220,17 @@ def test_calls_see_the_cache_as_it_is(tqlib):
     for t in (table.view(2, 8), table.view(4, 4), table.view(2, 8)[:, :3], table[8:].view(1, 8), None):
         c.page_table = t
         same()
+
+
+def test_caches_are_copied_and_pickled(tqlib):
+    """Also after a call has taken their views."""
+    import copy
+    import pickle
+
+    import torch
+    L = tb.make_layout(128, 32, 3)
+    c = tb.PackedKV.of(L, torch.ones(4, 2, 32, 48, dtype=torch.uint8), torch.ones(4, 2, 32, 4, dtype=torch.float16))
+    c._view_ref()
+    for d in (copy.copy(c), copy.deepcopy(c), pickle.loads(pickle.dumps(c))):
+        assert torch.equal(d.codes, c.codes) and bytes(d.layout) == bytes(c.layout)
+        assert d._view_ref()._obj.codes == d.codes.data_ptr()

@@ -339,6 +339,9 @@ class PackedKV:
 
     _kept = (None, None)
 
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k != "_kept"}   # addresses are not copied or pickled
+
     def _view_ref(self):
         """view() by reference, for a C call of this module: nobody changes it,
         so it is kept while all that it is made of is what it was."""
