@@ -234,3 +234,20 @@ def test_caches_are_copied_and_pickled(tqlib):
     for d in (copy.copy(c), copy.deepcopy(c), pickle.loads(pickle.dumps(c))):
         assert torch.equal(d.codes, c.codes) and bytes(d.layout) == bytes(c.layout)
         assert d._view_ref()._obj.codes == d.codes.data_ptr()
+
+
+def test_page_table_rows_are_contiguous(tqlib):
+    """Columns that lie apart are no table that the C side can read."""
+    import torch
+    L = tb.make_layout(128, 32, 3)
+    table = torch.zeros(4, 8, dtype=torch.int32)
+    c = tb.PackedKV.of(L, torch.zeros(16, 2, 32, 48, dtype=torch.uint8), torch.zeros(16, 2, 32, 4, dtype=torch.float16),
+                       page_table=table[:, :4])
+    assert c.view().pages_per_seq == 8
+    for t in (table[:, ::2], table.t()):
+        c.page_table = t
+        for call in (c.view, c._view_ref, c._table_stride):
+            with pytest.raises(ValueError):
+                call()
+    c.page_table = table[:, 3:4]
+    assert (c.view().pages_per_seq, c.capacity) == (8, 32)

@@ -358,7 +358,11 @@ class PackedKV:
     def _table_stride(self):
         """Entries between two rows of the table (its width unless it is part of a wider one)."""
         pt = self.page_table
-        return 0 if pt is None else pt.stride(0) if pt.shape[0] > 1 else pt.shape[1]
+        if pt is None:
+            return 0
+        if pt.shape[1] > 1 and pt.stride(1) != 1:
+            raise ValueError("a page table's rows must be contiguous")
+        return pt.stride(0) if pt.shape[0] > 1 else pt.shape[1]
 
     def nbytes(self):
         n = self.codes.numel() + 2 * self.scales.numel()
