@@ -601,33 +601,13 @@ __global__ void __launch_bounds__(192 + 32 * (NK + NV), 1) prefill_ws_kernel(con
   };
 
   if (warp >= 4) {
-    // whole warpgroups (4 warps) execute one instruction each
+    // whole warpgroups (4 warps) execute one instruction each.  The order of
+    // the roles below moves the compiler's choices: 512 queries over 65536
+    // tokens at head_dim 64 and 128, and over 131072 at 256, take 0.516, 0.544
+    // and 1.273 ms; with both decoders first 0.581, 0.621 and 1.299, with O, V,
+    // S, K 0.552, 0.581 and 1.264 (of 30 orders at 256 1.264 to 1.400)
     if (RB) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kDecRegs));
-    if (warp >= 6) {
-      // ================= decoders: NK warps fill the K ring, NV warps the V
-      // ring.  Each thread loads its items' packed words for tile t+1 into
-      // registers before decoding tile t, so the global latency hides behind
-      // the decode.
-      // the contiguous and the paged cache get their own copy of the role, so
-      // the contiguous one keeps its single base address
-      const ContigRec crec{(int64_t)bh * a.S_cap};
-      const PagedRec prec{a.pages, a.S_cap, a.Hkv, b, kvh};
-      if (warp < 6 + NK) {
-        if (a.pages.table)
-          decoder_role<D, kNK, NB, 1>(PK, s_tabs[0], a.kc, a.ks, tid - 192, kfull, kfree, aK(0), kTileBytes, prec, t_lo,
-                                      n_tiles, rank, n_valid_of, wait_cl, s_abort);
-        else
-          decoder_role<D, kNK, NB, 1>(PK, s_tabs[0], a.kc, a.ks, tid - 192, kfull, kfree, aK(0), kTileBytes, crec, t_lo,
-                                      n_tiles, rank, n_valid_of, wait_cl, s_abort);
-      } else {
-        if (a.pages.table)
-          decoder_role<D, kNV, NB, 2>(PV, s_tabs[1], a.vc, a.vs, tid - 192 - kNK, vfull, vfree, aV(0), kTileBytes,
-                                      prec, t_lo, n_tiles, rank, n_valid_of, wait_cl, s_abort);
-        else
-          decoder_role<D, kNV, NB, 2>(PV, s_tabs[1], a.vc, a.vs, tid - 192 - kNK, vfull, vfree, aV(0), kTileBytes,
-                                      crec, t_lo, n_tiles, rank, n_valid_of, wait_cl, s_abort);
-      }
-    } else if (warp == 4) {
+    if (warp == 4) {
       // ================= S issue: S(t) = Q^ (TMEM) K^(t)^T once K(t) is decoded
       // and S(t-1) has been read.  The whole warp walks the schedule, one
       // elected lane issues each MMA and commit.  S and O have a warp each, so
@@ -649,7 +629,30 @@ __global__ void __launch_bounds__(192 + 32 * (NK + NV), 1) prefill_ws_kernel(con
         commit_elect(s_full);
         commit_elect_pair(kfree + 8 * kb);
       }
-    } else if (warp == 5) {
+    } else if (warp >= 6 && warp < 6 + NK) {
+      // ================= decoders: NK warps fill the K ring, NV warps the V
+      // ring.  Each thread loads its items' packed words for tile t+1 into
+      // registers before decoding tile t, so the global latency hides behind
+      // the decode.  The contiguous and the paged cache get their own copy of
+      // the role, so the contiguous one keeps its single base address
+      const ContigRec crec{(int64_t)bh * a.S_cap};
+      const PagedRec prec{a.pages, a.S_cap, a.Hkv, b, kvh};
+      if (a.pages.table)
+        decoder_role<D, kNK, NB, 1>(PK, s_tabs[0], a.kc, a.ks, tid - 192, kfull, kfree, aK(0), kTileBytes, prec, t_lo,
+                                    n_tiles, rank, n_valid_of, wait_cl, s_abort);
+      else
+        decoder_role<D, kNK, NB, 1>(PK, s_tabs[0], a.kc, a.ks, tid - 192, kfull, kfree, aK(0), kTileBytes, crec, t_lo,
+                                    n_tiles, rank, n_valid_of, wait_cl, s_abort);
+    } else if (warp >= 6 + NK) {
+      const ContigRec crec{(int64_t)bh * a.S_cap};
+      const PagedRec prec{a.pages, a.S_cap, a.Hkv, b, kvh};
+      if (a.pages.table)
+        decoder_role<D, kNV, NB, 2>(PV, s_tabs[1], a.vc, a.vs, tid - 192 - kNK, vfull, vfree, aV(0), kTileBytes,
+                                    prec, t_lo, n_tiles, rank, n_valid_of, wait_cl, s_abort);
+      else
+        decoder_role<D, kNV, NB, 2>(PV, s_tabs[1], a.vc, a.vs, tid - 192 - kNK, vfull, vfree, aV(0), kTileBytes,
+                                    crec, t_lo, n_tiles, rank, n_valid_of, wait_cl, s_abort);
+    } else {
       // ================= O issue: O += P(t) (TMEM) V^(t) once P(t) is written
       // and V(t) decoded
       const uint32_t idesc_o = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kRowsTc >> 4) << 24);
