@@ -173,6 +173,29 @@ int tq_append_kv(const tq_layout* layout, const void* x, tq_dtype x_dtype, int B
                  int page_size, int pages_per_seq, const float* S, uint8_t* codes, uint16_t* scales,
                  uint8_t* qjl_bits, uint16_t* qjl_rnorm, void* stream);
 
+/* Quantise the rows of a ragged batch straight into their slots (device):
+ * requests of different lengths packed row behind row, as tq_batch_slots
+ * lays them out.
+ *   x            device, n_rows*H vectors ordered (row, head), vector i at
+ *                x + i*x_row_stride elements (as tq_quantize_kv)
+ *   slot         device int64 [n_rows]: head h of row r goes to record
+ *                (page*H + h)*slots_per_page + slot[r] % slots_per_page with
+ *                page = slot[r] / slots_per_page; rows whose slot is outside
+ *                [0, n_slots) (-1: none) are not written.  No two rows of a
+ *                call name the same slot
+ *   slots_per_page, n_slots
+ *                paged: page_size and num_pages*page_size.  Contiguous
+ *                [B, H, S_cap]: S_cap and B*S_cap (slot b*S_cap + t is slot t
+ *                of sequence b).  n_slots is a multiple of slots_per_page
+ *   codes, scales, qjl_bits, qjl_rnorm, S
+ *                as tq_append_kv
+ * The records written are identical to tq_quantize_kv of the same rows;
+ * n_rows*H == 0 is a no-op. */
+int tq_append_kv_slots(const tq_layout* layout, const void* x, tq_dtype x_dtype, int n_rows, int H,
+                       int64_t x_row_stride, const int64_t* slot, int64_t slots_per_page, int64_t n_slots,
+                       const float* S, uint8_t* codes, uint16_t* scales, uint8_t* qjl_bits, uint16_t* qjl_rnorm,
+                       void* stream);
+
 /* Decode n_vec packed vectors (device) into out [n_vec, d] (fp16 or fp32):
  * x~ = scale * D H (c + [QJL] rho sqrt(pi/2)/m H D S^T (2s - 1)), i.e.
  * unpack -> centroid lookup -> inverse rotation -> x scale
@@ -504,6 +527,105 @@ int tq_pages_compact(const tq_page_pool* pool, const tq_kv_view* caches, int n_c
 
 /* Workspace bytes of the two calls above (host). */
 int tq_pages_workspace_bytes(int n_seqs, int num_pages, int n, size_t* bytes);
+
+/* Where the rows of a ragged batch go.  Sequence b (of B) has kv_len[b] tokens
+ * in the cache (NULL: none) and new_len[b] new ones; their rows follow each
+ * other, sequence behind sequence, in a buffer of n_rows rows.
+ *   new_len, kv_len  device int32 [B]
+ *   S_cap, page_table, page_size, pages_per_seq
+ *                as tq_append_kv: a contiguous cache [B, H, S_cap] (NULL, 0, 0)
+ *                or pages; S_cap < 2^31 - 64
+ *   row_start    device int32 [B + 1]: first row of each sequence, then all
+ *   seq, pos, slot, row_len
+ *                device [n_rows], int32 but for slot (int64): row r's sequence,
+ *                position kv_len + j, slot page*page_size + offset (contiguous:
+ *                b*S_cap + position), which tq_append_kv_slots takes, and
+ *                position + 1, the tokens that the row attends to.  Rows behind
+ *                the last sequence have -1, -1, -1 and 0.  seq and row_len may
+ *                be NULL.  A negative page gives slot -1
+ *   row_table, row_pages
+ *                device int32 [n_rows, row_pages] or NULL: the first row_pages
+ *                entries of the sequence's table row for each row (0 behind the
+ *                last sequence).  With row_len it makes every row a sequence of
+ *                its own, as tq_decode_attn takes it for several new tokens a
+ *                sequence
+ *   result       device int32 [4] or NULL: {status, rows, 0, 0}.  status 0:
+ *                done.  > 0: so many rows more than n_rows.  -1: a negative
+ *                length, or kv_len + new_len past S_cap.  Unless it is 0 there
+ *                are no rows: row_start is 0, every row as behind the last
+ * Outputs do not overlap inputs.  seq, pos, slot and row_len are 16-byte
+ * aligned, the other arrays to their elements, else TQ_ERR_ALIGN. */
+int tq_batch_slots(const int32_t* new_len, const int32_t* kv_len, int B, int64_t S_cap, const int32_t* page_table,
+                   int page_size, int pages_per_seq, int n_rows, int32_t* row_start, int32_t* seq, int32_t* pos,
+                   int64_t* slot, int32_t* row_len, int32_t* row_table, int row_pages, int32_t* result, void* stream);
+
+/* ---- Beam search over the cache ------------------------------------------
+ * One step: of W beams' continuations by each of V tokens, the n_out best of
+ * each of B requests.  Candidate (w, v) has the score
+ *   scores[w] + logits[w][v] - log sum_u exp(logits[w][u]);
+ * a finished beam has one candidate, eos at its own score, and -inf for the
+ * rest.  Scores are compared in 64 bits; equal ones go to the lower w*V + v,
+ * -inf among them (those of one beam to the higher logit first).
+ *   logits       device, row b*W + w at logits + (b*W + w)*row_stride elements
+ *                (fp16 or fp32, aligned to an element); not read for a finished
+ *                beam or one whose score is -inf.  NaN counts as -inf and +inf
+ *                as the largest finite number, here and in scores
+ *   scores       device fp32 [B, W], NULL: 0
+ *   done         device uint8 [B, W] or NULL: beams that are finished (needs eos)
+ *   eos          the token that finishes a beam, or -1
+ *   n_out        candidates kept, at most W*V; at most 64, as W
+ *   keep_place   0: candidates by descending score.  1 (n_out == W): the best
+ *                child of each beam that has one is in the beam's own place, the
+ *                others, by score, in the places left, so that the state of a
+ *                beam that goes on need not move
+ *   out_scores, out_parent, out_token, out_done
+ *                device [B, n_out] fp32, int32 (row b*W + w), int32, uint8 (may be
+ *                NULL).  out_scores may be scores and out_done done where n_out
+ *                is W
+ *   workspace    tq_beam_workspace_bytes(...) bytes, 16-byte aligned */
+int tq_beam_select(const void* logits, tq_dtype dtype, int B, int W, int64_t V, int64_t row_stride,
+                   const float* scores, const uint8_t* done, int64_t eos, int n_out, int keep_place,
+                   float* out_scores, int32_t* out_parent, int32_t* out_token, uint8_t* out_done, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of tq_beam_select on the current device (host). */
+int tq_beam_workspace_bytes(int B, int W, int64_t V, int n_out, size_t* bytes);
+
+/* An array of per-sequence state, [n_seqs, heads, cap, bytes] (device): packed
+ * codes, norms, QJL bits, fp16 windows, token histories. */
+typedef struct {
+  void* data;
+  const int32_t* len;   /* device int32 [n_seqs]: slots in use, NULL: cap */
+  int64_t cap;          /* slots of a (sequence, head) */
+  int32_t heads;
+  int32_t bytes;        /* of a slot */
+} tq_state_array;
+
+/* Sequences take over other sequences' states, all at once and in place:
+ * sequence s gets the first len[p] slots of sequence p = parent[s] in every
+ * array, and the slots behind them stay as they are.  Sequences come in groups
+ * of W (at most 64) and p is one of s's group; a parent that is not leaves s
+ * as it is.  The lengths are read only (as an array of states they are one of
+ * their own, of another call behind this one); no two arrays overlap.
+ *   parent   device int32 [n_seqs] */
+int tq_states_reorder(const tq_state_array* states, int n_states, int n_seqs, int W, const int32_t* parent,
+                      void* stream);
+
+/* The same for a paged cache: entry i (of n), sequence seqs[i] (seqs NULL: i),
+ * takes over the pages of entry parent[i]'s sequence.  Table rows and counts
+ * change, no page is copied: tq_pages_fork, growing the sequences, replaces the
+ * pages that several then hold and are written.  A page that nobody holds any
+ * more is free.
+ *   parent   device int32 [n], in [0, n)
+ *   seqs     device int32 [n] or NULL
+ *   result   device int32 [4] or NULL: {status, entries with another parent, 0,
+ *            0}; status -1: a parent or sequence out of range, or a sequence
+ *            named twice; nothing has changed
+ *   workspace  tq_pages_reorder_workspace_bytes(n_seqs, pages_per_seq, n) bytes,
+ *            16-byte aligned */
+int tq_pages_reorder(const tq_page_pool* pool, const int32_t* parent, const int32_t* seqs, int n, int32_t* result,
+                     void* workspace, size_t workspace_bytes, void* stream);
+int tq_pages_reorder_workspace_bytes(int n_seqs, int pages_per_seq, int n, size_t* bytes);
 
 /* ---- Device-side waits and status ----------------------------------------
  * The tensor-core prefill (tq_prefill_attn), the shared-prefix decode

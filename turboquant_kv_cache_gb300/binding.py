@@ -45,6 +45,11 @@ class tq_page_pool(ctypes.Structure):
                 ("page_size", ctypes.c_int32)]
 
 
+class tq_state_array(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("len", ctypes.c_void_p), ("cap", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("bytes", ctypes.c_int32)]
+
+
 def _load():
     global _lib
     if _lib is not None:
@@ -82,6 +87,13 @@ def _load():
         "tq_pages_free": (I, [P, P, P, I, P]),
         "tq_pages_compact": (I, [P, P, I, I, P, P, SZ, P]),
         "tq_pages_workspace_bytes": (I, [I, I, I, P]),
+        "tq_append_kv_slots": (I, [P, P, I, I, I, I64, P, I64, I64, P, P, P, P, P, P]),
+        "tq_batch_slots": (I, [P, P, I, I64, P, I, I, I, P, P, P, P, P, P, I, P, P]),
+        "tq_beam_select": (I, [P, I, I, I, I64, I64, P, P, I64, I, I, P, P, P, P, P, SZ, P]),
+        "tq_beam_workspace_bytes": (I, [I, I, I64, I, P]),
+        "tq_states_reorder": (I, [P, I, I, I, P, P]),
+        "tq_pages_reorder": (I, [P, P, P, I, P, P, SZ, P]),
+        "tq_pages_reorder_workspace_bytes": (I, [I, I, I, P]),
         "tq_set_wait_limit_ns": (I, [ctypes.c_uint64]),
         "tq_device_status": (I, [I, I, P]),
         "tq_strerror": (ctypes.c_char_p, [I]),
@@ -797,6 +809,277 @@ def tq_pages_compact(pool, workspace=None, result=None, stream=None):
                                   workspace.data_ptr(), workspace.nbytes, _stream_on(stream, pool.dev))
     if st:
         _check(st, "tq_pages_compact")
+    return result
+
+
+# ------------------------------------------------------------------ ragged batches
+class BatchSlots:
+    """Where the rows of a ragged batch go (tq_batch_slots): row_start int32
+    [B + 1], and per row seq, pos, row_len int32 and slot int64 [n_rows],
+    row_table int32 [n_rows, row_pages] or None; result int32 [4], {status,
+    rows, 0, 0}."""
+
+    def __init__(self, row_start, seq, pos, slot, row_len, row_table, result):
+        self.row_start, self.seq, self.pos, self.slot, self.row_len = row_start, seq, pos, slot, row_len
+        self.row_table, self.result = row_table, result
+
+    @classmethod
+    def new(cls, B, n_rows, row_pages=0, device="cuda"):
+        e = lambda *shape, dt=torch.int32: torch.empty(shape, dtype=dt, device=device)  # noqa: E731
+        return cls(e(B + 1), e(n_rows), e(n_rows), e(n_rows, dt=torch.int64), e(n_rows),
+                   e(n_rows, row_pages) if row_pages else None, e(4))
+
+
+def tq_batch_slots(new_len, kv_len, n_rows=None, S_cap=None, page_table=None, page_size=0, row_table=False, out=None,
+                   stream=None):
+    """The place of every row of a ragged batch: sequence b has new_len[b] new
+    rows behind its kv_len[b] cached tokens (int32 CUDA tensors [B]; kv_len None:
+    0), packed row behind row in a buffer of n_rows.  The cache is contiguous
+    (S_cap) or paged (page_table int32 [B, pages_per_seq], page_size).  Returns
+    a BatchSlots, `out` where it is given (its n_rows is then the call's);
+    row_table: a table row for every row, for a new result."""
+    dev, B = new_len.get_device(), new_len.numel()
+    if dev < 0:
+        raise ValueError("new_len must be a CUDA tensor")
+    if dev != _current_device():
+        with _on(dev):
+            return tq_batch_slots(new_len, kv_len, n_rows, S_cap, page_table, page_size, row_table, out, stream)
+    _i32(new_len, B, "new_len", dev)
+    _i32(kv_len, B, "kv_len", dev)
+    stride = width = 0
+    if page_table is not None:
+        if (page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.shape[0] < B
+                or page_table.get_device() != dev or (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
+            raise ValueError("page_table must be an int32 tensor [B, pages_per_seq] with contiguous rows on the call's device")
+        width = page_table.shape[1]
+        stride = page_table.stride(0) if page_table.shape[0] > 1 else width
+        if S_cap is None:
+            S_cap = width * page_size
+        if S_cap > width * page_size or stride < width:
+            raise ValueError("S_cap must be at most pages_per_seq * page_size, rows of the table apart")
+    elif S_cap is None:
+        raise ValueError("a contiguous cache needs S_cap")
+    if out is None:
+        if n_rows is None:
+            raise ValueError("n_rows, the rows of the batch's buffer, or out")
+        out = _new(stream, BatchSlots.new, B, n_rows, width if row_table else 0, device=new_len.device)
+    else:
+        n = out.pos.numel()
+        t = out.row_table
+        if n_rows is not None and n_rows != n:
+            raise ValueError("n_rows is out's number of rows where out is given")
+        n_rows = n
+        _i32(out.row_start, B + 1, "out.row_start", dev)
+        for name in ("seq", "pos", "row_len"):
+            _i32(getattr(out, name), n, "out." + name, dev)
+        _i32(out.result, 4, "out.result", dev)
+        if not _is(out.slot, torch.int64, (n,), dev):
+            raise ValueError("out.slot must be a contiguous int64 tensor of n_rows values on the call's CUDA device")
+        if t is not None and not (t.dim() == 2 and _is(t, torch.int32, (n, t.shape[1]), dev) and 0 < t.shape[1] <= width):
+            raise ValueError("out.row_table must be a contiguous int32 tensor [n_rows, at most pages_per_seq]")
+    t = out.row_table
+    st = _load().tq_batch_slots(new_len.data_ptr(), _ptr(kv_len), B, S_cap, _ptr(page_table), page_size, stride, n_rows,
+                                out.row_start.data_ptr(), _ptr(out.seq), out.pos.data_ptr(), out.slot.data_ptr(),
+                                _ptr(out.row_len), _ptr(t), t.shape[1] if t is not None else 0, _ptr(out.result),
+                                _stream_on(stream, dev))
+    if st:
+        _check(st, "tq_batch_slots")
+    return out
+
+
+def tq_append_kv_slots(cache, x, slot, stream=None):
+    """Quantise the rows x [n_rows, H, d] of a ragged batch (fp16/fp32, CUDA,
+    last dim contiguous) into a PackedKV cache, contiguous [B, H, S_cap] or
+    paged: row r goes to slot[r] (int64 CUDA tensor [n_rows], BatchSlots.slot);
+    rows whose slot is outside the cache (-1) are skipped."""
+    layout, dev = cache.layout, x.get_device()
+    d = layout.head_dim
+    if x.dim() != 3 or x.shape[-1] != d or x.stride(-1) != 1 or dev < 0:
+        raise ValueError("x must be a CUDA tensor [n_rows, H, head_dim] with a contiguous last dimension")
+    if dev != _current_device():
+        with _on(dev):
+            return tq_append_kv_slots(cache, x, slot, stream)
+    n, H, _ = x.shape
+    lead = cache.lead_shape
+    if len(lead) != 3 or lead[1] != H or cache.codes.get_device() != dev:
+        raise ValueError("cache must have leading shape [B, H, S_cap] or [num_pages, H, page_size] on x's device")
+    if not _is(slot, torch.int64, (n,), dev):
+        raise ValueError("slot must be a contiguous int64 tensor of n_rows values on x's device")
+    if not x.is_contiguous():
+        x = _new(stream, x.contiguous)
+    st = _load().tq_append_kv_slots(ctypes.byref(layout), x.data_ptr(), _dtype_code(x.dtype), n, H, d, slot.data_ptr(),
+                                    lead[2], lead[0] * lead[2], _ptr(cache.S), cache.codes.data_ptr(),
+                                    cache.scales.data_ptr(), _ptr(cache.qjl), _ptr(cache.rnorm), _stream_on(stream, dev))
+    if st:
+        _check(st, "tq_append_kv_slots")
+    return cache
+
+
+# ------------------------------------------------------------------ beam search
+def tq_beam_workspace_bytes(B, W, V, n_out):
+    nb = ctypes.c_size_t()
+    _check(_load().tq_beam_workspace_bytes(B, W, V, n_out, ctypes.byref(nb)), "tq_beam_workspace_bytes")
+    return nb.value
+
+
+def tq_beam_select(logits, scores=None, n_out=None, done=None, eos=-1, keep_place=False, workspace=None, out=None,
+                   stream=None):
+    """The n_out (default W) best continuations of each request's W beams:
+    logits [B, W, V] (fp16/fp32, CUDA, last dim contiguous), scores fp32
+    [B, W] (None: 0), done uint8 or bool [B, W] (finished beams: only eos, at
+    their own score) or None.  Returns (scores fp32, parent int32, the row
+    b W + w, token int32, done uint8), each [B, n_out], or `out`, a tuple of
+    four such tensors.  keep_place (n_out == W): a beam's best child is in the
+    beam's place."""
+    dev, shape = logits.get_device(), logits.shape
+    if len(shape) != 3 or dev < 0 or logits.stride(2) != 1 and shape[2] != 1:
+        raise ValueError("logits must be a CUDA tensor [B, W, V] with a contiguous last dimension")
+    if dev != _current_device():
+        with _on(dev):
+            return tq_beam_select(logits, scores, n_out, done, eos, keep_place, workspace, out, stream)
+    B, W, V = shape
+    n = W if n_out is None else n_out
+    row = V
+    if not logits.is_contiguous():
+        sb, sw = logits.stride(0), logits.stride(1)
+        if (B > 1 and W > 1 and sb != W * sw) or logits.stride(2) != 1:
+            logits = _new(stream, logits.contiguous)
+        elif W > 1:
+            row = sw
+        elif B > 1:
+            row = sb
+        if row < V:   # rows that overlap, as of an expanded tensor
+            logits, row = _new(stream, logits.contiguous), V
+    if scores is not None and not _is(scores, torch.float32, (B, W), dev):
+        raise ValueError("scores must be a contiguous fp32 tensor [B, W] on logits' device")
+    if done is not None and not ((done.dtype is torch.uint8 or done.dtype is torch.bool) and _is(done, done.dtype, (B, W), dev)):
+        raise ValueError("done must be a contiguous uint8 or bool tensor [B, W] on logits' device")
+    if out is None:
+        out = (_new(stream, torch.empty, (B, n), dtype=torch.float32, device=logits.device),
+               *_new(stream, torch.empty, (2, B, n), dtype=torch.int32, device=logits.device).unbind(),
+               _new(stream, torch.empty, (B, n), dtype=torch.uint8, device=logits.device))
+    elif (len(out) != 4 or not _is(out[0], torch.float32, (B, n), dev) or not _is(out[1], torch.int32, (B, n), dev)
+          or not _is(out[2], torch.int32, (B, n), dev) or not _is(out[3], out[3].dtype, (B, n), dev)
+          or (out[3].dtype is not torch.uint8 and out[3].dtype is not torch.bool)):
+        raise ValueError("out must be four contiguous tensors [B, n_out]: fp32, int32, int32, uint8 or bool")
+    if workspace is None:
+        workspace = _new(stream, torch.empty, tq_beam_workspace_bytes(B, W, V, n), dtype=torch.uint8, device=logits.device)
+    else:
+        _check_workspace(workspace, dev)
+    st = _load().tq_beam_select(logits.data_ptr(), _dtype_code(logits.dtype), B, W, V, row, _ptr(scores), _ptr(done), eos, n,
+                                1 if keep_place else 0, out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(),
+                                out[3].data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream_on(stream, dev))
+    if st:
+        _check(st, "tq_beam_select")
+    return out
+
+
+class StateArrays:
+    """The states of n_seqs sequences that follow their parents: tensors
+    [n_seqs, heads, cap, ...] or [n_seqs, cap] (contiguous, one CUDA device: fp16
+    windows, token histories) and contiguous PackedKV caches (every array of
+    theirs); lens: int32 [n_seqs] slots in use, for all of them (None: cap), or a
+    list with one such tensor or None for each.  The call follows when a cache's
+    array, or an entry of `arrays` or `lens`, is replaced by another; none of them
+    must be given another storage in place (set_, resize_)."""
+
+    def __init__(self, arrays, lens=None):
+        self.arrays = list(arrays)
+        self.lens = list(lens) if isinstance(lens, (list, tuple)) else [lens] * len(self.arrays)
+        self._of = None
+        self.bound()
+
+    def _tensors(self):
+        if len(self.lens) != len(self.arrays):
+            raise ValueError("lens: one for all arrays, or one for each")
+        of = []
+        for a, n in zip(self.arrays, self.lens):
+            if isinstance(a, PackedKV):
+                of += [(t, n) for t in (a.codes, a.scales, a.qjl, a.rnorm) if t is not None]
+            else:
+                of.append((a, n))
+        return of
+
+    def bound(self):
+        """The C structs of the arrays as they are now."""
+        of, was = self._tensors(), self._of
+        if was is not None and len(of) == len(was) and all(a is b and m is n for (a, m), (b, n) in zip(of, was)):
+            return self.structs
+        self._of = None
+        if not of:
+            raise ValueError("no arrays")
+        dev, n_seqs = of[0][0].get_device(), of[0][0].shape[0]
+        if any(isinstance(a, PackedKV) and a.page_table is not None for a in self.arrays):
+            raise ValueError("a paged cache's states are its table rows (tq_pages_reorder)")
+        structs = (tq_state_array * len(of))()
+        spans = []
+        for s, (t, n) in zip(structs, of):
+            if t.dim() < 2 or t.shape[0] != n_seqs or t.get_device() != dev or dev < 0 or not t.is_contiguous():
+                raise ValueError("state arrays must be contiguous tensors [n_seqs, heads, cap, ...] or [n_seqs, cap] on one "
+                                 "CUDA device")
+            if n is not None:
+                _i32(n, n_seqs, "lens", dev)
+            heads, cap = (t.shape[1], t.shape[2]) if t.dim() > 2 else (1, t.shape[1])
+            size = t.element_size()
+            for k in t.shape[3:]:
+                size *= k
+            s.data, s.len, s.cap, s.heads, s.bytes = t.data_ptr(), _ptr(n), cap, heads, size
+            if t.numel():
+                spans.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), 0))
+        for p in {n.data_ptr() for _, n in of if n is not None and n_seqs}:
+            spans.append((p, p + 4 * n_seqs, 1))
+        spans.sort()
+        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+            raise ValueError("state arrays and their lengths must not overlap")
+        self.structs, self.dev, self.n_seqs, self._of = structs, dev, n_seqs, of
+        return structs
+
+
+def tq_states_reorder(states, parent, W, stream=None):
+    """Sequence s of the StateArrays takes over the state of sequence parent[s]
+    (int32 CUDA tensor [n_seqs]), one of its group of W, all at once and in
+    place; a parent outside the group leaves it as it is."""
+    structs, dev = states.bound(), states.dev
+    _i32(parent, states.n_seqs, "parent", dev)
+    if dev != _current_device():
+        with _on(dev):
+            return tq_states_reorder(states, parent, W, stream)
+    st = _load().tq_states_reorder(structs, len(structs), states.n_seqs, W, parent.data_ptr(), _stream_on(stream, dev))
+    if st:
+        _check(st, "tq_states_reorder")
+
+
+def tq_pages_reorder_workspace_bytes(n_seqs, pages_per_seq, n):
+    nb = ctypes.c_size_t()
+    _check(_load().tq_pages_reorder_workspace_bytes(n_seqs, pages_per_seq, n, ctypes.byref(nb)),
+           "tq_pages_reorder_workspace_bytes")
+    return nb.value
+
+
+def tq_pages_reorder(pool, parent, seqs=None, workspace=None, result=None, stream=None):
+    """Entry i, sequence seqs[i] of the pool (None: i), takes over the pages of
+    entry parent[i]'s sequence (int32 CUDA tensors of one length), all at once.
+    Returns the result tensor {status, entries with another parent, 0, 0}; status
+    -1: an entry is not valid, and nothing has changed."""
+    struct, n, dev = pool.books(), parent.numel(), pool.dev
+    _i32(parent, n, "parent", dev)
+    _i32(seqs, n, "seqs", dev)
+    if dev != _current_device():
+        with _on(dev):
+            return tq_pages_reorder(pool, parent, seqs, workspace, result, stream)
+    if workspace is None:
+        workspace = _new(stream, torch.empty, tq_pages_reorder_workspace_bytes(*pool.page_table.shape, n), dtype=torch.uint8,
+                         device=pool.ref.device)
+    else:
+        _check_workspace(workspace, dev)
+    if result is None:
+        result = _new(stream, torch.empty, 4, dtype=torch.int32, device=pool.ref.device)
+    else:
+        _i32(result, 4, "result", dev)
+    st = _load().tq_pages_reorder(struct, parent.data_ptr(), _ptr(seqs), n, result.data_ptr(), workspace.data_ptr(),
+                                  workspace.nbytes, _stream_on(stream, dev))
+    if st:
+        _check(st, "tq_pages_reorder")
     return result
 
 

@@ -442,7 +442,7 @@ int quantize_common(const tq_layout* layout, const void* x, tq_dtype x_dtype, in
 extern "C" int tq_quantize_kv(const tq_layout* layout, const void* x, tq_dtype x_dtype, int64_t n_vec,
                               int64_t x_row_stride, const float* S, uint8_t* codes, uint16_t* scales,
                               uint8_t* qjl_bits, uint16_t* qjl_rnorm, void* stream) {
-  const tq::RowMap identity{nullptr, 1, 1, 0, {nullptr, 0, 0}};
+  const tq::RowMap identity{nullptr, 1, 1, 0, {nullptr, 0, 0}, nullptr, 0};
   return tq::quantize_common(layout, x, x_dtype, n_vec, x_row_stride, S, codes, scales, qjl_bits, qjl_rnorm,
                              identity, stream);
 }
@@ -457,8 +457,22 @@ extern "C" int tq_append_kv(const tq_layout* layout, const void* x, tq_dtype x_d
   if (page_table && (page_size <= 0 || page_size % 32 || pages_per_seq <= 0 ||
                      (int64_t)page_size * pages_per_seq < S_cap))
     return TQ_ERR_ARG;
-  const tq::RowMap map{pos, n_new, H, S_cap, {page_table, page_table ? page_size : 0, page_table ? pages_per_seq : 0}};
+  const tq::RowMap map{pos, n_new, H, S_cap, {page_table, page_table ? page_size : 0, page_table ? pages_per_seq : 0},
+                       nullptr, 0};
   return tq::quantize_common(layout, x, x_dtype, (int64_t)B * H * n_new, x_row_stride, S, codes, scales, qjl_bits,
+                             qjl_rnorm, map, stream);
+}
+
+extern "C" int tq_append_kv_slots(const tq_layout* layout, const void* x, tq_dtype x_dtype, int n_rows, int H,
+                                  int64_t x_row_stride, const int64_t* slot, int64_t slots_per_page, int64_t n_slots,
+                                  const float* S, uint8_t* codes, uint16_t* scales, uint8_t* qjl_bits,
+                                  uint16_t* qjl_rnorm, void* stream) {
+  if (n_rows < 0 || H < 0 || slots_per_page < 0 || n_slots < 0) return TQ_ERR_ARG;
+  if ((int64_t)n_rows * H == 0) return TQ_OK;
+  if (!slot || slots_per_page == 0 || n_slots % slots_per_page) return TQ_ERR_ARG;
+  if ((reinterpret_cast<uintptr_t>(slot) & 7u) != 0) return TQ_ERR_ALIGN;
+  const tq::RowMap map{nullptr, 1, H, slots_per_page, {nullptr, 0, 0}, slot, n_slots};
+  return tq::quantize_common(layout, x, x_dtype, (int64_t)n_rows * H, x_row_stride, S, codes, scales, qjl_bits,
                              qjl_rnorm, map, stream);
 }
 

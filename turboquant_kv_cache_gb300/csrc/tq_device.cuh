@@ -30,9 +30,21 @@ __device__ __forceinline__ int64_t cache_rec(const PageMap& pm, int H, int64_t S
   return (page * H + h) * pm.page_size + t % pm.page_size;
 }
 
+// a / b for 0 <= a, 0 < b; 32-bit numbers, the usual ones, divide much faster.
+__device__ __forceinline__ int64_t div_small(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+  return a / b;
+}
+
 // Record of quantised vector i under a RowMap, or -1 when it is not stored.
 __device__ __forceinline__ int64_t map_row(const RowMap& m, int64_t i) {
-  if (!m.pos) return i;
+  if (!m.pos) {
+    if (!m.slot) return i;
+    const int64_t row = div_small(i, m.H), s = m.slot[row];
+    if (s < 0 || s >= m.n_slots) return -1;
+    const int64_t page = div_small(s, m.S_cap);
+    return (page * m.H + (i - row * m.H)) * m.S_cap + (s - page * m.S_cap);
+  }
   const int64_t bh = i / m.n_new;
   const int64_t slot = (int64_t)m.pos[bh / m.H] + (i - bh * m.n_new);
   if (slot < 0 || slot >= m.S_cap) return -1;

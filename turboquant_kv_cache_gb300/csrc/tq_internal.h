@@ -66,11 +66,16 @@ struct PageMap {
 // and S_cap slots, vector i = (b*H + h)*n_new + j, and it goes to the record
 // of slot pos[b] + j (contiguous or paged, see PageMap); a slot outside
 // [0, S_cap) is not written.
+// slot != NULL (then pos is): vector i is head i % H of row i / H, which goes
+// to slot[row] of a cache of n_slots slots a head in pages of S_cap; a slot
+// outside [0, n_slots) is not written.
 struct RowMap {
   const int32_t* pos;   // device [B], or NULL
   int32_t n_new, H;
   int64_t S_cap;
   PageMap pages;
+  const int64_t* slot;  // device [rows], or NULL
+  int64_t n_slots;
 };
 
 // Checks a view's paging against the call's S_cap; TQ_OK or TQ_ERR_ARG.

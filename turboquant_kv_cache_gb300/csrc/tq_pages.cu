@@ -49,7 +49,7 @@
 // 64 arrays (557 MB, 83 us) 107.3 us.
 #include <cuda_runtime.h>
 
-#include "tq_device.cuh"
+#include "tq_launch.cuh"
 
 namespace tq {
 
@@ -63,6 +63,7 @@ constexpr int kPlanThreads = 1024;
 // what one block takes: pages of the pool (8 or 4 a thread), entries of a fork, sequences of a compacted pool
 constexpr int kForkPages = 8192, kForkEntries = 1024;
 constexpr int kPackPages = 4096, kPackSeqs = 128;
+constexpr int kReorderPieces = 64;    // pieces of rows that one block takes over
 constexpr int kAhead = 8;             // table entries whose loads a thread has in flight
 constexpr int kMaxArrays = 128;       // cache arrays one move launch takes
 constexpr int kPiece = 16384;         // bytes one block copies at a time: four 16-byte loads in flight a thread
@@ -142,12 +143,6 @@ __device__ __forceinline__ int block_scan(int v, int* s_part, int* total) {
   __syncthreads();
   *total = s_part[32];
   return s_part[w] + x - v;
-}
-
-// Kernels of one call in a row: a kernel may start when the one before it
-// has, and waits here until that one has ended and its writes are visible.
-__device__ __forceinline__ void chain_begin() {
-  asm volatile("griddepcontrol.launch_dependents;\ngriddepcontrol.wait;\n" ::: "memory");
 }
 
 __device__ __forceinline__ int free_at(const int32_t* ref, int p, int n) { return p < n && ref[p] == 0 ? 1 : 0; }
@@ -643,22 +638,6 @@ __global__ void __launch_bounds__(kThreads) pages_free_kernel(const tq_page_pool
   }
 }
 
-// Launches a kernel of a call; chained: its set-up overlaps the kernel before
-// it, which it waits for itself (chain_begin).
-template <class... P, class... A>
-bool launch(void (*kern)(P...), int64_t blocks, int threads, bool chained, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = chained ? 1 : 0;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess;
-}
-
 int check_pool(const tq_page_pool* p) {
   if (!p || !p->page_table || !p->n_pages || !p->ref) return TQ_ERR_ARG;
   if (p->n_seqs <= 0 || p->pages_per_seq <= 0 || p->num_pages <= 0) return TQ_ERR_ARG;
@@ -718,8 +697,206 @@ int launch_moves(const tq_kv_view* caches, int n_caches, int Hkv, ForkArgs f, in
   return ok && cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
+// ---- sequences take over other sequences' pages
+struct ReorderArgs {
+  tq_page_pool pool;
+  const int32_t* parent;   // [n]
+  const int32_t* seqs;     // [n], or NULL: entry i is sequence i
+  int32_t* result;
+  int n;
+  int32_t* ok;             // 1: every entry is valid
+  int32_t* mark;           // [n_seqs] 1: an entry's sequence
+  int32_t* was;            // [n] pages that entry i's sequence held
+  int32_t* will;           // [n] pages that it holds then
+  int32_t* rows;           // [n][pages_per_seq] the rows that it takes over
+};
+
+size_t carve_reorder(void* ws, int n_seqs, int pages_per_seq, int n, ReorderArgs* a) {
+  uint8_t* p = static_cast<uint8_t*>(ws);
+  size_t at = 0;
+  auto take = [&](size_t count) {
+    int32_t* r = reinterpret_cast<int32_t*>(p + at);
+    at += (count * 4 + 255) / 256 * 256;
+    return r;
+  };
+  ReorderArgs t{};
+  t.ok = take(1);
+  t.mark = take(n_seqs);
+  t.was = take(n);
+  t.will = take(n);
+  t.rows = take((size_t)n * pages_per_seq);
+  if (a) {
+    a->ok = t.ok;
+    a->mark = t.mark;
+    a->was = t.was;
+    a->will = t.will;
+    a->rows = t.rows;
+  }
+  return at;
+}
+
+__device__ __forceinline__ int reorder_seq(const ReorderArgs& a, int i) { return a.seqs ? a.seqs[i] : i; }
+
+// Checks the entries and notes the counts; by one block of any size.
+__device__ bool check_reorder(const ReorderArgs& a, int* s_part) {
+  const tq_page_pool& p = a.pool;
+  if (a.seqs) {
+    for (int i = threadIdx.x; i < p.n_seqs; i += blockDim.x) a.mark[i] = 0;
+    __syncthreads();
+  }
+  int bad = 0, moved = 0;
+  for (int i = threadIdx.x; i < a.n; i += blockDim.x) {
+    const int s = reorder_seq(a, i), from = a.parent[i];
+    if (s < 0 || s >= p.n_seqs || from < 0 || from >= a.n) {
+      bad = 1;
+      continue;
+    }
+    if (a.seqs && atomicExch(&a.mark[s], 1)) bad = 1;   // the same sequence twice
+    const int t = reorder_seq(a, from);
+    if (t < 0 || t >= p.n_seqs) {
+      bad = 1;
+      continue;
+    }
+    const int was = p.n_pages[s], will = p.n_pages[t];
+    if (was < 0 || was > p.pages_per_seq || will < 0 || will > p.pages_per_seq) bad = 1;
+    a.was[i] = was;
+    a.will[i] = will;
+    moved += from != i;
+  }
+  const bool ok = !__syncthreads_or(bad);
+  int total;
+  block_scan(moved, s_part, &total);
+  if (threadIdx.x == 0) {
+    *a.ok = ok;
+    if (a.result) {
+      a.result[0] = ok ? 0 : -1;
+      a.result[1] = ok ? total : 0;
+      a.result[2] = a.result[3] = 0;
+    }
+  }
+  return ok;
+}
+
+// Entries [c, c + kAhead step) of the row that entry i takes over, to the workspace.
+__device__ __forceinline__ void read_row(const ReorderArgs& a, int i, int c, int step) {
+  const tq_page_pool& p = a.pool;
+  const int from = a.parent[i];
+  if (from < 0 || from >= a.n || from == i) return;
+  const int t = reorder_seq(a, from);
+  if (t < 0 || t >= p.n_seqs) return;
+  const int held = min(p.n_pages[t], p.pages_per_seq);
+  const int32_t* src = p.page_table + (int64_t)t * p.pages_per_seq;
+  int32_t* dst = a.rows + (int64_t)i * p.pages_per_seq;
+  int v[kAhead];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) v[u] = c + u * step < held ? src[c + u * step] : 0;
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (c + u * step < held) dst[c + u * step] = v[u];
+}
+
+// The same entries of the row and the counts of the pages that it loses and
+// gains; a page in the same place of both rows, as of a common prompt, keeps
+// its count without an atomic.
+__device__ __forceinline__ void write_row(const ReorderArgs& a, int i, int c, int step) {
+  const tq_page_pool& p = a.pool;
+  if (a.parent[i] == i) return;
+  const int s = reorder_seq(a, i), was = a.was[i], will = a.will[i];
+  int32_t* row = p.page_table + (int64_t)s * p.pages_per_seq;
+  const int32_t* src = a.rows + (int64_t)i * p.pages_per_seq;
+  if (c == 0) p.n_pages[s] = will;
+  int x[kAhead], y[kAhead];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) {
+    x[u] = c + u * step < was ? row[c + u * step] : -1;
+    y[u] = c + u * step < will ? src[c + u * step] : -1;
+  }
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) {
+    if (x[u] == y[u]) continue;
+    if (x[u] >= 0 && x[u] < p.num_pages) atomicSub(&p.ref[x[u]], 1);
+    if (y[u] >= 0 && y[u] < p.num_pages) atomicAdd(&p.ref[y[u]], 1);
+    if (c + u * step < will) row[c + u * step] = y[u];
+  }
+}
+
+constexpr int kRowPiece = kAhead * 32;   // table entries a warp takes at a time
+
+// A small batch: one block does it all.
+__global__ void __launch_bounds__(kPlanThreads) pages_reorder_small_kernel(const ReorderArgs a) {
+  __shared__ int s_part[33];
+  const int lane = threadIdx.x & 31, warps = kPlanThreads / 32;
+  const int pieces = (a.pool.pages_per_seq + kRowPiece - 1) / kRowPiece;
+  for (int it = threadIdx.x >> 5; it < a.n * pieces; it += warps)
+    read_row(a, it / pieces, it % pieces * kRowPiece + lane, 32);
+  if (!check_reorder(a, s_part)) return;
+  __syncthreads();
+  for (int it = threadIdx.x >> 5; it < a.n * pieces; it += warps)
+    write_row(a, it / pieces, it % pieces * kRowPiece + lane, 32);
+}
+
+// The first block checks while the others read.
+__global__ void __launch_bounds__(kThreads) pages_reorder_read_kernel(const ReorderArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");   // first of its call: nothing to wait for
+  __shared__ int s_part[33];
+  if (blockIdx.x == 0) {
+    check_reorder(a, s_part);
+    return;
+  }
+  const int lane = threadIdx.x & 31;
+  const int64_t pieces = (a.pool.pages_per_seq + kRowPiece - 1) / kRowPiece, items = a.n * pieces;
+  const int64_t warps = (int64_t)(gridDim.x - 1) * (kThreads / 32);
+  for (int64_t it = (int64_t)(blockIdx.x - 1) * (kThreads / 32) + (threadIdx.x >> 5); it < items; it += warps)
+    read_row(a, (int)(it / pieces), (int)(it % pieces) * kRowPiece + lane, 32);
+}
+
+__global__ void __launch_bounds__(kThreads) pages_reorder_write_kernel(const ReorderArgs a) {
+  chain_begin();
+  if (!*a.ok) return;
+  const int lane = threadIdx.x & 31;
+  const int64_t pieces = (a.pool.pages_per_seq + kRowPiece - 1) / kRowPiece, items = a.n * pieces;
+  const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
+  for (int64_t it = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); it < items; it += warps)
+    write_row(a, (int)(it / pieces), (int)(it % pieces) * kRowPiece + lane, 32);
+}
+
 }  // namespace
 }  // namespace tq
+
+extern "C" int tq_pages_reorder_workspace_bytes(int n_seqs, int pages_per_seq, int n, size_t* bytes) {
+  if (n_seqs <= 0 || pages_per_seq <= 0 || n < 0 || !bytes) return TQ_ERR_ARG;
+  *bytes = tq::carve_reorder(nullptr, n_seqs, pages_per_seq, n, nullptr);
+  return TQ_OK;
+}
+
+extern "C" int tq_pages_reorder(const tq_page_pool* pool, const int32_t* parent, const int32_t* seqs, int n,
+                                int32_t* result, void* workspace, size_t workspace_bytes, void* stream) {
+  const int st = tq::check_pool(pool);
+  if (st != TQ_OK) return st;
+  if (n < 0 || n > pool->n_seqs || (n && !parent)) return TQ_ERR_ARG;
+  if (!workspace || workspace_bytes < tq::carve_reorder(nullptr, pool->n_seqs, pool->pages_per_seq, n, nullptr))
+    return TQ_ERR_WORKSPACE;
+  if (!tq::aligned16(workspace)) return TQ_ERR_ALIGN;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  tq::ReorderArgs a{};
+  a.pool = *pool;
+  a.parent = parent;
+  a.seqs = seqs;
+  a.result = result;
+  a.n = n;
+  tq::carve_reorder(workspace, pool->n_seqs, pool->pages_per_seq, n, &a);
+  const int64_t pieces = (pool->pages_per_seq + tq::kRowPiece - 1) / tq::kRowPiece;
+  bool ok;
+  if (n * pieces <= tq::kReorderPieces) {
+    ok = tq::launch(tq::pages_reorder_small_kernel, 1, tq::kPlanThreads, false, s, a);
+  } else {
+    const int64_t all = (n * pieces + tq::kThreads / 32 - 1) / (tq::kThreads / 32), most = 8 * tq::sm_count();
+    const int64_t blocks = all > most ? most : all;
+    ok = tq::launch(tq::pages_reorder_read_kernel, blocks + 1, tq::kThreads, false, s, a) &&
+         tq::launch(tq::pages_reorder_write_kernel, blocks, tq::kThreads, true, s, a);
+  }
+  return ok && cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+}
 
 extern "C" int tq_pages_workspace_bytes(int n_seqs, int num_pages, int n, size_t* bytes) {
   if (n_seqs <= 0 || num_pages <= 0 || n < 0 || !bytes) return TQ_ERR_ARG;
