@@ -534,7 +534,7 @@ int tq_pages_workspace_bytes(int n_seqs, int num_pages, int n, size_t* bytes);
  *   new_len, kv_len  device int32 [B]
  *   S_cap, page_table, page_size, pages_per_seq
  *                as tq_append_kv: a contiguous cache [B, H, S_cap] (NULL, 0, 0)
- *                or pages; S_cap < 2^31 - 64
+ *                or pages; S_cap < 2^31 - 64, B <= 2^20
  *   row_start    device int32 [B + 1]: first row of each sequence, then all
  *   seq, pos, slot, row_len
  *                device [n_rows], int32 but for slot (int64): row r's sequence,
@@ -564,12 +564,13 @@ int tq_batch_slots(const int32_t* new_len, const int32_t* kv_len, int B, int64_t
  * each of B requests.  Candidate (w, v) has the score
  *   scores[w] + logits[w][v] - log sum_u exp(logits[w][u]);
  * a finished beam has one candidate, eos at its own score, and -inf for the
- * rest.  Scores are compared in 64 bits; equal ones go to the lower w*V + v,
+ * rest.  Scores are compared to 48 bits; equal ones go to the lower w*V + v,
  * -inf among them (those of one beam to the higher logit first).
  *   logits       device, row b*W + w at logits + (b*W + w)*row_stride elements
- *                (fp16 or fp32, aligned to an element); not read for a finished
- *                beam or one whose score is -inf.  NaN counts as -inf and +inf
- *                as the largest finite number, here and in scores
+ *                (fp16 or fp32, aligned to an element); the row of a finished
+ *                beam, or of one whose score is -inf, may hold anything.  NaN
+ *                counts as -inf and +inf as the largest finite number, here and
+ *                in scores
  *   scores       device fp32 [B, W], NULL: 0
  *   done         device uint8 [B, W] or NULL: beams that are finished (needs eos)
  *   eos          the token that finishes a beam, or -1

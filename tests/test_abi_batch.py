@@ -19,7 +19,7 @@ def _slots(lib, new=P16, have=P16, B=3, cap=256, table=P16, page=64, pps=4, n=10
     (dict(new=None), ARG), (dict(start=None), ARG), (dict(pos=None), ARG), (dict(slot=None), ARG), (dict(B=0), ARG),
     (dict(n=-1), ARG), (dict(cap=0), ARG), (dict(cap=257), ARG), (dict(page=48), ARG), (dict(page=0), ARG), (dict(pps=0), ARG),
     (dict(rtab=P16, rpages=5), ARG), (dict(rtab=P16, rpages=0), ARG), (dict(rpages=-1), ARG),
-    (dict(table=None, rtab=P16, rpages=1), ARG), (dict(table=None, cap=2**31 - 64), UNSUP),
+    (dict(table=None, rtab=P16, rpages=1), ARG), (dict(table=None, cap=2**31 - 64), UNSUP), (dict(B=(1 << 20) + 1), UNSUP),
     (dict(new=P2), ALIGN), (dict(have=P2), ALIGN), (dict(table=P2), ALIGN), (dict(start=P2), ALIGN), (dict(rtab=P2, rpages=1), ALIGN),
     (dict(result=P2), ALIGN), (dict(seq=P8), ALIGN), (dict(pos=P4), ALIGN), (dict(slot=P8), ALIGN), (dict(rlen=P8), ALIGN),
 ])

@@ -25,7 +25,8 @@ def reference(x, scores, n, done=None, eos=-1):
     m = x.max(-1, keepdims=True)
     m0 = np.where(np.isinf(m), 0.0, m)
     with np.errstate(divide="ignore", invalid="ignore"):
-        lp = x - (m0 + np.log(np.exp(x - m0).sum(-1, keepdims=True)))
+        # the difference first: next to a mask's lowest value the sum of m and the logarithm is m
+        lp = (x - m0) - np.log(np.exp(x - m0).sum(-1, keepdims=True))
     lp = np.where(np.isinf(x), -np.inf, lp)
     if done is not None:
         lp = np.where(done.astype(bool)[..., None], np.where(np.arange(V) == eos, 0.0, -np.inf), lp)

@@ -822,12 +822,42 @@ class BatchSlots:
     def __init__(self, row_start, seq, pos, slot, row_len, row_table, result):
         self.row_start, self.seq, self.pos, self.slot, self.row_len = row_start, seq, pos, slot, row_len
         self.row_table, self.result = row_table, result
+        self._of = None
 
     @classmethod
     def new(cls, B, n_rows, row_pages=0, device="cuda"):
         e = lambda *shape, dt=torch.int32: torch.empty(shape, dtype=dt, device=device)  # noqa: E731
         return cls(e(B + 1), e(n_rows), e(n_rows), e(n_rows, dt=torch.int64), e(n_rows),
                    e(n_rows, row_pages) if row_pages else None, e(4))
+
+    def __getstate__(self):
+        return {**self.__dict__, "_of": None}   # addresses are not copied or pickled
+
+    def bound(self):
+        """Addresses of the arrays as they are now, the number of rows and the
+        pages of a table row; checked anew where an array has been replaced by
+        another (none of them must be given another storage in place)."""
+        was = self._of
+        if (was is not None and self.row_start is was[0] and self.seq is was[1] and self.pos is was[2]
+                and self.slot is was[3] and self.row_len is was[4] and self.row_table is was[5] and self.result is was[6]):
+            return self.args
+        self._of = None
+        t, n, dev = self.row_table, self.pos.numel(), self.pos.get_device()
+        if dev < 0 or self.row_start is None or self.row_start.numel() < 2:
+            raise ValueError("the arrays of BatchSlots lie on a CUDA device, row_start has B + 1 values")
+        _i32(self.row_start, self.row_start.numel(), "row_start", dev)
+        for name in ("seq", "pos", "row_len"):
+            _i32(getattr(self, name), n, name, dev)
+        _i32(self.result, 4, "result", dev)
+        if not _is(self.slot, torch.int64, (n,), dev):
+            raise ValueError("slot must be a contiguous int64 tensor of n_rows values on the call's CUDA device")
+        if t is not None and not (t.dim() == 2 and t.shape[1] > 0 and _is(t, torch.int32, (n, t.shape[1]), dev)):
+            raise ValueError("row_table must be a contiguous int32 tensor [n_rows, pages]")
+        self.dev, self.B, self.n_rows, self.row_pages = dev, self.row_start.numel() - 1, n, t.shape[1] if t is not None else 0
+        self.args = (n, self.row_start.data_ptr(), _ptr(self.seq), self.pos.data_ptr(), self.slot.data_ptr(), _ptr(self.row_len),
+                     _ptr(t), self.row_pages, _ptr(self.result))
+        self._of = self.row_start, self.seq, self.pos, self.slot, self.row_len, t, self.result
+        return self.args
 
 
 def tq_batch_slots(new_len, kv_len, n_rows=None, S_cap=None, page_table=None, page_size=0, row_table=False, out=None,
@@ -845,42 +875,34 @@ def tq_batch_slots(new_len, kv_len, n_rows=None, S_cap=None, page_table=None, pa
         with _on(dev):
             return tq_batch_slots(new_len, kv_len, n_rows, S_cap, page_table, page_size, row_table, out, stream)
     _i32(new_len, B, "new_len", dev)
-    _i32(kv_len, B, "kv_len", dev)
-    stride = width = 0
+    if kv_len is not None:
+        _i32(kv_len, B, "kv_len", dev)
+    stride = width = table = 0
     if page_table is not None:
-        if (page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.shape[0] < B
-                or page_table.get_device() != dev or (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
+        rows, width = page_table.shape if page_table.dim() == 2 else (0, 0)
+        if page_table.dtype is not torch.int32 or rows < B or page_table.get_device() != dev:
             raise ValueError("page_table must be an int32 tensor [B, pages_per_seq] with contiguous rows on the call's device")
-        width = page_table.shape[1]
-        stride = page_table.stride(0) if page_table.shape[0] > 1 else width
+        stride = width
+        if not page_table.is_contiguous():
+            if width > 1 and page_table.stride(1) != 1 or rows > 1 and page_table.stride(0) < width:
+                raise ValueError("page_table must be an int32 tensor [B, pages_per_seq] with contiguous rows on the call's device")
+            stride = page_table.stride(0) if rows > 1 else width
         if S_cap is None:
             S_cap = width * page_size
-        if S_cap > width * page_size or stride < width:
-            raise ValueError("S_cap must be at most pages_per_seq * page_size, rows of the table apart")
+        elif S_cap > width * page_size:
+            raise ValueError("S_cap must be at most pages_per_seq * page_size")
+        table = page_table.data_ptr()
     elif S_cap is None:
         raise ValueError("a contiguous cache needs S_cap")
     if out is None:
         if n_rows is None:
             raise ValueError("n_rows, the rows of the batch's buffer, or out")
         out = _new(stream, BatchSlots.new, B, n_rows, width if row_table else 0, device=new_len.device)
-    else:
-        n = out.pos.numel()
-        t = out.row_table
-        if n_rows is not None and n_rows != n:
-            raise ValueError("n_rows is out's number of rows where out is given")
-        n_rows = n
-        _i32(out.row_start, B + 1, "out.row_start", dev)
-        for name in ("seq", "pos", "row_len"):
-            _i32(getattr(out, name), n, "out." + name, dev)
-        _i32(out.result, 4, "out.result", dev)
-        if not _is(out.slot, torch.int64, (n,), dev):
-            raise ValueError("out.slot must be a contiguous int64 tensor of n_rows values on the call's CUDA device")
-        if t is not None and not (t.dim() == 2 and _is(t, torch.int32, (n, t.shape[1]), dev) and 0 < t.shape[1] <= width):
-            raise ValueError("out.row_table must be a contiguous int32 tensor [n_rows, at most pages_per_seq]")
-    t = out.row_table
-    st = _load().tq_batch_slots(new_len.data_ptr(), _ptr(kv_len), B, S_cap, _ptr(page_table), page_size, stride, n_rows,
-                                out.row_start.data_ptr(), _ptr(out.seq), out.pos.data_ptr(), out.slot.data_ptr(),
-                                _ptr(out.row_len), _ptr(t), t.shape[1] if t is not None else 0, _ptr(out.result),
+    args = out.bound()
+    if out.B != B or out.dev != dev or out.row_pages > width or (n_rows is not None and n_rows != args[0]):
+        raise ValueError("out must be the BatchSlots of B sequences and n_rows rows on the call's device, with at most the "
+                         "table's pages in a row")
+    st = _load().tq_batch_slots(new_len.data_ptr(), _ptr(kv_len), B, S_cap, table, page_size, stride, *args,
                                 _stream_on(stream, dev))
     if st:
         _check(st, "tq_batch_slots")
@@ -955,9 +977,9 @@ def tq_beam_select(logits, scores=None, n_out=None, done=None, eos=-1, keep_plac
     if done is not None and not ((done.dtype is torch.uint8 or done.dtype is torch.bool) and _is(done, done.dtype, (B, W), dev)):
         raise ValueError("done must be a contiguous uint8 or bool tensor [B, W] on logits' device")
     if out is None:
-        out = (_new(stream, torch.empty, (B, n), dtype=torch.float32, device=logits.device),
-               *_new(stream, torch.empty, (2, B, n), dtype=torch.int32, device=logits.device).unbind(),
-               _new(stream, torch.empty, (B, n), dtype=torch.uint8, device=logits.device))
+        size, at, ids = (B, n), logits.device, torch.int32
+        out = (_new(stream, torch.empty, size, dtype=torch.float32, device=at), _new(stream, torch.empty, size, dtype=ids, device=at),
+               _new(stream, torch.empty, size, dtype=ids, device=at), _new(stream, torch.empty, size, dtype=torch.uint8, device=at))
     elif (len(out) != 4 or not _is(out[0], torch.float32, (B, n), dev) or not _is(out[1], torch.int32, (B, n), dev)
           or not _is(out[2], torch.int32, (B, n), dev) or not _is(out[3], out[3].dtype, (B, n), dev)
           or (out[3].dtype is not torch.uint8 and out[3].dtype is not torch.bool)):

@@ -26,6 +26,7 @@ constexpr int kSumThreads = 1024;
 constexpr int kOneLaunch = 4096;   // sequences whose sums every block does for itself
 constexpr int kRowsPerThread = 4;
 constexpr int kAhead = 4;          // table pieces a warp has in flight
+constexpr int kMostSeqs = 1 << 20;
 
 struct SlotArgs {
   const int32_t* new_len;
@@ -33,6 +34,7 @@ struct SlotArgs {
   const int32_t* page_table;   // NULL: contiguous
   int64_t S_cap;
   int32_t page_size, pages_per_seq, B, n_rows;
+  uint32_t page_mul, page_shift;   // p / page_size = p page_mul >> (32 + page_shift) for p < 2^31
   int32_t* row_start;          // [B + 1]
   int32_t* seq;                // [n_rows] or NULL
   int32_t* pos;                // [n_rows]
@@ -43,27 +45,32 @@ struct SlotArgs {
   int32_t* result;             // [4] or NULL
 };
 
-// Sum of v over the block's threads before this one; *total over all.  Every
-// thread calls it; s_part holds blockDim.x / 32 values.
-__device__ __forceinline__ int64_t scan64(int64_t v, int64_t* s_part, int64_t* total) {
+// Sum over the block's threads before this one of their v, modulo 2^32 (which
+// is what counts where all rows fit), and *total, the sum of all in 64 bits.
+// Every thread calls it; s_part holds a value for each warp and direction.
+__device__ __forceinline__ uint32_t scan_rows(int64_t v, uint32_t (*s_part)[3], int64_t* total) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  int64_t x = v;
+  uint32_t x = (uint32_t)v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(kFull, x, o);
+    const uint32_t y = __shfl_up_sync(kFull, x, o);
     if (lane >= o) x += y;
   }
+  // the sum of a thread in pieces of 22 bits
+  const uint32_t lo = __reduce_add_sync(kFull, (uint32_t)v & 0x3fffffu), hi = __reduce_add_sync(kFull, (uint32_t)(v >> 22));
   __syncthreads();   // the parts of an earlier call have been read
-  if (lane == 31) s_part[w] = x;
-  __syncthreads();
-  int64_t before = 0, all = 0;
-  for (int i = 0; i < nw; ++i) {
-    const int64_t p = s_part[i];
-    if (i < w) before += p;
-    all += p;
+  if (lane == 31) {
+    s_part[w][0] = x;
+    s_part[w][1] = lo;
+    s_part[w][2] = hi;
   }
-  *total = all;
-  return before + x - v;
+  __syncthreads();
+  const bool mine = lane < nw;
+  const uint32_t before = __reduce_add_sync(kFull, mine && lane < w ? s_part[lane][0] : 0u);
+  *total = (int64_t)__reduce_add_sync(kFull, mine ? s_part[lane][1] : 0u);
+  // (1024 threads of 2^41 rows at most, see kMostSeqs: the pieces add up in 32 bits)
+  *total += (int64_t)__reduce_add_sync(kFull, mine ? s_part[lane][2] : 0u) << 22;
+  return before + x - (uint32_t)v;
 }
 
 __device__ __forceinline__ bool length_ok(const SlotArgs& a, int len, int have) {
@@ -82,9 +89,9 @@ __device__ __forceinline__ int64_t report(const SlotArgs& a, bool bad, int64_t t
   return ok ? total : 0;
 }
 
-// The sequence of row r: the first whose rows end behind it (end[b] > r).
-__device__ __forceinline__ int find_seq(const int32_t* end, int B, int r) {
-  int lo = 0, hi = B - 1;   // a live row has one
+// The sequence of row r, one of [lo, hi]: the first whose rows end behind it
+// (end[b] > r).
+__device__ __forceinline__ int find_seq(const int32_t* end, int lo, int hi, int r) {
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
     if (end[mid] > r) hi = mid; else lo = mid + 1;
@@ -92,41 +99,57 @@ __device__ __forceinline__ int find_seq(const int32_t* end, int B, int r) {
   return lo;
 }
 
-// Rows and table rows of this block, given the ends of the sequences' rows and
-// their number of rows in all.
-__device__ __forceinline__ void write_rows(const SlotArgs& a, const int32_t* end, int total) {
+// Rows and table rows of this block, given the ends of the sequences' rows,
+// shift(b), what a row of sequence b lacks of its position, and the rows in all.
+template <class Shift>
+__device__ __forceinline__ void write_rows(const SlotArgs& a, const int32_t* end, Shift shift, int total) {
   constexpr int R = kRowsPerThread;
-  const int64_t tid = (int64_t)blockIdx.x * kThreads + threadIdx.x, threads = (int64_t)gridDim.x * kThreads;
-  for (int64_t r0 = tid * R; r0 < a.n_rows; r0 += threads * R) {
-    int seq[R], pos[R], len[R];
+  const uint32_t tid = blockIdx.x * kThreads + threadIdx.x, threads = gridDim.x * kThreads;
+  // (whole warps: they look for their sequences together)
+  for (uint32_t r0 = tid * R; r0 - (threadIdx.x & 31) * R < (uint32_t)a.n_rows; r0 += threads * R) {
+    int seq[R], pos[R], len[R], page[R];
     int64_t slot[R];
-    int b = -1, last = 0, shift = 0;   // b has rows up to last; position = row + shift
+    // the sequences of the warp's rows: lane 0 looks for the first, lane 1 for the last
+    const uint32_t w0 = r0 - (threadIdx.x & 31) * R, w1 = min(w0 + 32 * R, (uint32_t)total);
+    int lo = 0, hi = 0;
+    if (w0 < w1) {
+      const int found = find_seq(end, 0, a.B - 1, (int)((threadIdx.x & 31) == 0 ? w0 : w1 - 1));
+      lo = __shfl_sync(kFull, found, 0);
+      hi = __shfl_sync(kFull, found, 1);
+    }
+    int b = -1, last = 0;   // b has rows up to last
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       const int r = (int)r0 + k;
       seq[k] = pos[k] = -1;
       len[k] = 0;
-      slot[k] = -1;
-      if (r0 + k < total) {
+      if (r0 + k < (uint32_t)total) {
         if (b < 0 || r >= last) {
-          b = find_seq(end, a.B, r);
+          b = find_seq(end, b < 0 ? lo : b + 1, hi, r);
           last = end[b];
-          shift = (a.kv_len ? a.kv_len[b] : 0) - (b ? end[b - 1] : 0);
         }
-        const int p = r + shift;
         seq[k] = b;
-        pos[k] = p;
-        len[k] = p + 1;
-        if (a.page_table) {
-          const int pg = p / a.page_size;
-          const int page = a.page_table[(int64_t)b * a.pages_per_seq + pg];
-          slot[k] = page < 0 ? -1 : (int64_t)page * a.page_size + (p - pg * a.page_size);
-        } else {
-          slot[k] = b * a.S_cap + p;
-        }
+        pos[k] = r + shift(b);
+        len[k] = pos[k] + 1;
       }
     }
-    if (r0 + R <= a.n_rows) {
+    // the rows' pages, loaded together
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      page[k] = -1;
+      slot[k] = -1;
+      if (a.page_table && seq[k] >= 0) {
+        const uint32_t pg = __umulhi((uint32_t)pos[k], a.page_mul) >> a.page_shift;
+        page[k] = a.page_table[(int64_t)seq[k] * a.pages_per_seq + pg];
+        slot[k] = pos[k] - (int)pg * a.page_size;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      if (a.page_table) slot[k] = page[k] < 0 ? -1 : (int64_t)page[k] * a.page_size + slot[k];
+      else if (seq[k] >= 0) slot[k] = seq[k] * a.S_cap + pos[k];
+    }
+    if (r0 + R <= (uint32_t)a.n_rows) {
       if (a.seq) *reinterpret_cast<int4*>(a.seq + r0) = make_int4(seq[0], seq[1], seq[2], seq[3]);
       *reinterpret_cast<int4*>(a.pos + r0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
       if (a.row_len) *reinterpret_cast<int4*>(a.row_len + r0) = make_int4(len[0], len[1], len[2], len[3]);
@@ -135,7 +158,7 @@ __device__ __forceinline__ void write_rows(const SlotArgs& a, const int32_t* end
     } else {
 #pragma unroll
       for (int k = 0; k < R; ++k) {
-        if (r0 + k >= a.n_rows) break;
+        if (r0 + k >= (uint32_t)a.n_rows) break;
         if (a.seq) a.seq[r0 + k] = seq[k];
         a.pos[r0 + k] = pos[k];
         if (a.row_len) a.row_len[r0 + k] = len[k];
@@ -146,26 +169,23 @@ __device__ __forceinline__ void write_rows(const SlotArgs& a, const int32_t* end
   if (!a.row_table) return;
   // table rows in pieces of 32 entries, a warp each, kAhead of them in flight
   const int lane = threadIdx.x & 31;
-  const int pieces = (a.row_pages + 31) / 32;
+  const uint32_t pieces = (a.row_pages + 31) / 32;
   const int64_t items = (int64_t)a.n_rows * pieces, warps = threads / 32;
   for (int64_t it0 = tid / 32; it0 < items; it0 += warps * kAhead) {
     int v[kAhead];
+    int64_t to[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int64_t it = it0 + u * warps;
-      const int64_t r = it / pieces;
+      const int64_t r = div_small(it, pieces);
       const int j = (int)(it - r * pieces) * 32 + lane;
-      v[u] = it < items && r < total && j < a.row_pages
-                 ? a.page_table[(int64_t)find_seq(end, a.B, (int)r) * a.pages_per_seq + j]
-                 : 0;
+      v[u] = 0;
+      to[u] = it < items && j < a.row_pages ? r * a.row_pages + j : -1;
+      if (to[u] >= 0 && r < total) v[u] = a.page_table[(int64_t)find_seq(end, 0, a.B - 1, (int)r) * a.pages_per_seq + j];
     }
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int64_t it = it0 + u * warps;
-      const int64_t r = it / pieces;
-      const int j = (int)(it - r * pieces) * 32 + lane;
-      if (it < items && j < a.row_pages) a.row_table[r * a.row_pages + j] = v[u];
-    }
+    for (int u = 0; u < kAhead; ++u)
+      if (to[u] >= 0) a.row_table[to[u]] = v[u];
   }
 }
 
@@ -180,39 +200,55 @@ __device__ __forceinline__ int64_t run_sum(const SlotArgs& a, int b0, int b1, bo
   return sum;
 }
 
+template <int MOST>   // sequences of a thread
 __global__ void __launch_bounds__(kThreads) batch_slots_kernel(const SlotArgs a) {
-  __shared__ int32_t s_end[kOneLaunch];
-  __shared__ int64_t s_part[kThreads / 32];
+  extern __shared__ int32_t s_end[];   // [B], then what a row of each lacks of its position
+  int32_t* s_shift = s_end + a.B;
+  __shared__ uint32_t s_part[kThreads / 32][3];
   const int per = (a.B + kThreads - 1) / kThreads;
-  const int b0 = min(threadIdx.x * per, a.B), b1 = min(b0 + per, a.B);
+  const int b0 = min(threadIdx.x * per, a.B), n = min(per, a.B - b0);
+  int len[MOST], have[MOST];
+#pragma unroll
+  for (int k = 0; k < MOST; ++k) {   // all of a thread's loads in flight
+    len[k] = k < n ? a.new_len[b0 + k] : 0;
+    have[k] = k < n && a.kv_len ? a.kv_len[b0 + k] : 0;
+  }
   bool bad = false;
-  const int64_t sum = run_sum(a, b0, b1, &bad);
+  int64_t sum = 0;
+#pragma unroll
+  for (int k = 0; k < MOST; ++k) {
+    if (length_ok(a, len[k], have[k])) sum += len[k]; else bad = true;
+  }
   int64_t all;
-  int64_t at = scan64(sum, s_part, &all);
+  uint32_t at = scan_rows(sum, s_part, &all);
   const bool any_bad = __syncthreads_or(bad);
   const bool first = blockIdx.x == 0;
   const int total = (int)report(a, any_bad, all, first && threadIdx.x == 0);
   if (first && threadIdx.x == 0) a.row_start[0] = 0;
-  for (int b = b0; b < b1; ++b) {
-    if (total) at += a.new_len[b];
+#pragma unroll
+  for (int k = 0; k < MOST; ++k) {
+    if (k >= n) break;
+    const int start = (int)at;
+    if (total) at += len[k];
     const int end = total ? (int)at : 0;
-    s_end[b] = end;
-    if (first) a.row_start[b + 1] = end;
+    s_end[b0 + k] = end;
+    s_shift[b0 + k] = have[k] - start;
+    if (first) a.row_start[b0 + k + 1] = end;
   }
   __syncthreads();
-  write_rows(a, s_end, total);
+  write_rows(a, s_end, [&](int b) { return s_shift[b]; }, total);
 }
 
 // Many sequences: the sums by one block.
 __global__ void __launch_bounds__(kSumThreads) batch_sums_kernel(const SlotArgs a) {
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");   // first of its call: nothing to wait for
-  __shared__ int64_t s_part[kSumThreads / 32];
+  __shared__ uint32_t s_part[kSumThreads / 32][3];
   const int64_t per64 = (a.B + kSumThreads - 1) / kSumThreads;
   const int b0 = (int)imin64(threadIdx.x * per64, a.B), b1 = (int)imin64(b0 + per64, a.B);
   bool bad = false;
   const int64_t sum = run_sum(a, b0, b1, &bad);
   int64_t all;
-  int64_t at = scan64(sum, s_part, &all);
+  uint32_t at = scan_rows(sum, s_part, &all);
   const bool any_bad = __syncthreads_or(bad);
   const int64_t total = report(a, any_bad, all, threadIdx.x == 0);
   if (threadIdx.x == 0) a.row_start[0] = 0;
@@ -224,7 +260,7 @@ __global__ void __launch_bounds__(kSumThreads) batch_sums_kernel(const SlotArgs 
 
 __global__ void __launch_bounds__(kThreads) batch_rows_kernel(const SlotArgs a) {
   chain_begin();
-  write_rows(a, a.row_start + 1, a.row_start[a.B]);
+  write_rows(a, a.row_start + 1, [&](int b) { return (a.kv_len ? a.kv_len[b] : 0) - a.row_start[b]; }, a.row_start[a.B]);
 }
 
 }  // namespace
@@ -240,12 +276,21 @@ extern "C" int tq_batch_slots(const int32_t* new_len, const int32_t* kv_len, int
                      (int64_t)page_size * pages_per_seq < S_cap))
     return TQ_ERR_ARG;
   if (row_table && (!page_table || row_pages < 1 || row_pages > pages_per_seq)) return TQ_ERR_ARG;
-  if (S_cap > 0x7fffffff - 64) return TQ_ERR_UNSUPPORTED;   // positions are 32-bit
+  // positions are 32-bit, and a thread adds up 2^10 sequences at most
+  if (S_cap > 0x7fffffff - 64 || B > tq::kMostSeqs) return TQ_ERR_UNSUPPORTED;
   if (!tq::aligned16(seq) || !tq::aligned16(pos) || !tq::aligned16(slot) || !tq::aligned16(row_len)) return TQ_ERR_ALIGN;
   for (const void* p : {(const void*)new_len, (const void*)kv_len, (const void*)page_table, (const void*)row_start,
                         (const void*)row_table, (const void*)result})
     if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0) return TQ_ERR_ALIGN;
-  const tq::SlotArgs a{new_len, kv_len, page_table, S_cap, page_size, pages_per_seq, B, n_rows, row_start, seq, pos,
+  // division by a constant d of p < 2^31: with 2^L >= d, floor(2^(31 + L) / d) + 1 as the factor
+  uint32_t mul = 0, shift = 0;
+  if (page_table) {
+    int L = 5;
+    while (((int64_t)1 << L) < page_size) ++L;
+    mul = (uint32_t)(((uint64_t)1 << (31 + L)) / (uint64_t)page_size + 1);
+    shift = (uint32_t)(L - 1);
+  }
+  const tq::SlotArgs a{new_len, kv_len, page_table, S_cap, page_size, pages_per_seq, B, n_rows, mul, shift, row_start, seq, pos,
                        slot, row_len, row_table, row_table ? row_pages : 0, result};
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   // a thread's four rows, and where table rows are written four pieces a warp
@@ -256,7 +301,9 @@ extern "C" int tq_batch_slots(const int32_t* new_len, const int32_t* kv_len, int
   const int64_t grid = want < 1 ? 1 : want > most ? most : want;
   bool ok;
   if (B <= tq::kOneLaunch) {
-    ok = tq::launch(tq::batch_slots_kernel, grid, tq::kThreads, false, st, a);
+    const auto kern = B <= tq::kThreads ? tq::batch_slots_kernel<1> : tq::batch_slots_kernel<tq::kOneLaunch / tq::kThreads>;
+    kern<<<(unsigned)grid, tq::kThreads, 8 * (size_t)B, st>>>(a);
+    ok = true;
   } else {
     ok = tq::launch(tq::batch_sums_kernel, 1, tq::kSumThreads, false, st, a) &&
          (!n_rows || tq::launch(tq::batch_rows_kernel, grid, tq::kThreads, true, st, a));
