@@ -34,7 +34,7 @@ struct SlotArgs {
   const int32_t* page_table;   // NULL: contiguous
   int64_t S_cap;
   int32_t page_size, pages_per_seq, B, n_rows;
-  uint32_t page_mul, page_shift;   // p / page_size = p page_mul >> (32 + page_shift) for p < 2^31
+  FastDiv by_page;             // division by page_size
   int32_t* row_start;          // [B + 1]
   int32_t* seq;                // [n_rows] or NULL
   int32_t* pos;                // [n_rows]
@@ -139,7 +139,7 @@ __device__ __forceinline__ void write_rows(const SlotArgs& a, const int32_t* end
       page[k] = -1;
       slot[k] = -1;
       if (a.page_table && seq[k] >= 0) {
-        const uint32_t pg = __umulhi((uint32_t)pos[k], a.page_mul) >> a.page_shift;
+        const uint32_t pg = fast_div((uint32_t)pos[k], a.by_page);
         page[k] = a.page_table[(int64_t)seq[k] * a.pages_per_seq + pg];
         slot[k] = pos[k] - (int)pg * a.page_size;
       }
@@ -282,15 +282,8 @@ extern "C" int tq_batch_slots(const int32_t* new_len, const int32_t* kv_len, int
   for (const void* p : {(const void*)new_len, (const void*)kv_len, (const void*)page_table, (const void*)row_start,
                         (const void*)row_table, (const void*)result})
     if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0) return TQ_ERR_ALIGN;
-  // division by a constant d of p < 2^31: with 2^L >= d, floor(2^(31 + L) / d) + 1 as the factor
-  uint32_t mul = 0, shift = 0;
-  if (page_table) {
-    int L = 5;
-    while (((int64_t)1 << L) < page_size) ++L;
-    mul = (uint32_t)(((uint64_t)1 << (31 + L)) / (uint64_t)page_size + 1);
-    shift = (uint32_t)(L - 1);
-  }
-  const tq::SlotArgs a{new_len, kv_len, page_table, S_cap, page_size, pages_per_seq, B, n_rows, mul, shift, row_start, seq, pos,
+  const tq::SlotArgs a{new_len, kv_len, page_table, S_cap, page_size, pages_per_seq, B, n_rows,
+                       tq::make_div(page_table ? page_size : 1), row_start, seq, pos,
                        slot, row_len, row_table, row_table ? row_pages : 0, result};
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   // a thread's four rows, and where table rows are written four pieces a warp

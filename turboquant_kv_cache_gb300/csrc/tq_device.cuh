@@ -36,6 +36,9 @@ __device__ __forceinline__ int64_t div_small(int64_t a, int64_t b) {
   return a / b;
 }
 
+// n / d for n < 2^31, f = make_div(d).
+__device__ __forceinline__ uint32_t fast_div(uint32_t n, FastDiv f) { return __umulhi(n << 1, f.mul) >> f.shift; }
+
 // Record of quantised vector i under a RowMap, or -1 when it is not stored.
 __device__ __forceinline__ int64_t map_row(const RowMap& m, int64_t i) {
   if (!m.pos) {

@@ -78,6 +78,18 @@ struct RowMap {
   int64_t n_slots;
 };
 
+// Division of 0 <= n < 2^31 by a constant d > 0 as a product: with 2^L >= d the
+// factor floor(2^(31 + L) / d) + 1 gives n / d exactly.
+struct FastDiv {
+  uint32_t mul, shift;   // n / d = 2 n mul >> (32 + shift)
+};
+inline FastDiv make_div(int64_t d) {
+  if (d >> 31) return {0, 0};   // larger than every n
+  int L = 0;
+  while (((int64_t)1 << L) < d) ++L;
+  return {(uint32_t)(((uint64_t)1 << (31 + L)) / (uint64_t)d + 1), (uint32_t)L};
+}
+
 // Checks a view's paging against the call's S_cap; TQ_OK or TQ_ERR_ARG.
 inline int check_paging(const tq_kv_view* v, int64_t S_cap) {
   if (!v->page_table) return TQ_OK;

@@ -45,6 +45,8 @@ constexpr int kConsumers = 4 * kGroups;
 constexpr int kThreads = 32 * (kConsumers + 2);   // + a producer warp and an MMA warp
 constexpr int kTileCols = 64;               // input columns per tile: one or two rotation blocks
 constexpr int kStages = 10;                 // input stages (16 KB each)
+constexpr int kRows = 4096;                 // records of rows with slots in shared memory
+constexpr uint32_t kNoRecord = 0xffffffffu;
 constexpr int kAcc = 2 * kGroups;           // TMEM accumulators of 64 columns (two per group, all 512)
 
 // first failure status of a quantise launch since the last read (0 = none)
@@ -57,6 +59,10 @@ struct FastQuantArgs {
   uint32_t* codes;  // [records][words per vector]
   uint16_t* scales;
   RowMap map;       // vector -> record
+  // rows with slots: a CTA puts its rows' records into shared memory (numbers of
+  // 31 bits, at most kRows rows); division by map.H and map.S_cap
+  int staged;
+  FastDiv by_heads, by_page;
   int64_t n_tiles;  // ceil(n_vec / 128) * d / 64
   int64_t per_cta;  // tiles of each CTA (a contiguous range)
   uint64_t report_ns, hard_ns;   // wait limits (see WaitLimits)
@@ -87,6 +93,8 @@ __global__ void __launch_bounds__(kThreads, 1) quantize_tc_kernel(const CodecPar
   uint8_t* s_x = smem;                                           // [kStages][128 rows x 64 columns] swizzled
   uint8_t* s_b = smem + kStages * STAGE;                         // [nb][BLK n x BLK k] core matrices
   uint32_t* s_cell = reinterpret_cast<uint32_t*>(s_b + (size_t)nb * BLK * BLK * 2);   // [C + 1][32]
+
+  uint32_t* s_base = s_cell + (kMaxCells + 1) * 32;                                    // [kRows] where staged
 
   const int64_t t_begin = (int64_t)blockIdx.x * a.per_cta;
   const int64_t t_end = imin64(t_begin + a.per_cta, a.n_tiles);
@@ -139,6 +147,22 @@ __global__ void __launch_bounds__(kThreads, 1) quantize_tc_kernel(const CodecPar
         make_uint4(w[0], w[1], w[2], w[3]);
   }
   for (int idx = tid; idx < (a.ct.n_cells + 1) * 32; idx += kThreads) s_cell[idx] = a.ct.cell[idx >> 5];
+  // Records of this CTA's rows, beside the first tiles' loads.  A load per vector
+  // and tile instead waits for memory under those loads: 24.3 us for 262144
+  // vectors of 128 at 3 bits, 19.4 without slots
+  uint32_t row0 = 0;
+  if (a.staged) {
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");   // the slots may come from the kernel before this one
+    const uint32_t H = a.map.H, S = (uint32_t)a.map.S_cap;
+    row0 = fast_div((uint32_t)(t_begin / tpg * 128), a.by_heads);
+    const int64_t last = imin64(((t_end + tpg - 1) / tpg) * 128, a.n_vec) - 1;
+    const int rows = n > 0 ? (int)(fast_div((uint32_t)last, a.by_heads) - row0 + 1) : 0;
+    for (int k = tid; k < rows; k += kThreads) {
+      const int64_t slot = a.map.slot[row0 + k];
+      const uint32_t t = (uint32_t)slot;
+      s_base[k] = (uint64_t)slot < (uint64_t)a.map.n_slots ? t + S * (fast_div(t, a.by_page) * (H - 1)) : kNoRecord;
+    }
+  }
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(su32(&s_tmem)),
                  "n"(kCols)
@@ -225,6 +249,12 @@ __global__ void __launch_bounds__(kThreads, 1) quantize_tc_kernel(const CodecPar
     const int grp = warp >> 2, wq = warp & 3;   // group, quarter of the TMEM lanes
     int64_t vg = (t_begin + grp) / tpg;
     int jt = (int)(t_begin + grp - vg * tpg);
+    auto record_of = [&](int64_t v) -> int64_t {
+      if (v >= a.n_vec) return -1;
+      if (!a.staged) return map_row(a.map, v);
+      const uint32_t row = fast_div((uint32_t)v, a.by_heads), base = s_base[row - row0];
+      return base == kNoRecord ? -1 : (int64_t)(base + ((uint32_t)v - row * (uint32_t)a.map.H) * (uint32_t)a.map.S_cap);
+    };
     for (int i = grp; i < n; i += kGroups) {
       const int b = i % kAcc;
       if (!__all_sync(kFull, wait(su32(&s_tfull[b]), (uint32_t)(i / kAcc) & 1))) {
@@ -234,10 +264,11 @@ __global__ void __launch_bounds__(kThreads, 1) quantize_tc_kernel(const CodecPar
       fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(32 * wq) << 16) + (uint32_t)(b * kTileCols);
       const int64_t v = vg * 128 + 32 * wq + lane;
-      const int64_t r = v < a.n_vec ? map_row(a.map, v) : -1;
+      const int64_t r = record_of(v);
+      uint32_t W[BPT * WPB];      // the tile's packed words and norms, stored together
+      uint16_t norm[BPT];
 #pragma unroll
       for (int jj = 0; jj < BPT; ++jj) {
-        const int j = jt * BPT + jj;
         const uint32_t tb = taddr + jj * BLK;
         // pass 1: ||y||^2 = BLK ||x||^2 over the block's columns
         float2 s2 = make_float2(0.f, 0.f);
@@ -282,37 +313,40 @@ __global__ void __launch_bounds__(kThreads, 1) quantize_tc_kernel(const CodecPar
           }
         }
         // packed words of the block (32-code groups of four nibble words)
-        uint32_t W[WPB];
 #pragma unroll
         for (int gi = 0; gi < BLK / 32; ++gi) {
           const uint32_t* G = N + 4 * gi;
+          uint32_t* to = W + jj * WPB + BITS * gi;
           if (BITS == 4) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) W[4 * gi + w] = G[w];
+            for (int w = 0; w < 4; ++w) to[w] = G[w];
           } else if (BITS == 3) {
 #pragma unroll
-            for (int w = 0; w < 3; ++w) W[3 * gi + w] = G[w] | (((G[3] >> w) & 0x11111111u) << 3);
+            for (int w = 0; w < 3; ++w) to[w] = G[w] | (((G[3] >> w) & 0x11111111u) << 3);
           } else {
 #pragma unroll
-            for (int w = 0; w < 2; ++w) W[2 * gi + w] = G[w] | (G[w + 2] << 2);
+            for (int w = 0; w < 2; ++w) to[w] = G[w] | (G[w + 2] << 2);
           }
         }
-        if (r >= 0) {
-          uint32_t* dst = a.codes + r * words_per_vec + j * WPB;
-          // widest store the record and block alignment allow
-          if (WPB % 4 == 0 && words_per_vec % 4 == 0) {
+        norm[jj] = f2h(sqrtf(ss * (1.0f / BLK)));
+      }
+      if (r >= 0) {
+        // widest stores that the record allows (a record is words_per_vec words,
+        // a multiple of the tile's)
+        uint32_t* dst = a.codes + r * words_per_vec + jt * (BPT * WPB);
+        if constexpr (BPT * WPB % 4 == 0) {
 #pragma unroll
-            for (int w = 0; w < WPB; w += 4)
-              *reinterpret_cast<uint4*>(dst + w) = make_uint4(W[w], W[w + 1], W[w + 2], W[w + 3]);
-          } else if (WPB % 2 == 0 && words_per_vec % 2 == 0) {
+          for (int w = 0; w < BPT * WPB; w += 4)
+            *reinterpret_cast<uint4*>(dst + w) = make_uint4(W[w], W[w + 1], W[w + 2], W[w + 3]);
+        } else {
+          static_assert(BPT * WPB % 2 == 0, "whole 8-byte words");
 #pragma unroll
-            for (int w = 0; w < WPB; w += 2) *reinterpret_cast<uint2*>(dst + w) = make_uint2(W[w], W[w + 1]);
-          } else {
-#pragma unroll
-            for (int w = 0; w < WPB; ++w) dst[w] = W[w];
-          }
-          a.scales[r * nb + j] = f2h(sqrtf(ss * (1.0f / BLK)));
+          for (int w = 0; w < BPT * WPB; w += 2) *reinterpret_cast<uint2*>(dst + w) = make_uint2(W[w], W[w + 1]);
         }
+        if constexpr (BPT == 2)
+          *reinterpret_cast<uint32_t*>(a.scales + r * nb + 2 * jt) = (uint32_t)norm[0] | ((uint32_t)norm[1] << 16);
+        else
+          a.scales[r * nb + jt] = norm[0];
       }
       fence_before();
       __syncwarp();
@@ -358,7 +392,7 @@ int launch_fast(const CodecParams& P, FastQuantArgs& a, cudaStream_t st) {
       // stages (+ 1024 bytes of alignment slack), B of every block, cell table
       auto smem_of = [](int nb) {
         return 1024 + (size_t)kStages * 128 * kTileCols * 2 + (size_t)nb * BLK * BLK * 2 +
-               (size_t)(kMaxCells + 1) * 32 * 4;
+               (size_t)(kMaxCells + 1) * 32 * 4 + (size_t)kRows * 4;
       };
       const size_t smem = smem_of(P.nb);
       cudaFuncAttributes fa;
@@ -391,6 +425,8 @@ int launch_fast(const CodecParams& P, FastQuantArgs& a, cudaStream_t st) {
   const int64_t max_ctas = (int64_t)sh.sms * sh.occ;
   a.per_cta = (a.n_tiles + max_ctas - 1) / max_ctas;
   const int64_t blocks = (a.n_tiles + a.per_cta - 1) / a.per_cta;
+  const int64_t cta_rows = (a.per_cta * kTileCols / P.d + 2) * 128 / a.map.H + 2;   // at most
+  a.staged = a.map.slot && a.n_vec < (1ll << 31) - 256 && a.map.n_slots <= ((1ll << 31) - 1) / a.map.H && cta_rows <= kRows;
   // programmatic dependent launch: this kernel's set-up may overlap the tail
   // of the previous kernel in the stream (its loads wait for that kernel)
   cudaLaunchConfig_t cfg = {};
@@ -421,6 +457,8 @@ int launch_quantize_fast(const CodecParams& P, const void* x, int64_t n_vec, int
   FastQuantArgs a;
   if (!make_cells(P, &a.ct)) return TQ_ERR_UNSUPPORTED;
   a.map = map;
+  a.by_heads = make_div(map.H);
+  a.by_page = make_div(map.slot ? map.S_cap : 1);
   a.x = static_cast<const __half*>(x);
   a.n_vec = n_vec;
   a.stride = stride;
