@@ -567,10 +567,9 @@ int tq_batch_slots(const int32_t* new_len, const int32_t* kv_len, int B, int64_t
  * rest.  Scores are compared to 48 bits; equal ones go to the lower w*V + v,
  * -inf among them (those of one beam to the higher logit first).
  *   logits       device, row b*W + w at logits + (b*W + w)*row_stride elements
- *                (fp16 or fp32, aligned to an element); the row of a finished
- *                beam, or of one whose score is -inf, may hold anything.  NaN
- *                counts as -inf and +inf as the largest finite number, here and
- *                in scores
+ *                (fp16 or fp32, aligned to an element); not read for a finished
+ *                beam or one whose score is -inf.  NaN counts as -inf and +inf
+ *                as the largest finite number, here and in scores
  *   scores       device fp32 [B, W], NULL: 0
  *   done         device uint8 [B, W] or NULL: beams that are finished (needs eos)
  *   eos          the token that finishes a beam, or -1

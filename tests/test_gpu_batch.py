@@ -39,8 +39,8 @@ def check(out, ref, status=0):
 
 
 @pytest.mark.parametrize("B,n_rows,page,pps", [
-    (1, 1, 32, 1), (1, 0, 32, 2), (3, 7, 32, 5), (5, 131, 96, 3), (8, 96, 32, 64), (300, 4099, 64, 33), (4096, 9001, 32, 3),
-    (4097, 9001, 32, 3), (9000, 20003, 32, 2), (17, 5000, 0, 0), (5000, 70001, 0, 0)])
+    (1, 1, 32, 1), (1, 0, 32, 2), (3, 7, 32, 5), (5, 131, 96, 3), (8, 96, 32, 64), (300, 4099, 64, 33), (1025, 9001, 32, 3),
+    (2048, 9001, 32, 3), (2049, 9001, 32, 3), (4096, 9001, 32, 3), (4097, 9001, 32, 3), (9000, 20003, 32, 2), (17, 5000, 0, 0), (5000, 70001, 0, 0)])
 def test_batch_slots(tqlib, B, n_rows, page, pps):
     from turboquant_kv_cache_gb300 import binding as tb
     rng = np.random.default_rng(B + n_rows)

@@ -95,6 +95,24 @@ def test_states_reorder_caches_and_shapes(tqlib):
     assert lens.tolist() == [3, 77, 50, 50, 33, 76, 1, 20]
 
 
+def test_copies_know_their_own_arrays(tqlib):
+    """Copied and pickled handles follow the copy's arrays, not the first one's."""
+    import copy
+    import pickle
+
+    from turboquant_kv_cache_gb300 import binding as tb
+    a = torch.arange(8, dtype=torch.int32, device="cuda").view(4, 2)
+    states = tb.StateArrays([a])
+    tb.tq_states_reorder(states, i32([0, 1, 2, 3]), 4)
+    for again in (copy.deepcopy(states), pickle.loads(pickle.dumps(states))):
+        tb.tq_states_reorder(again, i32([3, 3, 3, 3]), 4)
+        assert (again.arrays[0] == a[3]).all() and a.flatten().tolist() == list(range(8))
+    slots = tb.tq_batch_slots(i32([1, 1]), None, 2, S_cap=8)
+    again = copy.deepcopy(slots)
+    tb.tq_batch_slots(i32([2, 0]), None, S_cap=8, out=again)
+    assert slots.seq.tolist() == [0, 1] and again.seq.tolist() == [0, 0]
+
+
 def test_states_reorder_refusals(tqlib):
     from turboquant_kv_cache_gb300 import binding as tb
     a = torch.zeros(8, 2, 16, 4, dtype=torch.uint8, device="cuda")

@@ -914,24 +914,24 @@ def tq_append_kv_slots(cache, x, slot, stream=None):
     last dim contiguous) into a PackedKV cache, contiguous [B, H, S_cap] or
     paged: row r goes to slot[r] (int64 CUDA tensor [n_rows], BatchSlots.slot);
     rows whose slot is outside the cache (-1) are skipped."""
-    layout, dev = cache.layout, x.get_device()
+    dev, shape, layout, lead, codes = x.get_device(), x.shape, cache.layout, cache.lead_shape, cache.codes
     d = layout.head_dim
-    if x.dim() != 3 or x.shape[-1] != d or x.stride(-1) != 1 or dev < 0:
+    if len(shape) != 3 or shape[2] != d or dev < 0 or x.stride(2) != 1:
         raise ValueError("x must be a CUDA tensor [n_rows, H, head_dim] with a contiguous last dimension")
     if dev != _current_device():
         with _on(dev):
             return tq_append_kv_slots(cache, x, slot, stream)
-    n, H, _ = x.shape
-    lead = cache.lead_shape
-    if len(lead) != 3 or lead[1] != H or cache.codes.get_device() != dev:
+    n, H, _ = shape
+    if len(lead) != 3 or lead[1] != H or codes.get_device() != dev:
         raise ValueError("cache must have leading shape [B, H, S_cap] or [num_pages, H, page_size] on x's device")
     if not _is(slot, torch.int64, (n,), dev):
         raise ValueError("slot must be a contiguous int64 tensor of n_rows values on x's device")
     if not x.is_contiguous():
         x = _new(stream, x.contiguous)
-    st = _load().tq_append_kv_slots(ctypes.byref(layout), x.data_ptr(), _dtype_code(x.dtype), n, H, d, slot.data_ptr(),
-                                    lead[2], lead[0] * lead[2], _ptr(cache.S), cache.codes.data_ptr(),
-                                    cache.scales.data_ptr(), _ptr(cache.qjl), _ptr(cache.rnorm), _stream_on(stream, dev))
+    page = lead[2]
+    st = _load().tq_append_kv_slots(ctypes.byref(layout), x.data_ptr(), _dtype_code(x.dtype), n, H, d, slot.data_ptr(), page,
+                                    lead[0] * page, _ptr(cache.S), codes.data_ptr(), cache.scales.data_ptr(), _ptr(cache.qjl),
+                                    _ptr(cache.rnorm), _stream_on(stream, dev))
     if st:
         _check(st, "tq_append_kv_slots")
     return cache
@@ -1010,6 +1010,9 @@ class StateArrays:
         self.lens = list(lens) if isinstance(lens, (list, tuple)) else [lens] * len(self.arrays)
         self._of = None
         self.bound()
+
+    def __getstate__(self):
+        return {"arrays": self.arrays, "lens": self.lens, "_of": None}   # addresses are not copied or pickled
 
     def _tensors(self):
         if len(self.lens) != len(self.arrays):

@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kSumThreads = 1024;
-constexpr int kOneLaunch = 4096;   // sequences whose sums every block does for itself
+constexpr int kOneLaunch = 2048;   // sequences whose sums every block does for itself
 constexpr int kRowsPerThread = 4;
 constexpr int kAhead = 4;          // table pieces a warp has in flight
 constexpr int kMostSeqs = 1 << 20;
@@ -74,7 +74,7 @@ __device__ __forceinline__ uint32_t scan_rows(int64_t v, uint32_t (*s_part)[3], 
 }
 
 __device__ __forceinline__ bool length_ok(const SlotArgs& a, int len, int have) {
-  return len >= 0 && have >= 0 && (int64_t)len + have <= a.S_cap;
+  return (len | have) >= 0 && (uint32_t)len + (uint32_t)have <= (uint32_t)a.S_cap;   // S_cap is below 2^31
 }
 
 // {status, rows, 0, 0} of the whole batch; rows that are not laid out are none.
@@ -290,11 +290,13 @@ extern "C" int tq_batch_slots(const int32_t* new_len, const int32_t* kv_len, int
   const int64_t by_rows = (n_rows + tq::kThreads * tq::kRowsPerThread - 1) / (tq::kThreads * tq::kRowsPerThread);
   const int64_t pieces = (int64_t)n_rows * ((a.row_pages + 31) / 32);
   const int64_t by_table = (pieces + tq::kAhead * tq::kThreads / 32 - 1) / (tq::kAhead * tq::kThreads / 32);
-  const int64_t want = by_rows > by_table ? by_rows : by_table, most = 8 * tq::sm_count();
+  const int64_t want = by_rows > by_table ? by_rows : by_table, most = 4 * tq::sm_count();
   const int64_t grid = want < 1 ? 1 : want > most ? most : want;
   bool ok;
   if (B <= tq::kOneLaunch) {
-    const auto kern = B <= tq::kThreads ? tq::batch_slots_kernel<1> : tq::batch_slots_kernel<tq::kOneLaunch / tq::kThreads>;
+    constexpr int T = tq::kThreads;
+    const auto kern = B <= T ? tq::batch_slots_kernel<1> : B <= 4 * T ? tq::batch_slots_kernel<4>
+                                                                     : tq::batch_slots_kernel<tq::kOneLaunch / T>;
     kern<<<(unsigned)grid, tq::kThreads, 8 * (size_t)B, st>>>(a);
     ok = true;
   } else {

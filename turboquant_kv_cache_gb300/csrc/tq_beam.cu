@@ -54,7 +54,6 @@ struct BeamArgs {
   const uint8_t* done;       // [B][W] or NULL
   int64_t eos;
   int32_t B, W, V, n_out, S, keep;
-  int32_t eager;             // chunk: load before looking whether the row is needed
   int32_t parts, span;       // of a row; of a CTA (S = parts / span, rounded up)
   float2* part;              // [B W][S] maximum, sum
   uint64_t* cand;            // [B W][S][n_out] keys, descending; 0: none
@@ -502,8 +501,9 @@ constexpr int kStreamBits = 32; // logits of a thread in a part that streams
 // rest streams through shared memory that each thread loads for itself, so no
 // thread waits for another: what is above the bound goes to the list (a later
 // equal one loses by its index), and the terms of the sum are relative to the
-// first part's maximum.  After two parts, two more, four more and so on the list
-// is merged and the bound rises, so that about n_out logits pass it each time.
+// first part's maximum.  After two parts, and as their number doubles or
+// quadruples, the list is merged and the bound rises, so that about one to three
+// times n_out logits pass it each time.
 // Where more pass than the list holds, or the sum leaves its range (a part's
 // logits far above the first's, NaN, +inf), or the first part leaves less than
 // n_out, the parts since the last merge are selected from one by one.
@@ -511,9 +511,6 @@ template <bool F32, int NV>
 __global__ void __launch_bounds__(kChunkThreads, 5) beam_chunk_kernel(const BeamArgs a) {
   constexpr int VEC = Vec<F32>::N, PER = kChunkThreads * NV * VEC;   // logits of a part
   constexpr bool STREAMS = NV * VEC == kStreamBits;
-  // first of its call: nothing to wait for.  The second launch may begin early
-  // where there is room for it on every SM
-  if (a.eager) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   __shared__ ChunkShared<NV> sh;
   __shared__ uint4 s_ring[STREAMS ? kStages : 1][kUnit][STREAMS ? kChunkThreads : 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -528,22 +525,18 @@ __global__ void __launch_bounds__(kChunkThreads, 5) beam_chunk_kernel(const Beam
   uint64_t* out = a.cand + (int64_t)list * a.n_out;
   const float score = beam_score(a, row);
   const bool done = beam_done(a, row);
-  auto not_read = [&]() {
-    if (!done && score != -INFINITY) return false;
+  if (done || score == -INFINITY) {   // a row that is not read
     if (tid == 0) a.part[list] = make_float2(-INFINITY, 0.f);
     synthetic_part(a, list, beam, p0 * PER - lead, (int64_t)p1 * PER - lead, done && score != -INFINITY);
-    return true;
-  };
-  // a small grid is bound by latency: it loads a row before it knows whether it needs it
-  if (!a.eager && not_read()) return;
-  Vec<F32> x[NV];
-  load_vectors(x, base, p0 * kChunkThreads * NV, lead, a.V);
-  // units of the stream, unit u in ring stage u % kStages; up to u_in they lie inside the row
+    return;
+  }
+  // units of the stream, unit u in ring stage u % kStages; but for an unaligned
+  // row's first they lie inside the row up to u_in
   const int u_end = p1 * (NV / kUnit), u_in = (int)(((int64_t)a.V + lead) / (kChunkThreads * kUnit * VEC));
   const uint4* vectors = reinterpret_cast<const uint4*>(base - lead * esz) + tid;
   auto fetch = [&](int u) {
     uint4* to = &s_ring[u % kStages][0][tid];
-    if (u < min(u_in, u_end)) {
+    if (u < min(u_in, u_end) && (u > 0 || lead == 0)) {
 #pragma unroll
       for (int j = 0; j < kUnit; ++j) copy_async(to + j * kChunkThreads, vectors + (u * kUnit + j) * kChunkThreads);
     } else if (u < u_end) {
@@ -553,18 +546,22 @@ __global__ void __launch_bounds__(kChunkThreads, 5) beam_chunk_kernel(const Beam
     }
     copy_commit();
   };
-  const bool one = p1 - p0 == 1;
-  if (STREAMS && !one) {
-#pragma unroll
-    for (int k = 0; k < kStages - 1; ++k) fetch((p0 + 1) * (NV / kUnit) + k);
-  }
-  if (a.eager && not_read()) return;   // (a grid of CTAs with one part each)
+  Vec<F32> x[NV];
   float m, l;
-  if (!STREAMS || one) {
+  if (!STREAMS || p1 - p0 == 1) {
+    load_vectors(x, base, p0 * kChunkThreads * NV, lead, a.V);
     m = select_part<F32, NV>(x, a, base, beam, lead, p0, sh, out);
     l = (sh.sum[0] + sh.sum[1]) + (sh.sum[2] + sh.sum[3]);
   } else {
+    constexpr int FIRST = STREAMS ? NV / kUnit : 1;   // units of a part
+    const int u0 = p0 * FIRST;
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) fetch(u0 + k);
     for (int r = tid; r < a.n_out; r += kChunkThreads) sh.best[0][r] = 0;
+    copy_wait<kStages - 1 - FIRST>();
+    auto in_ring = [&](int j) { return &s_ring[(u0 + j / kUnit) % kStages][j % kUnit][tid]; };   // the first part's
+#pragma unroll
+    for (int j = 0; j < NV; ++j) x[j].raw = *in_ring(j);
     float mine;
     m = part_bound(x, a.n_out, sh, &mine);
     l = 0.f;
@@ -577,11 +574,16 @@ __global__ void __launch_bounds__(kChunkThreads, 5) beam_chunk_kernel(const Beam
       for (uint32_t live = reach(x, bound); live; live &= live - 1) {
         const int k = __ffs(live) - 1, i = ((p0 * NV + k / VEC) * kChunkThreads + tid) * VEC + k % VEC - lead;
         const int at = atomicAdd(&sh.above, 1);
-        if (at < kListCap) sh.key[at] = key_of(logit_at<F32>(base, i), i, beam);
+        if (at < kListCap)
+          sh.key[at] = key_of(logit_at<F32>(reinterpret_cast<const uint8_t*>(in_ring(k / VEC)), k % VEC), i, beam);
       }
     }
-    // parts [p, q), of which the first of all is in the list already
-    for (int p = p0, q = min(p0 + 2, p1); p < p1; p = q, q = min(2 * q - p0, p1)) {
+#pragma unroll
+    for (int k = 0; k < FIRST; ++k) fetch(u0 + kStages - 1 + k);   // into the first part's stages and the one before
+    // parts [p, q), of which the first of all is in the list already.  Up to 32
+    // candidates the list holds what passes the bound while the parts quadruple
+    const int grow = a.n_out <= 32 ? 4 : 2;
+    for (int p = p0, q = min(p0 + 2, p1); p < p1; p = q, q = min(p0 + grow * (q - p0), p1)) {
       const bool fits = m != -INFINITY && fabsf(m) < 1e37f && (p > p0 || found);
       const float shift = m * kLog2e;
       for (int u = (p > p0 ? p : p0 + 1) * (NV / kUnit); u < q * (NV / kUnit); ++u) {
@@ -631,7 +633,9 @@ __global__ void __launch_bounds__(kChunkThreads, 5) beam_chunk_kernel(const Beam
     for (int r = tid; r < a.n_out; r += kChunkThreads) out[r] = sh.best[0][r];
   }
   if (tid == 0) a.part[list] = make_float2(m, l);
-  if (!a.eager) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  // the second launch's blocks come late, when there is room on every SM: early
+  // ones gather on the first that has some, and take twice the time
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 }
 
 // (s, r) += (t, u), what the sum of s and t rounds off going to r.
@@ -1050,7 +1054,7 @@ extern "C" int tq_beam_select(const void* logits, tq_dtype dtype, int B, int W, 
   if (!workspace || workspace_bytes < tq::beam_bytes(rows, S, n_out, &cand_at)) return TQ_ERR_WORKSPACE;
   if (!tq::aligned16(workspace)) return TQ_ERR_ALIGN;
   const tq::BeamArgs a{logits, row_stride, scores, done, eos, B, W, (int32_t)V, n_out, (int32_t)S, keep_place ? 1 : 0,
-                       rows * cut.parts <= 4 * tq::sm_count() ? 1 : 0, (int32_t)cut.parts, (int32_t)cut.span,
+                       (int32_t)cut.parts, (int32_t)cut.span,
                        static_cast<float2*>(workspace),
                        reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(workspace) + cand_at), out_scores, out_parent,
                        out_token, out_done};

@@ -63,7 +63,7 @@ constexpr int kPlanThreads = 1024;
 // what one block takes: pages of the pool (8 or 4 a thread), entries of a fork, sequences of a compacted pool
 constexpr int kForkPages = 8192, kForkEntries = 1024;
 constexpr int kPackPages = 4096, kPackSeqs = 128;
-constexpr int kReorderPieces = 64;    // pieces of rows that one block takes over
+constexpr int kReorderPieces = 16;    // pieces of rows that one block takes over
 constexpr int kAhead = 8;             // table entries whose loads a thread has in flight
 constexpr int kMaxArrays = 128;       // cache arrays one move launch takes
 constexpr int kPiece = 16384;         // bytes one block copies at a time: four 16-byte loads in flight a thread
