@@ -216,6 +216,19 @@ def test_beam_select_strides_and_outputs(tqlib):
     check(x, s0, W, out)
 
 
+def test_beam_select_long_rows(tqlib):
+    """Rows of millions of tokens: the bound does not grow with their length, and
+    the best are found at both ends."""
+    from turboquant_kv_cache_gb300 import binding as tb
+    V = 5_000_011
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x = torch.randn(1, 2, V, generator=g, device="cuda")
+    x[0, 0, 0] = x[0, 1, V - 1] = 9.0
+    scores = torch.tensor([[-1.0, -1.25]], device="cuda")
+    for t in (x, x.half()):
+        check(t, scores, 5, tb.tq_beam_select(t, scores, n_out=5))
+
+
 def test_beam_select_long_offsets(tqlib):
     """Rows that lie behind 2^31 logits."""
     from turboquant_kv_cache_gb300 import binding as tb

@@ -128,6 +128,13 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// (s, r) += (t, u), what the sum of s and t rounds off going to r.
+__device__ __forceinline__ void add_to(float& s, float& r, float t, float u) {
+  const float all = s + t, part = all - s;
+  r += u + ((s - (all - part)) + (t - part));
+  s = all;
+}
+
 // The M-th largest of the 32 K values that the lanes of a warp hold, K each
 // (equal ones count one by one).  32 are sorted by a network of exchanges, of
 // more each is counted against all.
@@ -565,8 +572,15 @@ __global__ void __launch_bounds__(kChunkThreads, 5) beam_chunk_kernel(const Beam
     float mine;
     m = part_bound(x, a.n_out, sh, &mine);
     l = 0.f;
-    float2 sums[2] = {};
-    add_exp(x, m * kLog2e, sums);
+    // a unit's terms are added up by themselves, and the units' sums as a pair:
+    // however long the row, the sum is off by a few steps
+    float total = 0.f, rest = 0.f;
+    auto add_unit = [&](float2 (&sums)[2]) { add_to(total, rest, (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y), 0.f); };
+    {
+      float2 sums[2] = {};
+      add_exp(x, m * kLog2e, sums);
+      add_unit(sums);
+    }
     __syncthreads();
     float bound = sh.bound;
     const bool found = bound != -INFINITY;   // else the first part leaves less than n_out
@@ -593,7 +607,9 @@ __global__ void __launch_bounds__(kChunkThreads, 5) beam_chunk_kernel(const Beam
 #pragma unroll
         for (int j = 0; j < kUnit; ++j) y[j].raw = from[j * kChunkThreads];
         fetch(u + kStages - 1);   // into the stage before this one, whose logits have been used
+        float2 sums[2] = {};
         add_exp(y, shift, sums);
+        add_unit(sums);
         if (fmaxf(fmaxf(y[0].most(), y[1].most()), fmaxf(y[2].most(), y[3].most())) > bound) {
           for (uint32_t live = reach(y, bound); live; live &= live - 1) {
             const int k = __ffs(live) - 1;
@@ -604,8 +620,8 @@ __global__ void __launch_bounds__(kChunkThreads, 5) beam_chunk_kernel(const Beam
           }
         }
       }
-      float sum = (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
-      sums[0] = sums[1] = make_float2(0.f, 0.f);
+      float sum = total + rest;
+      total = rest = 0.f;
 #pragma unroll
       for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
       if (lane == 0) sh.sum[warp] = sum;
@@ -636,13 +652,6 @@ __global__ void __launch_bounds__(kChunkThreads, 5) beam_chunk_kernel(const Beam
   // the second launch's blocks come late, when there is room on every SM: early
   // ones gather on the first that has some, and take twice the time
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-}
-
-// (s, r) += (t, u), what the sum of s and t rounds off going to r.
-__device__ __forceinline__ void add_to(float& s, float& r, float t, float u) {
-  const float all = s + t, part = all - s;
-  r += u + ((s - (all - part)) + (t - part));
-  s = all;
 }
 
 // Exclusive prefix sum of v over the block; every thread calls it.

@@ -18,6 +18,8 @@
 //           pages to move by rank (compact)
 //   rename  tables and counts follow (compact)
 //   move    a block per entry shares the parent's pages (fork); page contents
+// Rows that change hands (reorder) go through the workspace: one launch checks the
+// entries and reads, the next writes rows and counts.
 // A small pool's call is bound by its launches (2 us each on the GPU, 3 on the
 // host), so there one block does everything but the move, two launches instead
 // of four or five.  What bounds that block are the counts it reads, up to eight
@@ -40,13 +42,20 @@
 //     pool of 8192                       8 x 255         8.5      8.6
 //                                        64 x 127       10.6      7.8
 // so the limits are 8192 pages and 1024 entries, 4096 pages and 128 sequences.
+// For a reorder, entries x pages a row (a piece is 256 table entries of a row):
+//     16 x 33 (16 pieces)    3.6   4.0
+//     32 x 256 (32)          4.4   3.9
+//     64 x 256 (64)          6.6   4.4
+//     512 x 64 (512)        25.3   4.5
+// so one block takes up to 16 pieces.
 //
 // Bound: launches, and for large pools the copies, which read and write every
 // moved byte once.  Measured in graph replays, with the call that frees pages
 // and a reset of the books before each: 3 freed, 4 forked and 4 grown over 512
 // pages of 28 KB 11.1 us; 60, 150 and 40 over 2000 pages in 64 arrays (134 MB
 // moved, 20 us at a copy's rate) 31.6 us; 512 pages compacted 9.1 us, 2500 in
-// 64 arrays (557 MB, 83 us) 107.3 us.
+// 64 arrays (557 MB, 83 us) 107.3 us.  A reorder of 512 rows of up to 512 pages
+// with its reset 6.1 us: two launches that each wait for a few loads in a row.
 #include <cuda_runtime.h>
 
 #include "tq_launch.cuh"
