@@ -87,7 +87,7 @@ def check(x, scores, n, out, done=None, eos=-1, keep=False):
 
 SIZES = [  # B, W, V, n_out
     (1, 1, 1, 1), (1, 1, 5, 5), (2, 3, 2, 6), (1, 4, 37, 8), (3, 5, 1000, 5), (2, 4, 32000, 8), (1, 1, 50021, 16), (7, 5, 4097, 5),
-    (1, 64, 700, 64), (2, 16, 30011, 32), (40, 8, 8191, 8), (1, 2, 200003, 64), (5, 1, 128256, 64), (600, 2, 3001, 2), (1, 64, 33, 64)]
+    (1, 64, 700, 64), (2, 16, 30011, 32), (40, 8, 8191, 8), (1, 2, 200003, 64), (5, 1, 128256, 64), (600, 2, 3001, 2), (1, 64, 33, 64), (100, 4, 30011, 4), (37, 5, 50021, 12), (9, 7, 128256, 40)]
 
 
 @pytest.mark.parametrize("f32", [True, False])
