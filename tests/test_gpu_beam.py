@@ -4,8 +4,8 @@ Bound of a score's error: the logits are exact, so it is that of lse plus half
 a step of the fp32 result.  A term exp(x - m) is off by 2^-22 (ex2.approx) and by
 the roundings of x - m and of its product with log2 e, 2^-23 |x - m| together;
 weighted with the terms themselves the mean of |x - m| is at most log V.  A
-thread adds up to 128 terms, the parts of a row some ten more sums and one more
-exp: (4 + 2 log V) + 140 + (4 + 2 log V) in units of 2^-24."""
+thread adds up less than 128 terms before it keeps what a sum rounds off, the
+parts of a row are some ten more sums and one more exp: (4 + 2 log V) + 140 + (4 + 2 log V) in units of 2^-24."""
 import numpy as np
 import pytest
 import torch

@@ -865,7 +865,7 @@ def tq_batch_slots(new_len, kv_len, n_rows=None, S_cap=None, page_table=None, pa
     """The place of every row of a ragged batch: sequence b has new_len[b] new
     rows behind its kv_len[b] cached tokens (int32 CUDA tensors [B]; kv_len None:
     0), packed row behind row in a buffer of n_rows.  The cache is contiguous
-    (S_cap) or paged (page_table int32 [B, pages_per_seq], page_size).  Returns
+    [B, H, S_cap] or paged (page_table int32 [B, pages_per_seq], page_size).  Returns
     a BatchSlots, `out` where it is given (its n_rows is then the call's);
     row_table: a table row for every row, for a new result."""
     dev, B = new_len.get_device(), new_len.numel()
