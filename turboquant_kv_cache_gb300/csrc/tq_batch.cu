@@ -11,15 +11,16 @@
 // sequences of its first and last row, a thread between those two.  Graph
 // replays, one launch against two:
 //   sequences x rows    256 x 2000    4.0   6.1 us
-//                       2048 x 16000  5.2   8.5
+//                       2048 x 16000  5.0   8.5
 //                       4096 x 32000  9.2   9.8
-//                       2048 x 1000003  10.9  11.3
+//                       2048 x 1000003  9.0   11.3
 //                       4096 x 1000003  22.2  13.3
 //
 // Bound: a launch and the latency of the sums for small batches (8 sequences and
 // 96 rows with a table row each 4.4 us); for large ones instructions, about three
-// a row and thread: 1000003 rows of 2048 sequences take 10.9 us, their 20 MB 3 us
-// at a copy's rate (13 us with a search of all sequences by each thread).
+// a row and thread: 1000003 rows of 2048 sequences take 9.2 us, their 20 MB 3 us
+// at a copy's rate (13 us with a search of all sequences by each thread, 11 with
+// lengths loaded 4 bytes at a time; 11 with six blocks an SM, 9.5 with two).
 #include <cuda_runtime.h>
 
 #include "tq_launch.cuh"
@@ -214,13 +215,27 @@ __global__ void __launch_bounds__(kThreads) batch_slots_kernel(const SlotArgs a)
   extern __shared__ int32_t s_end[];   // [B], then what a row of each lacks of its position
   int32_t* s_shift = s_end + a.B;
   __shared__ uint32_t s_part[kThreads / 32][3];
-  const int per = (a.B + kThreads - 1) / kThreads;
-  const int b0 = min(threadIdx.x * per, a.B), n = min(per, a.B - b0);
+  const int b0 = min((int)threadIdx.x * MOST, a.B), n = min(MOST, a.B - b0);
   int len[MOST], have[MOST];
+  // all of a thread's loads in flight, 16 bytes at a time where its run is whole
+  const bool wide = MOST % 4 == 0 && n == MOST &&
+                    ((reinterpret_cast<uintptr_t>(a.new_len) | reinterpret_cast<uintptr_t>(a.kv_len)) & 15u) == 0;
+  if (wide) {
+    if constexpr (MOST % 4 == 0) {
 #pragma unroll
-  for (int k = 0; k < MOST; ++k) {   // all of a thread's loads in flight
-    len[k] = k < n ? a.new_len[b0 + k] : 0;
-    have[k] = k < n && a.kv_len ? a.kv_len[b0 + k] : 0;
+      for (int k = 0; k < MOST; k += 4) {
+        const int4 l = *reinterpret_cast<const int4*>(a.new_len + b0 + k);
+        const int4 h = a.kv_len ? *reinterpret_cast<const int4*>(a.kv_len + b0 + k) : make_int4(0, 0, 0, 0);
+        len[k] = l.x, len[k + 1] = l.y, len[k + 2] = l.z, len[k + 3] = l.w;
+        have[k] = h.x, have[k + 1] = h.y, have[k + 2] = h.z, have[k + 3] = h.w;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < MOST; ++k) {
+      len[k] = k < n ? a.new_len[b0 + k] : 0;
+      have[k] = k < n && a.kv_len ? a.kv_len[b0 + k] : 0;
+    }
   }
   bool bad = false;
   int64_t sum = 0;
