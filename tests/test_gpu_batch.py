@@ -91,6 +91,23 @@ def test_batch_slots_statuses_and_defaults(tqlib, B):
     assert (out.slot[out.seq == 0] == -1).all() and (out.slot[out.seq > 0] >= 0).all()
 
 
+def test_batch_slots_least_outputs_on_a_stream(tqlib):
+    """Only what has to be there, new lengths that start off 16 bytes, a stream."""
+    from turboquant_kv_cache_gb300 import binding as tb
+    lens = i32([9, 2, 0, 5, 1])
+    e = lambda n, dt=torch.int32: torch.empty(n, dtype=dt, device="cuda")  # noqa: E731
+    out = tb.BatchSlots(e(5), None, e(9), e(9, torch.int64), None, None, None)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    tb.tq_batch_slots(lens[1:], None, S_cap=16, out=out, stream=side)
+    new = tb.tq_batch_slots(lens[1:], lens[1:], 9, S_cap=16, stream=side)
+    side.synchronize()
+    ref = layout_of([2, 0, 5, 1], [0] * 4, 9, 16)
+    for name in ("row_start", "pos", "slot"):
+        assert getattr(out, name).tolist() == ref[name]
+    check(new, layout_of([2, 0, 5, 1], [2, 0, 5, 1], 9, 16))
+
+
 def test_batch_slots_refusals(tqlib):
     from turboquant_kv_cache_gb300 import binding as tb
     n, t = i32([1, 2]), i32([[0, 1], [2, 3]])

@@ -156,6 +156,49 @@ def test_beam_select_masks_and_ties(tqlib, mask, V, f32):
     check(x, scores, 2 * W, tb.tq_beam_select(x, scores, n_out=2 * W, done=done, eos=1), done, 1)
 
 
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("mask", ["inf", "lowest", "same", "few_values", "sorted", "rising", "first_inf", "first_lowest", "few_first",
+                                  "last_hot", "late_nan", "late_inf", "huge"])
+def test_beam_select_streamed_rows(tqlib, mask, f32):
+    """Rows long and many enough that a CTA streams several parts: what the first
+    part says of the rest is wrong in each of these, or leaves nothing."""
+    from turboquant_kv_cache_gb300 import binding as tb
+    B, W, V = 31, 5, 20011
+    g = torch.Generator(device="cuda").manual_seed(17)
+    x = 2 * torch.randn(B, W, V, generator=g, device="cuda")
+    x = x if f32 else x.half()
+    low = torch.finfo(x.dtype).min
+    some = torch.rand(B, W, V, generator=g, device="cuda")
+    if mask in ("inf", "lowest"):
+        v = -float("inf") if mask == "inf" else low
+        x[some > 20 / V] = v
+        x[0, 1] = x[1] = v
+    elif mask == "same":
+        x[:] = -3.5
+    elif mask == "few_values":
+        x = x.round().clamp_max(3)
+    elif mask in ("sorted", "rising"):
+        x = x.sort(-1, descending=mask == "sorted").values
+    elif mask in ("first_inf", "first_lowest"):
+        x[:, :, :9000] = -float("inf") if mask == "first_inf" else low
+    elif mask == "few_first":
+        x[:, :, :4300] = -float("inf")
+        x[:, 1, 77] = x[:, 2, 4000] = 1.0
+    elif mask == "last_hot":
+        x[:, :, -40:] += 150              # e^150 is out of the range of 32 bits
+        x[:, 3, 12000] = 90
+    elif mask == "late_nan":
+        x[:, :, 15000::7] = float("nan")
+    elif mask == "late_inf":
+        x[:, 1, 17000] = x[:, 2, 5000] = x[:, 2, 19000] = float("inf")
+    else:
+        x = (x.float() * (1e36 if f32 else 3e4)).to(x.dtype)
+    scores = -torch.rand(B, W, generator=g, device="cuda")
+    scores[2, 1:] = -float("inf")
+    for n in (W, 48):
+        check(x, scores, n, tb.tq_beam_select(x, scores, n_out=n))
+
+
 @pytest.mark.parametrize("M,W,V", [(64, 64, 200000), (64, 1, 200000), (50, 2, 70000)])
 def test_beam_select_full_lists(tqlib, M, W, V):
     """More candidates above the bounds than the lists hold: each row's largest

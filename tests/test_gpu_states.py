@@ -210,6 +210,42 @@ def test_pages_reorder(tqlib, n_seqs, W, pps, shared, kind):
         np.testing.assert_array_equal(pool.ref.cpu().numpy(), r)
 
 
+@pytest.mark.parametrize("n_seqs,pps", [(8, 40), (96, 300)])
+def test_pages_reorder_replayed_and_on_a_stream(tqlib, n_seqs, pps):
+    """One workspace for calls in a row; a captured call replayed; another stream."""
+    from turboquant_kv_cache_gb300 import binding as tb
+    rng = np.random.default_rng(2)
+    table, held, ref = pool_of(rng, n_seqs, pps, pps // 3, 5, 4)
+    pool = tb.PagePool(i32(table), i32(held), i32(ref), 32)
+    ws = torch.empty(tb.tq_pages_reorder_workspace_bytes(n_seqs, pps, n_seqs), dtype=torch.uint8, device="cuda")
+    parent = i32(np.arange(n_seqs))
+    result = i32([0] * 4)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    tb.tq_pages_reorder(pool, parent, workspace=ws, result=result, stream=side)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tb.tq_pages_reorder(pool, parent, workspace=ws, result=result)
+        tb.tq_pages_reorder(pool, parent, workspace=ws, result=result)   # the same again
+    for _ in range(4):
+        p = rng.integers(0, n_seqs, size=n_seqs)
+        parent.copy_(i32(p))
+        graph.replay()
+        for _ in range(2):
+            t, h, r = table.copy(), held.copy(), ref.copy()
+            for i in range(n_seqs):
+                np.subtract.at(r, table[i, :held[i]], 1)
+            for i in range(n_seqs):
+                t[i, :held[p[i]]] = table[p[i], :held[p[i]]]
+                h[i] = held[p[i]]
+                np.add.at(r, table[p[i], :held[p[i]]], 1)
+            table, held, ref = t, h, r
+        torch.cuda.synchronize()
+        for got, want in ((pool.page_table, table), (pool.n_pages, held), (pool.ref, ref)):
+            np.testing.assert_array_equal(got.cpu().numpy(), want)
+
+
 @pytest.mark.parametrize("n_seqs,pps", [(8, 40), (600, 40)])
 def test_pages_reorder_refused_entries_change_nothing(tqlib, n_seqs, pps):
     from turboquant_kv_cache_gb300 import binding as tb
