@@ -126,7 +126,7 @@ def test_batch_slots_refusals(tqlib):
 
 LAYOUTS = [  # head_dim, block, bits, qjl, norm_correct, fp32 input: over the quantise kernels
     (128, 32, 3, 0, 0, False), (64, 64, 4, 0, 0, False), (256, 32, 4, 0, 0, False), (128, 128, 2, 128, 0, False),
-    (128, 128, 2, 64, 1, False), (64, 64, 1, 0, 0, True), (128, 32, 8, 0, 0, False), (256, 256, 3, 0, 1, True)]
+    (256, 64, 3, 0, 0, False), (128, 128, 2, 64, 1, False), (64, 64, 1, 0, 0, True), (128, 32, 8, 0, 0, False), (256, 256, 3, 0, 1, True)]
 
 
 @pytest.mark.parametrize("page", [0, 32, 96])
@@ -159,6 +159,30 @@ def test_append_slots(tqlib, d, block, bits, m, nc, f32, page):
         for t, b, w in zip(arrays, before, (want.codes, want.scales, want.qjl, want.rnorm)):
             b[torch.from_numpy(page_of).cuda(), :, torch.from_numpy(off).cuda()] = w[torch.from_numpy(fine).cuda()]
             assert torch.equal(t.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("d,block,bits,H,n", [(64, 64, 4, 1, 700001), (128, 32, 3, 3, 300001), (64, 32, 2, 8, 90001)])
+def test_append_slots_many_rows(tqlib, d, block, bits, H, n):
+    """Rows on both sides of what a block keeps the records of; the last rows of
+    a batch and of a block."""
+    from turboquant_kv_cache_gb300 import binding as tb
+    L = tb.make_layout(d, block, bits)
+    page = 64
+    pages = n // page + 2
+    g = torch.Generator(device="cuda").manual_seed(n)
+    x = torch.randn(n, H, d, generator=g, device="cuda").half()
+    slot = torch.randperm(pages * page, generator=g, device="cuda")[:n]
+    slot[::13] = -1
+    cache = tb.PackedKV(L, (pages, H, page))
+    cache.codes.zero_()
+    cache.scales.zero_()
+    tb.tq_append_kv_slots(cache, x, slot)
+    want = tb.tq_quantize_kv(L, x)
+    for got, rows in ((cache.codes, want.codes), (cache.scales, want.scales)):
+        live = slot >= 0
+        ref = torch.zeros_like(got)
+        ref[slot[live] // page, :, slot[live] % page] = rows[live]
+        assert torch.equal(got.view(torch.uint8), ref.view(torch.uint8))
 
 
 def test_append_slots_refusals(tqlib):
