@@ -227,6 +227,165 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const CodecParams P,
   }
 }
 
+// The same for 1..4 bits without QJL and norm correction (fp32 input, rotation
+// blocks of 128 and 256, 1 bit: what the tensor-core kernels do not take).  Codes
+// by magnitude: the boundaries are symmetric about 0 (the launch checks that), so
+// with m = #{beta_j > 0 : |y| > beta_j} a code is K/2 + m above 0 and K/2 - 1 - m
+// below, where |y| = beta_j counts (code = #{k : y > beta_k} takes the lower cell):
+// one more in the ordered bits of |y| makes it count.  m by bisection over
+// boundaries in registers.  The next vectors' values load during this one's.
+//
+// Bound: issue slots, 76% busy: 370 instructions for a thread's 8 values, of which
+// the transform's shuffles, the bisection and the norm's root and quotient are most.
+// 262144 vectors of 128 with a norm per vector, 2 bits, fp16: 53 us, into slots 59
+// (quantize_kernel 98 and 111; 11 at a copy's rate).  524288 of 64, 4 bits, fp32: 64
+// and 70 (139 and 154; 22).
+template <int D, bool F32>
+struct Chunk {   // 8 values of a vector as loaded
+  uint4 w[F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const QuantArgs& a, int64_t v, int i0) {
+    const uint4* p = F32 ? reinterpret_cast<const uint4*>(static_cast<const float*>(a.x) + v * a.stride + i0)
+                         : reinterpret_cast<const uint4*>(static_cast<const __half*>(a.x) + v * a.stride + i0);
+    w[0] = p[0];
+    if (F32) w[F32 ? 1 : 0] = p[1];
+  }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+    if (F32) {
+      const uint4 u0 = w[0], u1 = w[F32 ? 1 : 0];
+      x[0] = __uint_as_float(u0.x); x[1] = __uint_as_float(u0.y); x[2] = __uint_as_float(u0.z);
+      x[3] = __uint_as_float(u0.w); x[4] = __uint_as_float(u1.x); x[5] = __uint_as_float(u1.y);
+      x[6] = __uint_as_float(u1.z); x[7] = __uint_as_float(u1.w);
+    } else {
+      const uint32_t h[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[r]));
+        x[2 * r] = f.x;
+        x[2 * r + 1] = f.y;
+      }
+    }
+  }
+};
+
+// wht8 and wht_cross on pairs of values: a sum or difference is one multiply-add
+// with 1 or -1, whose product is exact, so the results are the same bits.
+__device__ __forceinline__ void wht8_pairs(float2 (&p)[4]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) p[q] = make_float2(p[q].x + p[q].y, p[q].x - p[q].y);
+  const float2 minus = make_float2(-1.f, -1.f);
+#pragma unroll
+  for (int h = 1; h < 4; h <<= 1)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if ((q & h) == 0) {
+        const float2 a = p[q], b = p[q + h];
+        p[q] = __fadd2_rn(a, b);
+        p[q + h] = __ffma2_rn(b, minus, a);
+      }
+}
+__device__ __forceinline__ void wht_cross_pairs(float2 (&p)[4], int sub, int lanes) {
+  for (int o = 1; o < lanes; o <<= 1) {
+    const float s = (sub & o) ? -1.f : 1.f;
+    const float2 s2 = make_float2(s, s);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float2 other = make_float2(__shfl_xor_sync(kFull, p[q].x, o), __shfl_xor_sync(kFull, p[q].y, o));
+      p[q] = __ffma2_rn(p[q], s2, other);
+    }
+  }
+}
+
+struct PlainArgs {
+  QuantArgs q;
+  int quick;                   // rows with slots: vectors and records are numbered in 31 bits
+  FastDiv by_heads, by_page;   // division by map.H and map.S_cap
+};
+
+template <int D, bool F32, int BITS>
+__global__ void __launch_bounds__(kThreads) quantize_plain_kernel(const CodecParams P, const PlainArgs args) {
+  constexpr int TPV = D / 8, VPW = 32 / TPV;   // threads per vector, vectors per warp
+  constexpr int K = 1 << BITS, POS = K / 2 - 1;
+  const QuantArgs& a = args.q;
+  const int lane = threadIdx.x & 31, sub = lane % TPV, vs = lane / TPV, i0 = sub * 8;
+  const int tpb = P.blk / 8;   // threads per rotation block
+  const uint32_t sb = sign_byte(P, i0);
+  const float root = sqrtf((float)P.blk);
+  int beta[POS > 0 ? POS : 1];   // positive boundaries as ordered bits
+#pragma unroll
+  for (int j = 0; j < POS; ++j) beta[j] = __float_as_int(P.bounds[K / 2 + j]);
+  const int64_t step = (int64_t)gridDim.x * (kThreads / 32) * VPW;
+  int64_t v = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * VPW + vs;
+  Chunk<D, F32> next;
+  if (v < a.n_vec) next.load(a, v, i0);
+  for (; v - vs < a.n_vec; v += step) {   // whole warps: they shuffle
+    const bool valid = v < a.n_vec;
+    float x[8];
+    next.values(x);
+    int64_t rv = -1;   // output record
+    if (valid) {
+      if (!args.quick) {
+        rv = map_row(a.map, v);
+      } else {
+        const uint32_t H = a.map.H, row = fast_div((uint32_t)v, args.by_heads), head = (uint32_t)v - row * H;
+        const int64_t slot = a.map.slot[row];
+        if ((uint64_t)slot < (uint64_t)a.map.n_slots)   // page H S + head S + (slot - page S)
+          rv = (uint32_t)slot + (uint32_t)a.map.S_cap * (fast_div((uint32_t)slot, args.by_page) * (H - 1) + head);
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < 8; ++r) x[r] = 0.f;
+    }
+    if (v + step < a.n_vec) next.load(a, v + step, i0);
+    float ss = 0.f;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) ss = fmaf(x[r], x[r], ss);
+    ss = group_sum(ss, tpb);
+    const float n = sqrtf(ss);
+    float2 p[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      p[q] = make_float2(flip(x[2 * q], (sb >> (2 * q)) & 1u), flip(x[2 * q + 1], (sb >> (2 * q + 1)) & 1u));
+    wht8_pairs(p);
+    wht_cross_pairs(p, sub, tpb);
+    const float inv = n > 0.f ? 1.f / (n * root) : 0.f;
+    uint32_t nib = 0;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const float y = ((r & 1) ? p[r >> 1].y : p[r >> 1].x) * inv;
+      const int u = (int)((__float_as_uint(y) & 0x7fffffffu) + (__float_as_uint(y) >> 31));
+      uint32_t m = 0;
+      if constexpr (BITS == 4) {
+        const bool c1 = u > beta[3];
+        const bool c2 = u > (c1 ? beta[5] : beta[1]);
+        const bool c3 = u > (c1 ? (c2 ? beta[6] : beta[4]) : (c2 ? beta[2] : beta[0]));
+        m = (c1 ? 4u : 0u) + (c2 ? 2u : 0u) + (c3 ? 1u : 0u);
+      } else if constexpr (BITS == 3) {
+        const bool c1 = u > beta[1];
+        m = (c1 ? 2u : 0u) + (u > (c1 ? beta[2] : beta[0]) ? 1u : 0u);
+      } else if constexpr (BITS == 2) {
+        m = u > beta[0] ? 1u : 0u;
+      }
+      nib |= (y > 0.f ? (K / 2) | m : m ^ (uint32_t)POS) << (4 * r);
+    }
+    if (rv >= 0 && (sub % tpb) == 0) a.scales[rv * P.nb + sub / tpb] = f2h(n);
+    uint32_t* rec = a.codes + rv * (D * BITS / 32);
+    const int gi = sub >> 2, w = sub & 3;
+    if constexpr (BITS == 4) {
+      if (rv >= 0) rec[sub] = nib;
+    } else if constexpr (BITS == 3) {
+      const uint32_t n3 = __shfl_sync(kFull, nib, lane | 3);
+      if (rv >= 0 && w < 3) rec[gi * 3 + w] = nib | (((n3 >> w) & 0x11111111u) << 3);
+    } else if constexpr (BITS == 2) {
+      const uint32_t n2 = __shfl_sync(kFull, nib, lane + 2 < 32 ? lane + 2 : lane);
+      if (rv >= 0 && w < 2) rec[gi * 2 + w] = nib | (n2 << 2);
+    } else {
+      const uint32_t n1 = __shfl_sync(kFull, nib, lane | 1), n2 = __shfl_sync(kFull, nib, lane | 2),
+                     n3 = __shfl_sync(kFull, nib, lane | 3);
+      if (rv >= 0 && w == 0) rec[gi] = nib | (n1 << 1) | (n2 << 2) | (n3 << 3);
+    }
+  }
+}
+
 struct DequantArgs {
   const uint32_t* codes;
   const uint16_t* scales;
@@ -375,6 +534,26 @@ int launch_quantize(const CodecParams& P, const QuantArgs& a, bool f32, const Co
   return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
+// Whether the boundaries are symmetric about 0, as every Lloyd-Max codebook's are.
+bool symmetric(const CodecParams& P) {
+  const int K = 1 << P.bits;
+  for (int j = 0; j < K - 1; ++j)
+    if (P.bounds[j] != -P.bounds[K - 2 - j]) return false;
+  return true;
+}
+
+template <int D, bool F32>
+int launch_plain(const CodecParams& P, const PlainArgs& a, cudaStream_t st) {
+  const int g = grid_for(a.q.n_vec, 32 / (D / 8));
+  switch (P.bits) {
+    case 4: quantize_plain_kernel<D, F32, 4><<<g, kThreads, 0, st>>>(P, a); break;
+    case 3: quantize_plain_kernel<D, F32, 3><<<g, kThreads, 0, st>>>(P, a); break;
+    case 2: quantize_plain_kernel<D, F32, 2><<<g, kThreads, 0, st>>>(P, a); break;
+    default: quantize_plain_kernel<D, F32, 1><<<g, kThreads, 0, st>>>(P, a); break;
+  }
+  return cudaGetLastError() == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+}
+
 template <int D>
 int launch_dequantize(const CodecParams& P, const DequantArgs& a, bool f32, const Codebook8& cb8, cudaStream_t st) {
   const int g = grid_for(a.n_vec, 32 / (D / 8));
@@ -429,6 +608,15 @@ int quantize_common(const tq_layout* layout, const void* x, tq_dtype x_dtype, in
   }
   if (quantize_qjl_eligible(P))
     return launch_quantize_qjl(P, x, f32, n_vec, x_row_stride, S, codes, scales, qjl_bits, qjl_rnorm, map, s);
+  if (P.bits <= 4 && !P.m && !P.nc && symmetric(P)) {
+    const PlainArgs p{a, map.slot && n_vec < (1ll << 31) && map.n_slots <= ((1ll << 31) - 1) / map.H, make_div(map.H),
+                      make_div(map.slot ? map.S_cap : 1)};
+    switch (P.d) {
+      case 64: return f32 ? launch_plain<64, true>(P, p, s) : launch_plain<64, false>(P, p, s);
+      case 128: return f32 ? launch_plain<128, true>(P, p, s) : launch_plain<128, false>(P, p, s);
+      default: return f32 ? launch_plain<256, true>(P, p, s) : launch_plain<256, false>(P, p, s);
+    }
+  }
   switch (P.d) {
     case 64: return launch_quantize<64>(P, a, f32, cb8, s);
     case 128: return launch_quantize<128>(P, a, f32, cb8, s);
