@@ -582,7 +582,8 @@ int tq_batch_slots(const int32_t* new_len, const int32_t* kv_len, int B, int64_t
  *                device [B, n_out] fp32, int32 (row b*W + w), int32, uint8 (may be
  *                NULL).  out_scores may be scores and out_done done where n_out
  *                is W
- *   workspace    tq_beam_workspace_bytes(...) bytes, 16-byte aligned */
+ *   workspace    tq_beam_workspace_bytes(...) bytes, 16-byte aligned; calls that
+ *                share one do not overlap on the GPU */
 int tq_beam_select(const void* logits, tq_dtype dtype, int B, int W, int64_t V, int64_t row_stride,
                    const float* scores, const uint8_t* done, int64_t eos, int n_out, int keep_place,
                    float* out_scores, int32_t* out_parent, int32_t* out_token, uint8_t* out_done, void* workspace,
@@ -622,7 +623,8 @@ int tq_states_reorder(const tq_state_array* states, int n_states, int n_seqs, in
  *            0}; status -1: a parent or sequence out of range, or a sequence
  *            named twice; nothing has changed
  *   workspace  tq_pages_reorder_workspace_bytes(n_seqs, pages_per_seq, n) bytes,
- *            16-byte aligned */
+ *            16-byte aligned; the calls on one pool, and those that share a
+ *            workspace, do not overlap on the GPU */
 int tq_pages_reorder(const tq_page_pool* pool, const int32_t* parent, const int32_t* seqs, int n, int32_t* result,
                      void* workspace, size_t workspace_bytes, void* stream);
 int tq_pages_reorder_workspace_bytes(int n_seqs, int pages_per_seq, int n, size_t* bytes);
