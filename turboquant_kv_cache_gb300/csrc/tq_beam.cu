@@ -108,6 +108,18 @@ struct Vec {
     const uint32_t w = (&raw.x)[p];
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
   }
+  // The same less m, conversion and difference of a half in one instruction.
+  __device__ __forceinline__ float2 pair_less(int p, float m) const {
+    if constexpr (F32) {
+      return __fadd2_rn(pair(p), make_float2(-m, -m));
+    } else {
+      float2 d;
+      asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\nadd.rn.f32.f16 %0, a, %3;\nadd.rn.f32.f16 %1, b, %3;\n}\n"
+          : "=f"(d.x), "=f"(d.y)
+          : "r"((&raw.x)[p]), "f"(-m));
+      return d;
+    }
+  }
   // The largest of the vector, -inf where all are NaN.
   __device__ __forceinline__ float most() const {
     if (F32) return fmaxf(fmaxf(fmaxf(at(0), at(1)), fmaxf(at(2), at(3))), -INFINITY);
@@ -227,17 +239,19 @@ __device__ __forceinline__ void synthetic_part(const BeamArgs& a, int64_t list, 
   }
 }
 
-// sum += exp(x - m) log2-wise, of a thread's logits in pairs: 2^(x log2 e - shift)
-// with shift = m log2 e, one multiply-add a term, whose product is not rounded.
-// What the rounding of shift adds to all of them is for the caller to take out.
+// sum += exp(x - m) of a thread's logits in pairs.  The difference comes first,
+// so that the term of m itself is 1 and no term's exponent is off by more than two
+// roundings of its own: one multiply-add, x log2 e less a rounded m log2 e, puts that
+// rounding into every term, and from logits of 2^30 on it is a factor that leaves
+// the range of 32 bits.
 template <bool F32, int NV>
-__device__ __forceinline__ void add_exp(const Vec<F32> (&x)[NV], float shift, float2 (&sum)[2]) {
-  const float2 by = make_float2(kLog2e, kLog2e), off = make_float2(-shift, -shift);
+__device__ __forceinline__ void add_exp(const Vec<F32> (&x)[NV], float m, float2 (&sum)[2]) {
+  const float2 by = make_float2(kLog2e, kLog2e);
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int q = 0; q < Vec<F32>::N / 2; ++q) {
-      const float2 t = __ffma2_rn(x[j].pair(q), by, off);
+      const float2 t = __fmul2_rn(x[j].pair_less(q, m), by);
       sum[q & 1] = __fadd2_rn(sum[q & 1], make_float2(ex2(t.x), ex2(t.y)));
     }
 }
@@ -245,12 +259,11 @@ __device__ __forceinline__ void add_exp(const Vec<F32> (&x)[NV], float shift, fl
 // Sum of exp(x - m) of a thread's logits, m finite.
 template <bool F32, int NV>
 __device__ __forceinline__ float sum_exp(Vec<F32> (&x)[NV], float m) {
-  const float shift = m * kLog2e;
   float2 sum[2] = {};
 #pragma unroll
   for (int j = 0; j < NV; ++j) x[j].keep_raw();
-  add_exp(x, shift, sum);
-  return ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) * ex2(-fmaf(m, kLog2e, -shift));
+  add_exp(x, m, sum);
+  return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
 // Shared memory of a chunk CTA.
@@ -344,7 +357,7 @@ __device__ __forceinline__ float select_part(Vec<F32> (&x)[NV], const BeamArgs& 
   const float m = part_bound(x, a.n_out, sh, &mine);
   const float mref = m == -INFINITY ? 0.f : m;
   float sum = sum_exp(x, mref);
-  if (!(sum < INFINITY) || fabsf(mref) > 1e37f) {   // NaN or +inf among them, or a product out of range
+  if (!(sum < INFINITY)) {   // NaN or +inf among them
     sum = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -585,7 +598,7 @@ __global__ void __launch_bounds__(kChunkThreads, 5) beam_chunk_kernel(const Beam
     auto add_unit = [&](float2 (&sums)[2]) { add_to(total, rest, (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y), 0.f); };
     {
       float2 sums[2] = {};
-      add_exp(x, m * kLog2e, sums);
+      add_exp(x, m, sums);
       add_unit(sums);
     }
     __syncthreads();
@@ -605,8 +618,7 @@ __global__ void __launch_bounds__(kChunkThreads, 5) beam_chunk_kernel(const Beam
     // candidates the list holds what passes the bound while the parts quadruple
     const int grow = a.n_out <= 32 ? 4 : 2;
     for (int p = p0, q = min(p0 + 2, p1); p < p1; p = q, q = min(p0 + grow * (q - p0), p1)) {
-      const bool fits = m != -INFINITY && fabsf(m) < 1e37f && (p > p0 || found);
-      const float shift = m * kLog2e;
+      const bool fits = m != -INFINITY && (p > p0 || found);
       for (int u = (p > p0 ? p : p0 + 1) * (NV / kUnit); u < q * (NV / kUnit); ++u) {
         copy_wait<kStages - 2>();
         const uint4* from = &s_ring[u % kStages][0][tid];
@@ -615,7 +627,7 @@ __global__ void __launch_bounds__(kChunkThreads, 5) beam_chunk_kernel(const Beam
         for (int j = 0; j < kUnit; ++j) y[j].raw = from[j * kChunkThreads];
         fetch(u + kStages - 1);   // into the stage before this one, whose logits have been used
         float2 sums[2] = {};
-        add_exp(y, shift, sums);
+        add_exp(y, m, sums);
         add_unit(sums);
         if (fmaxf(fmaxf(y[0].most(), y[1].most()), fmaxf(y[2].most(), y[3].most())) > bound) {
           for (uint32_t live = reach(y, bound); live; live &= live - 1) {
@@ -634,7 +646,7 @@ __global__ void __launch_bounds__(kChunkThreads, 5) beam_chunk_kernel(const Beam
       if (lane == 0) sh.sum[warp] = sum;
       __syncthreads();
       const int n = sh.above;
-      const float part = ((sh.sum[0] + sh.sum[1]) + (sh.sum[2] + sh.sum[3])) * ex2(-fmaf(m, kLog2e, -shift));
+      const float part = (sh.sum[0] + sh.sum[1]) + (sh.sum[2] + sh.sum[3]);
       if (fits && part < 1e30f && n <= kListCap) {
         merge_best(sh, a.n_out, n, false);
         l += part;
