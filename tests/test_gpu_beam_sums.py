@@ -49,3 +49,102 @@ def test_beam_select_large_logits_streamed(tqlib, at, sign):
     out = tb.tq_beam_select(x, scores, n_out=W)
     check(x, scores, W, out)
     assert torch.equal(out[0], scores.sort(-1, descending=True).values) and (out[2] == at).all()
+
+
+U = 2.0 ** -24   # half a step at 1: what a rounding to 32 bits is off by, at most, of its result
+
+
+def _sparse(B, V, f32, gap, seed):
+    """Rows of two tokens, 0 among the first 4000 and a larger one by gap to gap + 1
+    behind them; all others have no weight in 32 bits (exp(-200))."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.full((B, V), -200.0, device="cuda")
+    r = torch.arange(B, device="cuda")
+    first = torch.randint(0, 4000, (B,), generator=g, device="cuda")
+    last = torch.randint(4200, V, (B,), generator=g, device="cuda")
+    last[0], last[-1] = V - 1, 4200
+    x[r, first] = 0.0
+    x[r, last] = gap + torch.rand(B, generator=g, device="cuda")
+    return (x if f32 else x.half()), first, last
+
+
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("gap", [1, 5, 10, 20, 40, 60])
+@pytest.mark.parametrize("B", [800, 200, 3])
+def test_beam_select_late_maximum(tqlib, B, gap, f32):
+    """The first logits say little of the row's largest, as where a trained model is
+    sure of a token (a CTA for a row, for a few parts of one, for each part).
+
+    S = 1 + exp(-g): the one is exact, the other off by a step and a half in its
+    change of reference (expf a step, a product), their sum by a rounding, and the
+    logarithm, below 0.32, by a step of its own (logf)."""
+    from turboquant_kv_cache_gb300 import binding as tb
+    V = 20011
+    x, first, last = _sparse(B, V, f32, gap, B + gap)
+    score, parent, token, _ = tb.tq_beam_select(x.unsqueeze(1), n_out=2)
+    assert torch.equal(token[:, 0].long(), last) and torch.equal(token[:, 1].long(), first)
+    g = x.double()[torch.arange(B, device="cuda"), last]
+    log_s = torch.log1p(torch.exp(-g))
+    tol = U * (1 + 3 * torch.exp(-g)) + 2 * U * log_s
+    for k, want in enumerate((-log_s, -g - log_s)):
+        err = (score[:, k].double() - want).abs()
+        assert (err <= tol + U * want.abs()).all(), (k, (err - U * want.abs()).max().item())
+
+
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("gap", [30, 60])
+def test_beam_select_sure_rows(tqlib, gap, f32):
+    """The same with ordinary logits around: what they add to S is below half a step
+    of 1, so the best score is the beam's own."""
+    from turboquant_kv_cache_gb300 import binding as tb
+    B, W, V = 160, 5, 20011
+    g = torch.Generator(device="cuda").manual_seed(gap)
+    x = 2 * torch.randn(B, W, V, generator=g, device="cuda")
+    at = torch.randint(4200, V, (B, W, 1), generator=g, device="cuda")
+    x.scatter_(2, at, x.amax(-1, keepdim=True) + gap + torch.rand(B, W, 1, generator=g, device="cuda"))
+    x = x if f32 else x.half()
+    d = x.double()
+    assert ((torch.logsumexp(d, -1) - d.amax(-1)) < U / 2).all()
+    scores = -5 * torch.rand(B, W, generator=g, device="cuda")
+    out = tb.tq_beam_select(x, scores, n_out=W)
+    check(x, scores, W, out)
+    want, order = scores.sort(-1, descending=True)
+    assert torch.equal(out[0], want) and torch.equal(out[2].long(), at.squeeze(-1).gather(1, order))
+
+
+@pytest.mark.parametrize("f32", [True, False])
+def test_beam_select_orders_rows_of_different_gaps(tqlib, f32):
+    """Beams whose scores differ by 3e-7, each sure of its token by another amount:
+    S is 1 for all (gaps from 20 on), so the beams' own scores order the candidates."""
+    from turboquant_kv_cache_gb300 import binding as tb
+    B, W, V = 160, 5, 20011
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.cat([_sparse(B, V, f32, gap, gap)[0].unsqueeze(1) for gap in (20, 30, 40, 50, 60)], 1)
+    x = x[:, torch.randperm(W, generator=g, device="cuda")].contiguous()
+    place = torch.rand(B, W, generator=g, device="cuda").argsort(-1)
+    scores = -3e-7 * place
+    out = tb.tq_beam_select(x, scores, n_out=W)
+    rows = torch.arange(B, device="cuda")[:, None] * W + place.argsort(-1)
+    assert torch.equal(out[1].long(), rows)
+    assert (out[0].double() - scores.double().sort(-1, descending=True).values).abs().max() <= 2.1e-9 + 13e-7 * U
+
+
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("B", [800, 200, 3])
+def test_beam_select_rising_maxima(tqlib, B, f32):
+    """A row's largest logit replaced again and again, by steps of 1: sixteen terms
+    are added up in some order and change their reference, the sum with them
+    (a step and a half of a third of it each time): 15 + 3.4 roundings, and the
+    logarithm of 1.58 with its own step."""
+    from turboquant_kv_cache_gb300 import binding as tb
+    V = 20011
+    x = torch.full((B, 1, V), -200.0, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(B)
+    for k in range(16):
+        at = torch.randint(1200 * k, 1200 * (k + 1), (B, 1, 1), generator=g, device="cuda")
+        x.scatter_(2, at, float(k))
+    x = x if f32 else x.half()
+    score = tb.tq_beam_select(x, n_out=16)[0].double()
+    want = torch.arange(15, -1, -1, device="cuda").double()
+    want = want - torch.logsumexp(want, 0)
+    assert ((score - want).abs() <= 19 * U + U + U * want.abs()).all(), (score - want).abs().max()
