@@ -148,3 +148,28 @@ def test_beam_select_rising_maxima(tqlib, B, f32):
     want = torch.arange(15, -1, -1, device="cuda").double()
     want = want - torch.logsumexp(want, 0)
     assert ((score - want).abs() <= 19 * U + U + U * want.abs()).all(), (score - want).abs().max()
+
+
+@pytest.mark.parametrize("W,score,size", [(1, 1e30, 1e-10), (3, 1e30, 1e-10), (2, -3e38, 1e-10), (1, 0.0, 1e-19), (2, -4.5, 1e-19)])
+def test_beam_select_equal_scores_of_different_logits(tqlib, W, score, size):
+    """Logits whose differences a score does not hold: with a range of 2 size around 0
+    they are below half a step of a pair of floats (2^-48 of the score, or 2^-24 of
+    lse = log V where the score takes the first of the pair).  All candidates are equal then,
+    those of the lower beam come first and of one beam the higher logits, wherever in
+    the row they are; more of them than the list takes."""
+    from turboquant_kv_cache_gb300 import binding as tb
+    V, M = 128256, 64
+    g = torch.Generator(device="cuda").manual_seed(W)
+    x = size * (2 * torch.rand(1, W, V, generator=g, device="cuda") - 1)
+    out = tb.tq_beam_select(x, torch.full((1, W), score, device="cuda"), n_out=M)
+    order = np.lexsort((np.arange(V), -x[0, 0].double().cpu().numpy()))[:M]
+    assert (out[1] == 0).all() and out[2][0].tolist() == order.tolist()
+
+
+@pytest.mark.parametrize("f32", [True, False])
+def test_beam_select_equal_logits(tqlib, f32):
+    """Rows of one value: equal scores of equal logits go by place, also where they are more than the list takes."""
+    from turboquant_kv_cache_gb300 import binding as tb
+    x = torch.full((2, 3, 128256), 0.5, device="cuda", dtype=torch.float32 if f32 else torch.float16)
+    out = tb.tq_beam_select(x, torch.tensor([[-1.0, -1.0, -1.0], [-2.0, -1.0, -1.0]], device="cuda"), n_out=64)
+    assert out[2].tolist() == [list(range(64))] * 2 and out[1].tolist() == [[0] * 64, [4] * 64]

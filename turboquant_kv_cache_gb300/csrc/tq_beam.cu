@@ -742,9 +742,118 @@ __device__ __forceinline__ uint64_t second_key(uint64_t key) {
 __device__ __forceinline__ int key_beam(uint64_t second) { return kMaxBeams - 1 - (int)(second >> 58); }
 __device__ __forceinline__ int key_token(uint64_t second) { return (int)(kTokenMask - ((uint32_t)second & kTokenMask)); }
 
-__global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamArgs a) {
+// An entry's score as an ordered key; 0: none.  A pair is brought into the one form
+// in which it orders as (first, second).  `row`: of each beam, its maximum and what a
+// logit less that lacks of its score.
+__device__ __forceinline__ uint64_t score_key(const float4* row, uint64_t k) {
+  if (!k) return 0;
+  const float x = unordered((uint32_t)(k >> 32));
+  if (x == -INFINITY) return kNothing;
+  const float4 q = row[kMaxBeams - 1 - ((uint32_t)k >> 26)];
+  float hi = x, lo = 0.f;
+  add_to(hi, lo, -q.x, 0.f);
+  add_to(hi, lo, q.y, q.z);
+  const float top = hi + lo;
+  if (!(top > -INFINITY)) return kNothing + 1;   // out of the range of 32 bits
+  return ((uint64_t)ordered(top) << 32) | ordered(lo - (top - hi));
+}
+
+// The entries [*first, *end) of a list (M, descending) whose score is `bound`.
+__device__ __forceinline__ void equal_range(const float4* row, const uint64_t* list, int M, uint64_t bound, int* first, int* end) {
+  int lo = 0, hi = M;   // the first that is not above it
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    if (score_key(row, list[mid]) > bound) lo = mid + 1; else hi = mid;
+  }
+  *first = lo;
+  hi = M;               // the first that is below it, or none
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    const uint64_t k = score_key(row, list[mid]);
+    if (k >= bound && k != 0) lo = mid + 1; else hi = mid;
+  }
+  *end = lo;
+}
+
+// Whether entries of one beam have the score `bound` and different logits (tiny
+// differences beside a large score, which a pair does not hold).
+__device__ __forceinline__ bool equal_of_many(const float4* row, const uint64_t* cand, int M, int W, int S, uint64_t bound) {
+  __shared__ uint32_t s_low[kMaxBeams], s_high[kMaxBeams];
+  const int tid = threadIdx.x;
+  if (tid < kMaxBeams) {
+    s_low[tid] = 0xffffffffu;
+    s_high[tid] = 0;
+  }
+  __syncthreads();
+  for (int h = tid; h < W * S; h += kPickThreads) {
+    const uint64_t* list = cand + (int64_t)h * M;
+    int first, end;
+    equal_range(row, list, M, bound, &first, &end);
+    if (first < end) {
+      atomicMax(&s_high[h / S], (uint32_t)(list[first] >> 32));
+      atomicMin(&s_low[h / S], (uint32_t)(list[end - 1] >> 32));
+    }
+  }
+  __syncthreads();
+  return __syncthreads_or(tid < W && s_low[tid] < s_high[tid]);
+}
+
+// The M best entries from `least` on, one after the other, each the best behind the
+// last, to `to` and `to2` (scores and what orders equal ones); `mine`: the best of this
+// thread's lists.
+__device__ __forceinline__ void one_by_one(const float4* row, const uint64_t* cand, int M, int lists, uint64_t least, uint64_t mine,
+                                        uint64_t* to, uint64_t* to2) {
   constexpr int WARPS = kPickThreads / 32;
-  __shared__ float4 s_row[kMaxBeams];   // a row's maximum, and what a logit then lacks of its score
+  __shared__ uint64_t s_top[WARPS], s_top2[WARPS];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint64_t last = ~0ull, last2 = ~0ull;
+  for (int r0 = 0; r0 < M; ++r0) {
+    uint64_t best = 0, best2 = 0;
+    if (mine >= least)
+      for (int h = tid; h < lists; h += kPickThreads)
+        for (int r = 0; r < M; ++r) {
+          const uint64_t raw = cand[(int64_t)h * M + r], k = score_key(row, raw), second = second_key(raw);
+          if (k < least || k < best) break;
+          if ((k < last || (k == last && second < last2)) && (k > best || second > best2)) {
+            best = k;
+            best2 = second;
+          }
+        }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      const uint64_t k = __shfl_xor_sync(kFull, best, o), k2 = __shfl_xor_sync(kFull, best2, o);
+      if (k > best || (k == best && k2 > best2)) {
+        best = k;
+        best2 = k2;
+      }
+    }
+    __syncthreads();   // the last round's results have been read
+    if (lane == 0) {
+      s_top[warp] = best;
+      s_top2[warp] = best2;
+    }
+    __syncthreads();
+    for (int w = 0; w < WARPS; ++w) {
+      if (s_top[w] > best || (s_top[w] == best && s_top2[w] > best2)) {
+        best = s_top[w];
+        best2 = s_top2[w];
+      }
+    }
+    if (tid == 0) {
+      to[r0] = best;
+      to2[r0] = best2;
+    }
+    last = best;
+    last2 = best2;
+  }
+}
+
+// (Four blocks an SM: 64 registers instead of 40, which the compiler takes by itself.
+// 2 requests of 4 beams 7.2 -> 7.1 us, 12 of 32 beams and 64 kept 220 -> 214; with two
+// blocks 1000 requests of 4 beams take 100 us instead of 98)
+__global__ void __launch_bounds__(kPickThreads, 4) beam_pick_kernel(const BeamArgs a) {
+  constexpr int WARPS = kPickThreads / 32;
+  __shared__ float4 s_row[kMaxBeams];   // see score_key
   __shared__ uint32_t s_max[kPickThreads];
   __shared__ int s_list[kPickThreads], s_lists;
   __shared__ uint64_t s_score[kPickCap], s_second[kPickCap];
@@ -804,20 +913,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamArgs 
     }
   }
   __syncthreads();
-  // an entry's score as an ordered key; 0: none.  A pair is brought into the one
-  // form in which it orders as (first, second)
-  auto score_of = [&](uint64_t k) -> uint64_t {
-    if (!k) return 0;
-    const float x = unordered((uint32_t)(k >> 32));
-    if (x == -INFINITY) return kNothing;
-    const float4 q = s_row[kMaxBeams - 1 - ((uint32_t)k >> 26)];
-    float hi = x, lo = 0.f;
-    add_to(hi, lo, -q.x, 0.f);
-    add_to(hi, lo, q.y, q.z);
-    const float top = hi + lo;
-    if (!(top > -INFINITY)) return kNothing + 1;   // out of the range of 32 bits
-    return ((uint64_t)ordered(top) << 32) | ordered(lo - (top - hi));
-  };
+  auto score_of = [&](uint64_t k) { return score_key(s_row, k); };
   // entry r of list h (descending in r)
   auto entry = [&](int h, int r, uint64_t* second) {
     const uint64_t k = cand[(int64_t)h * M + r];
@@ -910,48 +1006,11 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamArgs 
     __syncthreads();
     n = gather(bound + 1);
   }
-  if (n > kPickCap) {
-    // one after the other, each the best behind the last
-    uint64_t last = ~0ull, last2 = ~0ull;
-    for (int r0 = 0; r0 < M; ++r0) {
-      uint64_t best = 0, best2 = 0;
-      if (mine > bound)
-        for (int h = tid; h < lists; h += kPickThreads)
-          for (int r = 0; r < M; ++r) {
-            const uint64_t k = entry(h, r, &second);
-            if (k <= bound || k < best) break;
-            if ((k < last || (k == last && second < last2)) && (k > best || second > best2)) {
-              best = k;
-              best2 = second;
-            }
-          }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        const uint64_t k = __shfl_xor_sync(kFull, best, o), k2 = __shfl_xor_sync(kFull, best2, o);
-        if (k > best || (k == best && k2 > best2)) {
-          best = k;
-          best2 = k2;
-        }
-      }
-      __syncthreads();
-      if (lane == 0) {
-        s_score[warp] = best;
-        s_second[warp] = best2;
-      }
-      __syncthreads();
-      for (int w = 0; w < WARPS; ++w) {
-        if (s_score[w] > best || (s_score[w] == best && s_second[w] > best2)) {
-          best = s_score[w];
-          best2 = s_second[w];
-        }
-      }
-      if (tid == 0) {
-        s_best[r0] = best;
-        s_best2[r0] = best2;
-      }
-      last = best;
-      last2 = best2;
-    }
+  // more are equal to the bound than the list takes: those of one logit go by place,
+  // as the lists do; different ones of a beam may lie in any of its lists
+  const bool of_many = n < M && bound > kNothing && equal_of_many(s_row, cand, M, a.W, a.S, bound);
+  if (n > kPickCap || of_many) {
+    one_by_one(s_row, cand, M, lists, of_many ? bound : bound + 1, mine, s_best, s_best2);
     n = M;
   } else {
     for (int i = tid; i < n; i += kPickThreads) {
@@ -965,25 +1024,12 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamArgs 
       }
     }
   }
-  // what is equal to the bound, in order of place, as lists and their equal entries are
+  // what is equal to the bound, in order of place, as lists and their equal entries of one logit are
   if (n < M) {
     for (int h0 = 0, got = n; got < M && h0 < lists; h0 += kPickThreads) {
       const int h = h0 + tid;
       int first = 0, end = 0;
-      if (h < lists) {
-        int hi = M;   // the first entry that is not above the bound
-        while (first < hi) {
-          const int mid = (first + hi) / 2;
-          if (entry(h, mid, &second) > bound) first = mid + 1; else hi = mid;
-        }
-        end = first;
-        hi = M;       // the first that is below it, or none
-        while (end < hi) {
-          const int mid = (end + hi) / 2;
-          const uint64_t k = entry(h, mid, &second);
-          if (k >= bound && k != 0) end = mid + 1; else hi = mid;
-        }
-      }
+      if (h < lists) equal_range(s_row, cand + (int64_t)h * M, M, bound, &first, &end);
       int total;
       const int at = got + scan_block(end - first, s_part, &total);
       for (int r = first; r < end && at + r - first < M; ++r) s_from[at + r - first] = h * M + r;
