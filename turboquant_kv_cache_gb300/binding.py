@@ -1020,6 +1020,8 @@ class StateArrays:
         of = []
         for a, n in zip(self.arrays, self.lens):
             if isinstance(a, PackedKV):
+                if a.page_table is not None:
+                    raise ValueError("a paged cache's states are its table rows (tq_pages_reorder)")
                 of += [(t, n) for t in (a.codes, a.scales, a.qjl, a.rnorm) if t is not None]
             else:
                 of.append((a, n))
@@ -1034,8 +1036,6 @@ class StateArrays:
         if not of:
             raise ValueError("no arrays")
         dev, n_seqs = of[0][0].get_device(), of[0][0].shape[0]
-        if any(isinstance(a, PackedKV) and a.page_table is not None for a in self.arrays):
-            raise ValueError("a paged cache's states are its table rows (tq_pages_reorder)")
         structs = (tq_state_array * len(of))()
         spans = []
         for s, (t, n) in zip(structs, of):
