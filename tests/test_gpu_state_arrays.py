@@ -26,3 +26,11 @@ def test_cache_that_became_paged_is_refused(tqlib):
     cache.page_table = None
     tb.tq_states_reorder(states, parent, 4)
     assert torch.equal(cache.codes, codes[[1, 0, 3, 2]])
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 1, 2**32 + 16), (1, 2**32 + 1, 1)])
+def test_sizes_past_32_bits_are_refused(tqlib, shape):
+    """Slots of 4 GB and more, or as many heads: a slot of 2^32 + 16 bytes is not one of 16."""
+    from turboquant_kv_cache_gb300 import binding as tb
+    with pytest.raises(ValueError):
+        tb.StateArrays([torch.empty(shape, dtype=torch.uint8, device="cuda")])

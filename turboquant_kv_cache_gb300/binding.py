@@ -1048,6 +1048,8 @@ class StateArrays:
             size = t.element_size()
             for k in t.shape[3:]:
                 size *= k
+            if heads > 0x7fffffff or size > 0x7fffffff:
+                raise ValueError("a state array has fewer than 2^31 heads, and slots of fewer than 2^31 bytes")
             s.data, s.len, s.cap, s.heads, s.bytes = t.data_ptr(), _ptr(n), cap, heads, size
             if t.numel():
                 spans.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), 0))
