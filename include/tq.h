@@ -624,7 +624,8 @@ int tq_states_reorder(const tq_state_array* states, int n_states, int n_seqs, in
  *            named twice; nothing has changed
  *   workspace  tq_pages_reorder_workspace_bytes(n_seqs, pages_per_seq, n) bytes,
  *            16-byte aligned; the calls on one pool, and those that share a
- *            workspace, do not overlap on the GPU */
+ *            workspace, do not overlap on the GPU
+ * TQ_ERR_ALIGN where workspace, or an array to its elements, is not aligned. */
 int tq_pages_reorder(const tq_page_pool* pool, const int32_t* parent, const int32_t* seqs, int n, int32_t* result,
                      void* workspace, size_t workspace_bytes, void* stream);
 int tq_pages_reorder_workspace_bytes(int n_seqs, int pages_per_seq, int n, size_t* bytes);

@@ -886,6 +886,8 @@ extern "C" int tq_pages_reorder(const tq_page_pool* pool, const int32_t* parent,
   if (!workspace || workspace_bytes < tq::carve_reorder(nullptr, pool->n_seqs, pool->pages_per_seq, n, nullptr))
     return TQ_ERR_WORKSPACE;
   if (!tq::aligned16(workspace)) return TQ_ERR_ALIGN;
+  for (const int32_t* p : {parent, seqs, static_cast<const int32_t*>(result)})
+    if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0) return TQ_ERR_ALIGN;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   tq::ReorderArgs a{};
   a.pool = *pool;
