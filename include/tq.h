@@ -528,7 +528,7 @@ int tq_pages_compact(const tq_page_pool* pool, const tq_kv_view* caches, int n_c
 /* Workspace bytes of the two calls above (host). */
 int tq_pages_workspace_bytes(int n_seqs, int num_pages, int n, size_t* bytes);
 
-/* Where the rows of a ragged batch go.  Sequence b (of B) has kv_len[b] tokens
+/* Where the rows of a ragged batch go.  Sequence b (of B, 1 or more) has kv_len[b] tokens
  * in the cache (NULL: none) and new_len[b] new ones; their rows follow each
  * other, sequence behind sequence, in a buffer of n_rows rows.
  *   new_len, kv_len  device int32 [B]
@@ -565,7 +565,10 @@ int tq_batch_slots(const int32_t* new_len, const int32_t* kv_len, int B, int64_t
  *   scores[w] + logits[w][v] - log sum_u exp(logits[w][u]);
  * a finished beam has one candidate, eos at its own score, and -inf for the
  * rest.  Scores are compared to 48 bits; equal ones go to the lower w*V + v,
- * -inf among them (those of one beam to the higher logit first).
+ * -inf among them (those of one beam to the higher logit first).  The sum of a
+ * row is formed in 32 bits, relative to its largest logit: the order in one row
+ * is exact, and its logarithm, which counts between rows, is off by 5e-7 at most
+ * as measured, and exact where one token leaves the others no weight.
  *   logits       device, row b*W + w at logits + (b*W + w)*row_stride elements
  *                (fp16 or fp32, aligned to an element); not read for a finished
  *                beam or one whose score is -inf.  NaN counts as -inf and +inf
@@ -573,6 +576,7 @@ int tq_batch_slots(const int32_t* new_len, const int32_t* kv_len, int B, int64_t
  *   scores       device fp32 [B, W], NULL: 0
  *   done         device uint8 [B, W] or NULL: beams that are finished (needs eos)
  *   eos          the token that finishes a beam, or -1
+ *   B            1 or more
  *   n_out        candidates kept, at most W*V; at most 64, as W
  *   keep_place   0: candidates by descending score.  1 (n_out == W): the best
  *                child of each beam that has one is in the beam's own place, the
@@ -608,7 +612,7 @@ typedef struct {
  * of W (at most 64) and p is one of s's group; a parent that is not leaves s
  * as it is.  The lengths are read only (as an array of states they are one of
  * their own, of another call behind this one); no two arrays overlap.
- *   parent   device int32 [n_seqs] */
+ *   parent   device int32 [n_seqs], in none of the arrays */
 int tq_states_reorder(const tq_state_array* states, int n_states, int n_seqs, int W, const int32_t* parent,
                       void* stream);
 

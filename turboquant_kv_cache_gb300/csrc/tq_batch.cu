@@ -17,9 +17,11 @@
 //                       4096 x 1000003  22.2  13.3
 //
 // Bound: a launch and the latency of the sums for small batches (8 sequences and
-// 96 rows with a table row each 4.4 us); for large ones instructions, about three
-// a row and thread: 1000003 rows of 2048 sequences take 9.2 us, their 20 MB 3 us
-// at a copy's rate (13 us with a search of all sequences by each thread, 11 with
+// 96 rows with a table row each 4.4 us; 16000 rows of 2048 sequences 5.0).  Large
+// ones have that too, before a block's first row: 1000003 rows of 2048 sequences take
+// 9.2 us, their 20 MB 3 us at a copy's rate.  140 instructions a row keep 44% of the
+// issue slots busy, and the rows are 1.6 rounds of the grid: latency and instructions
+// about alike (13 us with a search of all sequences by each thread, 11 with
 // lengths loaded 4 bytes at a time; 11 with six blocks an SM, 9.5 with two).
 #include <cuda_runtime.h>
 

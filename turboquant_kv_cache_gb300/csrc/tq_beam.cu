@@ -30,13 +30,19 @@
 // Bound.  Small: two launches, each a few loads, sorts and rankings in a row, in
 // code that runs once (short code is faster here than unrolled code): 8 rows of
 // 32000 fp16 logits 6.9 us.  Large: 512 rows of 128256, a fifth of them finished,
-// 53 us: 46 for the logits at 4.6 TB/s (a copy's rate would be 31), the rest is
-// the second launch.  There a part's bound and the merges of its lists are
-// latency that its own loads do not cover, and a fp16 logit's seven instructions
-// (half of them conversion, exp and sum) bound a row of them: 42 us for 512 rows,
-// 19 at a copy's rate.  Steps: selection in registers with 64-bit floating-point
-// scores 177 us; scores in pairs of floats, lists without divisions 70; rows
-// streamed through shared memory 58; bounds from a sorting network 53.
+// 49 us: 41 for the logits at 5.0 TB/s (a copy's rate would be 31), the rest is
+// the second launch.  There a part's bound and the merges of its lists are latency
+// that three CTAs of four warps an SM do not cover (16% of the warps are live, 39%
+// of the issue slots taken, of fp16 rows 51%): all 512 rows 54 us, of fp16 43 to 46,
+// where a copy's rate would be 39 and 19.  Wide: with more than 16 kept the lists of
+// few rows do not give the second launch's bound enough groups, and most entries
+// pass it; above kPickCap they are selected one after the other.  8 requests of 32
+// beams, 32000 fp32: 16 kept 21 us, 32 78, 64 180.
+// Steps: selection in registers with 64-bit floating-point scores 177 us; scores in
+// pairs of floats, lists without divisions 70; rows streamed through shared memory
+// 58; bounds from a sorting network 53; a unit's terms added up behind the branch for
+// what goes to the list 49.  Not kept: sums of threads and warps as pairs of floats
+// (lse within 3e-7 instead of 5e-7) 55.
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -1084,8 +1090,8 @@ Cut cut_of(int64_t rows, int64_t V, bool f32) {
   const int64_t vec = f32 ? 4 : 8, sms = sm_count();
   // as many vectors as leave at least four CTAs an SM, for fewer candidates and
   // one selection per more logits; at most kStreamBits logits of a thread.  Whole
-  // calls with four, two and eight CTAs an SM: 64 rows of 32000 fp32 7.9, 8.8, 9.2
-  // us, 16 of 128256 8.7, 8.2, 11.1
+  // calls with four, two and eight CTAs an SM: 64 rows of 32000 fp32 7.6, 8.4, 8.8
+  // us, 16 of 128256 8.1, 7.8, 11.0
   Cut c{f32 ? 2 : 1, 0, 1, 0};
   for (int64_t nv = kStreamBits / vec; nv > c.nv; nv /= 2) {
     const int64_t per = kChunkThreads * nv * vec;
@@ -1095,7 +1101,7 @@ Cut cut_of(int64_t rows, int64_t V, bool f32) {
   c.parts = (V + vec - 1 + per - 1) / per;
   if (c.nv * vec == kStreamBits) {
     // the CTAs that run at a time, whole rows where there are more of those.  512
-    // rows of 128256: one CTA a row 61 us, two 66
+    // rows of 128256: one CTA a row 54 us, two 66
     const int64_t most = 5 * sms, lists = rows < most ? most / rows : 1;
     c.span = (c.parts + lists - 1) / lists;
   }
